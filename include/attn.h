@@ -542,6 +542,196 @@ attn_status attn_decode_schedule_host(int B, int Hkv, int S_q, int S_cap, attn_m
                                       const int* cache_len, int n_sm, int* n_cta, int* tile_prefix,
                                       long long* share);
 
+/*
+ * ---------------------------------------------------------------- rotary positions
+ * Rotary position embedding of query and key rows, and its gradient: pair p of a row turns
+ * by the angle t = f_p * position,
+ *
+ *     (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t),   p = 0 .. rot/2 - 1,
+ *
+ * with the frequencies f_p = base^(-2p / rot) ("Transformer 架构及其变体" (aaai.latere.ai), the section on RoPE:
+ * rotations applied to q and k before the score).  The elements behind the first `rot` are
+ * copied.  Pairs are elements (p, p + rot/2), ATTN_ROPE_HALF, or (2p, 2p + 1),
+ * ATTN_ROPE_INTERLEAVED.  For contexts s = factor times longer than the original:
+ *   ATTN_ROPE_LINEAR  f_p / s (positions interpolated);
+ *   ATTN_ROPE_NTK     base * s^(rot / (rot - 2)) in place of base (the lowest frequency is
+ *                     divided by s, the highest kept; rot > 2);
+ *   ATTN_ROPE_YARN    f_p (g + (1 - g) / s), g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ *                     with r = original_len f_p / (2 pi) the turns of the pair within the
+ *                     original context; amplitude 0.1 ln s + 1.
+ * ("Transformer 演进与变体" (ai.icyfenix.cn), the sections on RoPE, NTK and YaRN.)
+ * Angles are exact to 2^-65 turns per position, so far positions lose nothing; the cosines and
+ * sines and the products are float32, and the result is rounded once.
+ */
+typedef enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 } attn_rope_layout;
+typedef enum { ATTN_ROPE_PLAIN = 0, ATTN_ROPE_LINEAR = 1, ATTN_ROPE_NTK = 2, ATTN_ROPE_YARN = 3 } attn_rope_scaling;
+typedef struct attn_rope_plan* attn_rope_handle;
+
+/* Rows of d contiguous elements: element e of the row (b, h, s) is
+ * data[b * stride_b + h * stride_h + s * stride_s + e].  data is 16-byte aligned and every stride a
+ * multiple of 16 bytes, so that views of a packed projection [B, S, heads, d] can be passed as they are. */
+typedef struct {
+    void* data;
+    long long stride_b, stride_h, stride_s; /* in elements */
+} attn_rows;
+
+/*
+ * attn_rope_create -- the frequencies, on the host (no CUDA call; the handle belongs to no device,
+ * holds no buffer, and may be used by any number of calls at once).
+ *   d         : head width, a multiple of 16, at most 256.
+ *   rot       : rotated elements, even, 2 .. d.
+ *   base      : > 1.   factor : >= 1 (ignored by ATTN_ROPE_PLAIN).
+ *   original_len, beta_fast, beta_slow : ATTN_ROPE_YARN only; original_len >= 1, beta_fast > beta_slow.
+ *   amplitude : 0 for the default (1, or YaRN's), or the factor itself.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (d), ATTN_ERR_OOM.
+ */
+attn_status attn_rope_create(attn_rope_handle* out, int d, int rot, attn_rope_layout layout, double base,
+                             attn_rope_scaling scaling, double factor, int original_len, double beta_fast,
+                             double beta_slow, double amplitude);
+/* attn_rope_frequencies -- freq[rot / 2] and the amplitude of a handle (host). */
+attn_status attn_rope_frequencies(attn_rope_handle h, double* freq, double* amplitude);
+/* attn_rope_destroy -- free the handle; NULL is ignored.  Calls already enqueued keep their own copy. */
+attn_status attn_rope_destroy(attn_rope_handle h);
+
+/*
+ * attn_rope_forward -- rotate the rows of Q [B, Hq, S, d] and K [B, Hk, S, d] in one launch on the
+ * current device (Hk = 0: Q alone; K and K_out are then ignored).
+ *   dtype     : ATTN_BF16 or ATTN_F32, of inputs and outputs.
+ *   Q_out, K_out : may be Q and K themselves (same data and strides); any other overlap is undefined.
+ *   positions : int32 device array, entry (b, s) at b * pos_stride_b + s * pos_stride_s (stride 0
+ *               broadcasts; negative positions turn backwards); NULL: the position is s.
+ *   S = 0 is accepted and does nothing.
+ * Errors: ATTN_ERR_INVALID_ARG (a NULL or misaligned pointer, a stride that is no multiple of 16
+ * bytes, sizes), ATTN_ERR_UNSUPPORTED (B * S > 2^30), ATTN_ERR_CUDA.
+ */
+attn_status attn_rope_forward(attn_rope_handle h, attn_dtype dtype, int B, int S, int Hq, const attn_rows* Q,
+                              const attn_rows* Q_out, int Hk, const attn_rows* K, const attn_rows* K_out,
+                              const int* positions, long long pos_stride_b, long long pos_stride_s, void* stream);
+/*
+ * attn_rope_backward -- the gradients with respect to the unrotated rows, from those with respect to
+ * the rotated ones (dQ_out, dK_out): the transposed map, which is the same rotation by -t with the same
+ * amplitude.  Arguments and errors as attn_rope_forward.
+ */
+attn_status attn_rope_backward(attn_rope_handle h, attn_dtype dtype, int B, int S, int Hq, const attn_rows* dQ_out,
+                               const attn_rows* dQ, int Hk, const attn_rows* dK_out, const attn_rows* dK,
+                               const int* positions, long long pos_stride_b, long long pos_stride_s, void* stream);
+
+/*
+ * ---------------------------------------------------------------- paged key/value cache
+ * A cache in pages of `page` positions, shared by the sequences of a batch through a page table:
+ * position j of sequence b is slot j % page of the page page_table[b][j / page].  ("第 8 章 现代大模型架构"
+ * (theaiera.top), the sections on KV-cache layouts and paging.)
+ *
+ *   pages  : [n_pages, Hkv, 2, page, d], keys at index 0 and values at index 1 of the third dimension;
+ *            bf16, or E4M3 codes.
+ *   scales : E4M3 only, uint8 [n_pages, Hkv, page / 16, 2, 16]: the biased exponent e of each row's
+ *            factor.  A row x is held as k = min { k : max|x| 2^-k <= 448 }, codes
+ *            round_to_e4m3(x 2^-k) and e = k + 127; it stands for code * 2^k.  A row with an
+ *            infinity or a NaN gets NaN codes and e = 255 and reads back as NaN throughout.
+ *
+ * Page tables (int32 [B][max_pages], row stride table_stride) and lengths (int32 [B]) are DEVICE arrays, read by
+ * the kernels: a captured call follows what they hold when it is replayed.  A length beyond max_pages * page or a
+ * page number outside [0, n_pages) that a call needs is not followed; it is recorded in the cache's
+ * error word (attn_cache_poll_device_error) and the outputs of that call are undefined for the sequence.
+ * Entries no position needs may hold anything.
+ */
+typedef struct attn_cache_plan* attn_cache_handle;
+
+/*
+ * attn_cache_create -- a cache over the caller's buffers on the current device, to which the handle
+ * belongs.  The buffers must outlive it; the handle owns an error word.
+ *   page : a multiple of 16, 16 .. 1024.   d : 64 or 128.
+ *   dtype : ATTN_BF16 or ATTN_FP8_E4M3.   pages, scales : 16-byte aligned (scales NULL for bf16).
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_OOM, ATTN_ERR_CUDA.
+ */
+attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int page, int d, attn_dtype dtype,
+                              void* pages, void* scales);
+
+/*
+ * attn_cache_write -- append rows: row i of sequence b, i < new_len[b], goes to position
+ * cache_len[b] - new_len[b] + i (cache_len counts the new rows, as attn_decode_forward's does).
+ *   K, V    : bf16 rows [B, Hkv, S_new, d].
+ *   new_len : int32 device [B], at most S_new, or NULL: S_new rows of every sequence.  Rows at or
+ *             past new_len[b], and rows whose position would be negative, are padding and are not written.
+ *   rope    : NULL, or the rotation of the keys (and of Q) by their positions; the cache holds rotated
+ *             keys, rounded once.
+ *   Hq, Q, Q_out : bf16 rows [B, Hq, S_new, d] of the same tokens' queries, rotated in the same launch
+ *             (Hq = 0: none); padding rows of Q_out are zeros.  Q_out may be Q itself.
+ * Rows of one call must go to different slots: of two rows for one slot, which values and which
+ * exponent remain is unspecified.
+ * Errors: ATTN_ERR_INVALID_ARG (pointers, strides, sizes, a rope of another head width, a current device
+ * other than the cache's), ATTN_ERR_UNSUPPORTED (B > ATTN_DECODE_MAX_BATCH), ATTN_ERR_CUDA.
+ */
+attn_status attn_cache_write(attn_cache_handle h, int B, int S_new, const attn_rows* K, const attn_rows* V,
+                             const int* page_table, long long table_stride, int max_pages, const int* cache_len,
+                             const int* new_len, attn_rope_handle rope, int Hq, const attn_rows* Q,
+                             const attn_rows* Q_out, void* stream);
+
+/*
+ * attn_cache_read -- the positions first .. first + S - 1 of every sequence as dense bf16 rows
+ * K, V [B, Hkv, S, d]; rows at or past cache_len[b] are left as they were.  E4M3 rows come back exactly
+ * (a code times a power of two is a bf16 number, up to 2^127).  Errors: as attn_cache_write.
+ */
+attn_status attn_cache_read(attn_cache_handle h, int B, int S, int first, const attn_rows* K, const attn_rows* V,
+                            const int* page_table, long long table_stride, int max_pages, const int* cache_len,
+                            void* stream);
+
+/*
+ * attn_cache_poll_device_error -- synchronise the device, read the cache's error word into *code (bits:
+ * 1 a length beyond the table, 2 a page number out of range, 4 a bounded wait that ran out), and clear it.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG (bits 1, 2) or ATTN_ERR_DEVICE_TIMEOUT (bit 4).
+ */
+attn_status attn_cache_poll_device_error(attn_cache_handle h, int* code);
+
+/* attn_cache_destroy -- free the handle (synchronises the device first); NULL is ignored. */
+attn_status attn_cache_destroy(attn_cache_handle h);
+
+/*
+ * ---------------------------------------------------------------- paged decode
+ * attn_decode_forward's operation over a paged cache: S_q new rows per sequence, row i at position
+ * t = cache_len[b] - S_q + i, its own key and value already written.  Masks, layouts of Q, O and LSE and
+ * limits are those of the decode entry points; lengths are on the device and may be 0.  A row that sees no
+ * key (an empty sequence, or t < 0) gives O = 0 and LSE = -inf.  Positions at or past the length, and
+ * positions no row's window reaches, are never used, whatever they hold.  With S_q > 1, an infinity or a NaN
+ * in a position that only some rows of a sequence see may reach the other rows of the same kv head.
+ *
+ * A handle owns the partial results of sequences that are split over the grid; it must not be used by
+ * two calls in flight at once, captured graphs included.  Distinct handles are independent.
+ */
+typedef struct attn_paged_plan* attn_paged_handle;
+
+/* attn_paged_create -- arguments as attn_decode_create (d 64 or 128; ATTN_MASK_FULL, CAUSAL,
+ * CAUSAL_SLIDING), on the current device, to which the handle belongs. */
+attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, int S_q, int d, float scale,
+                              attn_mask_kind kind, int window);
+
+/*
+ * attn_paged_forward -- enqueue one decode step over `cache` on `stream`: one kernel.
+ *   Q, O : bf16 [B, Hq, S_q, d], contiguous, 16-byte aligned.   LSE : float32 [B, Hq, S_q] or NULL.
+ * Errors: ATTN_ERR_INVALID_ARG (pointers; a cache of another device, head count or width; a current device
+ * other than the handle's), ATTN_ERR_UNSUPPORTED (max_pages * page > 2^26), ATTN_ERR_CUDA.
+ * Device errors are read by attn_cache_poll_device_error of the cache.
+ */
+attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
+                               long long table_stride, int max_pages, const int* cache_len, void* O, float* LSE,
+                               void* stream);
+
+/* attn_paged_set_grid_limit -- test hook, as attn_decode_set_grid_limit. */
+attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas);
+
+/* attn_paged_destroy -- free the handle (synchronises the device first); NULL is ignored. */
+attn_status attn_paged_destroy(attn_paged_handle h);
+
+/*
+ * attn_paged_split_host -- how attn_paged_forward cuts its work, on the host only.  rows = (Hq / Hkv) * S_q.
+ * Each part is 8 ints: CTA, sequence, kv head, first key block, one past the last, key blocks of the unit,
+ * first and last CTA that hold blocks of the unit.  parts may be NULL with cap = 0 to query *n_parts.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED.
+ */
+attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dtype, attn_mask_kind kind, int window,
+                                  const int* cache_len, int grid, int rows, int* n_cta, int* parts, int cap,
+                                  int* n_parts);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,16 +33,29 @@ EXPORTED = ("attn_create", "attn_forward", "attn_destroy", "attn_status_string",
             "attn_decode_set_alibi", "attn_set_fp8_descale", "attn_kv_schedule_host",
             "attn_backward", "attn_bwd_dq_schedule_host", "attn_set_bias", "attn_decode_set_merge_mode",
             "attn_decode_launch_count", "attn_selftest_device_once", "attn_forward_noalloc_poll_error",
-            "attn_forward_noalloc_set_watchdog", "attn_bwd_lg_lists_host")
+            "attn_forward_noalloc_set_watchdog", "attn_bwd_lg_lists_host",
+            "attn_rope_create", "attn_rope_frequencies", "attn_rope_forward", "attn_rope_backward",
+            "attn_rope_destroy", "attn_cache_create", "attn_cache_write", "attn_cache_read",
+            "attn_cache_poll_device_error", "attn_cache_destroy", "attn_paged_create", "attn_paged_forward",
+            "attn_paged_set_grid_limit", "attn_paged_destroy", "attn_paged_split_host")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DECODE_MAX_BATCH = 1024
 DECODE_MAX_ROWS = 64
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+CACHE_ERR_POSITION, CACHE_ERR_PAGE, CACHE_ERR_WAIT = 1, 2, 4
 
 
 class AttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {attn_status_string(status)} (status {status})")
         self.status = status
+
+
+class attn_rows(ctypes.Structure):
+    """Rows of contiguous elements: data pointer and strides (in elements) over batch, head and position."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_s", ctypes.c_longlong)]
 
 
 def _load():
@@ -107,6 +120,22 @@ def _load():
     lib.attn_decode_schedule_host.restype = I
     lib.attn_decode_set_grid_limit.argtypes = [P, I]
     lib.attn_decode_set_grid_limit.restype = I
+    D, R = ctypes.c_double, ctypes.POINTER(attn_rows)
+    rope = [P, I, I, I, I, R, R, I, R, R, P, LL, LL, P]
+    for name, args in (("attn_rope_create", [ctypes.POINTER(P), I, I, I, D, I, D, I, D, D, D]),
+                       ("attn_rope_frequencies", [P, P, P]), ("attn_rope_forward", rope),
+                       ("attn_rope_backward", rope), ("attn_rope_destroy", [P]),
+                       ("attn_cache_create", [ctypes.POINTER(P), I, I, I, I, I, P, P]),
+                       ("attn_cache_write", [P, I, I, R, R, P, LL, I, P, P, P, I, R, R, P]),
+                       ("attn_cache_read", [P, I, I, I, R, R, P, LL, I, P, P]),
+                       ("attn_cache_poll_device_error", [P, ctypes.POINTER(I)]), ("attn_cache_destroy", [P]),
+                       ("attn_paged_create", [ctypes.POINTER(P), I, I, I, I, I, F, I, I]),
+                       ("attn_paged_forward", [P, P, P, P, LL, I, P, P, P, P]),
+                       ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_destroy", [P]),
+                       ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, I, ctypes.POINTER(I), P, I,
+                                                  ctypes.POINTER(I)])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I
     return lib
 
 
@@ -390,6 +419,442 @@ class DecodeAttention:
         st = _lib.attn_decode_set_merge_mode(self.handle, int(mode))
         if st != ATTN_OK:
             raise AttnError(st, "attn_decode_set_merge_mode")
+
+
+# ---------------------------------------------------------------- rotary positions, paged cache, paged decode
+
+def attn_rope_create(d, rot, layout=0, base=10000.0, scaling=0, factor=1.0, original_len=0, beta_fast=32.0,
+                     beta_slow=1.0, amplitude=0.0) -> int:
+    """Returns a rope handle (int; host only); raises AttnError on a non-OK status."""
+    h = ctypes.c_void_p()
+    st = _lib.attn_rope_create(ctypes.byref(h), int(d), int(rot), int(layout), float(base), int(scaling),
+                               float(factor), int(original_len), float(beta_fast), float(beta_slow),
+                               float(amplitude))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_rope_create")
+    return h.value
+
+
+def attn_rope_frequencies(handle: int, rot: int):
+    """(frequencies float64 [rot / 2], amplitude) of a rope handle."""
+    f, amp = np.zeros(int(rot) // 2), ctypes.c_double(0)
+    st = _lib.attn_rope_frequencies(handle, f.ctypes.data_as(ctypes.c_void_p),
+                                    ctypes.cast(ctypes.byref(amp), ctypes.c_void_p))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_rope_frequencies")
+    return f, amp.value
+
+
+def attn_rope_forward(handle, dtype, B, S, Hq, Q, Q_out, Hk=0, K=None, K_out=None, positions=0, pos_stride_b=0,
+                      pos_stride_s=0, stream=0) -> int:
+    """Rotate rows (attn_rows structures); returns the status."""
+    return _lib.attn_rope_forward(handle, dtype, B, S, Hq, Q, Q_out, Hk, K, K_out, positions or None, pos_stride_b,
+                                  pos_stride_s, stream or None)
+
+
+def attn_rope_backward(handle, dtype, B, S, Hq, dQ_out, dQ, Hk=0, dK_out=None, dK=None, positions=0, pos_stride_b=0,
+                       pos_stride_s=0, stream=0) -> int:
+    """Gradients of attn_rope_forward; returns the status."""
+    return _lib.attn_rope_backward(handle, dtype, B, S, Hq, dQ_out, dQ, Hk, dK_out, dK, positions or None,
+                                   pos_stride_b, pos_stride_s, stream or None)
+
+
+def attn_rope_destroy(handle: int) -> int:
+    return _lib.attn_rope_destroy(handle)
+
+
+def attn_cache_create(n_pages, Hkv, page, d, dtype, pages_ptr, scales_ptr=0) -> int:
+    """Returns a cache handle (int) over the given device buffers; raises AttnError."""
+    h = ctypes.c_void_p()
+    st = _lib.attn_cache_create(ctypes.byref(h), int(n_pages), int(Hkv), int(page), int(d), int(dtype),
+                                pages_ptr or None, scales_ptr or None)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_create")
+    return h.value
+
+
+def attn_cache_write(handle, B, S_new, K, V, table_ptr, table_stride, max_pages, len_ptr, new_len_ptr=0, rope=0, Hq=0,
+                     Q=None, Q_out=None, stream=0) -> int:
+    """Append rows to the cache (attn_rows structures, device pointers); returns the status."""
+    return _lib.attn_cache_write(handle, B, S_new, K, V, table_ptr, table_stride, max_pages, len_ptr,
+                                 new_len_ptr or None, rope or None, Hq, Q, Q_out, stream or None)
+
+
+def attn_cache_read(handle, B, S, first, K, V, table_ptr, table_stride, max_pages, len_ptr, stream=0) -> int:
+    """Positions of every sequence as dense rows; returns the status."""
+    return _lib.attn_cache_read(handle, B, S, first, K, V, table_ptr, table_stride, max_pages, len_ptr,
+                                stream or None)
+
+
+def attn_cache_poll_device_error(handle: int):
+    code = ctypes.c_int(0)
+    st = _lib.attn_cache_poll_device_error(handle, ctypes.byref(code))
+    return st, code.value
+
+
+def attn_cache_destroy(handle: int) -> int:
+    return _lib.attn_cache_destroy(handle)
+
+
+def attn_paged_create(B, Hq, Hkv, S_q, d, scale, kind, window=0) -> int:
+    """Returns a paged decode handle (int); raises AttnError on a non-OK status."""
+    h = ctypes.c_void_p()
+    st = _lib.attn_paged_create(ctypes.byref(h), int(B), int(Hq), int(Hkv), int(S_q), int(d), float(scale), int(kind),
+                                int(window))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_create")
+    return h.value
+
+
+def attn_paged_forward(handle, cache, q_ptr, table_ptr, table_stride, max_pages, len_ptr, o_ptr, lse_ptr=0,
+                       stream=0) -> int:
+    """Enqueue one decode step over a paged cache; returns the status."""
+    return _lib.attn_paged_forward(handle, cache, q_ptr, table_ptr, table_stride, max_pages, len_ptr, o_ptr,
+                                   lse_ptr or None, stream or None)
+
+
+def attn_paged_set_grid_limit(handle: int, max_ctas: int) -> int:
+    return _lib.attn_paged_set_grid_limit(handle, int(max_ctas))
+
+
+def attn_paged_destroy(handle: int) -> int:
+    return _lib.attn_paged_destroy(handle)
+
+
+def attn_paged_split_host(B, Hkv, S_q, d, dtype, kind, window, cache_len, grid, rows):
+    """Host-only split of the paged decode: (n_cta, int32 [parts, 8]: CTA, sequence, kv head, first key block,
+    one past the last, key blocks of the unit, first and last CTA of the unit).  Raises AttnError."""
+    lens, _ = _int_array(cache_len)
+    n_cta, n = ctypes.c_int(0), ctypes.c_int(0)
+    args = (int(B), int(Hkv), int(S_q), int(d), int(dtype), int(kind), int(window),
+            ctypes.cast(lens, ctypes.c_void_p), int(grid), int(rows))
+    st = _lib.attn_paged_split_host(*args, ctypes.byref(n_cta), None, 0, ctypes.byref(n))
+    parts = np.zeros((max(n.value, 1), 8), dtype=np.int32)
+    if st == ATTN_OK:
+        st = _lib.attn_paged_split_host(*args, ctypes.byref(n_cta), parts.ctypes.data_as(ctypes.c_void_p), n.value,
+                                        ctypes.byref(n))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_split_host")
+    return n_cta.value, parts[:n.value]
+
+
+def _rows(name, t, shape, dtype, device):
+    """attn_rows of a tensor view [B, H, S, d] whose last dimension is contiguous."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    sb, sh, ss, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return attn_rows(t.data_ptr(), sb, sh, ss)
+
+
+class _Launch:
+    """The current device and stream of a call: makes the tensors' device current for the call, and tells the caching
+    allocator about tensors used on a stream other than the current one."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+        self._old = None
+        if device.index != torch.cuda.current_device():
+            self._old = torch.cuda.current_device()
+            torch.cuda.set_device(device)
+        current = torch.cuda.current_stream()
+        self._foreign = stream is not None and stream != current
+        self._stream = stream if self._foreign else current
+        self.stream = self._stream.cuda_stream
+
+    def used(self, *tensors):
+        if self._foreign:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self._stream)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self._old is not None:
+            import torch
+            torch.cuda.set_device(self._old)
+        return False
+
+
+class RotaryPositions:
+    """Rotary position embedding of Q and K (``attn_rope_*``), and its gradient.
+
+    d: head width (a multiple of 16, at most 256); rotary_dim: how many of its elements are rotated, the first
+    ones (default d); layout: pairs "half" (p, p + rotary_dim / 2) or "interleaved" (2p, 2p + 1); scaling: "none",
+    "linear", "ntk" or "yarn" for contexts ``factor`` times longer ("yarn" with original_len, beta_fast,
+    beta_slow); amplitude: factor on the rotated elements (default 1, or YaRN's 0.1 ln factor + 1).
+    """
+
+    def __init__(self, d, rotary_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=0,
+                 beta_fast=32.0, beta_slow=1.0, amplitude=None):
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            raise ValueError(f"layout is one of {sorted(ROPE_LAYOUTS)}, scaling one of {sorted(ROPE_SCALINGS)}")
+        if amplitude is not None and not amplitude > 0:
+            raise ValueError("amplitude must be positive")
+        self.d, self.rotary_dim = int(d), int(d if rotary_dim is None else rotary_dim)
+        self.handle = attn_rope_create(d, self.rotary_dim, ROPE_LAYOUTS[layout], base, ROPE_SCALINGS[scaling], factor,
+                                       original_len, beta_fast, beta_slow, amplitude or 0.0)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            attn_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def frequencies(self):
+        """(radians per position of each pair, float64 array; amplitude)."""
+        return attn_rope_frequencies(self.handle, self.rotary_dim)
+
+    def __call__(self, Q, K=None, positions=None, Q_out=None, K_out=None, stream=None):
+        """Rotated Q [B, Hq, S, d] and K [B, Hk, S, d] (bf16 or float32 views, last dimension contiguous, rows
+        16-byte aligned) by positions, int32 [B, S] or [S] (default 0 .. S - 1).  Returns (Q_out, K_out), or
+        Q_out without K; the outputs may be the inputs."""
+        return self._apply(_lib.attn_rope_forward, "attn_rope_forward", Q, K, positions, Q_out, K_out, stream)
+
+    def backward(self, dQ_out, dK_out=None, positions=None, dQ=None, dK=None, stream=None):
+        """Gradients with respect to the unrotated Q and K from those with respect to the rotated ones."""
+        return self._apply(_lib.attn_rope_backward, "attn_rope_backward", dQ_out, dK_out, positions, dQ, dK, stream)
+
+    def _apply(self, fn, name, Q, K, positions, Q_out, K_out, stream):
+        import torch
+        if Q.dim() != 4 or Q.shape[3] != self.d or Q.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"Q must be a bfloat16 or float32 tensor [B, Hq, S, {self.d}]")
+        B, Hq, S, d = Q.shape
+        if K is not None and (K.dim() != 4 or K.shape[1] < 1):
+            raise ValueError(f"K must be a tensor [B, Hk, S, {d}] with at least one head")
+        ps = (0, 0)
+        if positions is not None:
+            if positions.dtype != torch.int32 or positions.device != Q.device or positions.shape not in ((B, S), (S,)):
+                raise ValueError(f"positions must be an int32 tensor of shape {(B, S)} or {(S,)} on {Q.device}")
+            ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
+        with _Launch(Q.device, stream) as at:
+            if Q_out is None:
+                Q_out = torch.empty((B, Hq, S, d), dtype=Q.dtype, device=Q.device)
+            q, qo = _rows("Q", Q, Q.shape, Q.dtype, Q.device), _rows("Q_out", Q_out, Q.shape, Q.dtype, Q.device)
+            k = ko = None
+            if K is not None:
+                shape = torch.Size((B, K.shape[1], S, d))
+                if K_out is None:
+                    K_out = torch.empty(shape, dtype=Q.dtype, device=Q.device)
+                k, ko = _rows("K", K, shape, Q.dtype, Q.device), _rows("K_out", K_out, shape, Q.dtype, Q.device)
+            at.used(Q, K, positions, Q_out, K_out)
+            if B * S * Hq:
+                st = fn(self.handle, ATTN_BF16 if Q.dtype == torch.bfloat16 else ATTN_F32, B, S, Hq, q, qo,
+                        0 if K is None else K.shape[1], k, ko, None if positions is None else positions.data_ptr(),
+                        ps[0], ps[1], at.stream)
+                if st != ATTN_OK:
+                    raise AttnError(st, name)
+        return Q_out if K is None else (Q_out, K_out)
+
+
+class PagedCache:
+    """A key/value cache in pages (``attn_cache_*``).
+
+    pages: [n_pages, Hkv, 2, page, d] bfloat16 or float8_e4m3fn, keys and values at index 0 and 1; scales (E4M3):
+    uint8 [n_pages, Hkv, page / 16, 2, 16], the biased exponent of each row's factor.  Both are allocated (zeroed)
+    unless given, and stay the caller's to use.  page_table: int32 CUDA [B, max_pages]; cache_len: int32 CUDA [B], the
+    positions of each sequence with the rows of the call counted in.  Both are read on the device.
+    """
+
+    def __init__(self, n_pages, Hkv, page, d, dtype="bf16", pages=None, scales=None, device=None):
+        import torch
+        kinds = {"bf16": (ATTN_BF16, torch.bfloat16), "e4m3": (ATTN_FP8_E4M3, torch.float8_e4m3fn)}
+        if dtype not in kinds:
+            raise ValueError(f"dtype is one of {sorted(kinds)}")
+        code, tdt = kinds[dtype]
+        self.shape, self.dtype = (int(n_pages), int(Hkv), int(page), int(d)), dtype
+        n_pages, Hkv, page, d = self.shape
+        if min(self.shape) < 1 or page % 16:
+            raise ValueError("n_pages, Hkv and d must be positive, page a positive multiple of 16")
+        want = (n_pages, Hkv, 2, page, d)
+        if pages is None:
+            pages = torch.zeros(want, dtype=torch.uint8 if dtype == "e4m3" else tdt,
+                                device=device or torch.device("cuda", torch.cuda.current_device()))
+            pages = pages.view(tdt)
+        if tuple(pages.shape) != want or pages.dtype != tdt or not pages.is_cuda or not pages.is_contiguous():
+            raise ValueError(f"pages must be a contiguous CUDA {tdt} tensor of shape {want}")
+        self.device = pages.device
+        if dtype == "e4m3":
+            want = (n_pages, Hkv, page // 16, 2, 16)
+            if scales is None:
+                scales = torch.zeros(want, dtype=torch.uint8, device=self.device)
+            if (tuple(scales.shape) != want or scales.dtype != torch.uint8 or scales.device != self.device
+                    or not scales.is_contiguous()):
+                raise ValueError(f"scales must be a contiguous uint8 tensor of shape {want} on {self.device}")
+        elif scales is not None:
+            raise ValueError("a bf16 cache has no scales")
+        self.pages, self.scales = pages, scales
+        with torch.cuda.device(self.device):
+            self.handle = attn_cache_create(n_pages, Hkv, page, d, code, pages.data_ptr(),
+                                            0 if scales is None else scales.data_ptr())
+
+    def close(self):
+        if getattr(self, "handle", None):
+            import torch
+            with torch.cuda.device(self.device):
+                attn_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _table(self, page_table, cache_len):
+        import torch
+        if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != self.device
+                or page_table.shape[1] < 1 or page_table.stride(1) != 1):
+            raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on {self.device}")
+        B = page_table.shape[0]
+        if (cache_len.dtype != torch.int32 or tuple(cache_len.shape) != (B,) or cache_len.device != self.device
+                or not cache_len.is_contiguous()):
+            raise ValueError(f"cache_len must be a contiguous int32 tensor of shape {(B,)} on {self.device}")
+        return B, page_table.data_ptr(), page_table.stride(0), page_table.shape[1], cache_len.data_ptr()
+
+    def write(self, K, V, page_table, cache_len, new_len=None, rope=None, Q=None, Q_out=None, stream=None):
+        """Append K, V [B, Hkv, S_new, d] (bf16 views): row i < new_len[b] (int32 CUDA [B]; default S_new) of
+        sequence b goes to position cache_len[b] - new_len[b] + i.  With ``rope`` (RotaryPositions) the keys, and
+        Q [B, Hq, S_new, d] if given, are rotated by those positions; returns the rotated Q, or None."""
+        import torch
+        _, Hkv, _, d = self.shape
+        B, table, stride, wide, lens = self._table(page_table, cache_len)
+        if K.dim() != 4:
+            raise ValueError(f"K must be a tensor [{B}, {Hkv}, S_new, {d}]")
+        S = K.shape[2]
+        if rope is None and Q is not None:
+            raise ValueError("Q is only taken to be rotated: give rope")
+        if rope is not None and rope.d != d:
+            raise ValueError("rope is for another head width")
+        if new_len is not None and (new_len.dtype != torch.int32 or tuple(new_len.shape) != (B,)
+                                    or new_len.device != self.device or not new_len.is_contiguous()):
+            raise ValueError(f"new_len must be a contiguous int32 tensor of shape {(B,)} on {self.device}")
+        with _Launch(self.device, stream) as at:
+            shape = torch.Size((B, Hkv, S, d))
+            k = _rows("K", K, shape, torch.bfloat16, self.device)
+            v = _rows("V", V, shape, torch.bfloat16, self.device)
+            q = qo = None
+            Hq = 0
+            if Q is not None:
+                if Q.dim() != 4 or Q.shape[1] < 1:
+                    raise ValueError(f"Q must be a tensor [{B}, Hq, {S}, {d}] with at least one head")
+                Hq = Q.shape[1]
+                shape = torch.Size((B, Hq, S, d))
+                if Q_out is None:
+                    Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+                q = _rows("Q", Q, shape, torch.bfloat16, self.device)
+                qo = _rows("Q_out", Q_out, shape, torch.bfloat16, self.device)
+            at.used(K, V, Q, Q_out, page_table, cache_len, new_len, self.pages, self.scales)
+            if B:
+                st = _lib.attn_cache_write(self.handle, B, S, k, v, table, stride, wide, lens,
+                                           None if new_len is None else new_len.data_ptr(),
+                                           None if rope is None else rope.handle, Hq, q, qo, at.stream)
+                if st != ATTN_OK:
+                    raise AttnError(st, "attn_cache_write")
+        return Q_out if Q is not None else None
+
+    def read(self, page_table, cache_len, first=0, length=None, K=None, V=None, stream=None):
+        """Positions first .. first + length - 1 of every sequence as dense (K, V), bf16 [B, Hkv, length, d].
+        Rows at or past cache_len[b] are left as they were (zeros in tensors allocated here)."""
+        import torch
+        _, Hkv, _, d = self.shape
+        B, table, stride, wide, lens = self._table(page_table, cache_len)
+        if length is None:
+            if K is None and V is None:
+                raise ValueError("give length, or the tensors to fill")
+            length = (K if K is not None else V).shape[2]
+        with _Launch(self.device, stream) as at:
+            shape = torch.Size((B, Hkv, int(length), d))
+            with torch.cuda.stream(stream):  # a new tensor's zeros come before the rows
+                if K is None:
+                    K = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+                if V is None:
+                    V = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+            k = _rows("K", K, shape, torch.bfloat16, self.device)
+            v = _rows("V", V, shape, torch.bfloat16, self.device)
+            at.used(K, V, page_table, cache_len, self.pages, self.scales)
+            if B:
+                st = _lib.attn_cache_read(self.handle, B, int(length), int(first), k, v, table, stride, wide, lens,
+                                          at.stream)
+                if st != ATTN_OK:
+                    raise AttnError(st, "attn_cache_read")
+        return K, V
+
+    def poll_device_error(self):
+        """(status, code): synchronise; code has the CACHE_ERR_* bits recorded since the last poll."""
+        import torch
+        with torch.cuda.device(self.device):
+            return attn_cache_poll_device_error(self.handle)
+
+
+class PagedDecodeAttention:
+    """A decode plan over a PagedCache: S_q new query rows per sequence, lengths and page table on the device.
+
+    Q: [B, Hq, S_q, d] bf16; row i of sequence b sits at position cache_len[b] - S_q + i, its own key and value
+    already written.  Returns (O like Q, LSE float32 [B, Hq, S_q]); a row that sees no key gives zeros and -inf.
+    """
+
+    def __init__(self, B, Hq, Hkv, S_q, d, scale=None, kind=MASK_CAUSAL, window=0, device=None):
+        import math
+        import torch
+        self.shape = (int(B), int(Hq), int(Hkv), int(S_q), int(d))
+        self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(d)
+        self.kind, self.window = int(kind), int(window)
+        with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+            self.device = torch.device("cuda", torch.cuda.current_device())
+            self.handle = attn_paged_create(B, Hq, Hkv, S_q, d, self.scale, self.kind, self.window)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            import torch
+            with torch.cuda.device(self.device):
+                attn_paged_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __call__(self, Q, cache, page_table, cache_len, O=None, LSE=None, stream=None, want_lse=True):
+        import torch
+        B, Hq, Hkv, S_q, d = self.shape
+        rows, table, stride, wide, lens = cache._table(page_table, cache_len)
+        if rows != B:
+            raise ValueError(f"page_table must have {B} rows")
+        for name, t, shape, dt in (("Q", Q, (B, Hq, S_q, d), torch.bfloat16), ("O", O, (B, Hq, S_q, d), torch.bfloat16),
+                                   ("LSE", LSE, (B, Hq, S_q), torch.float32)):
+            if t is not None and (t.device != self.device or t.dtype != dt or not t.is_contiguous()
+                                  or tuple(t.shape) != shape):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape} on {self.device}")
+        with _Launch(self.device, stream) as at:
+            if O is None:
+                O = torch.empty_like(Q)
+            if LSE is None and want_lse:
+                LSE = torch.empty((B, Hq, S_q), dtype=torch.float32, device=Q.device)
+            at.used(Q, O, LSE, page_table, cache_len, cache.pages, cache.scales)
+            st = _lib.attn_paged_forward(self.handle, cache.handle, Q.data_ptr(), table, stride, wide, lens,
+                                         O.data_ptr(), None if LSE is None else LSE.data_ptr(), at.stream)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_paged_forward")
+        return O, LSE
+
+    def set_grid_limit(self, max_ctas: int):
+        """Test hook: at most max_ctas CTAs per launch (long shares on small problems)."""
+        st = attn_paged_set_grid_limit(self.handle, max_ctas)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_paged_set_grid_limit")
 
 
 # ---------------------------------------------------------------- torch convenience

@@ -1,0 +1,180 @@
+// Rotary positions applied to the rows of Q and K, and the gradient of that rotation.
+//
+//     (x_p, x_p') -> amp (x_p cos t - x_p' sin t,  x_p sin t + x_p' cos t),  t = f_p * position,
+//
+// over the rot / 2 pairs of a row; the d - rot elements behind them are copied.  The gradient is the transpose:
+// the same with -t.  Bound by memory: every element is read once and written once, about 3 flops each.
+//
+// A row is held by d / 16 neighbouring threads, 16 elements each, as two 16-byte runs of bf16 (four of fp32), so
+// that the loads and stores of a warp cover whole rows.  A thread keeps one token and walks over heads: its eight
+// cosines and sines, about 8 x 40 instructions, serve every head of the token.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "paged.h"
+#include "rope.h"
+
+namespace attn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RopeParams {
+    RopeTable t;
+    RopeRows q, k;
+    int Hq, H;  // query heads; query and key heads
+    int S, tokens, d;
+    int tb, hb;       // tokens and heads of a block side by side: tb * hb rows
+    int heads_block;  // heads a block walks over
+    const int* positions;
+    long long pos_b, pos_s;
+    float sign;  // -1: the gradient
+};
+
+// STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
+// memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
+template <class T, bool STAGED>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ float stage[];
+    __shared__ unsigned long long step[kRopeMaxPairs];
+    if ((int)threadIdx.x < p.t.rot / 2) step[threadIdx.x] = p.t.step[threadIdx.x];
+    __syncthreads();
+    const int lanes = p.d / 16, u = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+    const int token = blockIdx.x * p.tb + slot / p.hb;
+    const bool live = slot < p.tb * p.hb && token < p.tokens;
+    const int b = live ? token / p.S : 0, s = live ? token - b * p.S : 0;
+    const bool halves = !p.t.interleaved;
+    float c[8], sn[8];
+    const int pos = !live ? 0 : p.positions ? p.positions[b * p.pos_b + s * p.pos_s] : s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int q = 8 * u + e;
+        c[e] = 1.f;
+        sn[e] = 0.f;
+        if (2 * q < p.t.rot) {
+            rope_cos_sin(pos, step[q], c[e], sn[e]);
+            c[e] *= p.t.amp;
+            sn[e] *= p.t.amp * p.sign;
+        }
+    }
+    int off_a = 16 * u, off_b = 16 * u + 8;
+    if (!STAGED) rope_runs(halves, p.t.rot, u, off_a, off_b);
+    const bool across = !STAGED && halves && 16 * u < p.t.rot;
+    const int h_first = blockIdx.y * p.heads_block, h_last = min(p.H, h_first + p.heads_block);
+    constexpr int U = STAGED ? 1 : 4;  // rows in flight per thread
+    for (int h0 = h_first; h0 < h_last; h0 += U * p.hb) {
+        float run[U][16];
+        T* out[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = h0 + i * p.hb + slot % p.hb;
+            out[i] = nullptr;
+            if (!live || h >= h_last) continue;
+            const RopeRows& r = h < p.Hq ? p.q : p.k;
+            const int hh = h < p.Hq ? h : h - p.Hq;
+            const T* in = reinterpret_cast<const T*>(r.src) + (b * r.sb + hh * r.sh + s * r.ss);
+            out[i] = reinterpret_cast<T*>(r.dst) + (b * r.db + hh * r.dh + s * r.ds);
+            load8(in + off_a, run[i]);
+            load8(in + off_b, run[i] + 8);
+        }
+        if (STAGED) {
+            float* row = stage + slot * p.d;
+            if (out[0]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) row[16 * u + e] = run[0][e];
+            }
+            __syncthreads();
+            float x[16];
+            if (out[0]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    int i0, i1;
+                    rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                    x[2 * e] = row[i0];
+                    x[2 * e + 1] = row[i1];
+                }
+                rope_turn(x, c, sn);
+            }
+            __syncthreads();
+            if (out[0]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    int i0, i1;
+                    rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                    row[i0] = x[2 * e];
+                    row[i1] = x[2 * e + 1];
+                }
+            }
+            __syncthreads();
+            if (out[0]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) run[0][e] = row[16 * u + e];
+                store8(out[0] + off_a, run[0]);
+                store8(out[0] + off_b, run[0] + 8);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (!out[i]) continue;
+                float x[16];
+                runs_to_pairs(across, run[i], run[i] + 8, x);
+                rope_turn(x, c, sn);
+                pairs_to_runs(across, x, run[i], run[i] + 8);
+                store8(out[i] + off_a, run[i]);
+                store8(out[i] + off_b, run[i] + 8);
+            }
+        }
+    }
+}
+
+int pow2_at_least(int n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k, int Hq, int Hk, int B, int S, int d,
+                        const int* positions, long long pos_b, long long pos_s, bool inverse, bool f32, int n_sm,
+                        cudaStream_t stream) {
+    RopeParams p{};
+    p.t = t;
+    p.q = q;
+    p.k = k;
+    p.Hq = Hq;
+    p.H = Hq + Hk;
+    p.S = S;
+    p.tokens = B * S;
+    p.d = d;
+    p.positions = positions;
+    p.pos_b = pos_b;
+    p.pos_s = pos_s;
+    p.sign = inverse ? -1.f : 1.f;
+    const int rows = kThreads / (d / 16);
+    // Eight heads side by side (their rows are neighbours in a [B, S, H, d] projection), the other rows of a block
+    // are neighbouring tokens (neighbours in [B, H, S, d]); few tokens leave more rows to the heads.
+    p.tb = std::min(std::max(1, rows / 8), pow2_at_least(p.tokens));
+    p.hb = rows / p.tb;
+    // A block walks over all heads of its tokens unless that leaves multiprocessors without four blocks.
+    const long long blocks_x = (p.tokens + (long long)p.tb - 1) / p.tb;
+    const int rounds = (p.H + p.hb - 1) / p.hb;
+    const long long want = 4LL * n_sm;
+    const int split = (int)std::min<long long>(rounds, std::max<long long>(1, (want + blocks_x - 1) / blocks_x));
+    p.heads_block = (rounds + split - 1) / split * p.hb;
+    const dim3 grid((unsigned)blocks_x, (unsigned)((p.H + p.heads_block - 1) / p.heads_block));
+    const bool staged = !t.interleaved && t.rot % 16 != 0;
+    const size_t smem = staged ? sizeof(float) * (size_t)rows * d : 0;
+    if (f32) {
+        if (staged) rope_kernel<float, true><<<grid, kThreads, smem, stream>>>(p);
+        else rope_kernel<float, false><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+        if (staged) rope_kernel<__nv_bfloat16, true><<<grid, kThreads, smem, stream>>>(p);
+        else rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace attn

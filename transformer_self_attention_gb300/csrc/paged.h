@@ -1,0 +1,100 @@
+// Launch parameters of the rotary, paged-cache and paged-decode kernels, and the arithmetic that host and device
+// share: how the paged decode work is cut over the grid.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "rope.h"
+
+namespace attn {
+
+// One launch for the rows of Q and K (Hk = 0: Q alone).
+cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k, int Hq, int Hk, int B, int S, int d,
+                        const int* positions, long long pos_b, long long pos_s, bool inverse, bool f32, int n_sm,
+                        cudaStream_t stream);
+
+// ---------------------------------------------------------------- cache
+// Bits of a cache's device error word.
+constexpr int kCacheErrPosition = 1;  // a length or a row's position lies outside the page table
+constexpr int kCacheErrPage = 2;      // a page number outside [0, n_pages)
+constexpr int kCacheErrWait = 4;      // a bounded wait of the decode kernel ran out
+
+// Layout: pages [n_pages, Hkv, 2, page, d] (keys, then values), bf16 or E4M3; scales (E4M3)
+// [n_pages, Hkv, page / 16, 2, 16], the biased exponent e of each row's factor 2^(e - 127), 255 for a row
+// that held an infinity or a NaN.  One 32-byte block of scales belongs to 16 positions of one kv head.
+struct CacheView {
+    char* pages = nullptr;
+    uint8_t* scales = nullptr;
+    int n_pages = 0, Hkv = 0, page = 0, d = 0;
+    int* err = nullptr;
+};
+struct PageTable {
+    const int* pages = nullptr;  // [B, max_pages], row stride `stride`
+    const int* len = nullptr;    // [B]
+    long long stride = 0;
+    int max_pages = 0;
+};
+struct CacheWriteParams {
+    CacheView c;
+    PageTable t;
+    RopeTable rope;       // rot = 0: K and Q are taken as they are
+    RopeRows q, k, v;     // dst of k and v unused
+    const int* new_len;   // [B], or null: S rows of every sequence
+    int Hq, B, S;
+};
+struct CacheReadParams {
+    CacheView c;
+    PageTable t;
+    RopeRows k, v;  // src unused
+    int B, S, first;
+};
+cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, int n_sm, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged decode
+// Work units are (sequence, kv head), in that order; a unit of a sequence with n key blocks costs n + kPagedOverhead
+// (its start, its merge and its output cost about as much as that many blocks).  Sequences without keys
+// cost nothing.  The cost line [0, W) is cut into C equal intervals, one per CTA; inside a unit the blocks
+// follow the overhead, so that an interval holds the blocks whose cost position it covers.
+constexpr int kPagedOverhead = 6;
+constexpr int kPagedMaxBatch = ATTN_DECODE_MAX_BATCH;
+
+// Key blocks [lo, hi) of `keys` positions that some row of a sequence of length n can see.
+__host__ __device__ inline void paged_blocks(int n, int S_q, int window, int keys, int& lo, int& hi) {
+    hi = (n + keys - 1) / keys;
+    const int first = window < 0 ? 0 : n - S_q - window;
+    lo = first > 0 ? first / keys : 0;
+}
+__host__ __device__ inline long long paged_cut(long long W, int C, int c) { return W * c / C; }
+// The CTA whose interval holds cost position x.
+__host__ __device__ inline int paged_owner(long long W, int C, long long x) { return (int)(((x + 1) * C - 1) / W); }
+// CTAs in use: one per unit, more where the intervals still cost `least` (one round of a CTA's warps).
+__host__ __device__ inline int paged_ctas(long long W, long long units, int grid, int least) {
+    const long long c = W / least > units ? W / least : units;
+    return c < 1 ? 1 : c < grid ? (int)c : grid;
+}
+
+struct PagedParams {
+    CUtensorMap tm;  // the pages: {inner, slots, halves of a row, K / V, page * Hkv + head}
+    const void* q;   // [B, Hq, S_q, d] bf16
+    void* o;
+    float* lse;      // may be null
+    CacheView c;
+    PageTable t;
+    float* part_o;        // [2 * grid][rows_pad][d], two slots per CTA: its first and its last stretch
+    float2* part_ml;      // [2 * grid][rows_pad]: the row maximum (base 2) and sum
+    unsigned* counters;   // [B * Hkv] partial results of a unit that have arrived
+    int B, Hq, Hkv, S_q, rows;
+    int window;           // -1: none
+    int causal;           // 0: every row sees every cached position
+    float scale_log2;
+    long long watchdog_ns;
+};
+int paged_block_keys(int d, bool e4m3);   // positions per key block
+int paged_rows_pad(int rows);             // 16, 32 or 64
+cudaError_t launch_paged_decode(const PagedParams& p, bool e4m3, int grid, cudaStream_t stream);
+
+}  // namespace attn

@@ -1,0 +1,107 @@
+// Rotary positions: what the host hands to the kernels, and the device parts they share.
+//
+// Pair p of a head turns by the angle f_p * position.  The angle is kept as a fraction of a turn in 64-bit
+// fixed point: step[p] = f_p / (2 pi) * 2^64 modulo 2^64, so position * step[p] modulo 2^64 is the phase with all
+// whole turns gone, off by at most position * 2^-65 turns however far the position is.  A float32 product f_p *
+// position would be off by 2^-24 of the whole angle (0.06 rad at position 2^20 for p = 0), and float64 runs at a
+// small fraction of the integer rate on this GPU.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace attn {
+
+constexpr int kRopeMaxPairs = 128;
+
+struct RopeTable {
+    unsigned long long step[kRopeMaxPairs];
+    float amp = 1.f;      // factor on the rotated elements
+    int rot = 0;          // rotated elements of a head, the first ones (even)
+    int interleaved = 0;  // pairs (2p, 2p + 1); otherwise (p, p + rot / 2)
+};
+
+struct RopeRows {  // rows of d contiguous elements; strides in elements
+    const char* src = nullptr;
+    char* dst = nullptr;
+    long long sb = 0, sh = 0, ss = 0;  // src
+    long long db = 0, dh = 0, ds = 0;  // dst
+};
+
+#ifdef __CUDACC__
+// cos and sin of the phase of one pair.  The top 32 bits of the phase, as a signed number, are the angle in
+// turns times 2^32 (off by 1.5e-9 rad); sincospif is accurate to about an ulp for every argument.
+__device__ __forceinline__ void rope_cos_sin(int position, unsigned long long step, float& c, float& s) {
+    const unsigned long long phase = (unsigned long long)(long long)position * step;
+    const float half_turns = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
+    sincospif(half_turns, &s, &c);
+}
+
+// The 16 elements a lane holds, as two runs of 8 (a, b), and where the runs start in the row.  Lane u of the d / 16
+// lanes of a row owns the pairs 8u .. 8u + 7, counted over the row as the rotated pairs first and then the elements
+// that stay, two by two.  Interleaved pairs are then 16 neighbouring elements; pairs of halves are two runs of 8,
+// which start on 8-element boundaries when rot is a multiple of 16 (other rot: rope_pair_index, element by element).
+__device__ __forceinline__ void rope_runs(bool halves, int rot, int u, int& off_a, int& off_b) {
+    const bool turned = halves && 16 * u < rot;
+    off_a = turned ? 8 * u : 16 * u;
+    off_b = turned ? rot / 2 + 8 * u : 16 * u + 8;
+}
+__device__ __forceinline__ void rope_pair_index(bool halves, int rot, int q, int& i0, int& i1) {
+    const bool turned = halves && 2 * q < rot;
+    i0 = turned ? q : 2 * q;
+    i1 = turned ? q + rot / 2 : 2 * q + 1;
+}
+// x = the lane's pairs (x[2e], x[2e + 1]).
+__device__ __forceinline__ void rope_turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        x[2 * e] = a * c[e] - b * s[e];
+        x[2 * e + 1] = a * s[e] + b * c[e];
+    }
+}
+// Eight neighbouring elements as float.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4 v = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+// Runs <-> pairs: pairs of halves sit across the two runs, neighbouring pairs inside them.
+__device__ __forceinline__ void runs_to_pairs(bool across, const float* a, const float* b, float (&x)[16]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[2 * e] = across ? a[e] : (e < 4 ? a[2 * e] : b[2 * e - 8]);
+        x[2 * e + 1] = across ? b[e] : (e < 4 ? a[2 * e + 1] : b[2 * e - 7]);
+    }
+}
+__device__ __forceinline__ void pairs_to_runs(bool across, const float (&x)[16], float* a, float* b) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        a[e] = across ? x[2 * e] : x[e];
+        b[e] = across ? x[2 * e + 1] : x[8 + e];
+    }
+}
+#endif
+
+}  // namespace attn
