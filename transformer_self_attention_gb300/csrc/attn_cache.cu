@@ -43,14 +43,36 @@ template <int D, bool E4M3, bool STAGED>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
     constexpr int LANES = D / 16;
     __shared__ unsigned long long step[D / 2];
-    __shared__ float stage[STAGED ? kThreads * 16 : 1];
+    __shared__ float stage[STAGED ? kThreads / LANES * (D + 1) : 1];
     const CacheWriteParams& p = a.p;
-    if ((int)threadIdx.x < p.rope.rot / 2) step[threadIdx.x] = p.rope.step[threadIdx.x];
-    __syncthreads();
     const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const int token = blockIdx.x * a.tb + slot / a.hb;
     const bool live = slot < a.tb * a.hb && token < a.tokens;
     const int b = live ? token / p.S : 0, i = live ? token - b * p.S : 0;
+    const bool halves = !p.rope.interleaved;
+    int off_a = 16 * u, off_b = 16 * u + 8;
+    if (!STAGED) rope_runs(halves, p.rope.rot, u, off_a, off_b);
+    const bool across = !STAGED && halves && 16 * u < p.rope.rot;
+    const int H = p.Hq + 2 * p.c.Hkv;
+    const int h_first = blockIdx.y * a.heads_block, h_last = min(H, h_first + a.heads_block);
+    constexpr int U = STAGED ? 1 : 2;
+    // The next U rows, on their way before what they need is known (rows of padding are read too, and not used).
+    Raw8<__nv_bfloat16> raw[U][2];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int h = h0 + j * a.hb + slot % a.hb;
+            if (!live || h >= h_last) continue;
+            const int kind = h < p.Hq ? 1 : h < p.Hq + p.c.Hkv ? 2 : 3;
+            const RopeRows& r = kind == 1 ? p.q : kind == 2 ? p.k : p.v;
+            const int head = h - (kind == 1 ? 0 : kind == 2 ? p.Hq : p.Hq + p.c.Hkv);
+            const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(r.src) + (b * r.sb + head * r.sh + i * r.ss);
+            const bool apart = across && kind != 3;
+            fetch8(in + (apart ? off_a : 16 * u), raw[j][0]);
+            fetch8(in + (apart ? off_b : 16 * u + 8), raw[j][1]);
+        }
+    };
+    fetch(h_first);
     const int len = p.t.len[b];
     const int fresh = p.new_len ? p.new_len[b] : p.S;
     const int pos = len - fresh + i;
@@ -70,7 +92,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         placed = bad == 0;
         if (bad && u == 0) atomicOr(p.c.err, bad);
     }
-    const bool halves = !p.rope.interleaved;
+    if ((int)threadIdx.x < p.rope.rot / 2) step[threadIdx.x] = p.rope.step[threadIdx.x];
+    __syncthreads();
     float c[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -83,12 +106,6 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             sn[e] *= p.rope.amp;
         }
     }
-    int off_a = 16 * u, off_b = 16 * u + 8;
-    if (!STAGED) rope_runs(halves, p.rope.rot, u, off_a, off_b);
-    const bool across = !STAGED && halves && 16 * u < p.rope.rot;
-    const int H = p.Hq + 2 * p.c.Hkv;
-    const int h_first = blockIdx.y * a.heads_block, h_last = min(H, h_first + a.heads_block);
-    constexpr int U = STAGED ? 1 : 2;
     for (int h0 = h_first; h0 < h_last; h0 += U * a.hb) {
         float run[U][16];
         int what[U], head[U];  // 0: nothing, 1: a query, 2: a key, 3: a value
@@ -99,19 +116,17 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             what[j] = !live || h >= h_last ? 0 : h < p.Hq ? 1 : h < p.Hq + p.c.Hkv ? 2 : 3;
             head[j] = h - (what[j] == 1 ? 0 : what[j] == 2 ? p.Hq : p.Hq + p.c.Hkv);
             swap[j] = across && what[j] != 3;
+            widen8(raw[j][0], run[j]);
+            widen8(raw[j][1], run[j] + 8);
+            if (what[j] == 0 || !valid)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) run[j][e] = 0.f;
-            if (what[j] == 0 || !valid) continue;
-            const RopeRows& r = what[j] == 1 ? p.q : what[j] == 2 ? p.k : p.v;
-            const __nv_bfloat16* in =
-                reinterpret_cast<const __nv_bfloat16*>(r.src) + (b * r.sb + head[j] * r.sh + i * r.ss);
-            load8(in + (swap[j] ? off_a : 16 * u), run[j]);
-            load8(in + (swap[j] ? off_b : 16 * u + 8), run[j] + 8);
+                for (int e = 0; e < 16; ++e) run[j][e] = 0.f;
         }
+        fetch(h0 + U * a.hb);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (STAGED) {  // pairs of halves off the 8-element grid: through shared memory, within the row's warp
-                float* row = stage + slot * D;
+                float* row = stage + slot * (D + 1);
                 float x[16];
                 __syncwarp();
 #pragma unroll
@@ -262,7 +277,8 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     a.p = p;
     a.tokens = p.B * p.S;
     const int rows = kThreads / (D / 16), H = p.Hq + 2 * p.c.Hkv;
-    a.tb = std::min(rows / 8, pow2_at_least(a.tokens));
+    const int heads = std::min(8, pow2_at_least(H / 8 / 2 + 1));  // side by side, as in launch_rope
+    a.tb = std::min(rows / heads, pow2_at_least(a.tokens));
     a.hb = rows / a.tb;
     const long long blocks_x = (a.tokens + (long long)a.tb - 1) / a.tb;
     const int rounds = (H + a.hb - 1) / a.hb;
@@ -278,12 +294,10 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
 }
 
 template <int D, bool E4M3>
-cudaError_t read_d(const CacheReadParams& p, int n_sm, cudaStream_t stream) {
+cudaError_t read_d(const CacheReadParams& p, cudaStream_t stream) {
     const int rows = kThreads / (D / 16);
     const unsigned gx = (unsigned)((p.S + rows - 1) / rows);
-    // heads in one thread only where the positions alone fill the GPU four times over
-    const int per = (int)std::max<long long>(1, std::min<long long>(p.c.Hkv, (long long)gx * p.B * p.c.Hkv / (8LL * n_sm)));
-    const dim3 grid(gx, (unsigned)((p.c.Hkv + per - 1) / per), (unsigned)p.B);
+    const dim3 grid(gx, (unsigned)std::min(p.c.Hkv, 65535), (unsigned)p.B);
     cache_read_kernel<D, E4M3><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -294,9 +308,9 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, c
     if (p.c.d == 64) return e4m3 ? write_d<64, true>(p, n_sm, stream) : write_d<64, false>(p, n_sm, stream);
     return e4m3 ? write_d<128, true>(p, n_sm, stream) : write_d<128, false>(p, n_sm, stream);
 }
-cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, int n_sm, cudaStream_t stream) {
-    if (p.c.d == 64) return e4m3 ? read_d<64, true>(p, n_sm, stream) : read_d<64, false>(p, n_sm, stream);
-    return e4m3 ? read_d<128, true>(p, n_sm, stream) : read_d<128, false>(p, n_sm, stream);
+cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t stream) {
+    if (p.c.d == 64) return e4m3 ? read_d<64, true>(p, stream) : read_d<64, false>(p, stream);
+    return e4m3 ? read_d<128, true>(p, stream) : read_d<128, false>(p, stream);
 }
 
 }  // namespace attn

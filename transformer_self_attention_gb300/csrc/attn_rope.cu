@@ -31,23 +31,52 @@ struct RopeParams {
     const int* positions;
     long long pos_b, pos_s;
     float sign;  // -1: the gradient
+    int warp_rows;  // no row spans two warps
 };
 
 // STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
 // memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
-template <class T, bool STAGED>
+// Orders the shared-memory accesses of a row's threads.
+__device__ __forceinline__ void row_sync(int warp_rows) {
+    if (warp_rows) __syncwarp();
+    else __syncthreads();
+}
+
+// U rows a thread are fetched before the cosines and sines are computed, and the next U before the present ones are
+// turned, so that loads are always under way.
+// STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
+// memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
+template <class T, bool STAGED, int U>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    extern __shared__ float stage[];
+    extern __shared__ uint32_t stage[];
     __shared__ unsigned long long step[kRopeMaxPairs];
-    if ((int)threadIdx.x < p.t.rot / 2) step[threadIdx.x] = p.t.step[threadIdx.x];
-    __syncthreads();
     const int lanes = p.d / 16, u = threadIdx.x % lanes, slot = threadIdx.x / lanes;
     const int token = blockIdx.x * p.tb + slot / p.hb;
     const bool live = slot < p.tb * p.hb && token < p.tokens;
     const int b = live ? token / p.S : 0, s = live ? token - b * p.S : 0;
     const bool halves = !p.t.interleaved;
-    float c[8], sn[8];
+    int off_a = 16 * u, off_b = 16 * u + 8;
+    if (!STAGED) rope_runs(halves, p.t.rot, u, off_a, off_b);
+    const bool across = !STAGED && halves && 16 * u < p.t.rot;
+    const int h_first = blockIdx.y * p.heads_block, h_last = min(p.H, h_first + p.heads_block);
     const int pos = !live ? 0 : p.positions ? p.positions[b * p.pos_b + s * p.pos_s] : s;
+
+    Raw8<T> raw[U][2];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = h0 + i * p.hb + slot % p.hb;
+            if (!live || h >= h_last) continue;
+            const RopeRows& r = h < p.Hq ? p.q : p.k;
+            const T* in = reinterpret_cast<const T*>(r.src) + (b * r.sb + (h < p.Hq ? h : h - p.Hq) * r.sh + s * r.ss);
+            fetch8(in + off_a, raw[i][0]);
+            fetch8(in + off_b, raw[i][1]);
+        }
+    };
+    fetch(h_first);
+    if ((int)threadIdx.x < p.t.rot / 2) step[threadIdx.x] = p.t.step[threadIdx.x];
+    __syncthreads();
+    float c[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int q = 8 * u + e;
@@ -59,72 +88,77 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             sn[e] *= p.t.amp * p.sign;
         }
     }
-    int off_a = 16 * u, off_b = 16 * u + 8;
-    if (!STAGED) rope_runs(halves, p.t.rot, u, off_a, off_b);
-    const bool across = !STAGED && halves && 16 * u < p.t.rot;
-    const int h_first = blockIdx.y * p.heads_block, h_last = min(p.H, h_first + p.heads_block);
-    constexpr int U = STAGED ? 1 : 4;  // rows in flight per thread
     for (int h0 = h_first; h0 < h_last; h0 += U * p.hb) {
         float run[U][16];
-        T* out[U];
+        Raw8<T> raw_now[U][2];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (STAGED) {
+                raw_now[i][0] = raw[i][0];
+                raw_now[i][1] = raw[i][1];
+            } else {
+                widen8(raw[i][0], run[i]);
+                widen8(raw[i][1], run[i] + 8);
+            }
+        }
+        fetch(h0 + U * p.hb);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = h0 + i * p.hb + slot % p.hb;
-            out[i] = nullptr;
-            if (!live || h >= h_last) continue;
-            const RopeRows& r = h < p.Hq ? p.q : p.k;
-            const int hh = h < p.Hq ? h : h - p.Hq;
-            const T* in = reinterpret_cast<const T*>(r.src) + (b * r.sb + hh * r.sh + s * r.ss);
-            out[i] = reinterpret_cast<T*>(r.dst) + (b * r.db + hh * r.dh + s * r.ds);
-            load8(in + off_a, run[i]);
-            load8(in + off_b, run[i] + 8);
-        }
-        if (STAGED) {
-            float* row = stage + slot * p.d;
-            if (out[0]) {
+            const bool row_live = live && h < h_last;
+            if (STAGED) {
+                // Word by word, rows one word apart in the banks: at most two lanes of a warp meet in a bank.
+                constexpr int kWords = 16 * sizeof(T) / 4;
+                const bool on = slot < p.tb * p.hb;
+                uint32_t* row = stage + slot * (p.d * (int)sizeof(T) / 4 + 1);
+                T* row_t = reinterpret_cast<T*>(row);
+                const uint32_t* mine = reinterpret_cast<const uint32_t*>(raw_now[i]);
+                row_sync(p.warp_rows);
+                if (on)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) row[16 * u + e] = run[0][e];
-            }
-            __syncthreads();
-            float x[16];
-            if (out[0]) {
+                    for (int e = 0; e < kWords; ++e) row[kWords * u + e] = mine[e];
+                row_sync(p.warp_rows);
+                float x[16];
+                if (on) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int i0, i1;
-                    rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
-                    x[2 * e] = row[i0];
-                    x[2 * e + 1] = row[i1];
+                    for (int e = 0; e < 8; ++e) {
+                        int i0, i1;
+                        rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                        x[2 * e] = (float)row_t[i0];
+                        x[2 * e + 1] = (float)row_t[i1];
+                    }
+                    rope_turn(x, c, sn);
                 }
-                rope_turn(x, c, sn);
-            }
-            __syncthreads();
-            if (out[0]) {
+                row_sync(p.warp_rows);
+                if (on)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int i0, i1;
-                    rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
-                    row[i0] = x[2 * e];
-                    row[i1] = x[2 * e + 1];
-                }
-            }
-            __syncthreads();
-            if (out[0]) {
+                    for (int e = 0; e < 8; ++e) {
+                        int i0, i1;
+                        rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                        row_t[i0] = (T)x[2 * e];
+                        row_t[i1] = (T)x[2 * e + 1];
+                    }
+                row_sync(p.warp_rows);
+                if (!row_live) continue;
+                const RopeRows& r = h < p.Hq ? p.q : p.k;
+                uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<T*>(r.dst) +
+                                                      (b * r.db + (h < p.Hq ? h : h - p.Hq) * r.dh + s * r.ds) + 16 * u);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) run[0][e] = row[16 * u + e];
-                store8(out[0] + off_a, run[0]);
-                store8(out[0] + off_b, run[0] + 8);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (!out[i]) continue;
+                for (int e = 0; e < kWords; e += 4)
+                    out[e / 4] = make_uint4(row[kWords * u + e], row[kWords * u + e + 1], row[kWords * u + e + 2],
+                                            row[kWords * u + e + 3]);
+                continue;
+            } else {
                 float x[16];
                 runs_to_pairs(across, run[i], run[i] + 8, x);
                 rope_turn(x, c, sn);
                 pairs_to_runs(across, x, run[i], run[i] + 8);
-                store8(out[i] + off_a, run[i]);
-                store8(out[i] + off_b, run[i] + 8);
             }
+            if (!row_live) continue;
+            const RopeRows& r = h < p.Hq ? p.q : p.k;
+            T* out = reinterpret_cast<T*>(r.dst) + (b * r.db + (h < p.Hq ? h : h - p.Hq) * r.dh + s * r.ds);
+            store8(out + off_a, run[i]);
+            store8(out + off_b, run[i] + 8);
         }
     }
 }
@@ -154,9 +188,13 @@ cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k
     p.pos_s = pos_s;
     p.sign = inverse ? -1.f : 1.f;
     const int rows = kThreads / (d / 16);
-    // Eight heads side by side (their rows are neighbours in a [B, S, H, d] projection), the other rows of a block
-    // are neighbouring tokens (neighbours in [B, H, S, d]); few tokens leave more rows to the heads.
-    p.tb = std::min(std::max(1, rows / 8), pow2_at_least(p.tokens));
+    p.warp_rows = 32 % (d / 16) == 0;
+    // Up to eight heads side by side (their rows are neighbours in a [B, S, H, d] projection), fewer where a thread would
+    // walk over less than eight (its cosines and sines cost as much as several rows: 40 heads, 16K tokens, 58 us with 4
+    // heads side by side, 68 us with 8); the other rows of a block are neighbouring tokens (neighbours in [B, H, S, d]).
+    // Few tokens leave more rows to the heads.
+    const int heads = std::min(8, pow2_at_least(p.H / 8 / 2 + 1));
+    p.tb = std::min(std::max(1, rows / heads), pow2_at_least(p.tokens));
     p.hb = rows / p.tb;
     // A block walks over all heads of its tokens unless that leaves multiprocessors without four blocks.
     const long long blocks_x = (p.tokens + (long long)p.tb - 1) / p.tb;
@@ -166,13 +204,13 @@ cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k
     p.heads_block = (rounds + split - 1) / split * p.hb;
     const dim3 grid((unsigned)blocks_x, (unsigned)((p.H + p.heads_block - 1) / p.heads_block));
     const bool staged = !t.interleaved && t.rot % 16 != 0;
-    const size_t smem = staged ? sizeof(float) * (size_t)rows * d : 0;
+    const size_t smem = staged ? (size_t)rows * (d * (f32 ? 4 : 2) + 4) : 0;
     if (f32) {
-        if (staged) rope_kernel<float, true><<<grid, kThreads, smem, stream>>>(p);
-        else rope_kernel<float, false><<<grid, kThreads, 0, stream>>>(p);
+        if (staged) rope_kernel<float, true, 1><<<grid, kThreads, smem, stream>>>(p);
+        else rope_kernel<float, false, 2><<<grid, kThreads, 0, stream>>>(p);
     } else {
-        if (staged) rope_kernel<__nv_bfloat16, true><<<grid, kThreads, smem, stream>>>(p);
-        else rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(p);
+        if (staged) rope_kernel<__nv_bfloat16, true, 1><<<grid, kThreads, smem, stream>>>(p);
+        else rope_kernel<__nv_bfloat16, false, 2><<<grid, kThreads, 0, stream>>>(p);
     }
     return cudaGetLastError();
 }

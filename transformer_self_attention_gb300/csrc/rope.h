@@ -60,9 +60,26 @@ __device__ __forceinline__ void rope_turn(float (&x)[16], const float (&c)[8], c
         x[2 * e + 1] = a * s[e] + b * c[e];
     }
 }
-// Eight neighbouring elements as float.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+// Eight neighbouring elements as they are in memory, and as float.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 v;
+};
+template <>
+struct Raw8<float> {
+    float4 v, w;
+};
+__device__ __forceinline__ void fetch8(const __nv_bfloat16* p, Raw8<__nv_bfloat16>& r) {
+    r.v = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void fetch8(const float* p, Raw8<float>& r) {
+    r.v = reinterpret_cast<const float4*>(p)[0];
+    r.w = reinterpret_cast<const float4*>(p)[1];
+}
+__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16>& r, float* x) {
+    const uint4 v = r.v;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -70,10 +87,15 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 v = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float* x) {
+    x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
+    x[4] = r.w.x; x[5] = r.w.y; x[6] = r.w.z; x[7] = r.w.w;
+}
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float* x) {
+    Raw8<T> r;
+    fetch8(p, r);
+    widen8(r, x);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
