@@ -706,10 +706,12 @@ attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, in
                               attn_mask_kind kind, int window);
 
 /*
- * attn_paged_forward -- enqueue one decode step over `cache` on `stream`: one kernel.
+ * attn_paged_forward -- enqueue one decode step over `cache` on `stream`: one kernel, and a second one that joins
+ * the parts of split sequences, unless the page table is too small for any to be split.
  *   Q, O : bf16 [B, Hq, S_q, d], contiguous, 16-byte aligned.   LSE : float32 [B, Hq, S_q] or NULL.
  * Errors: ATTN_ERR_INVALID_ARG (pointers; a cache of another device, head count or width; a current device
- * other than the handle's), ATTN_ERR_UNSUPPORTED (max_pages * page > 2^26), ATTN_ERR_CUDA.
+ * other than the handle's), ATTN_ERR_UNSUPPORTED (max_pages * page > 2^30, or B * Hkv * max_pages * page
+ * beyond about 2^35), ATTN_ERR_CUDA.
  * Device errors are read by attn_cache_poll_device_error of the cache.
  */
 attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
@@ -723,14 +725,13 @@ attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas);
 attn_status attn_paged_destroy(attn_paged_handle h);
 
 /*
- * attn_paged_split_host -- how attn_paged_forward cuts its work, on the host only.  rows = (Hq / Hkv) * S_q.
+ * attn_paged_split_host -- how attn_paged_forward cuts its work over a grid of CTAs, on the host only.
  * Each part is 8 ints: CTA, sequence, kv head, first key block, one past the last, key blocks of the unit,
  * first and last CTA that hold blocks of the unit.  parts may be NULL with cap = 0 to query *n_parts.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED.
  */
 attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dtype, attn_mask_kind kind, int window,
-                                  const int* cache_len, int grid, int rows, int* n_cta, int* parts, int cap,
-                                  int* n_parts);
+                                  const int* cache_len, int grid, int* n_cta, int* parts, int cap, int* n_parts);
 
 #ifdef __cplusplus
 }

@@ -90,27 +90,40 @@ def test_paged_create_refuses(args, status):
     assert e.value.status == status
 
 
+def test_split_refuses_a_cost_line_beyond_31_bits():
+    with pytest.raises(tsa.AttnError) as e:
+        tsa.attn_paged_split_host(1024, 64, 1, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, [1 << 24] * 1024, 304)
+    assert e.value.status == tsa.ATTN_ERR_UNSUPPORTED
+
+
+def test_short_units_are_not_cut():
+    """As many CTAs as units, one whole unit each, while the grid is large enough."""
+    for lens in ([100], [1, 384, 17, 0, 90]):
+        n_cta, parts = tsa.attn_paged_split_host(len(lens), 8, 1, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, lens, 304)
+        assert n_cta == len(parts) == 8 * sum(n > 0 for n in lens)
+        assert all(p[3] == 0 and p[4] == p[5] for p in parts.tolist())
+
+
 def _cases():
     rng = np.random.default_rng(5)
-    yield [0, 0, 0], 2, tsa.MASK_CAUSAL, 0, 152, 4
-    yield [1], 1, tsa.MASK_CAUSAL, 0, 152, 1
-    yield [100], 8, tsa.MASK_CAUSAL, 0, 152, 4
-    yield [1 << 20, 5, 0, 1 << 20], 8, tsa.MASK_CAUSAL, 0, 152, 8
-    yield [1 << 24] * 1024, 64, tsa.MASK_CAUSAL, 0, 152, 8  # the cost line passes 32 bits
+    yield [0, 0, 0], 2, tsa.MASK_CAUSAL, 0, 152
+    yield [1], 1, tsa.MASK_CAUSAL, 0, 152
+    yield [100], 8, tsa.MASK_CAUSAL, 0, 152
+    yield [1 << 20, 5, 0, 1 << 20], 8, tsa.MASK_CAUSAL, 0, 152
+    yield [1 << 20] * 500, 50, tsa.MASK_CAUSAL, 0, 304  # a cost line of more than 2^30
     for _ in range(60):
         B = int(rng.integers(1, 60))
         lens = (rng.integers(0, 2, B) * np.exp(rng.uniform(0, 10, B))).astype(int).tolist()
         kind = [tsa.MASK_FULL, tsa.MASK_CAUSAL, tsa.MASK_CAUSAL_SLIDING][rng.integers(3)]
-        yield lens, int(rng.integers(1, 9)), kind, int(rng.integers(0, 3000)), int(rng.integers(1, 153)), \
-            int(rng.integers(1, 65))
+        yield lens, int(rng.integers(1, 9)), kind, int(rng.integers(0, 3000)), int(rng.integers(1, 305))
 
 
-@pytest.mark.parametrize("lens,Hkv,kind,window,grid,rows", list(_cases()))
+@pytest.mark.parametrize("lens,Hkv,kind,window,grid", list(_cases()))
 @pytest.mark.parametrize("d,dtype", [(128, tsa.ATTN_BF16), (64, tsa.ATTN_FP8_E4M3)])
-def test_split_covers_every_block_once(lens, Hkv, kind, window, grid, rows, d, dtype):
+def test_split_covers_every_block_once(lens, Hkv, kind, window, grid, d, dtype):
     """Every visible key block of every unit in exactly one part; the CTAs named as a unit's first and last are those
     that hold its blocks, without a gap; a CTA leaves at most two units unfinished, which have different slots."""
-    n_cta, parts = tsa.attn_paged_split_host(len(lens), Hkv, 1, d, dtype, kind, window, lens, grid, rows)
+    n_cta, parts = tsa.attn_paged_split_host(len(lens), Hkv, 1, d, dtype, kind, window, lens, grid)
     keys = {(128, tsa.ATTN_BF16): 16, (64, tsa.ATTN_FP8_E4M3): 32}[(d, dtype)]
     assert 0 <= n_cta <= grid
     want = {}

@@ -132,7 +132,7 @@ def _load():
                        ("attn_paged_create", [ctypes.POINTER(P), I, I, I, I, I, F, I, I]),
                        ("attn_paged_forward", [P, P, P, P, LL, I, P, P, P, P]),
                        ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_destroy", [P]),
-                       ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, I, ctypes.POINTER(I), P, I,
+                       ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, ctypes.POINTER(I), P, I,
                                                   ctypes.POINTER(I)])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
@@ -521,13 +521,13 @@ def attn_paged_destroy(handle: int) -> int:
     return _lib.attn_paged_destroy(handle)
 
 
-def attn_paged_split_host(B, Hkv, S_q, d, dtype, kind, window, cache_len, grid, rows):
+def attn_paged_split_host(B, Hkv, S_q, d, dtype, kind, window, cache_len, grid):
     """Host-only split of the paged decode: (n_cta, int32 [parts, 8]: CTA, sequence, kv head, first key block,
     one past the last, key blocks of the unit, first and last CTA of the unit).  Raises AttnError."""
     lens, _ = _int_array(cache_len)
     n_cta, n = ctypes.c_int(0), ctypes.c_int(0)
     args = (int(B), int(Hkv), int(S_q), int(d), int(dtype), int(kind), int(window),
-            ctypes.cast(lens, ctypes.c_void_p), int(grid), int(rows))
+            ctypes.cast(lens, ctypes.c_void_p), int(grid))
     st = _lib.attn_paged_split_host(*args, ctypes.byref(n_cta), None, 0, ctypes.byref(n))
     parts = np.zeros((max(n.value, 1), 8), dtype=np.int32)
     if st == ATTN_OK:
@@ -538,47 +538,52 @@ def attn_paged_split_host(B, Hkv, S_q, d, dtype, kind, window, cache_len, grid, 
     return n_cta.value, parts[:n.value]
 
 
+torch = None  # the torch module, once a class below is used (the C ABI functions above do without it)
+
+
+def _need_torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+    return torch
+
+
 def _rows(name, t, shape, dtype, device):
-    """attn_rows of a tensor view [B, H, S, d] whose last dimension is contiguous."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    """attn_rows of a tensor view [B, H, S, d] (shape: a tuple) whose last dimension is contiguous, on CUDA device
+    number `device`."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{device}")
     sb, sh, ss, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return attn_rows(t.data_ptr(), sb, sh, ss)
 
 
-class _Launch:
-    """The current device and stream of a call: makes the tensors' device current for the call, and tells the caching
-    allocator about tensors used on a stream other than the current one."""
+def _int32(name, t, shape, device):
+    """Pointer of a contiguous int32 tensor."""
+    if t.dtype is not torch.int32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
+    return t.data_ptr()
 
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        self._old = None
-        if device.index != torch.cuda.current_device():
-            self._old = torch.cuda.current_device()
-            torch.cuda.set_device(device)
-        current = torch.cuda.current_stream()
-        self._foreign = stream is not None and stream != current
-        self._stream = stream if self._foreign else current
-        self.stream = self._stream.cuda_stream
 
-    def used(self, *tensors):
-        if self._foreign:
-            for t in tensors:
+def _call(device, stream, fn, args, used):
+    """fn(*args, stream) with CUDA device number `device` current; `used`: the tensors of the call, reported to the
+    caching allocator when the stream is not the current one.  Returns fn's status."""
+    old = torch._C._cuda_getDevice()
+    if old != device:
+        torch.cuda.set_device(device)
+    try:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+        if stream is not None and stream.cuda_stream != raw:
+            raw = stream.cuda_stream
+            for t in used:
                 if t is not None:
-                    t.record_stream(self._stream)
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self._old is not None:
-            import torch
-            torch.cuda.set_device(self._old)
-        return False
+                    t.record_stream(stream)
+        return fn(*args, raw)
+    finally:
+        if old != device:
+            torch.cuda.set_device(old)
 
 
 class RotaryPositions:
@@ -596,6 +601,7 @@ class RotaryPositions:
             raise ValueError(f"layout is one of {sorted(ROPE_LAYOUTS)}, scaling one of {sorted(ROPE_SCALINGS)}")
         if amplitude is not None and not amplitude > 0:
             raise ValueError("amplitude must be positive")
+        _need_torch()
         self.d, self.rotary_dim = int(d), int(d if rotary_dim is None else rotary_dim)
         self.handle = attn_rope_create(d, self.rotary_dim, ROPE_LAYOUTS[layout], base, ROPE_SCALINGS[scaling], factor,
                                        original_len, beta_fast, beta_slow, amplitude or 0.0)
@@ -626,34 +632,37 @@ class RotaryPositions:
         return self._apply(_lib.attn_rope_backward, "attn_rope_backward", dQ_out, dK_out, positions, dQ, dK, stream)
 
     def _apply(self, fn, name, Q, K, positions, Q_out, K_out, stream):
-        import torch
-        if Q.dim() != 4 or Q.shape[3] != self.d or Q.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"Q must be a bfloat16 or float32 tensor [B, Hq, S, {self.d}]")
-        B, Hq, S, d = Q.shape
-        if K is not None and (K.dim() != 4 or K.shape[1] < 1):
-            raise ValueError(f"K must be a tensor [B, Hk, S, {d}] with at least one head")
-        ps = (0, 0)
+        dtype, device, shape = Q.dtype, Q.get_device(), Q.shape
+        if (dtype is not torch.bfloat16 and dtype is not torch.float32) or len(shape) != 4 or shape[3] != self.d \
+                or device < 0:
+            raise ValueError(f"Q must be a CUDA bfloat16 or float32 tensor [B, Hq, S, {self.d}]")
+        B, Hq, S, d = shape
+        q = _rows("Q", Q, shape, dtype, device)
+        if Q_out is None:
+            Q_out = torch.empty(shape, dtype=dtype, device=Q.device)
+        qo = _rows("Q_out", Q_out, shape, dtype, device)
+        Hk, k, ko = 0, None, None
+        if K is not None:
+            if K.dim() != 4 or K.shape[1] < 1:
+                raise ValueError(f"K must be a tensor [B, Hk, S, {d}] with at least one head")
+            Hk = K.shape[1]
+            shape = (B, Hk, S, d)
+            k = _rows("K", K, shape, dtype, device)
+            if K_out is None:
+                K_out = torch.empty(shape, dtype=dtype, device=Q.device)
+            ko = _rows("K_out", K_out, shape, dtype, device)
+        pos, pb, ps = None, 0, 0
         if positions is not None:
-            if positions.dtype != torch.int32 or positions.device != Q.device or positions.shape not in ((B, S), (S,)):
+            if positions.dtype is not torch.int32 or positions.get_device() != device \
+                    or (positions.shape != (B, S) and positions.shape != (S,)):
                 raise ValueError(f"positions must be an int32 tensor of shape {(B, S)} or {(S,)} on {Q.device}")
-            ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
-        with _Launch(Q.device, stream) as at:
-            if Q_out is None:
-                Q_out = torch.empty((B, Hq, S, d), dtype=Q.dtype, device=Q.device)
-            q, qo = _rows("Q", Q, Q.shape, Q.dtype, Q.device), _rows("Q_out", Q_out, Q.shape, Q.dtype, Q.device)
-            k = ko = None
-            if K is not None:
-                shape = torch.Size((B, K.shape[1], S, d))
-                if K_out is None:
-                    K_out = torch.empty(shape, dtype=Q.dtype, device=Q.device)
-                k, ko = _rows("K", K, shape, Q.dtype, Q.device), _rows("K_out", K_out, shape, Q.dtype, Q.device)
-            at.used(Q, K, positions, Q_out, K_out)
-            if B * S * Hq:
-                st = fn(self.handle, ATTN_BF16 if Q.dtype == torch.bfloat16 else ATTN_F32, B, S, Hq, q, qo,
-                        0 if K is None else K.shape[1], k, ko, None if positions is None else positions.data_ptr(),
-                        ps[0], ps[1], at.stream)
-                if st != ATTN_OK:
-                    raise AttnError(st, name)
+            pos = positions.data_ptr()
+            pb, ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
+        if B * S * Hq:
+            st = _call(device, stream, fn, (self.handle, ATTN_BF16 if dtype is torch.bfloat16 else ATTN_F32, B, S, Hq, q,
+                                            qo, Hk, k, ko, pos, pb, ps), (Q, K, positions, Q_out, K_out))
+            if st != ATTN_OK:
+                raise AttnError(st, name)
         return Q_out if K is None else (Q_out, K_out)
 
 
@@ -667,7 +676,7 @@ class PagedCache:
     """
 
     def __init__(self, n_pages, Hkv, page, d, dtype="bf16", pages=None, scales=None, device=None):
-        import torch
+        _need_torch()
         kinds = {"bf16": (ATTN_BF16, torch.bfloat16), "e4m3": (ATTN_FP8_E4M3, torch.float8_e4m3fn)}
         if dtype not in kinds:
             raise ValueError(f"dtype is one of {sorted(kinds)}")
@@ -683,7 +692,7 @@ class PagedCache:
             pages = pages.view(tdt)
         if tuple(pages.shape) != want or pages.dtype != tdt or not pages.is_cuda or not pages.is_contiguous():
             raise ValueError(f"pages must be a contiguous CUDA {tdt} tensor of shape {want}")
-        self.device = pages.device
+        self.device, self._device = pages.device, pages.get_device()
         if dtype == "e4m3":
             want = (n_pages, Hkv, page // 16, 2, 16)
             if scales is None:
@@ -700,7 +709,6 @@ class PagedCache:
 
     def close(self):
         if getattr(self, "handle", None):
-            import torch
             with torch.cuda.device(self.device):
                 attn_cache_destroy(self.handle)
             self.handle = None
@@ -712,87 +720,77 @@ class PagedCache:
             pass
 
     def _table(self, page_table, cache_len):
-        import torch
-        if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != self.device
+        """(B, arguments of the C calls: table pointer, row stride, pages a row, lengths pointer)."""
+        if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != self._device
                 or page_table.shape[1] < 1 or page_table.stride(1) != 1):
             raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on {self.device}")
-        B = page_table.shape[0]
-        if (cache_len.dtype != torch.int32 or tuple(cache_len.shape) != (B,) or cache_len.device != self.device
-                or not cache_len.is_contiguous()):
-            raise ValueError(f"cache_len must be a contiguous int32 tensor of shape {(B,)} on {self.device}")
-        return B, page_table.data_ptr(), page_table.stride(0), page_table.shape[1], cache_len.data_ptr()
+        B, wide = page_table.shape
+        return B, (page_table.data_ptr(), page_table.stride(0), wide,
+                   _int32("cache_len", cache_len, (B,), self._device))
 
     def write(self, K, V, page_table, cache_len, new_len=None, rope=None, Q=None, Q_out=None, stream=None):
         """Append K, V [B, Hkv, S_new, d] (bf16 views): row i < new_len[b] (int32 CUDA [B]; default S_new) of
         sequence b goes to position cache_len[b] - new_len[b] + i.  With ``rope`` (RotaryPositions) the keys, and
         Q [B, Hq, S_new, d] if given, are rotated by those positions; returns the rotated Q, or None."""
-        import torch
         _, Hkv, _, d = self.shape
-        B, table, stride, wide, lens = self._table(page_table, cache_len)
+        device = self._device
+        B, table = self._table(page_table, cache_len)
         if K.dim() != 4:
             raise ValueError(f"K must be a tensor [{B}, {Hkv}, S_new, {d}]")
         S = K.shape[2]
-        if rope is None and Q is not None:
-            raise ValueError("Q is only taken to be rotated: give rope")
+        shape = (B, Hkv, S, d)
+        k = _rows("K", K, shape, torch.bfloat16, device)
+        v = _rows("V", V, shape, torch.bfloat16, device)
         if rope is not None and rope.d != d:
             raise ValueError("rope is for another head width")
-        if new_len is not None and (new_len.dtype != torch.int32 or tuple(new_len.shape) != (B,)
-                                    or new_len.device != self.device or not new_len.is_contiguous()):
-            raise ValueError(f"new_len must be a contiguous int32 tensor of shape {(B,)} on {self.device}")
-        with _Launch(self.device, stream) as at:
-            shape = torch.Size((B, Hkv, S, d))
-            k = _rows("K", K, shape, torch.bfloat16, self.device)
-            v = _rows("V", V, shape, torch.bfloat16, self.device)
-            q = qo = None
-            Hq = 0
-            if Q is not None:
-                if Q.dim() != 4 or Q.shape[1] < 1:
-                    raise ValueError(f"Q must be a tensor [{B}, Hq, {S}, {d}] with at least one head")
-                Hq = Q.shape[1]
-                shape = torch.Size((B, Hq, S, d))
-                if Q_out is None:
-                    Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-                q = _rows("Q", Q, shape, torch.bfloat16, self.device)
-                qo = _rows("Q_out", Q_out, shape, torch.bfloat16, self.device)
-            at.used(K, V, Q, Q_out, page_table, cache_len, new_len, self.pages, self.scales)
-            if B:
-                st = _lib.attn_cache_write(self.handle, B, S, k, v, table, stride, wide, lens,
-                                           None if new_len is None else new_len.data_ptr(),
-                                           None if rope is None else rope.handle, Hq, q, qo, at.stream)
-                if st != ATTN_OK:
-                    raise AttnError(st, "attn_cache_write")
+        Hq, q, qo = 0, None, None
+        if Q is not None:
+            if rope is None:
+                raise ValueError("Q is only taken to be rotated: give rope")
+            if Q.dim() != 4 or Q.shape[1] < 1:
+                raise ValueError(f"Q must be a tensor [{B}, Hq, {S}, {d}] with at least one head")
+            Hq = Q.shape[1]
+            shape = (B, Hq, S, d)
+            q = _rows("Q", Q, shape, torch.bfloat16, device)
+            if Q_out is None:
+                Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device)
+        new = None if new_len is None else _int32("new_len", new_len, (B,), device)
+        if B:
+            st = _call(device, stream, _lib.attn_cache_write,
+                       (self.handle, B, S, k, v, *table, new, None if rope is None else rope.handle, Hq, q, qo),
+                       (K, V, Q, Q_out, page_table, cache_len, new_len, self.pages, self.scales))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_cache_write")
         return Q_out if Q is not None else None
 
     def read(self, page_table, cache_len, first=0, length=None, K=None, V=None, stream=None):
         """Positions first .. first + length - 1 of every sequence as dense (K, V), bf16 [B, Hkv, length, d].
         Rows at or past cache_len[b] are left as they were (zeros in tensors allocated here)."""
-        import torch
         _, Hkv, _, d = self.shape
-        B, table, stride, wide, lens = self._table(page_table, cache_len)
+        B, table = self._table(page_table, cache_len)
         if length is None:
             if K is None and V is None:
                 raise ValueError("give length, or the tensors to fill")
             length = (K if K is not None else V).shape[2]
-        with _Launch(self.device, stream) as at:
-            shape = torch.Size((B, Hkv, int(length), d))
+        shape = (B, Hkv, int(length), d)
+        if K is None or V is None:
             with torch.cuda.stream(stream):  # a new tensor's zeros come before the rows
                 if K is None:
                     K = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
                 if V is None:
                     V = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-            k = _rows("K", K, shape, torch.bfloat16, self.device)
-            v = _rows("V", V, shape, torch.bfloat16, self.device)
-            at.used(K, V, page_table, cache_len, self.pages, self.scales)
-            if B:
-                st = _lib.attn_cache_read(self.handle, B, int(length), int(first), k, v, table, stride, wide, lens,
-                                          at.stream)
-                if st != ATTN_OK:
-                    raise AttnError(st, "attn_cache_read")
+        k = _rows("K", K, shape, torch.bfloat16, self._device)
+        v = _rows("V", V, shape, torch.bfloat16, self._device)
+        if B:
+            st = _call(self._device, stream, _lib.attn_cache_read, (self.handle, B, int(length), int(first), k, v, *table),
+                       (K, V, page_table, cache_len, self.pages, self.scales))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_cache_read")
         return K, V
 
     def poll_device_error(self):
         """(status, code): synchronise; code has the CACHE_ERR_* bits recorded since the last poll."""
-        import torch
         with torch.cuda.device(self.device):
             return attn_cache_poll_device_error(self.handle)
 
@@ -806,17 +804,17 @@ class PagedDecodeAttention:
 
     def __init__(self, B, Hq, Hkv, S_q, d, scale=None, kind=MASK_CAUSAL, window=0, device=None):
         import math
-        import torch
+        _need_torch()
         self.shape = (int(B), int(Hq), int(Hkv), int(S_q), int(d))
         self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(d)
         self.kind, self.window = int(kind), int(window)
         with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-            self.device = torch.device("cuda", torch.cuda.current_device())
+            self._device = torch.cuda.current_device()
+            self.device = torch.device("cuda", self._device)
             self.handle = attn_paged_create(B, Hq, Hkv, S_q, d, self.scale, self.kind, self.window)
 
     def close(self):
         if getattr(self, "handle", None):
-            import torch
             with torch.cuda.device(self.device):
                 attn_paged_destroy(self.handle)
             self.handle = None
@@ -828,26 +826,25 @@ class PagedDecodeAttention:
             pass
 
     def __call__(self, Q, cache, page_table, cache_len, O=None, LSE=None, stream=None, want_lse=True):
-        import torch
-        B, Hq, Hkv, S_q, d = self.shape
-        rows, table, stride, wide, lens = cache._table(page_table, cache_len)
+        B, Hq, _, S_q, d = self.shape
+        rows, table = cache._table(page_table, cache_len)
         if rows != B:
             raise ValueError(f"page_table must have {B} rows")
-        for name, t, shape, dt in (("Q", Q, (B, Hq, S_q, d), torch.bfloat16), ("O", O, (B, Hq, S_q, d), torch.bfloat16),
-                                   ("LSE", LSE, (B, Hq, S_q), torch.float32)):
-            if t is not None and (t.device != self.device or t.dtype != dt or not t.is_contiguous()
-                                  or tuple(t.shape) != shape):
-                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape} on {self.device}")
-        with _Launch(self.device, stream) as at:
-            if O is None:
-                O = torch.empty_like(Q)
-            if LSE is None and want_lse:
-                LSE = torch.empty((B, Hq, S_q), dtype=torch.float32, device=Q.device)
-            at.used(Q, O, LSE, page_table, cache_len, cache.pages, cache.scales)
-            st = _lib.attn_paged_forward(self.handle, cache.handle, Q.data_ptr(), table, stride, wide, lens,
-                                         O.data_ptr(), None if LSE is None else LSE.data_ptr(), at.stream)
-            if st != ATTN_OK:
-                raise AttnError(st, "attn_paged_forward")
+        shape = (B, Hq, S_q, d)
+        if O is None:
+            O = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        if LSE is None and want_lse:
+            LSE = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
+        for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
+                                  ("LSE", LSE, shape[:3], torch.float32)):
+            if t is not None and (t.dtype is not dt or t.get_device() != self._device or t.shape != want
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {want} on {self.device}")
+        st = _call(self._device, stream, _lib.attn_paged_forward,
+                   (self.handle, cache.handle, Q.data_ptr(), *table, O.data_ptr(), None if LSE is None else LSE.data_ptr()),
+                   (Q, O, LSE, page_table, cache_len, cache.pages, cache.scales))
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_paged_forward")
         return O, LSE
 
     def set_grid_limit(self, max_ctas: int):

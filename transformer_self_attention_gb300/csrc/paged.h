@@ -52,14 +52,16 @@ struct CacheReadParams {
     int B, S, first;
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, cudaStream_t stream);
-cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, int n_sm, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged decode
-// Work units are (sequence, kv head), in that order; a unit of a sequence with n key blocks costs n + kPagedOverhead
-// (its start, its merge and its output cost about as much as that many blocks).  Sequences without keys
-// cost nothing.  The cost line [0, W) is cut into C equal intervals, one per CTA; inside a unit the blocks
-// follow the overhead, so that an interval holds the blocks whose cost position it covers.
-constexpr int kPagedOverhead = 6;
+// Work units are (sequence, kv head), in that order.  A unit of n key blocks costs max(n, kPagedMin) + kPagedOverhead:
+// its start, its merge and its output cost about as much as kPagedOverhead blocks, and a unit of few blocks is not worth
+// cutting (joining its parts costs more than the other blocks' time), so that units up to kPagedMin all cost the same
+// and the cuts fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals,
+// equal but for one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost
+// positions its interval covers.
+constexpr unsigned kPagedOverhead = 6, kPagedMin = 24;
 constexpr int kPagedMaxBatch = ATTN_DECODE_MAX_BATCH;
 
 // Key blocks [lo, hi) of `keys` positions that some row of a sequence of length n can see.
@@ -68,13 +70,29 @@ __host__ __device__ inline void paged_blocks(int n, int S_q, int window, int key
     const int first = window < 0 ? 0 : n - S_q - window;
     lo = first > 0 ? first / keys : 0;
 }
-__host__ __device__ inline long long paged_cut(long long W, int C, int c) { return W * c / C; }
-// The CTA whose interval holds cost position x.
-__host__ __device__ inline int paged_owner(long long W, int C, long long x) { return (int)(((x + 1) * C - 1) / W); }
-// CTAs in use: one per unit, more where the intervals still cost `least` (one round of a CTA's warps).
-__host__ __device__ inline int paged_ctas(long long W, long long units, int grid, int least) {
-    const long long c = W / least > units ? W / least : units;
-    return c < 1 ? 1 : c < grid ? (int)c : grid;
+__host__ __device__ inline unsigned paged_cost(int n) {
+    return n == 0 ? 0 : ((unsigned)n < kPagedMin ? kPagedMin : (unsigned)n) + kPagedOverhead;
+}
+struct PagedCuts {
+    unsigned C, q, r;  // CTAs; the intervals cost q + 1 for the first r, q for the others
+    // One CTA per unit, more where the intervals still cost as much as a short unit.
+    __host__ __device__ PagedCuts(unsigned W, unsigned units, unsigned grid) {
+        C = W / (kPagedMin + kPagedOverhead);
+        C = C < units ? units : C;
+        C = C < grid ? C : grid;
+        C = C < 1 ? 1 : C;
+        q = W / C;
+        r = W - q * C;
+    }
+    __host__ __device__ unsigned begin(unsigned c) const { return c * q + (c < r ? c : r); }
+    __host__ __device__ unsigned owner(unsigned x) const {  // the CTA whose interval holds cost position x
+        const unsigned wide = r * (q + 1);
+        return x < wide ? x / (q + 1) : r + (x - wide) / q;
+    }
+};
+// Whether a launch may cut a unit at all, for any lengths up to `room` positions.
+__host__ __device__ inline bool paged_may_cut(long long units, long long room, int keys, int grid) {
+    return units > grid || room > (long long)kPagedMin * keys;
 }
 
 struct PagedParams {
@@ -84,9 +102,9 @@ struct PagedParams {
     float* lse;      // may be null
     CacheView c;
     PageTable t;
-    float* part_o;        // [2 * grid][rows_pad][d], two slots per CTA: its first and its last stretch
+    float* part_o;        // [2 * grid][rows_pad][d] unscaled sums, two slots per CTA: its first and its last stretch
     float2* part_ml;      // [2 * grid][rows_pad]: the row maximum (base 2) and sum
-    unsigned* counters;   // [B * Hkv] partial results of a unit that have arrived
+    int2* cut;            // [grid]: the unit that begins in a CTA and ends in a later one, and that CTA; unit -1: none
     int B, Hq, Hkv, S_q, rows;
     int window;           // -1: none
     int causal;           // 0: every row sees every cached position
@@ -95,6 +113,9 @@ struct PagedParams {
 };
 int paged_block_keys(int d, bool e4m3);   // positions per key block
 int paged_rows_pad(int rows);             // 16, 32 or 64
-cudaError_t launch_paged_decode(const PagedParams& p, bool e4m3, int grid, cudaStream_t stream);
+int paged_ctas_per_sm();
+
+// `merge`: launch the joining kernel behind it (a unit may be cut).
+cudaError_t launch_paged_decode(const PagedParams& p, bool e4m3, int grid, bool merge, cudaStream_t stream);
 
 }  // namespace attn

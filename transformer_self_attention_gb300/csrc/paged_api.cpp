@@ -30,12 +30,12 @@ struct attn_cache_plan {
 
 struct attn_paged_plan {
     int B = 0, Hq = 0, Hkv = 0, S_q = 0, d = 0, kind = 0, window = 0;
-    int device = 0, n_sm = 0, grid = 0;
+    int device = 0, n_sm = 0, grid = 0, max_grid = 0;
     long long watchdog_ns = 2000000000LL;
     float scale = 0.f;
     float* d_part = nullptr;
     float2* d_ml = nullptr;
-    unsigned* d_counters = nullptr;
+    int2* d_cut = nullptr;
 };
 
 namespace {
@@ -138,7 +138,7 @@ void free_paged(attn_paged_plan* h) {
     if (!h) return;
     if (h->d_part) cudaFree(h->d_part);
     if (h->d_ml) cudaFree(h->d_ml);
-    if (h->d_counters) cudaFree(h->d_counters);
+    if (h->d_cut) cudaFree(h->d_cut);
     delete h;
 }
 
@@ -284,7 +284,7 @@ attn_status attn_cache_read(attn_cache_handle h, int B, int S, int first, const 
     p.k = rows_of(nullptr, K);
     p.v = rows_of(nullptr, V);
     p.B = B; p.S = S; p.first = first;
-    const cudaError_t e = attn::launch_cache_read(p, h->e4m3, h->n_sm, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = attn::launch_cache_read(p, h->e4m3, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -324,13 +324,11 @@ attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, in
     cudaError_t e = cudaGetDevice(&h->device);
     if (e != cudaSuccess) return fail(e);
     if ((h->n_sm = attn::current_sm_count()) < 1) return fail(cudaErrorUnknown);
-    h->grid = h->n_sm;
+    h->grid = h->max_grid = h->n_sm * attn::paged_ctas_per_sm();
     const size_t rows = 2 * (size_t)h->grid * attn::paged_rows_pad(Hq / Hkv * S_q);
     if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_part), rows * d * sizeof(float))) != cudaSuccess) return fail(e);
     if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_ml), rows * sizeof(float2))) != cudaSuccess) return fail(e);
-    const size_t counters = sizeof(unsigned) * (size_t)B * Hkv;
-    if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_counters), counters)) != cudaSuccess) return fail(e);
-    if ((e = cudaMemset(h->d_counters, 0, counters)) != cudaSuccess) return fail(e);
+    if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_cut), sizeof(int2) * h->grid)) != cudaSuccess) return fail(e);
     *out = h;
     return ATTN_OK;
 }
@@ -342,25 +340,30 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (cache->c.Hkv != h->Hkv || cache->c.d != h->d || cache->device != h->device || !on_device(h->device))
         return ATTN_ERR_INVALID_ARG;
-    if ((long long)max_pages * cache->c.page > (1 << 26)) return ATTN_ERR_UNSUPPORTED;
+    const long long room = (long long)max_pages * cache->c.page;
+    const int keys = attn::paged_block_keys(h->d, cache->e4m3);
+    const long long most = attn::kPagedMin + attn::kPagedOverhead + room / keys + 1;  // a unit's cost
+    // positions, and places on the cost line, fit an int
+    if (room > (1 << 30) || most * h->B * h->Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
     attn::PagedParams p{};
     p.tm = cache->map;
     p.q = Q; p.o = O; p.lse = LSE;
     p.c = cache->c;
     p.t.pages = page_table; p.t.len = cache_len; p.t.stride = table_stride; p.t.max_pages = max_pages;
-    p.part_o = h->d_part; p.part_ml = h->d_ml; p.counters = h->d_counters;
+    p.part_o = h->d_part; p.part_ml = h->d_ml; p.cut = h->d_cut;
     p.B = h->B; p.Hq = h->Hq; p.Hkv = h->Hkv; p.S_q = h->S_q; p.rows = h->Hq / h->Hkv * h->S_q;
     p.window = h->window;
     p.causal = h->kind != ATTN_MASK_FULL;
     p.scale_log2 = (float)((double)h->scale * 1.4426950408889634);
     p.watchdog_ns = h->watchdog_ns;
-    const cudaError_t e = attn::launch_paged_decode(p, cache->e4m3, h->grid, static_cast<cudaStream_t>(stream));
+    const bool merge = attn::paged_may_cut((long long)h->B * h->Hkv, room, keys, h->grid);
+    const cudaError_t e = attn::launch_paged_decode(p, cache->e4m3, h->grid, merge, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas) {
     if (!h || max_ctas < 1) return ATTN_ERR_INVALID_ARG;
-    h->grid = std::min(max_ctas, h->n_sm);
+    h->grid = std::min(max_ctas, h->max_grid);
     return ATTN_OK;
 }
 
@@ -372,49 +375,48 @@ attn_status attn_paged_destroy(attn_paged_handle h) {
 }
 
 attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dtype, attn_mask_kind kind, int window,
-                                  const int* cache_len, int grid, int rows, int* n_cta, int* parts, int cap,
+                                  const int* cache_len, int grid, int* n_cta, int* parts, int cap,
                                   int* n_parts) {
-    if (!cache_len || !n_cta || !n_parts || grid < 1 || rows < 1 || rows > ATTN_DECODE_MAX_ROWS || (cap > 0 && !parts))
+    if (!cache_len || !n_cta || !n_parts || grid < 1 || (cap > 0 && !parts))
         return ATTN_ERR_INVALID_ARG;
     const attn_status vs = validate_paged(B, Hkv, Hkv, 1, kind, window);
     if (vs != ATTN_OK) return vs;
     if (S_q < 1 || (dtype != ATTN_BF16 && dtype != ATTN_FP8_E4M3) || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
     const int w = kind == ATTN_MASK_CAUSAL_SLIDING ? window : -1;
     const int keys = attn::paged_block_keys(d, dtype == ATTN_FP8_E4M3);
-    const int rings = 8 / (attn::paged_rows_pad(rows) / 16);
-    std::vector<long long> cost(B + 1, 0);
+    std::vector<unsigned> cost(B + 1, 0);
     std::vector<int> n(B);
-    long long units = 0;
+    unsigned units = 0;
     for (int b = 0; b < B; ++b) {
         int lo, hi;
         if (cache_len[b] < 0) return ATTN_ERR_INVALID_ARG;
         attn::paged_blocks(cache_len[b], S_q, w, keys, lo, hi);
         n[b] = hi - lo;
         if (n[b]) units += Hkv;
-        cost[b + 1] = cost[b] + (n[b] ? (long long)Hkv * (n[b] + attn::kPagedOverhead) : 0);
+        if ((long long)attn::paged_cost(n[b]) * Hkv + cost[b] > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+        cost[b + 1] = cost[b] + Hkv * attn::paged_cost(n[b]);
     }
-    const long long W = cost[B];
-    *n_cta = W ? attn::paged_ctas(W, units, grid, rings + attn::kPagedOverhead) : 0;
+    const unsigned W = cost[B];
+    const attn::PagedCuts cuts(W, units, grid);
+    *n_cta = W ? cuts.C : 0;
     *n_parts = 0;
     for (int c = 0; c < *n_cta; ++c) {
-        long long at = attn::paged_cut(W, *n_cta, c);
-        const long long end = attn::paged_cut(W, *n_cta, c + 1);
+        unsigned at = cuts.begin(c);
+        const unsigned end = cuts.begin(c + 1);
         int b = 0;
         while (at < end) {
             while (cost[b + 1] <= at) ++b;
-            const int per = n[b] + attn::kPagedOverhead;
-            const int g = (int)((at - cost[b]) / per), off = (int)((at - cost[b]) % per);
-            const int to = (int)std::min<long long>(per, off + (end - at));
-            const int g0 = std::max(0, off - attn::kPagedOverhead), g1 = std::max(0, to - attn::kPagedOverhead);
+            const unsigned per = attn::paged_cost(n[b]), g = (at - cost[b]) / per, off = (at - cost[b]) % per;
+            const unsigned to = std::min(per, off + (end - at)), over = attn::kPagedOverhead;
+            const int g0 = std::min<int>(n[b], off > over ? off - over : 0);
+            const int g1 = std::min<int>(n[b], to > over ? to - over : 0);
             at += to - off;
             if (g0 >= g1) continue;
             if (cap > 0) {
                 if (*n_parts >= cap) return ATTN_ERR_INVALID_ARG;
-                const long long u0 = cost[b] + (long long)g * per + attn::kPagedOverhead;
-                int* q = parts + 8 * *n_parts;
-                q[0] = c; q[1] = b; q[2] = g; q[3] = g0; q[4] = g1; q[5] = n[b];
-                q[6] = attn::paged_owner(W, *n_cta, u0);
-                q[7] = attn::paged_owner(W, *n_cta, u0 + n[b] - 1);
+                const unsigned u0 = cost[b] + g * per + over;
+                const int part[8] = {c, b, (int)g, g0, g1, n[b], (int)cuts.owner(u0), (int)cuts.owner(u0 + n[b] - 1)};
+                std::copy(part, part + 8, parts + 8 * (size_t)*n_parts);
             }
             ++*n_parts;
         }
