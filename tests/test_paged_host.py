@@ -124,7 +124,7 @@ def test_split_covers_every_block_once(lens, Hkv, kind, window, grid, d, dtype):
     """Every visible key block of every unit in exactly one part; the CTAs named as a unit's first and last are those
     that hold its blocks, without a gap; a CTA leaves at most two units unfinished, which have different slots."""
     n_cta, parts = tsa.attn_paged_split_host(len(lens), Hkv, 1, d, dtype, kind, window, lens, grid)
-    keys = {(128, tsa.ATTN_BF16): 16, (64, tsa.ATTN_FP8_E4M3): 32}[(d, dtype)]
+    keys = {(128, tsa.ATTN_BF16): 16, (64, tsa.ATTN_FP8_E4M3): 128}[(d, dtype)]
     assert 0 <= n_cta <= grid
     want = {}
     for b, n in enumerate(lens):

@@ -1,0 +1,557 @@
+// Attention of a few new rows per sequence over a paged E4M3 cache.
+//
+//     O_i = sum_j softmax_j(scale q_i . k_j) v_j,   k_j = 2^a_j K_j,  v_j = 2^b_j V_j   (K_j, V_j: rows of E4M3 codes)
+//
+// Bound by memory: 2 (d + 1) bytes a position and kv head, read once.  The work is cut over the CTAs as in attn_paged.cu.
+//
+// The codes go into the tensor cores as they are.  Turning them into 16-bit numbers in registers takes 1260 instructions
+// for 32 positions and was the limit (141 us for 456 MB, 48% of the measured copy rate; m16n8k32 products do the same
+// inside, and measured 118 us).  Here the 128 positions of a tile fill the product's M dimension and the rows of the
+// kv head its N dimension,
+//
+//     S^T [128 x N] = K [128 x d] Q^T [d x N],     D^T [d x N] = V^T [d x 128] P^T [128 x N],
+//
+// with tcgen05.mma, both operands in shared memory.  Q and P are 16-bit numbers at least, so each is the sum of two
+// E4M3 numbers, x = hi + lo / 16, in columns of their own: N = 2 * rows.  The two sums meet in float32:
+//   Q: a row is scaled by a power of two to at most 2^8; the two parts hold all eight bits of a bf16 number, down to
+//      2^-22 of the row's largest.
+//   P: weights times the value factors, scaled for each tile and row so that the largest weight and the largest factor
+//      together give 2^8; the two parts are within 2^-8 of a weight (a bf16 number's rounding) and 2^-22 of that.
+// Thread t of the four computing warps owns position t of a tile (tensor-memory lane t), where both row factors are its
+// own, and element t of D^T.  D^T is added to the thread's float32 output after every tile, in terms of a reference
+// that moves only when a score passes it by 2^16; l is summed by position and added over the threads at the end.
+//
+//   warps 0-3: Q parts, S^T -> P parts, output      warp 4: TMA loads      warp 5: one thread issues the products
+//
+// S^T is double-buffered: the product of tile n + 1 runs while the weights of tile n are formed, and that of V with
+// the weights of tile n runs while tile n + 1 is prepared.  Two CTAs a multiprocessor up to 16 rows, one above.
+#include <cuda_bf16.h>
+
+#include <cstddef>
+
+#include "device_once.h"
+#include "paged_device.h"
+
+namespace attn {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kLoader = 4, kIssuer = 5;
+constexpr int kKeys = 128;
+constexpr int kMostStages = 8;
+
+template <int RP>
+struct Shared {
+    unsigned cost[kPagedMaxBatch + 4];
+    unsigned long long full[kMostStages], empty[kMostStages], s_full[2], s_free[2], p_full, d_full, q_full;
+    alignas(16) float top[2][4][RP];  // a tile's row maxima, by warp
+    alignas(16) float factor[2][4];   // and its largest value exponent
+    float qs[RP];                     // what a row's product is multiplied by, 2^up * scale * log2 e
+    float sum[4][RP];
+    int last[RP], first[RP];          // the positions a row sees
+    unsigned scan[kThreads / 32];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int D, int RP>
+struct Cfg {
+    static constexpr int kN = 2 * RP;
+    static constexpr int kCtas = RP <= 16 ? 2 : 1;
+    static constexpr int kTile = kKeys * D;                 // bytes of a tile's keys, or values
+    static constexpr int kStage = 2 * kTile;
+    static constexpr int kScale = 2 * kKeys;                // its exponents
+    static constexpr int kZero = D == 64 ? 32 * 64 : 0;     // rows 64 .. 127 of V^T, for the product's 128 rows
+    static constexpr int kQ = kN * D, kP = kN * kKeys;
+    static constexpr int kLimit = kCtas == 2 ? 115712 : 232448;
+    static constexpr int kFit = (kLimit - 1024 - kZero - kQ - kP - (int)sizeof(Shared<RP>)) / (kStage + kScale);
+    static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;
+    static constexpr int kOffZero = kStages * kStage, kOffQ = kOffZero + kZero, kOffP = kOffQ + kQ;
+    static constexpr int kOffScale = kOffP + kP, kOffShared = kOffScale + kStages * kScale;
+    static constexpr int kSmem = 1024 + kOffShared + (int)sizeof(Shared<RP>);
+    static constexpr uint32_t kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 3 * kN <= 256 ? 256 : 512;
+    static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // rows of 128 or 64 bytes
+    static_assert(kStages >= 3 && kSmem <= kLimit && kCols * kCtas <= 512, "shared and tensor memory");
+    static_assert(kOffP % 1024 == 0 && kOffQ % 512 == 0 && kOffScale % 16 == 0 && kOffShared % 16 == 0, "alignment");
+};
+
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int kv,
+                                              int unit) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slot), "r"(kv), "r"(unit), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ float exponent_factor(uint32_t e) {  // 2^(e - 127); e = 255 (NaN codes beside it): inf
+    return __uint_as_float(max(e << 23, 0x00400000u));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t e;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(addr) : "memory");
+    return e;
+}
+__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A wait with a limit; after one has run out every wait of the CTA returns at once and its outputs are undefined.
+struct Watch {
+    volatile int* abort;
+    int* err;
+    long long ns;
+};
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch& w) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (n % 64 == 0) {
+            if (*w.abort) return false;
+            if ((long long)(globaltimer() - t0) > w.ns) {
+                *w.abort = 1;
+                atomicOr(w.err, kCacheErrWait);
+                return false;
+            }
+        }
+    }
+}
+
+// Columns [c, c + n) of the thread's tensor-memory lane, n = 8 or 16 hi columns and as many lo columns RP further on.
+template <int RP>
+__device__ __forceinline__ void load_parts(uint32_t addr, int c, float (&hi)[16], float (&lo)[16]) {
+    uint32_t a[16], b[16];
+    if constexpr (RP == 8) {
+        tmem_ld16(addr, a);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            hi[i] = __uint_as_float(a[i]);
+            lo[i] = __uint_as_float(a[8 + i]);
+        }
+    } else {
+        tmem_ld16(addr + c, a);
+        tmem_ld16(addr + RP + c, b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            hi[i] = __uint_as_float(a[i]);
+            lo[i] = __uint_as_float(b[i]);
+        }
+    }
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
+    using C = Cfg<D, RP>;
+    constexpr PagedShape shape = paged_shape(D, true);
+    static_assert(shape.keys == kKeys, "a tile is a key block");
+    constexpr int N = C::kN, kStages = C::kStages;
+    constexpr int kChunk = RP < 16 ? RP : 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Shared<RP>& sh = *reinterpret_cast<Shared<RP>*>(smem + C::kOffShared);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t s_stage = smem_u32(smem), s_zero = s_stage + C::kOffZero, s_q = s_stage + C::kOffQ;
+    const uint32_t s_p = s_stage + C::kOffP, s_scale = s_stage + C::kOffScale;
+    auto full = [&](int st) { return smem_u32(&sh.full[st]); };
+    auto empty = [&](int st) { return smem_u32(&sh.empty[st]); };
+
+    if (tid == 0) {
+        prefetch_tmap(&p.tm);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.s_free[i]), 4);
+        }
+        mbar_init(smem_u32(&sh.p_full), 4);
+        mbar_init(smem_u32(&sh.d_full), 1);
+        mbar_init(smem_u32(&sh.q_full), 4);
+        sh.abort = 0;
+    }
+    if (D == 64)
+        for (int i = tid; i < C::kZero / 16; i += kThreads)
+            *reinterpret_cast<uint4*>(smem + C::kOffZero + 16 * i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    fence_barrier_init();
+    int busy;
+    const unsigned W = paged_prefix<kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.Hkv;
+    const PagedCuts cuts(W, busy * p.Hkv, gridDim.x, shape);
+    // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
+    if (tid == 0) p.cut[blockIdx.x] = make_int2(-1, 0);
+    if (blockIdx.x >= cuts.C || W == 0) return;
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&sh.tmem), C::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem, t_d = tmem + 2 * N;
+    const Watch watch{&sh.abort, p.c.err, p.watchdog_ns};
+    Walk w = paged_begin(p, cuts, sh.cost);
+
+    if (warp == kLoader) {
+        // =================================================== loads: a batch of four tiles, eight lanes each
+        int g = 0, st = 0, n = 0;
+        const int box = p.box_rows, part = lane % 8;
+        const uint32_t box_bytes = 2 * box * D + 2 * box;
+        struct Batch {
+            int tiles, unit, slot;
+        };
+        auto fetch = [&](Batch& f) {
+            f.tiles = 0;
+            while (g >= w.g1) {
+                if (w.at >= w.end) return;
+                paged_open<kKeys>(p, shape, sh.cost, w);
+                g = w.g0;
+            }
+            f.tiles = min(4, w.g1 - g);
+            const int pos = (w.lo + g + lane / 8) * kKeys + 16 * part;
+            f.unit = -1;
+            if (lane / 8 < f.tiles && 16 * part % box == 0 && pos < w.len && pos + box > w.seen) {
+                const int index = (unsigned)pos / (unsigned)p.c.page;
+                f.slot = pos - index * p.c.page;
+                int page = p.t.pages[w.b * p.t.stride + index];
+                if (page < 0 || page >= p.c.n_pages) {
+                    atomicOr(p.c.err, kCacheErrPage);
+                    page = 0;
+                }
+                f.unit = page * p.Hkv + w.h;
+            }
+            g += 4;
+        };
+        Batch now, then;
+        fetch(now);
+        bool ok = true;
+        while (now.tiles && ok) {
+            fetch(then);
+            for (int i = 0; i < now.tiles; ++i, ++n) {
+                if (n >= kStages) ok = wait(empty(st), (n / kStages - 1) & 1, watch);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const bool mine = lane / 8 == i && now.unit >= 0;
+                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+                if (lane == 0) mbar_arrive_expect_tx(full(st), boxes * box_bytes);
+                __syncwarp();
+                if (mine) {
+                    const uint32_t dst = s_stage + st * C::kStage + 16 * part * D;
+                    tma_load_rows(dst, &p.tm, full(st), now.slot, 0, now.unit);
+                    tma_load_rows(dst + C::kTile, &p.tm, full(st), now.slot, 1, now.unit);
+                    bulk_load(s_scale + st * C::kScale + 32 * part,
+                              p.c.scales + ((long long)now.unit * (p.c.page / 16) + now.slot / 16) * 32, 2 * box, full(st));
+                }
+                st = st + 1 == kStages ? 0 : st + 1;
+            }
+            now = then;
+        }
+    } else if (warp == kIssuer) {
+        // =================================================== products (lane 0)
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_e4m3_f32(kKeys, N, false);
+            constexpr uint32_t idesc_d = idesc_e4m3_f32(kKeys, N, false) | (1u << 15);  // V: elements of d contiguous
+            constexpr uint32_t sbo = 8 * D;
+            int n = 0, stretch = 0;
+            bool ok = true;
+            auto values = [&](int m) {  // D^T of tile m
+                if (!(ok = wait(smem_u32(&sh.p_full), m & 1, watch))) return;
+                tc_fence_after();
+                const int st = m % kStages;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 32; ++kk) {
+                    const uint32_t a = s_stage + st * C::kStage + C::kTile + kk * 32 * D;
+                    const uint32_t lbo = D == 64 ? s_zero - a : 16;
+                    mma_ss_f8(t_d, sdesc_sw(a, lbo, sbo, C::kSwizzle), sdesc_sw(s_p + 32 * kk, 16, 1024, 2), idesc_d, kk > 0);
+                }
+                mma_commit(smem_u32(&sh.d_full));
+                mma_commit(empty(st));
+            };
+            while (w.at < w.end && ok) {
+                paged_open<kKeys>(p, shape, sh.cost, w);
+                for (int g = w.g0; g < w.g1 && ok; ++g, ++n) {
+                    const int st = n % kStages;
+                    // the queries of a new stretch are written once the last tile before it is done
+                    if (g == w.g0) {
+                        if (n > 0) values(n - 1);
+                        if (ok) ok = wait(smem_u32(&sh.q_full), stretch++ & 1, watch);
+                    }
+                    if (ok) ok = wait(full(st), (n / kStages) & 1, watch);
+                    if (ok && n >= 2) ok = wait(smem_u32(&sh.s_free[n & 1]), (n / 2 - 1) & 1, watch);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_ss_f8(tmem + (n & 1) * N, sdesc_sw(s_stage + st * C::kStage + 32 * kk, 16, sbo, C::kSwizzle),
+                                  sdesc_sw(s_q + 32 * kk, 16, sbo, C::kSwizzle), idesc_s, kk > 0);
+                    mma_commit(smem_u32(&sh.s_full[n & 1]));
+                    if (g > w.g0) values(n - 1);
+                }
+            }
+            if (ok && n > 0) values(n - 1);
+        }
+        __syncwarp();
+    } else {
+        // =================================================== weights and output
+        const float ninf = __int_as_float(0xFF800000);
+        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        int n = 0;
+        while (w.at < w.end) {
+            paged_open<kKeys>(p, shape, sh.cost, w);
+            if (w.g0 >= w.g1) continue;  // overhead alone (the same for every thread)
+            const int len = w.len, seen = w.seen;
+            // ---- the queries' two parts; a warp per row, four elements a lane
+            {
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + ((long long)w.b * p.Hkv + w.h) * p.rows * D;
+                uint2 v[(RP + 3) / 4];
+#pragma unroll
+                for (int i = 0; i < (RP + 3) / 4; ++i) {
+                    const int row = warp + 4 * i;
+                    v[i] = make_uint2(0, 0);
+                    if (row < p.rows && lane < D / 4) v[i] = *reinterpret_cast<const uint2*>(q + (long long)row * D + 4 * lane);
+                }
+#pragma unroll
+                for (int i = 0; i < (RP + 3) / 4; ++i) {
+                    const int row = warp + 4 * i;
+                    uint32_t big = __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu);  // as bits of a bf16
+                    big = __reduce_max_sync(0xFFFFFFFFu, max(big & 0xFFFFu, big >> 16));
+                    // exponent field f: the row is below 2^(f - 126), so below 2^8 once scaled by 2^(134 - f).  A row
+                    // below 2^-100 is taken as zeros in part; one with an infinity or a NaN becomes NaN.
+                    const int f = max((int)(big >> 7), 27);
+                    const float down = f == 255 ? __int_as_float(0x7FFFFFFF) : __uint_as_float((uint32_t)(261 - f) << 23);
+                    const float up = f == 255 ? __int_as_float(0x7FFFFFFF) : __uint_as_float((uint32_t)(f - 7) << 23);
+                    uint32_t hi, lo;
+                    split_e4m3(__uint_as_float(v[i].x << 16) * down, __uint_as_float(v[i].x & 0xFFFF0000u) * down,
+                               __uint_as_float(v[i].y << 16) * down, __uint_as_float(v[i].y & 0xFFFF0000u) * down, hi, lo);
+                    if (lane < D / 4) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int r = half * RP + row, chunk = lane / 4;
+                            const int sw = D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3);
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_q + r * D + 16 * sw + 4 * (lane % 4)),
+                                         "r"(half ? lo : hi)
+                                         : "memory");
+                        }
+                    }
+                    if (lane == 0) {
+                        const int t = len - p.S_q + row % p.S_q;
+                        sh.qs[row] = p.scale_log2 * up;
+                        sh.last[row] = row >= p.rows ? -1 : p.causal ? t : len - 1;
+                        sh.first[row] = p.window < 0 ? 0 : max(0, t - p.window);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+                named_bar_sync(1, 128);
+            }
+            // positions every real row sees need no test: [all_from, all_to)
+            const int all_to = p.causal ? len - p.S_q + 1 : len;
+            const int all_from = p.window < 0 ? 0 : max(0, len - 1 - p.window);
+            float acc[RP], l[RP], m[RP], back[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                acc[r] = l[r] = back[r] = 0.f;
+                m[r] = ninf;
+            }
+            // D^T of the tile before is added to the output
+            auto add_values = [&](int tile) {
+                wait(smem_u32(&sh.d_full), tile & 1, watch);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < RP; c += kChunk) {
+                    float hi[16], lo[16];
+                    load_parts<RP>(t_d + t_lane, c, hi, lo);
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) acc[c + i] = fmaf(fmaf(lo[i], 0.0625f, hi[i]), back[c + i], acc[c + i]);
+                }
+            };
+            for (int g = w.g0; g < w.g1; ++g, ++n) {
+                const int st = n % kStages;
+                const int first = (w.lo + g) * kKeys, pos = first + tid;
+                wait(smem_u32(&sh.s_full[n & 1]), (n / 2) & 1, watch);
+                wait(full(st), (n / kStages) & 1, watch);  // seen by this thread too: it reads and clears what was loaded
+                __syncwarp();
+                tc_fence_after();
+                const bool inside = pos >= seen && pos < len;
+                const uint32_t sc = s_scale + st * C::kScale + 32 * (tid / 16) + tid % 16;
+                const uint32_t ek = lds_u8(sc), ev = lds_u8(sc + 16);
+                const float kf = exponent_factor(ek);
+                const float kv = inside ? (float)((int)ev - 127) : -127.f;
+                float s[RP];
+#pragma unroll
+                for (int c = 0; c < RP; c += kChunk) {
+                    float hi[16], lo[16];
+                    load_parts<RP>(tmem + (n & 1) * N + t_lane, c, hi, lo);
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) s[c + i] = fmaf(lo[i], 0.0625f, hi[i]) * (kf * sh.qs[c + i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[n & 1]));
+                if (first < all_from || first + kKeys > all_to) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        if (!inside || pos > sh.last[r] || pos < sh.first[r]) s[r] = ninf;
+                }
+                // ---- the tile's largest score of each row, and its largest value exponent
+                const float kv_top = warp_max(kv);
+                if (lane == 0) sh.factor[n & 1][warp] = kv_top;
+                float mine[RP <= 32 ? 1 : 2];
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    const float t = warp_max(s[r]);
+                    if (lane == r % 32) mine[r / 32] = t;
+                }
+#pragma unroll
+                for (int i = 0; i < (RP + 31) / 32; ++i)
+                    if (lane + 32 * i < RP) sh.top[n & 1][warp][lane + 32 * i] = mine[i];
+                named_bar_sync(1, 128);
+                if (g > w.g0) add_values(n - 1);
+                // ---- weights, scaled to at most 2^8
+                const uint32_t p_at = s_p + tid % 16, p_chunk = tid / 16;
+                const float4 k4 = *reinterpret_cast<const float4*>(&sh.factor[n & 1][0]);
+                const float k_top = fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w));
+#pragma unroll
+                for (int r0 = 0; r0 < RP; r0 += 4) {
+                    float y[4];
+                    const float4 t0 = *reinterpret_cast<const float4*>(&sh.top[n & 1][0][r0]);
+                    const float4 t1 = *reinterpret_cast<const float4*>(&sh.top[n & 1][1][r0]);
+                    const float4 t2 = *reinterpret_cast<const float4*>(&sh.top[n & 1][2][r0]);
+                    const float4 t3 = *reinterpret_cast<const float4*>(&sh.top[n & 1][3][r0]);
+                    const float top4[4] = {fmaxf(fmaxf(t0.x, t1.x), fmaxf(t2.x, t3.x)),
+                                           fmaxf(fmaxf(t0.y, t1.y), fmaxf(t2.y, t3.y)),
+                                           fmaxf(fmaxf(t0.z, t1.z), fmaxf(t2.z, t3.z)),
+                                           fmaxf(fmaxf(t0.w, t1.w), fmaxf(t2.w, t3.w))};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + i;
+                        const float top = top4[i];
+                        if (top > m[r] + 16.f) {  // the same in every thread
+                            const float fix = m[r] == ninf ? 0.f : ex2(m[r] - top);
+                            acc[r] *= fix;
+                            l[r] *= fix;
+                            m[r] = top;
+                        }
+                        const float base = m[r] == ninf ? 0.f : m[r];
+                        // the reference first: what is left is small, and adding the exponents loses nothing
+                        const float x = s[r] - base;
+                        const float ref = top == ninf ? 0.f : top - base + (k_top - 8.f);
+                        l[r] += ex2(x);
+                        back[r] = top == ninf ? 0.f : ex2(ref);
+                        y[i] = ex2(x + (kv - ref));
+                    }
+                    uint32_t hi, lo;
+                    split_e4m3(y[0], y[1], y[2], y[3], hi, lo);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + i;
+                        sts_u8(p_at + r * kKeys + 16 * (p_chunk ^ (r & 7)), hi >> (8 * i));
+                        sts_u8(p_at + (RP + r) * kKeys + 16 * (p_chunk ^ (r & 7)), lo >> (8 * i));
+                    }
+                }
+                if (!inside) {
+                    // positions past the length or before the window may hold anything: weight zero times a NaN is a
+                    // NaN, so their values become zero
+                    const uint32_t v = s_stage + st * C::kStage + C::kTile + tid * D;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + 16 * c), "r"(0) : "memory");
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.p_full));
+            }
+            add_values(n - 1);
+            tc_fence_before();
+            // ---- the rows' sums over the threads, and the stretch's result
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
+                if (lane == 0) sh.sum[warp][r] = l[r];
+            }
+            named_bar_sync(1, 128);
+            const bool final = w.g0 == 0 && w.g1 == w.n;
+            const long long unit = (long long)w.b * p.Hkv + w.h;
+            const long long slot = (2LL * blockIdx.x + (w.g0 > 0 ? 0 : 1)) * RP;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                if (r >= p.rows) break;
+                const float L = (sh.sum[0][r] + sh.sum[1][r]) + (sh.sum[2][r] + sh.sum[3][r]);
+                if (tid < D) {
+                    if (final)
+                        reinterpret_cast<__nv_bfloat16*>(p.o)[(unit * p.rows + r) * D + tid] =
+                            __float2bfloat16(L == 0.f ? 0.f : acc[r] / L);
+                    else
+                        __stcg(p.part_o + (slot + r) * D + tid, acc[r]);
+                }
+                if (tid == 0) {
+                    if (!final) __stcg(&p.part_ml[slot + r], make_float2(m[r], L));
+                    else if (p.lse) p.lse[unit * p.rows + r] = (m[r] + log2f(L)) * 0.6931471805599453f;
+                }
+            }
+            if (!final && w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w);
+            // before sh.sum, the queries and the row bounds are written again
+            named_bar_sync(1, 128);
+        }
+    }
+    // after a wait that ran out, copies and products may still be under way: wait for them, with a limit
+    __syncthreads();
+    if (sh.abort) {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 10000000ULL) __nanosleep(1000);
+        __syncthreads();
+    }
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+}
+
+template <int D, int RP>
+cudaError_t launch_rp(const PagedParams& p, int grid, cudaStream_t stream) {
+    auto* f = paged_e4m3_kernel<D, RP>;
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), Cfg<D, RP>::kSmem);
+    if (e != cudaSuccess) return e;
+    f<<<grid, kThreads, Cfg<D, RP>::kSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {
+    switch (paged_rows_pad(p.rows, true)) {
+        case 8: return launch_rp<D, 8>(p, grid, stream);
+        case 16: return launch_rp<D, 16>(p, grid, stream);
+        case 32: return launch_rp<D, 32>(p, grid, stream);
+        default: return launch_rp<D, 64>(p, grid, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_e4m3(const PagedParams& p, int grid, cudaStream_t stream) {
+    return p.c.d == 64 ? launch_d<64>(p, grid, stream) : launch_d<128>(p, grid, stream);
+}
+
+}  // namespace attn

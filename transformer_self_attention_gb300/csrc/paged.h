@@ -55,13 +55,21 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, c
 cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged decode
-// Work units are (sequence, kv head), in that order.  A unit of n key blocks costs max(n, kPagedMin) + kPagedOverhead:
-// its start, its merge and its output cost about as much as kPagedOverhead blocks, and a unit of few blocks is not worth
-// cutting (joining its parts costs more than the other blocks' time), so that units up to kPagedMin all cost the same
-// and the cuts fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals,
-// equal but for one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost
-// positions its interval covers.
-constexpr unsigned kPagedOverhead = 6, kPagedMin = 24;
+// Work units are (sequence, kv head), in that order.  A unit of n key blocks costs max(n, least) + overhead: its start,
+// its merge and its output cost about as much as `overhead` blocks, and a unit of few blocks is not worth cutting
+// (joining its parts costs more than the other blocks' time), so that units up to `least` all cost the same and the cuts
+// fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals, equal but for
+// one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost positions its
+// interval covers.
+// Measured, bf16 (blocks of 8 KB): overheads of 6, 10, 16 and 24 blocks give 33.0, 31.8, 29.5 and 29.0 us for 16 ragged
+// multi-query sequences of up to 16K positions and 170, 171, 167.5 and 169 us for 256 of up to 2K.
+struct PagedShape {
+    int keys;  // positions of a key block
+    unsigned overhead, least;
+};
+__host__ __device__ constexpr PagedShape paged_shape(int d, bool e4m3) {
+    return e4m3 ? PagedShape{128, 3, 4} : PagedShape{d == 64 ? 32 : 16, 16, 24};
+}
 constexpr int kPagedMaxBatch = ATTN_DECODE_MAX_BATCH;
 
 // Key blocks [lo, hi) of `keys` positions that some row of a sequence of length n can see.
@@ -70,14 +78,14 @@ __host__ __device__ inline void paged_blocks(int n, int S_q, int window, int key
     const int first = window < 0 ? 0 : n - S_q - window;
     lo = first > 0 ? first / keys : 0;
 }
-__host__ __device__ inline unsigned paged_cost(int n) {
-    return n == 0 ? 0 : ((unsigned)n < kPagedMin ? kPagedMin : (unsigned)n) + kPagedOverhead;
+__host__ __device__ inline unsigned paged_cost(int n, PagedShape s) {
+    return n == 0 ? 0 : ((unsigned)n < s.least ? s.least : (unsigned)n) + s.overhead;
 }
 struct PagedCuts {
     unsigned C, q, r;  // CTAs; the intervals cost q + 1 for the first r, q for the others
     // One CTA per unit, more where the intervals still cost as much as a short unit.
-    __host__ __device__ PagedCuts(unsigned W, unsigned units, unsigned grid) {
-        C = W / (kPagedMin + kPagedOverhead);
+    __host__ __device__ PagedCuts(unsigned W, unsigned units, unsigned grid, PagedShape s) {
+        C = W / (s.least + s.overhead);
         C = C < units ? units : C;
         C = C < grid ? C : grid;
         C = C < 1 ? 1 : C;
@@ -91,31 +99,34 @@ struct PagedCuts {
     }
 };
 // Whether a launch may cut a unit at all, for any lengths up to `room` positions.
-__host__ __device__ inline bool paged_may_cut(long long units, long long room, int keys, int grid) {
-    return units > grid || room > (long long)kPagedMin * keys;
+__host__ __device__ inline bool paged_may_cut(long long units, long long room, int grid, PagedShape s) {
+    return units > grid || room > (long long)s.least * s.keys;
 }
 
 struct PagedParams {
-    CUtensorMap tm;  // the pages: {inner, slots, halves of a row, K / V, page * Hkv + head}
+    CUtensorMap tm;  // the pages, one box: 16 positions' keys and values (bf16), or box_rows keys or values (E4M3)
     const void* q;   // [B, Hq, S_q, d] bf16
     void* o;
     float* lse;      // may be null
     CacheView c;
     PageTable t;
     float* part_o;        // [2 * grid][rows_pad][d] unscaled sums, two slots per CTA: its first and its last stretch
-    float2* part_ml;      // [2 * grid][rows_pad]: the row maximum (base 2) and sum
+    float2* part_ml;      // [2 * grid][rows_pad]: the rows' reference (base 2) and sum
     int2* cut;            // [grid]: the unit that begins in a CTA and ends in a later one, and that CTA; unit -1: none
     int B, Hq, Hkv, S_q, rows;
     int window;           // -1: none
     int causal;           // 0: every row sees every cached position
+    int box_rows;         // E4M3: positions of a TMA box, a divisor of the page size
     float scale_log2;
     long long watchdog_ns;
 };
-int paged_block_keys(int d, bool e4m3);   // positions per key block
-int paged_rows_pad(int rows);             // 16, 32 or 64
-int paged_ctas_per_sm();
-
-// `merge`: launch the joining kernel behind it (a unit may be cut).
-cudaError_t launch_paged_decode(const PagedParams& p, bool e4m3, int grid, bool merge, cudaStream_t stream);
+// Rows a slot of the partial results is padded to, and the CTAs of a full grid per multiprocessor.
+int paged_rows_pad(int rows, bool e4m3);
+int paged_ctas_per_sm(int rows, bool e4m3);
+constexpr int kPagedMostCtasPerSm = 2;
+cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_e4m3(const PagedParams& p, int grid, cudaStream_t stream);
+// Joins the parts of cut units; enqueued behind either as a programmatic dependent.
+cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream);
 
 }  // namespace attn

@@ -25,12 +25,14 @@ struct attn_cache_plan {
     attn::CacheView c;
     CUtensorMap map{};
     bool e4m3 = false;
+    int box_rows = 16;
     int device = 0, n_sm = 0;
 };
 
 struct attn_paged_plan {
     int B = 0, Hq = 0, Hkv = 0, S_q = 0, d = 0, kind = 0, window = 0;
-    int device = 0, n_sm = 0, grid = 0, max_grid = 0;
+    int device = 0, n_sm = 0;
+    int grid_limit = 1 << 30;
     long long watchdog_ns = 2000000000LL;
     float scale = 0.f;
     float* d_part = nullptr;
@@ -54,22 +56,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// The pages as {row part, slots, parts of a row, K / V, page * Hkv + head}: a row of more than 128 bytes comes in parts
-// of 128, one box holds 16 positions' keys and values of one head.
-bool encode_pages(CUtensorMap* map, const attn::CacheView& c, bool e4m3) {
+// bf16 pages as {row part, slots, parts of a row, K / V, page * Hkv + head}: a row comes in parts of 128 bytes, one box
+// holds 16 positions' keys and values of one head.
+bool encode_bf16(CUtensorMap* map, const attn::CacheView& c) {
     auto enc = encoder();
     if (!enc) return false;
-    const int el = e4m3 ? 1 : 2, row = c.d * el, inner = row < 128 ? row : 128, parts = row / inner;
-    cuuint64_t dims[5] = {(cuuint64_t)(inner / el), (cuuint64_t)c.page, (cuuint64_t)parts, 2,
-                          (cuuint64_t)c.n_pages * c.Hkv};
-    cuuint64_t strides[4] = {(cuuint64_t)row, (cuuint64_t)inner, (cuuint64_t)c.page * row,
-                             (cuuint64_t)2 * c.page * row};
-    cuuint32_t box[5] = {(cuuint32_t)(inner / el), 16, (cuuint32_t)parts, 2, 1};
+    const int row = c.d * 2, parts = row / 128;
+    cuuint64_t dims[5] = {64, (cuuint64_t)c.page, (cuuint64_t)parts, 2, (cuuint64_t)c.n_pages * c.Hkv};
+    cuuint64_t strides[4] = {(cuuint64_t)row, 128, (cuuint64_t)c.page * row, (cuuint64_t)2 * c.page * row};
+    cuuint32_t box[5] = {64, 16, (cuuint32_t)parts, 2, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    return enc(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c.pages, dims, strides,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c.pages, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// E4M3 pages as {row, slots, K / V, page * Hkv + head}; one box holds `rows` positions' keys or values of one head.
+bool encode_e4m3(CUtensorMap* map, const attn::CacheView& c, int rows) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, 2, (cuuint64_t)c.n_pages * c.Hkv};
+    cuuint64_t strides[3] = {(cuuint64_t)c.d, (cuuint64_t)c.page * c.d, (cuuint64_t)2 * c.page * c.d};
+    cuuint32_t box[4] = {(cuuint32_t)c.d, (cuuint32_t)rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.pages, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -239,7 +250,9 @@ attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int 
     const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->c.err), sizeof(int));
     if (e != cudaSuccess) return fail(e == cudaErrorMemoryAllocation ? ATTN_ERR_OOM : ATTN_ERR_CUDA);
     if (cudaMemset(h->c.err, 0, sizeof(int)) != cudaSuccess) return fail(ATTN_ERR_CUDA);
-    if (!encode_pages(&h->map, h->c, h->e4m3)) return fail(ATTN_ERR_CUDA);
+    // the largest power of two that divides the page, up to a decode tile
+    while (h->box_rows < 128 && page % (2 * h->box_rows) == 0) h->box_rows *= 2;
+    if (!(h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows) : encode_bf16(&h->map, h->c))) return fail(ATTN_ERR_CUDA);
     *out = h;
     return ATTN_OK;
 }
@@ -324,11 +337,12 @@ attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, in
     cudaError_t e = cudaGetDevice(&h->device);
     if (e != cudaSuccess) return fail(e);
     if ((h->n_sm = attn::current_sm_count()) < 1) return fail(cudaErrorUnknown);
-    h->grid = h->max_grid = h->n_sm * attn::paged_ctas_per_sm();
-    const size_t rows = 2 * (size_t)h->grid * attn::paged_rows_pad(Hq / Hkv * S_q);
+    // room for either type of cache
+    const size_t grid = (size_t)h->n_sm * attn::kPagedMostCtasPerSm;
+    const size_t rows = 2 * grid * attn::paged_rows_pad(Hq / Hkv * S_q, false);
     if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_part), rows * d * sizeof(float))) != cudaSuccess) return fail(e);
     if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_ml), rows * sizeof(float2))) != cudaSuccess) return fail(e);
-    if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_cut), sizeof(int2) * h->grid)) != cudaSuccess) return fail(e);
+    if ((e = cudaMalloc(reinterpret_cast<void**>(&h->d_cut), sizeof(int2) * grid)) != cudaSuccess) return fail(e);
     *out = h;
     return ATTN_OK;
 }
@@ -340,9 +354,9 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (cache->c.Hkv != h->Hkv || cache->c.d != h->d || cache->device != h->device || !on_device(h->device))
         return ATTN_ERR_INVALID_ARG;
+    const attn::PagedShape shape = attn::paged_shape(h->d, cache->e4m3);
     const long long room = (long long)max_pages * cache->c.page;
-    const int keys = attn::paged_block_keys(h->d, cache->e4m3);
-    const long long most = attn::kPagedMin + attn::kPagedOverhead + room / keys + 1;  // a unit's cost
+    const long long most = shape.least + shape.overhead + room / shape.keys + 1;  // a unit's cost
     // positions, and places on the cost line, fit an int
     if (room > (1 << 30) || most * h->B * h->Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
     attn::PagedParams p{};
@@ -356,14 +370,19 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     p.causal = h->kind != ATTN_MASK_FULL;
     p.scale_log2 = (float)((double)h->scale * 1.4426950408889634);
     p.watchdog_ns = h->watchdog_ns;
-    const bool merge = attn::paged_may_cut((long long)h->B * h->Hkv, room, keys, h->grid);
-    const cudaError_t e = attn::launch_paged_decode(p, cache->e4m3, h->grid, merge, static_cast<cudaStream_t>(stream));
+    p.box_rows = cache->box_rows;
+    const int rows_pad = attn::paged_rows_pad(p.rows, cache->e4m3);
+    const int grid = std::min(h->n_sm * attn::paged_ctas_per_sm(p.rows, cache->e4m3), h->grid_limit);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cache->e4m3 ? attn::launch_paged_e4m3(p, grid, st) : attn::launch_paged_bf16(p, grid, st);
+    if (e == cudaSuccess && attn::paged_may_cut((long long)h->B * h->Hkv, room, grid, shape))
+        e = attn::launch_paged_merge(p, grid, rows_pad, st);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas) {
     if (!h || max_ctas < 1) return ATTN_ERR_INVALID_ARG;
-    h->grid = std::min(max_ctas, h->max_grid);
+    h->grid_limit = max_ctas;
     return ATTN_OK;
 }
 
@@ -383,21 +402,21 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
     if (vs != ATTN_OK) return vs;
     if (S_q < 1 || (dtype != ATTN_BF16 && dtype != ATTN_FP8_E4M3) || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
     const int w = kind == ATTN_MASK_CAUSAL_SLIDING ? window : -1;
-    const int keys = attn::paged_block_keys(d, dtype == ATTN_FP8_E4M3);
+    const attn::PagedShape shape = attn::paged_shape(d, dtype == ATTN_FP8_E4M3);
     std::vector<unsigned> cost(B + 1, 0);
     std::vector<int> n(B);
     unsigned units = 0;
     for (int b = 0; b < B; ++b) {
         int lo, hi;
         if (cache_len[b] < 0) return ATTN_ERR_INVALID_ARG;
-        attn::paged_blocks(cache_len[b], S_q, w, keys, lo, hi);
+        attn::paged_blocks(cache_len[b], S_q, w, shape.keys, lo, hi);
         n[b] = hi - lo;
         if (n[b]) units += Hkv;
-        if ((long long)attn::paged_cost(n[b]) * Hkv + cost[b] > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
-        cost[b + 1] = cost[b] + Hkv * attn::paged_cost(n[b]);
+        if ((long long)attn::paged_cost(n[b], shape) * Hkv + cost[b] > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+        cost[b + 1] = cost[b] + Hkv * attn::paged_cost(n[b], shape);
     }
     const unsigned W = cost[B];
-    const attn::PagedCuts cuts(W, units, grid);
+    const attn::PagedCuts cuts(W, units, grid, shape);
     *n_cta = W ? cuts.C : 0;
     *n_parts = 0;
     for (int c = 0; c < *n_cta; ++c) {
@@ -406,8 +425,8 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
         int b = 0;
         while (at < end) {
             while (cost[b + 1] <= at) ++b;
-            const unsigned per = attn::paged_cost(n[b]), g = (at - cost[b]) / per, off = (at - cost[b]) % per;
-            const unsigned to = std::min(per, off + (end - at)), over = attn::kPagedOverhead;
+            const unsigned per = attn::paged_cost(n[b], shape), g = (at - cost[b]) / per, off = (at - cost[b]) % per;
+            const unsigned to = std::min(per, off + (end - at)), over = shape.overhead;
             const int g0 = std::min<int>(n[b], off > over ? off - over : 0);
             const int g1 = std::min<int>(n[b], to > over ? to - over : 0);
             at += to - off;
