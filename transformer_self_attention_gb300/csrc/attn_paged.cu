@@ -487,18 +487,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     const int unit = cut.x, k1 = cut.y;
     const float ninf = __int_as_float(0xFF800000);
     auto at = [&](int k) { return (long long)(2 * k + (k == k0)) * rows_pad + row; };
-    float M = ninf, L = 0.f;
+    float M, L = 0.f;
     constexpr int kVec = D / 32;
     float v[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = 0.f;
-    for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(k)]).x);
+    // the first 32 parts' maxima and sums stay in registers: mostly there are no more
+    const float2 t0 = k0 + lane <= k1 ? __ldcg(&p.part_ml[at(k0 + lane)]) : make_float2(ninf, 0.f);
+    M = t0.x;
+    for (int k = k0 + 32 + lane; k <= k1; k += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(k)]).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
     for (int kk = k0; kk <= k1; kk += 32) {
         float f = 0.f;
         if (kk + lane <= k1) {
-            const float2 t = __ldcg(&p.part_ml[at(kk + lane)]);
+            const float2 t = kk == k0 ? t0 : __ldcg(&p.part_ml[at(kk + lane)]);
             // a part without a maximum has seen nothing (sum 0), or only NaN
             f = t.x == ninf ? t.y : ex2(t.x - M);
             L += t.x == ninf ? t.y : t.y * f;

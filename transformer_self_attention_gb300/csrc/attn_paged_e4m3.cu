@@ -17,11 +17,12 @@
 //      2^-22 of the row's largest.
 //   P: weights times the value factors, scaled for each tile and row so that the largest weight and the largest factor
 //      together give 2^8; the two parts are within 2^-8 of a weight (a bf16 number's rounding) and 2^-22 of that.
-// Thread t of the four computing warps owns position t of a tile (tensor-memory lane t), where both row factors are its
-// own, and element t of D^T.  D^T is added to the thread's float32 output after every tile, in terms of a reference
+// Thread t of a group of four computing warps owns position t of a tile (tensor-memory lane t), where both row factors
+// are its own, and element t of D^T, for the group's rows: all of them up to 8, half of them, in two groups that share
+// nothing but the tiles, above.  D^T is added to the thread's float32 output after every tile, in terms of a reference
 // that moves only when a score passes it by 2^16; l is summed by position and added over the threads at the end.
 //
-//   warps 0-3: Q parts, S^T -> P parts, output      warp 4: TMA loads      warp 5: one thread issues the products
+//   computing warps: Q parts, S^T -> P parts, output      then one warp for the TMA loads, and one thread for the products
 //
 // S^T is double-buffered: the product of tile n + 1 runs while the weights of tile n are formed, and that of V with
 // the weights of tile n runs while tile n + 1 is prepared.  Two CTAs a multiprocessor up to 16 rows, one above.
@@ -38,17 +39,16 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kLoader = 4, kIssuer = 5;
 constexpr int kKeys = 128;
 constexpr int kMostStages = 8;
 
 template <int RP>
 struct Shared {
+    static constexpr int kGroups = RP <= 8 ? 1 : 2, kThreads = 128 * kGroups + 64;
     unsigned cost[kPagedMaxBatch + 4];
     unsigned long long full[kMostStages], empty[kMostStages], s_full[2], s_free[2], p_full, d_full, q_full;
     alignas(16) float top[2][4][RP];  // a tile's row maxima, by warp
-    alignas(16) float factor[2][4];   // and its largest value exponent
+    alignas(16) float factor[2][2][4];  // and its largest value exponent, by group and warp
     float qs[RP];                     // what a row's product is multiplied by, 2^up * scale * log2 e
     float sum[4][RP];
     int last[RP], first[RP];          // the positions a row sees
@@ -61,6 +61,8 @@ template <int D, int RP>
 struct Cfg {
     static constexpr int kN = 2 * RP;
     static constexpr int kCtas = RP <= 16 ? 2 : 1;
+    static constexpr int kGroups = Shared<RP>::kGroups, kThreads = Shared<RP>::kThreads;
+    static constexpr int kRows = RP / kGroups;              // of a thread
     static constexpr int kTile = kKeys * D;                 // bytes of a tile's keys, or values
     static constexpr int kStage = 2 * kTile;
     static constexpr int kScale = 2 * kKeys;                // its exponents
@@ -75,7 +77,7 @@ struct Cfg {
     static constexpr uint32_t kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 3 * kN <= 256 ? 256 : 512;
     static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // rows of 128 or 64 bytes
     static_assert(kStages >= 3 && kSmem <= kLimit && kCols * kCtas <= 512, "shared and tensor memory");
-    static_assert(kOffP % 1024 == 0 && kOffQ % 512 == 0 && kOffScale % 16 == 0 && kOffShared % 16 == 0, "alignment");
+    static_assert(kOffP % 128 == 0 && kOffQ % 1024 == 0 && kOffScale % 16 == 0 && kOffShared % 16 == 0, "alignment");
 };
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int kv,
@@ -99,8 +101,11 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(addr) : "memory");
     return e;
 }
-__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// 32 lanes x 8 columns of 32 bit
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ float warp_max(float x) {
     float y;
@@ -130,21 +135,23 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch&
     }
 }
 
-// Columns [c, c + n) of the thread's tensor-memory lane, n = 8 or 16 hi columns and as many lo columns RP further on.
-template <int RP>
-__device__ __forceinline__ void load_parts(uint32_t addr, int c, float (&hi)[16], float (&lo)[16]) {
-    uint32_t a[16], b[16];
-    if constexpr (RP == 8) {
-        tmem_ld16(addr, a);
+// R rows of the thread's tensor-memory lane: the hi column of row c + i, and its lo column RP further on.
+template <int RP, int R>
+__device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[R], float (&lo)[R]) {
+    if constexpr (R == 8) {
+        uint32_t a[8], b[8];
+        tmem_ld8(addr, a);
+        tmem_ld8(addr + RP, b);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             hi[i] = __uint_as_float(a[i]);
-            lo[i] = __uint_as_float(a[8 + i]);
+            lo[i] = __uint_as_float(b[i]);
         }
     } else {
-        tmem_ld16(addr + c, a);
-        tmem_ld16(addr + RP + c, b);
+        uint32_t a[16], b[16];
+        tmem_ld16(addr, a);
+        tmem_ld16(addr + RP, b);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -155,12 +162,12 @@ __device__ __forceinline__ void load_parts(uint32_t addr, int c, float (&hi)[16]
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
     using C = Cfg<D, RP>;
     constexpr PagedShape shape = paged_shape(D, true);
     static_assert(shape.keys == kKeys, "a tile is a key block");
-    constexpr int N = C::kN, kStages = C::kStages;
-    constexpr int kChunk = RP < 16 ? RP : 16;
+    constexpr int N = C::kN, kStages = C::kStages, kThreads = C::kThreads, kLoader = 4 * C::kGroups;
+    constexpr int kRows = C::kRows, kChunk = kRows < 16 ? kRows : 16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Shared<RP>& sh = *reinterpret_cast<Shared<RP>*>(smem + C::kOffShared);
@@ -178,11 +185,11 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.s_free[i]), 4);
+            mbar_init(smem_u32(&sh.s_free[i]), 4 * C::kGroups);
         }
-        mbar_init(smem_u32(&sh.p_full), 4);
+        mbar_init(smem_u32(&sh.p_full), 4 * C::kGroups);
         mbar_init(smem_u32(&sh.d_full), 1);
-        mbar_init(smem_u32(&sh.q_full), 4);
+        mbar_init(smem_u32(&sh.q_full), 4 * C::kGroups);
         sh.abort = 0;
     }
     if (D == 64)
@@ -243,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
         fetch(now);
         bool ok = true;
         while (now.tiles && ok) {
-            fetch(then);
             for (int i = 0; i < now.tiles; ++i, ++n) {
                 if (n >= kStages) ok = wait(empty(st), (n / kStages - 1) & 1, watch);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -262,14 +268,16 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
                               p.c.scales + ((long long)now.unit * (p.c.page / 16) + now.slot / 16) * 32, 2 * box, full(st));
                 }
                 st = st + 1 == kStages ? 0 : st + 1;
+                if (i == min(1, now.tiles - 1)) fetch(then);  // its page numbers: two tiles are on their way by now
             }
             now = then;
         }
-    } else if (warp == kIssuer) {
+    } else if (warp == kLoader + 1) {
         // =================================================== products (lane 0)
         if (lane == 0) {
             constexpr uint32_t idesc_s = idesc_e4m3_f32(kKeys, N, false);
-            constexpr uint32_t idesc_d = idesc_e4m3_f32(kKeys, N, false) | (1u << 15);  // V: elements of d contiguous
+            // V: elements of d contiguous; P: columns contiguous, 16 bytes to a position
+            constexpr uint32_t idesc_d = idesc_e4m3_f32(kKeys, N, true) | (1u << 15);
             constexpr uint32_t sbo = 8 * D;
             int n = 0, stretch = 0;
             bool ok = true;
@@ -281,7 +289,10 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
                 for (int kk = 0; kk < kKeys / 32; ++kk) {
                     const uint32_t a = s_stage + st * C::kStage + C::kTile + kk * 32 * D;
                     const uint32_t lbo = D == 64 ? s_zero - a : 16;
-                    mma_ss_f8(t_d, sdesc_sw(a, lbo, sbo, C::kSwizzle), sdesc_sw(s_p + 32 * kk, 16, 1024, 2), idesc_d, kk > 0);
+                    // P: 16 columns of 8 positions are 128 bytes; the next 8 positions follow, the next 16 columns
+                    // come behind all positions
+                    mma_ss_f8(t_d, sdesc_sw(a, lbo, sbo, C::kSwizzle), sdesc_plain(s_p + 32 * 16 * kk, 128, 16 * kKeys),
+                              idesc_d, kk > 0);
                 }
                 mma_commit(smem_u32(&sh.d_full));
                 mma_commit(empty(st));
@@ -313,7 +324,9 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
     } else {
         // =================================================== weights and output
         const float ninf = __int_as_float(0xFF800000);
-        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        const int group = warp / 4, gwarp = warp % 4, gtid = tid % 128;
+        const int row0 = group * kRows;  // of the group's rows
+        const uint32_t t_lane = (uint32_t)(gwarp * 32) << 16;
         int n = 0;
         while (w.at < w.end) {
             paged_open<kKeys>(p, shape, sh.cost, w);
@@ -322,16 +335,16 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
             // ---- the queries' two parts; a warp per row, four elements a lane
             {
                 const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + ((long long)w.b * p.Hkv + w.h) * p.rows * D;
-                uint2 v[(RP + 3) / 4];
+                uint2 v[kRows / 4];
 #pragma unroll
-                for (int i = 0; i < (RP + 3) / 4; ++i) {
-                    const int row = warp + 4 * i;
+                for (int i = 0; i < kRows / 4; ++i) {
+                    const int row = row0 + gwarp + 4 * i;
                     v[i] = make_uint2(0, 0);
                     if (row < p.rows && lane < D / 4) v[i] = *reinterpret_cast<const uint2*>(q + (long long)row * D + 4 * lane);
                 }
 #pragma unroll
-                for (int i = 0; i < (RP + 3) / 4; ++i) {
-                    const int row = warp + 4 * i;
+                for (int i = 0; i < kRows / 4; ++i) {
+                    const int row = row0 + gwarp + 4 * i;
                     uint32_t big = __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu);  // as bits of a bf16
                     big = __reduce_max_sync(0xFFFFFFFFu, max(big & 0xFFFFu, big >> 16));
                     // exponent field f: the row is below 2^(f - 126), so below 2^8 once scaled by 2^(134 - f).  A row
@@ -362,14 +375,14 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-                named_bar_sync(1, 128);
+                named_bar_sync(1 + group, 128);
             }
             // positions every real row sees need no test: [all_from, all_to)
             const int all_to = p.causal ? len - p.S_q + 1 : len;
             const int all_from = p.window < 0 ? 0 : max(0, len - 1 - p.window);
-            float acc[RP], l[RP], m[RP], back[RP];
+            float acc[kRows], l[kRows], m[kRows], back[kRows];
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < kRows; ++r) {
                 acc[r] = l[r] = back[r] = 0.f;
                 m[r] = ninf;
             }
@@ -379,101 +392,120 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < RP; c += kChunk) {
-                    float hi[16], lo[16];
-                    load_parts<RP>(t_d + t_lane, c, hi, lo);
+                for (int c = 0; c < kRows; c += kChunk) {
+                    float hi[kChunk], lo[kChunk];
+                    load_parts<RP, kChunk>(t_d + t_lane + row0 + c, hi, lo);
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) acc[c + i] = fmaf(fmaf(lo[i], 0.0625f, hi[i]), back[c + i], acc[c + i]);
                 }
             };
             for (int g = w.g0; g < w.g1; ++g, ++n) {
                 const int st = n % kStages;
-                const int first = (w.lo + g) * kKeys, pos = first + tid;
+                const int first = (w.lo + g) * kKeys, pos = first + gtid;
                 wait(smem_u32(&sh.s_full[n & 1]), (n / 2) & 1, watch);
                 wait(full(st), (n / kStages) & 1, watch);  // seen by this thread too: it reads and clears what was loaded
                 __syncwarp();
                 tc_fence_after();
                 const bool inside = pos >= seen && pos < len;
-                const uint32_t sc = s_scale + st * C::kScale + 32 * (tid / 16) + tid % 16;
+                const uint32_t sc = s_scale + st * C::kScale + 32 * (gtid / 16) + gtid % 16;
                 const uint32_t ek = lds_u8(sc), ev = lds_u8(sc + 16);
                 const float kf = exponent_factor(ek);
                 const float kv = inside ? (float)((int)ev - 127) : -127.f;
-                float s[RP];
+                float s[kRows];
 #pragma unroll
-                for (int c = 0; c < RP; c += kChunk) {
-                    float hi[16], lo[16];
-                    load_parts<RP>(tmem + (n & 1) * N + t_lane, c, hi, lo);
+                for (int c = 0; c < kRows; c += kChunk) {
+                    float hi[kChunk], lo[kChunk];
+                    load_parts<RP, kChunk>(tmem + (n & 1) * N + t_lane + row0 + c, hi, lo);
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) s[c + i] = fmaf(lo[i], 0.0625f, hi[i]) * (kf * sh.qs[c + i]);
+                    for (int i = 0; i < kChunk; ++i) s[c + i] = fmaf(lo[i], 0.0625f, hi[i]) * (kf * sh.qs[row0 + c + i]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[n & 1]));
                 if (first < all_from || first + kKeys > all_to) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r)
-                        if (!inside || pos > sh.last[r] || pos < sh.first[r]) s[r] = ninf;
+                    for (int r = 0; r < kRows; ++r)
+                        if (!inside || pos > sh.last[row0 + r] || pos < sh.first[row0 + r]) s[r] = ninf;
                 }
                 // ---- the tile's largest score of each row, and its largest value exponent
                 const float kv_top = warp_max(kv);
-                if (lane == 0) sh.factor[n & 1][warp] = kv_top;
-                float mine[RP <= 32 ? 1 : 2];
+                float mine = kv_top;
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
+                for (int r = 0; r < kRows; ++r) {
                     const float t = warp_max(s[r]);
-                    if (lane == r % 32) mine[r / 32] = t;
+                    if (lane == r) mine = t;
                 }
-#pragma unroll
-                for (int i = 0; i < (RP + 31) / 32; ++i)
-                    if (lane + 32 * i < RP) sh.top[n & 1][warp][lane + 32 * i] = mine[i];
-                named_bar_sync(1, 128);
+                if (lane < kRows) sh.top[n & 1][gwarp][row0 + lane] = mine;
+                if (lane == 0) sh.factor[n & 1][group][gwarp] = kv_top;
+                named_bar_sync(1 + group, 128);
                 if (g > w.g0) add_values(n - 1);
-                // ---- weights, scaled to at most 2^8
-                const uint32_t p_at = s_p + tid % 16, p_chunk = tid / 16;
-                const float4 k4 = *reinterpret_cast<const float4*>(&sh.factor[n & 1][0]);
-                const float k_top = fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w));
+                const float4 k4 = *reinterpret_cast<const float4*>(&sh.factor[n & 1][group][0]);
+                const float k_top = fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w)) - 8.f;
+                float top[kRows];
+                bool moves = false;  // the same in every thread of the group
 #pragma unroll
-                for (int r0 = 0; r0 < RP; r0 += 4) {
+                for (int r0 = 0; r0 < kRows; r0 += 4) {
+                    const float4 t0 = *reinterpret_cast<const float4*>(&sh.top[n & 1][0][row0 + r0]);
+                    const float4 t1 = *reinterpret_cast<const float4*>(&sh.top[n & 1][1][row0 + r0]);
+                    const float4 t2 = *reinterpret_cast<const float4*>(&sh.top[n & 1][2][row0 + r0]);
+                    const float4 t3 = *reinterpret_cast<const float4*>(&sh.top[n & 1][3][row0 + r0]);
+                    top[r0] = fmaxf(fmaxf(t0.x, t1.x), fmaxf(t2.x, t3.x));
+                    top[r0 + 1] = fmaxf(fmaxf(t0.y, t1.y), fmaxf(t2.y, t3.y));
+                    top[r0 + 2] = fmaxf(fmaxf(t0.z, t1.z), fmaxf(t2.z, t3.z));
+                    top[r0 + 3] = fmaxf(fmaxf(t0.w, t1.w), fmaxf(t2.w, t3.w));
+#pragma unroll
+                    for (int i = r0; i < r0 + 4; ++i) moves |= top[i] > m[i] + 16.f;
+                }
+                if (moves) {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const float to = fmaxf(m[r], top[r]);
+                        const float fix = m[r] == ninf ? 0.f : ex2(m[r] - to);
+                        acc[r] *= fix;
+                        l[r] *= fix;
+                        m[r] = to;
+                    }
+                }
+                // ---- weights, scaled to at most 2^8
+                uint32_t hi[kRows / 4], lo[kRows / 4];
+#pragma unroll
+                for (int r0 = 0; r0 < kRows; r0 += 4) {
                     float y[4];
-                    const float4 t0 = *reinterpret_cast<const float4*>(&sh.top[n & 1][0][r0]);
-                    const float4 t1 = *reinterpret_cast<const float4*>(&sh.top[n & 1][1][r0]);
-                    const float4 t2 = *reinterpret_cast<const float4*>(&sh.top[n & 1][2][r0]);
-                    const float4 t3 = *reinterpret_cast<const float4*>(&sh.top[n & 1][3][r0]);
-                    const float top4[4] = {fmaxf(fmaxf(t0.x, t1.x), fmaxf(t2.x, t3.x)),
-                                           fmaxf(fmaxf(t0.y, t1.y), fmaxf(t2.y, t3.y)),
-                                           fmaxf(fmaxf(t0.z, t1.z), fmaxf(t2.z, t3.z)),
-                                           fmaxf(fmaxf(t0.w, t1.w), fmaxf(t2.w, t3.w))};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = r0 + i;
-                        const float top = top4[i];
-                        if (top > m[r] + 16.f) {  // the same in every thread
-                            const float fix = m[r] == ninf ? 0.f : ex2(m[r] - top);
-                            acc[r] *= fix;
-                            l[r] *= fix;
-                            m[r] = top;
-                        }
                         const float base = m[r] == ninf ? 0.f : m[r];
                         // the reference first: what is left is small, and adding the exponents loses nothing
                         const float x = s[r] - base;
-                        const float ref = top == ninf ? 0.f : top - base + (k_top - 8.f);
+                        const float ref = top[r] == ninf ? 0.f : top[r] - base + k_top;
                         l[r] += ex2(x);
-                        back[r] = top == ninf ? 0.f : ex2(ref);
+                        back[r] = top[r] == ninf ? 0.f : ex2(ref);
                         y[i] = ex2(x + (kv - ref));
                     }
-                    uint32_t hi, lo;
-                    split_e4m3(y[0], y[1], y[2], y[3], hi, lo);
+                    split_e4m3(y[0], y[1], y[2], y[3], hi[r0 / 4], lo[r0 / 4]);
+                }
+                // column c of position t: 16 columns side by side, then the positions, then the next 16 columns
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + i;
-                        sts_u8(p_at + r * kKeys + 16 * (p_chunk ^ (r & 7)), hi >> (8 * i));
-                        sts_u8(p_at + (RP + r) * kKeys + 16 * (p_chunk ^ (r & 7)), lo >> (8 * i));
+                for (int c = 0; c < kRows; c += kRows < 16 ? 8 : 16) {
+                    const int ch = row0 + c, cl = RP + row0 + c;
+                    const uint32_t at_h = s_p + (ch / 16) * 16 * kKeys + 16 * gtid + ch % 16;
+                    const uint32_t at_l = s_p + (cl / 16) * 16 * kKeys + 16 * gtid + cl % 16;
+                    if constexpr (kRows < 16) {
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at_h), "r"(hi[0]), "r"(hi[1]) : "memory");
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at_l), "r"(lo[0]), "r"(lo[1]) : "memory");
+                    } else {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at_h), "r"(hi[c / 4]),
+                                     "r"(hi[c / 4 + 1]), "r"(hi[c / 4 + 2]), "r"(hi[c / 4 + 3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at_l), "r"(lo[c / 4]),
+                                     "r"(lo[c / 4 + 1]), "r"(lo[c / 4 + 2]), "r"(lo[c / 4 + 3])
+                                     : "memory");
                     }
                 }
-                if (!inside) {
+                if (!inside && group == 0) {
                     // positions past the length or before the window may hold anything: weight zero times a NaN is a
                     // NaN, so their values become zero
-                    const uint32_t v = s_stage + st * C::kStage + C::kTile + tid * D;
+                    const uint32_t v = s_stage + st * C::kStage + C::kTile + gtid * D;
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + 16 * c), "r"(0) : "memory");
@@ -487,34 +519,35 @@ __global__ void __launch_bounds__(kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kerne
             tc_fence_before();
             // ---- the rows' sums over the threads, and the stretch's result
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < kRows; ++r) {
 #pragma unroll
                 for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-                if (lane == 0) sh.sum[warp][r] = l[r];
+                if (lane == 0) sh.sum[gwarp][row0 + r] = l[r];
             }
-            named_bar_sync(1, 128);
+            named_bar_sync(1 + group, 128);
             const bool final = w.g0 == 0 && w.g1 == w.n;
             const long long unit = (long long)w.b * p.Hkv + w.h;
             const long long slot = (2LL * blockIdx.x + (w.g0 > 0 ? 0 : 1)) * RP;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                if (r >= p.rows) break;
-                const float L = (sh.sum[0][r] + sh.sum[1][r]) + (sh.sum[2][r] + sh.sum[3][r]);
-                if (tid < D) {
+            for (int r = 0; r < kRows; ++r) {
+                const int row = row0 + r;
+                if (row >= p.rows) break;
+                const float L = (sh.sum[0][row] + sh.sum[1][row]) + (sh.sum[2][row] + sh.sum[3][row]);
+                if (gtid < D) {
                     if (final)
-                        reinterpret_cast<__nv_bfloat16*>(p.o)[(unit * p.rows + r) * D + tid] =
-                            __float2bfloat16(L == 0.f ? 0.f : acc[r] / L);
+                        reinterpret_cast<__nv_bfloat16*>(p.o)[(unit * p.rows + row) * D + gtid] =
+                            __float2bfloat16(L == 0.f ? 0.f : acc[r] * __frcp_rn(L));
                     else
-                        __stcg(p.part_o + (slot + r) * D + tid, acc[r]);
+                        __stcg(p.part_o + (slot + row) * D + gtid, acc[r]);
                 }
-                if (tid == 0) {
-                    if (!final) __stcg(&p.part_ml[slot + r], make_float2(m[r], L));
-                    else if (p.lse) p.lse[unit * p.rows + r] = (m[r] + log2f(L)) * 0.6931471805599453f;
+                if (gtid == 0) {
+                    if (!final) __stcg(&p.part_ml[slot + row], make_float2(m[r], L));
+                    else if (p.lse) p.lse[unit * p.rows + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
                 }
             }
             if (!final && w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w);
             // before sh.sum, the queries and the row bounds are written again
-            named_bar_sync(1, 128);
+            named_bar_sync(1 + group, 128);
         }
     }
     // after a wait that ran out, copies and products may still be under way: wait for them, with a limit
@@ -535,7 +568,7 @@ cudaError_t launch_rp(const PagedParams& p, int grid, cudaStream_t stream) {
     auto* f = paged_e4m3_kernel<D, RP>;
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), Cfg<D, RP>::kSmem);
     if (e != cudaSuccess) return e;
-    f<<<grid, kThreads, Cfg<D, RP>::kSmem, stream>>>(p);
+    f<<<grid, Cfg<D, RP>::kThreads, Cfg<D, RP>::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 template <int D>
