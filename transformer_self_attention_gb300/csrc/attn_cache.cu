@@ -23,6 +23,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWriteBlocks = 2;  // of the write kernel per multiprocessor
 
 __device__ __forceinline__ float exponent_factor(int e) {  // 2^(e - 127); NaN for 255
     return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FFFFFFFu : (uint32_t)e << 23);
@@ -34,157 +35,214 @@ __device__ __forceinline__ int row_exponent(float big) {
     return max(k, -127);
 }
 
-struct WriteLaunch {
-    CacheWriteParams p;
-    int tb, hb, heads_block, tokens;
+// x / n for 0 <= x < 2^31 by a multiplication: mul = ceil(2^(31 + shift) / n) with 2^shift >= n (exact for 31-bit x).
+struct Divisor {
+    unsigned n = 1, mul = 0, shift = 0;
+    Divisor() = default;
+    explicit Divisor(unsigned n_) : n(n_) {
+        while ((1ull << shift) < n) ++shift;
+        mul = (unsigned)(((1ull << (31 + shift)) + n - 1) / n);
+    }
+    __device__ __forceinline__ int div(int x) const { return (int)(((unsigned long long)(unsigned)x * mul) >> (31 + shift)); }
 };
 
-template <int D, bool E4M3, bool STAGED>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
-    constexpr int LANES = D / 16;
-    __shared__ unsigned long long step[D / 2];
-    __shared__ float stage[STAGED ? kThreads / LANES * (D + 1) : 1];
-    const CacheWriteParams& p = a.p;
-    const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
-    const int token = blockIdx.x * a.tb + slot / a.hb;
-    const bool live = slot < a.tb * a.hb && token < a.tokens;
-    const int b = live ? token / p.S : 0, i = live ? token - b * p.S : 0;
-    const bool halves = !p.rope.interleaved;
-    int off_a = 16 * u, off_b = 16 * u + 8;
-    if (!STAGED) rope_runs(halves, p.rope.rot, u, off_a, off_b);
-    const bool across = !STAGED && halves && 16 * u < p.rope.rot;
-    const int H = p.Hq + 2 * p.c.Hkv;
-    const int h_first = blockIdx.y * a.heads_block, h_last = min(H, h_first + a.heads_block);
-    constexpr int U = STAGED ? 1 : 2;
-    // The next U rows, on their way before what they need is known (rows of padding are read too, and not used).
-    Raw8<__nv_bfloat16> raw[U][2];
-    auto fetch = [&](int h0) {
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int h = h0 + j * a.hb + slot % a.hb;
-            if (!live || h >= h_last) continue;
-            const int kind = h < p.Hq ? 1 : h < p.Hq + p.c.Hkv ? 2 : 3;
-            const RopeRows& r = kind == 1 ? p.q : kind == 2 ? p.k : p.v;
-            const int head = h - (kind == 1 ? 0 : kind == 2 ? p.Hq : p.Hq + p.c.Hkv);
-            const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(r.src) + (b * r.sb + head * r.sh + i * r.ss);
-            const bool apart = across && kind != 3;
-            fetch8(in + (apart ? off_a : 16 * u), raw[j][0]);
-            fetch8(in + (apart ? off_b : 16 * u + 8), raw[j][1]);
-        }
-    };
-    fetch(h_first);
-    const int len = p.t.len[b];
-    const int fresh = p.new_len ? p.new_len[b] : p.S;
-    const int pos = len - fresh + i;
-    const bool valid = live && i < fresh && pos >= 0;  // a sequence shorter than its rows: padding in front
-    // where the token's rows go; a bad one is recorded and skipped
-    bool placed = false;
-    int page = 0, in_page = 0;
-    if (valid) {
-        int bad = 0;
-        if (pos >= (long long)p.t.max_pages * p.c.page) {
-            bad = kCacheErrPosition;
-        } else {
-            page = p.t.pages[b * p.t.stride + pos / p.c.page];
-            in_page = pos % p.c.page;
-            if (page < 0 || page >= p.c.n_pages) bad = kCacheErrPage;
-        }
-        placed = bad == 0;
-        if (bad && u == 0) atomicOr(p.c.err, bad);
+struct WriteLaunch {
+    CacheWriteParams p;
+    int tokens, items, chunks, items_chunk;  // items of a token: two queries, or a key and its value
+    Divisor by_S, by_page, by_chunks;
+};
+
+// Largest of |x| and y; NaN if either is one.
+__device__ __forceinline__ float max_abs_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(fabsf(x)), "f"(y));
+    return z;
+}
+
+// Turns the lane's runs of a row, through shared memory where the pairs do not sit on the 8-element grid (STAGED).
+template <bool HALVES, bool STAGED>
+__device__ __forceinline__ void turn_row(float (&run)[16], float* row, int rot, int u, const float (&c)[8],
+                                         const float (&s)[8]) {
+    if (!STAGED) {
+        rope_turn_runs<HALVES>(run, c, s);
+        return;
     }
-    if ((int)threadIdx.x < p.rope.rot / 2) step[threadIdx.x] = p.rope.step[threadIdx.x];
-    __syncthreads();
-    float c[8], sn[8];
+    float x[16];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) row[16 * u + e] = run[e];
+    __syncwarp();
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int q = 8 * u + e;
-        c[e] = 1.f;
-        sn[e] = 0.f;
-        if (2 * q < p.rope.rot) {
-            rope_cos_sin(pos, step[q], c[e], sn[e]);
-            c[e] *= p.rope.amp;
-            sn[e] *= p.rope.amp;
-        }
+        int i0, i1;
+        rope_pair_index(HALVES, rot, 8 * u + e, i0, i1);
+        x[2 * e] = row[i0];
+        x[2 * e + 1] = row[i1];
     }
-    for (int h0 = h_first; h0 < h_last; h0 += U * a.hb) {
-        float run[U][16];
-        int what[U], head[U];  // 0: nothing, 1: a query, 2: a key, 3: a value
-        bool swap[U];          // the lane's runs are the two halves of pairs
+    rope_turn(x, c, s);
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int h = h0 + j * a.hb + slot % a.hb;
-            what[j] = !live || h >= h_last ? 0 : h < p.Hq ? 1 : h < p.Hq + p.c.Hkv ? 2 : 3;
-            head[j] = h - (what[j] == 1 ? 0 : what[j] == 2 ? p.Hq : p.Hq + p.c.Hkv);
-            swap[j] = across && what[j] != 3;
+    for (int e = 0; e < 8; ++e) {
+        int i0, i1;
+        rope_pair_index(HALVES, rot, 8 * u + e, i0, i1);
+        row[i0] = x[2 * e];
+        row[i1] = x[2 * e + 1];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) run[e] = row[16 * u + e];
+}
+
+// HALVES: the rotated pairs are (p, p + rot / 2), otherwise neighbours.  STAGED: pairs of halves off the 8-element grid.
+// A thread takes two rows at a time: two queries, or a head's key and value.  (One row at a time, with its kind and place
+// found anew, took 300 instructions a row and 103 us for 49K tokens of 8 heads, 4 TB/s.)
+template <int D, bool E4M3, bool HALVES, bool STAGED>
+__global__ void __launch_bounds__(kThreads, kWriteBlocks) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
+    constexpr int LANES = D / 16, SLOTS = 32 / LANES, WARPS = kThreads / 32;
+    __shared__ float2 turns[WARPS][D / 2];
+    __shared__ unsigned long long step[D / 2];
+    __shared__ float stage[STAGED ? WARPS * SLOTS * (D + 1) : 1];
+    const CacheWriteParams& p = a.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, u = lane % LANES, slot = lane / LANES;
+    const int pairs = p.rope.rot / 2, q_items = (p.Hq + 1) / 2;
+    int off_a = 16 * u, off_b = 16 * u + 8;
+    if (!STAGED) rope_runs(HALVES, p.rope.rot, u, off_a, off_b);
+    typedef const __nv_bfloat16* Src;
+
+    // A warp takes one token's items (a chunk of them where there are few tokens) after another; what the next step needs is
+    // always on its way.
+    struct Job {
+        int token, b, i, fresh, item, end;  // item: the lane's next; end: behind the chunk
+        int pos, entry, slot;               // position (-1: padding), its page-table entry and slot
+    };
+    auto open = [&](int job) {
+        Job j;
+        j.token = a.by_chunks.div(job);
+        const int chunk = job - j.token * a.chunks;
+        j.item = chunk * a.items_chunk + slot;
+        j.end = min(a.items, (chunk + 1) * a.items_chunk);
+        j.b = a.by_S.div(j.token);
+        j.i = j.token - j.b * p.S;
+        j.fresh = p.new_len ? p.new_len[j.b] : p.S;
+        j.pos = p.t.len[j.b] - j.fresh + j.i;
+        j.entry = -1;
+        j.slot = 0;
+        if (j.i >= j.fresh || j.pos < 0) {
+            j.pos = -1;  // padding; also in front of a sequence shorter than its rows
+        } else if (j.pos >= (long long)p.t.max_pages * p.c.page) {
+            j.entry = -2;
+        } else {
+            const int index = a.by_page.div(j.pos);
+            j.slot = j.pos - index * p.c.page;
+            j.entry = p.t.pages[j.b * p.t.stride + index];
+        }
+        return j;
+    };
+    Raw8<__nv_bfloat16> raw[2][2] = {};
+    auto fetch = [&](const Job& j, int item) {
+        if (item >= j.end || j.i >= j.fresh) return;  // rows of padding are not read
+        const bool query = item < q_items;
+        const int h = query ? 2 * item : item - q_items;
+        const RopeRows& r = query ? p.q : p.k;
+        const Src r0 = reinterpret_cast<Src>(r.src) + (j.b * r.sb + j.i * r.ss + h * r.sh);
+        fetch8(r0 + off_a, raw[0][0]);
+        fetch8(r0 + off_b, raw[0][1]);
+        if (query) {
+            if (h + 1 < p.Hq) {
+                fetch8(r0 + p.q.sh + off_a, raw[1][0]);
+                fetch8(r0 + p.q.sh + off_b, raw[1][1]);
+            }
+        } else {
+            const Src r1 = reinterpret_cast<Src>(p.v.src) + (j.b * p.v.sb + j.i * p.v.ss + h * p.v.sh) + 16 * u;
+            fetch8(r1, raw[1][0]);
+            fetch8(r1 + 8, raw[1][1]);
+        }
+    };
+    // (the frequencies lie in the parameters, where 32 different words take 32 reads)
+    if ((int)threadIdx.x < pairs) step[threadIdx.x] = p.rope.step[threadIdx.x];
+    __syncthreads();
+    const int jobs = a.tokens * a.chunks, stride = gridDim.x * WARPS;
+    int job = blockIdx.x * WARPS + warp;
+    if (job >= jobs) return;
+    Job now = open(job);
+    fetch(now, now.item);
+    for (; job < jobs; job += stride) {
+        Job next = now;
+        const bool more = job + stride < jobs;
+        if (more) next = open(job + stride);
+        for (int q = lane; q < pairs; q += 32) {
+            float cq, sq;
+            rope_cos_sin(now.pos, step[q], cq, sq);
+            turns[warp][q] = make_float2(cq * p.rope.amp, sq * p.rope.amp);
+        }
+        __syncwarp();
+        float c[8], sn[8];
+        rope_lane_turns(turns[warp], u, p.rope.rot, c, sn);
+        __syncwarp();
+        struct {
+            int pos, page, slot;
+        } at{now.pos, now.entry, now.slot};
+        if (at.pos >= 0 && (at.page < 0 || at.page >= p.c.n_pages)) {  // a bad place is recorded and skipped
+            if (lane == 0) atomicOr(p.c.err, at.page == -2 && at.pos >= (long long)p.t.max_pages * p.c.page ? kCacheErrPosition : kCacheErrPage);
+            at.page = -1;
+        }
+        const int b = now.b, i = now.i;
+    // the token's slot in kv head 0 of its page, and the bytes from one head to the next
+    constexpr int kRow = D * (E4M3 ? 1 : 2);
+    const long long head_bytes = 2LL * p.c.page * kRow;
+    char* const keys = p.c.pages + (long long)at.page * p.c.Hkv * head_bytes + at.slot * kRow;
+    for (int item = now.item; __any_sync(0xFFFFFFFFu, item < now.end); item += SLOTS) {
+        float run[2][16];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
             widen8(raw[j][0], run[j]);
             widen8(raw[j][1], run[j] + 8);
-            if (what[j] == 0 || !valid)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) run[j][e] = 0.f;
         }
-        fetch(h0 + U * a.hb);
+        const bool last = !__any_sync(0xFFFFFFFFu, item + SLOTS < now.end);
+        if (!last) fetch(now, item + SLOTS);
+        else if (more) fetch(next, next.item);
+        const bool query = item < q_items;
+        turn_row<HALVES, STAGED>(run[0], stage + (STAGED ? (warp * SLOTS + slot) * (D + 1) : 0), p.rope.rot, u, c, sn);
+        float second[16];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (STAGED) {  // pairs of halves off the 8-element grid: through shared memory, within the row's warp
-                float* row = stage + slot * (D + 1);
-                float x[16];
-                __syncwarp();
+        for (int e = 0; e < 16; ++e) second[e] = run[1][e];
+        turn_row<HALVES, STAGED>(second, stage + (STAGED ? (warp * SLOTS + slot) * (D + 1) : 0), p.rope.rot, u, c, sn);
+        float big[2] = {0.f, 0.f};
+        if (E4M3) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) row[16 * u + e] = run[j][e];
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int i0, i1;
-                    rope_pair_index(halves, p.rope.rot, 8 * u + e, i0, i1);
-                    x[2 * e] = row[i0];
-                    x[2 * e + 1] = row[i1];
-                }
-                if (what[j] != 3) rope_turn(x, c, sn);
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int i0, i1;
-                    rope_pair_index(halves, p.rope.rot, 8 * u + e, i0, i1);
-                    row[i0] = x[2 * e];
-                    row[i1] = x[2 * e + 1];
-                }
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) run[j][e] = row[16 * u + e];
-            } else if (what[j] == 1 || what[j] == 2) {
-                float x[16];
-                runs_to_pairs(swap[j], run[j], run[j] + 8, x);
-                rope_turn(x, c, sn);
-                pairs_to_runs(swap[j], x, run[j], run[j] + 8);
+            for (int e = 0; e < 16; ++e) {
+                big[0] = max_abs_nan(run[0][e], big[0]);
+                big[1] = max_abs_nan(run[1][e], big[1]);
             }
-            float big = 0.f;
-            bool odd = false;  // an infinity or a NaN in the row
-            if (E4M3) {
+            // the lanes of a row: LANES neighbours, on a multiple of LANES
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float m = fabsf(run[j][e]);
-                    big = fmaxf(big, m);
-                    odd |= !(m <= 3.402823466e38f);
-                }
-                // the lanes of a row: LANES neighbours, on a multiple of LANES
+            for (int o = LANES / 2; o; o >>= 1)
 #pragma unroll
-                for (int o = LANES / 2; o; o >>= 1) {
-                    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-                    odd |= __shfl_xor_sync(0xFFFFFFFFu, (int)odd, o) != 0;
-                }
+                for (int j = 0; j < 2; ++j) big[j] = max_abs_nan(__shfl_xor_sync(0xFFFFFFFFu, big[j], o), big[j]);
+        }
+        if (item >= now.end) continue;
+        if (query) {
+            const int h = 2 * item;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.q.dst) + (b * p.q.db + h * p.q.dh + i * p.q.ds);
+            if (at.pos < 0)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) run[0][e] = second[e] = 0.f;
+            store8(out + off_a, run[0]);
+            store8(out + off_b, run[0] + 8);
+            if (h + 1 < p.Hq) {
+                store8(out + p.q.dh + off_a, second);
+                store8(out + p.q.dh + off_b, second + 8);
             }
-            const int ra = swap[j] ? off_a : 16 * u, rb = swap[j] ? off_b : 16 * u + 8;
-            if (what[j] == 1) {
-                __nv_bfloat16* out =
-                    reinterpret_cast<__nv_bfloat16*>(p.q.dst) + (b * p.q.db + head[j] * p.q.dh + i * p.q.ds);
-                store8(out + ra, run[j]);
-                store8(out + rb, run[j] + 8);
-            } else if (what[j] >= 2 && placed) {
-                const long long unit = (long long)page * p.c.Hkv + head[j];
-                const int kv = what[j] - 2;
-                const long long row = (unit * 2 + kv) * p.c.page + in_page;
+        } else if (at.page >= 0) {
+            const int h = item - q_items;
+            char* const key = keys + h * head_bytes;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                char* const out = key + j * (head_bytes / 2);
+                const int ra = j ? 16 * u : off_a, rb = j ? 16 * u + 8 : off_b;
                 if (E4M3) {
-                    const int k = odd ? 128 : row_exponent(big);
+                    const bool odd = !(big[j] <= 3.402823466e38f);  // an infinity or a NaN in the row
+                    const int k = odd ? 128 : row_exponent(big[j]);
                     const float f = exponent_factor(max(0, 127 - k));  // 2^-k
                     uint32_t w[4];
 #pragma unroll
@@ -192,19 +250,19 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
                         w[g] = odd ? 0x7F7F7F7Fu
                                    : ptx::pack_e4m3x4(run[j][4 * g] * f, run[j][4 * g + 1] * f, run[j][4 * g + 2] * f,
                                                       run[j][4 * g + 3] * f);
-                    char* out = p.c.pages + row * D;
                     *reinterpret_cast<uint2*>(out + ra) = make_uint2(w[0], w[1]);
                     *reinterpret_cast<uint2*>(out + rb) = make_uint2(w[2], w[3]);
-                    if (u == 0)
-                        p.c.scales[((unit * (p.c.page / 16) + in_page / 16) * 2 + kv) * 16 + in_page % 16] =
-                            (uint8_t)(k + 127);
+                    if (u == 0) {
+                        const long long unit = (long long)at.page * p.c.Hkv + h;
+                        p.c.scales[((unit * (p.c.page / 16) + at.slot / 16) * 2 + j) * 16 + at.slot % 16] = (uint8_t)(k + 127);
+                    }
                 } else {
-                    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.c.pages) + row * D;
-                    store8(out + ra, run[j]);
-                    store8(out + rb, run[j] + 8);
+                    store8(reinterpret_cast<__nv_bfloat16*>(out) + ra, run[j]);
+                    store8(reinterpret_cast<__nv_bfloat16*>(out) + rb, run[j] + 8);
                 }
             }
         }
+    }    now = next;
     }
 }
 
@@ -276,20 +334,22 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     WriteLaunch a{};
     a.p = p;
     a.tokens = p.B * p.S;
-    const int rows = kThreads / (D / 16), H = p.Hq + 2 * p.c.Hkv;
-    const int heads = std::min(8, pow2_at_least(H / 8 / 2 + 1));  // side by side, as in launch_rope
-    a.tb = std::min(rows / heads, pow2_at_least(a.tokens));
-    a.hb = rows / a.tb;
-    const long long blocks_x = (a.tokens + (long long)a.tb - 1) / a.tb;
-    const int rounds = (H + a.hb - 1) / a.hb;
-    const long long want = 4LL * n_sm;
-    const int split = (int)std::min<long long>(rounds, std::max<long long>(1, (want + blocks_x - 1) / blocks_x));
-    a.heads_block = (rounds + split - 1) / split * a.hb;
-    const dim3 grid((unsigned)blocks_x, (unsigned)((H + a.heads_block - 1) / a.heads_block));
-    if (!p.rope.interleaved && p.rope.rot % 16 != 0)
-        cache_write_kernel<D, E4M3, true><<<grid, kThreads, 0, stream>>>(a);
-    else
-        cache_write_kernel<D, E4M3, false><<<grid, kThreads, 0, stream>>>(a);
+    a.items = (p.Hq + 1) / 2 + p.c.Hkv;
+    a.by_S = Divisor(p.S);
+    a.by_page = Divisor(p.c.page);
+    // a warp takes all items of a token unless that leaves multiprocessors without their warps
+    const int slots = 32 / (D / 16), rounds = (a.items + slots - 1) / slots, warps = kThreads / 32;
+    const long long want = (long long)kWriteBlocks * warps * n_sm;
+    const int split = (int)std::min<long long>(rounds, std::max<long long>(1, (want + a.tokens - 1) / a.tokens));
+    a.items_chunk = (rounds + split - 1) / split * slots;
+    a.chunks = (a.items + a.items_chunk - 1) / a.items_chunk;
+    a.by_chunks = Divisor(a.chunks);
+    const long long blocks = ((long long)a.tokens * a.chunks + warps - 1) / warps;
+    const unsigned grid = (unsigned)std::min<long long>(blocks, (long long)kWriteBlocks * n_sm);
+    auto go = [&](auto* f) { f<<<grid, kThreads, 0, stream>>>(a); };
+    if (p.rope.interleaved) go(cache_write_kernel<D, E4M3, false, false>);
+    else if (p.rope.rot % 16 != 0) go(cache_write_kernel<D, E4M3, true, true>);
+    else go(cache_write_kernel<D, E4M3, true, false>);
     return cudaGetLastError();
 }
 

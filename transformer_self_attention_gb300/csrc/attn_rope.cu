@@ -6,8 +6,8 @@
 // the same with -t.  Bound by memory: every element is read once and written once, about 3 flops each.
 //
 // A row is held by d / 16 neighbouring threads, 16 elements each, as two 16-byte runs of bf16 (four of fp32), so
-// that the loads and stores of a warp cover whole rows.  A thread keeps one token and walks over heads: its eight
-// cosines and sines, about 8 x 40 instructions, serve every head of the token.
+// that the loads and stores of a warp cover whole rows.  A thread keeps one token and walks over heads.  The cosines and
+// sines of a block's tokens (about 45 instructions each) are computed once, into shared memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -46,20 +46,18 @@ __device__ __forceinline__ void row_sync(int warp_rows) {
 // turned, so that loads are always under way.
 // STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
 // memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
-template <class T, bool STAGED, int U>
+template <class T, bool HALVES, bool STAGED, int U>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ uint32_t stage[];
+    __shared__ float2 turns[kThreads * 8];  // rows of a block * rot / 2 at most
     __shared__ unsigned long long step[kRopeMaxPairs];
     const int lanes = p.d / 16, u = threadIdx.x % lanes, slot = threadIdx.x / lanes;
     const int token = blockIdx.x * p.tb + slot / p.hb;
     const bool live = slot < p.tb * p.hb && token < p.tokens;
     const int b = live ? token / p.S : 0, s = live ? token - b * p.S : 0;
-    const bool halves = !p.t.interleaved;
     int off_a = 16 * u, off_b = 16 * u + 8;
-    if (!STAGED) rope_runs(halves, p.t.rot, u, off_a, off_b);
-    const bool across = !STAGED && halves && 16 * u < p.t.rot;
+    if (!STAGED) rope_runs(HALVES, p.t.rot, u, off_a, off_b);
     const int h_first = blockIdx.y * p.heads_block, h_last = min(p.H, h_first + p.heads_block);
-    const int pos = !live ? 0 : p.positions ? p.positions[b * p.pos_b + s * p.pos_s] : s;
 
     Raw8<T> raw[U][2];
     auto fetch = [&](int h0) {
@@ -74,20 +72,21 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     };
     fetch(h_first);
-    if ((int)threadIdx.x < p.t.rot / 2) step[threadIdx.x] = p.t.step[threadIdx.x];
+    // (the frequencies lie in the parameters, where 32 different words take 32 reads)
+    const int pairs = p.t.rot / 2;
+    if ((int)threadIdx.x < pairs) step[threadIdx.x] = p.t.step[threadIdx.x];
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.tb * pairs; i += kThreads) {
+        const int q = i % pairs, t = min((int)blockIdx.x * p.tb + i / pairs, p.tokens - 1);
+        const int tb = t / p.S, ts = t - tb * p.S;
+        const int pos = p.positions ? p.positions[tb * p.pos_b + ts * p.pos_s] : ts;
+        float cq, sq;
+        rope_cos_sin(pos, step[q], cq, sq);
+        turns[i] = make_float2(cq * p.t.amp, sq * (p.t.amp * p.sign));
+    }
     __syncthreads();
     float c[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int q = 8 * u + e;
-        c[e] = 1.f;
-        sn[e] = 0.f;
-        if (2 * q < p.t.rot) {
-            rope_cos_sin(pos, step[q], c[e], sn[e]);
-            c[e] *= p.t.amp;
-            sn[e] *= p.t.amp * p.sign;
-        }
-    }
+    rope_lane_turns(turns + min(slot / p.hb, p.tb - 1) * pairs, u, p.t.rot, c, sn);
     for (int h0 = h_first; h0 < h_last; h0 += U * p.hb) {
         float run[U][16];
         Raw8<T> raw_now[U][2];
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         int i0, i1;
-                        rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                        rope_pair_index(HALVES, p.t.rot, 8 * u + e, i0, i1);
                         x[2 * e] = (float)row_t[i0];
                         x[2 * e + 1] = (float)row_t[i1];
                     }
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         int i0, i1;
-                        rope_pair_index(halves, p.t.rot, 8 * u + e, i0, i1);
+                        rope_pair_index(HALVES, p.t.rot, 8 * u + e, i0, i1);
                         row_t[i0] = (T)x[2 * e];
                         row_t[i1] = (T)x[2 * e + 1];
                     }
@@ -149,10 +148,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                                             row[kWords * u + e + 3]);
                 continue;
             } else {
-                float x[16];
-                runs_to_pairs(across, run[i], run[i] + 8, x);
-                rope_turn(x, c, sn);
-                pairs_to_runs(across, x, run[i], run[i] + 8);
+                rope_turn_runs<HALVES>(run[i], c, sn);
             }
             if (!row_live) continue;
             const RopeRows& r = h < p.Hq ? p.q : p.k;
@@ -188,13 +184,13 @@ cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k
     p.pos_s = pos_s;
     p.sign = inverse ? -1.f : 1.f;
     const int rows = kThreads / (d / 16);
+    const int heads_wide = p.H >= 64 ? 8 : 4;
     p.warp_rows = 32 % (d / 16) == 0;
-    // Up to eight heads side by side (their rows are neighbours in a [B, S, H, d] projection), fewer where a thread would
-    // walk over less than eight (its cosines and sines cost as much as several rows: 40 heads, 16K tokens, 58 us with 4
-    // heads side by side, 68 us with 8); the other rows of a block are neighbouring tokens (neighbours in [B, H, S, d]).
-    // Few tokens leave more rows to the heads.
-    const int heads = std::min(8, pow2_at_least(p.H / 8 / 2 + 1));
-    p.tb = std::min(std::max(1, rows / heads), pow2_at_least(p.tokens));
+    // Four or eight heads side by side (their rows are neighbours in a [B, S, H, d] projection), so that a thread still
+    // walks over eight or so; the other rows of a block are neighbouring tokens (neighbours in [B, H, S, d]); few tokens
+    // leave more rows to the heads.  With 2, 4, 8, 16 heads side by side: 64 heads x 8K tokens 49.8, 46.8, 44.6, 47.0 us,
+    // 40 heads x 16K tokens 57.9, 55.2, 58.8, 70.3 us.
+    p.tb = std::min(std::max(1, rows / heads_wide), pow2_at_least(p.tokens));
     p.hb = rows / p.tb;
     // A block walks over all heads of its tokens unless that leaves multiprocessors without four blocks.
     const long long blocks_x = (p.tokens + (long long)p.tb - 1) / p.tb;
@@ -205,13 +201,10 @@ cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k
     const dim3 grid((unsigned)blocks_x, (unsigned)((p.H + p.heads_block - 1) / p.heads_block));
     const bool staged = !t.interleaved && t.rot % 16 != 0;
     const size_t smem = staged ? (size_t)rows * (d * (f32 ? 4 : 2) + 4) : 0;
-    if (f32) {
-        if (staged) rope_kernel<float, true, 1><<<grid, kThreads, smem, stream>>>(p);
-        else rope_kernel<float, false, 2><<<grid, kThreads, 0, stream>>>(p);
-    } else {
-        if (staged) rope_kernel<__nv_bfloat16, true, 1><<<grid, kThreads, smem, stream>>>(p);
-        else rope_kernel<__nv_bfloat16, false, 2><<<grid, kThreads, 0, stream>>>(p);
-    }
+    auto go = [&](auto* f) { f<<<grid, kThreads, smem, stream>>>(p); };
+    if (staged) f32 ? go(rope_kernel<float, true, true, 1>) : go(rope_kernel<__nv_bfloat16, true, true, 1>);
+    else if (t.interleaved) f32 ? go(rope_kernel<float, false, false, 2>) : go(rope_kernel<__nv_bfloat16, false, false, 2>);
+    else f32 ? go(rope_kernel<float, true, false, 2>) : go(rope_kernel<__nv_bfloat16, true, false, 2>);
     return cudaGetLastError();
 }
 

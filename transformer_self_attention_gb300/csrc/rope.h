@@ -109,19 +109,26 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-// Runs <-> pairs: pairs of halves sit across the two runs, neighbouring pairs inside them.
-__device__ __forceinline__ void runs_to_pairs(bool across, const float* a, const float* b, float (&x)[16]) {
+// Turns the pairs of a lane's two runs x[0 .. 7], x[8 .. 15]: across the runs (pairs of halves), or inside them.  Lanes
+// behind the rotated elements have c = 1, s = 0, for which the pairing does not matter.
+template <bool HALVES>
+__device__ __forceinline__ void rope_turn_runs(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        x[2 * e] = across ? a[e] : (e < 4 ? a[2 * e] : b[2 * e - 8]);
-        x[2 * e + 1] = across ? b[e] : (e < 4 ? a[2 * e + 1] : b[2 * e - 7]);
+        const int i0 = HALVES ? e : 2 * e, i1 = HALVES ? 8 + e : 2 * e + 1;
+        const float a = x[i0], b = x[i1];
+        x[i0] = a * c[e] - b * s[e];
+        x[i1] = a * s[e] + b * c[e];
     }
 }
-__device__ __forceinline__ void pairs_to_runs(bool across, const float (&x)[16], float* a, float* b) {
+// The lane's cosines and sines from a table of its token's pairs, times amp.
+__device__ __forceinline__ void rope_lane_turns(const float2* table, int u, int rot, float (&c)[8], float (&s)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        a[e] = across ? x[2 * e] : x[e];
-        b[e] = across ? x[2 * e + 1] : x[8 + e];
+        const int q = 8 * u + e;
+        const float2 t = 2 * q < rot ? table[q] : make_float2(1.f, 0.f);
+        c[e] = t.x;
+        s[e] = t.y;
     }
 }
 #endif
