@@ -560,6 +560,11 @@ def _rows(name, t, shape, dtype, device):
     return attn_rows(t.data_ptr(), sb, sh, ss)
 
 
+def _new_rows(t, H, S, d):
+    """attn_rows of a tensor [B, H, S, d] allocated here."""
+    return attn_rows(t.data_ptr(), H * S * d, S * d, d)
+
+
 def _int32(name, t, shape, device):
     """Pointer of a contiguous int32 tensor."""
     if t.dtype is not torch.int32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
@@ -640,7 +645,9 @@ class RotaryPositions:
         q = _rows("Q", Q, shape, dtype, device)
         if Q_out is None:
             Q_out = torch.empty(shape, dtype=dtype, device=Q.device)
-        qo = _rows("Q_out", Q_out, shape, dtype, device)
+            qo = _new_rows(Q_out, Hq, S, d)
+        else:
+            qo = _rows("Q_out", Q_out, shape, dtype, device)
         Hk, k, ko = 0, None, None
         if K is not None:
             if K.dim() != 4 or K.shape[1] < 1:
@@ -650,7 +657,9 @@ class RotaryPositions:
             k = _rows("K", K, shape, dtype, device)
             if K_out is None:
                 K_out = torch.empty(shape, dtype=dtype, device=Q.device)
-            ko = _rows("K_out", K_out, shape, dtype, device)
+                ko = _new_rows(K_out, Hk, S, d)
+            else:
+                ko = _rows("K_out", K_out, shape, dtype, device)
         pos, pb, ps = None, 0, 0
         if positions is not None:
             if positions.dtype is not torch.int32 or positions.get_device() != device \
@@ -754,7 +763,9 @@ class PagedCache:
             q = _rows("Q", Q, shape, torch.bfloat16, device)
             if Q_out is None:
                 Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-            qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device)
+                qo = _new_rows(Q_out, Hq, S, d)
+            else:
+                qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device)
         new = None if new_len is None else _int32("new_len", new_len, (B,), device)
         if B:
             st = _call(device, stream, _lib.attn_cache_write,
@@ -831,15 +842,15 @@ class PagedDecodeAttention:
         if rows != B:
             raise ValueError(f"page_table must have {B} rows")
         shape = (B, Hq, S_q, d)
+        for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
+                                  ("LSE", LSE, shape[:3], torch.float32)):
+            if (t is not None or name == "Q") and (t.dtype is not dt or t.get_device() != self._device
+                                                   or t.shape != want or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {want} on {self.device}")
         if O is None:
             O = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         if LSE is None and want_lse:
             LSE = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
-        for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
-                                  ("LSE", LSE, shape[:3], torch.float32)):
-            if t is not None and (t.dtype is not dt or t.get_device() != self._device or t.shape != want
-                                  or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {want} on {self.device}")
         st = _call(self._device, stream, _lib.attn_paged_forward,
                    (self.handle, cache.handle, Q.data_ptr(), *table, O.data_ptr(), None if LSE is None else LSE.data_ptr()),
                    (Q, O, LSE, page_table, cache_len, cache.pages, cache.scales))

@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     }
     if (tid == 0) prefetch_tmap(&p.tm);
     fence_barrier_init();
+    wait_for_kernel_before();
     int busy;
     const unsigned W = paged_prefix<C::kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * Hkv;
     const PagedCuts cuts(W, busy * Hkv, gridDim.x, shape);
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
 constexpr int kMergeWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedParams p, int rows_pad) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_kernel_before();
     const int row = blockIdx.y * kMergeWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
     const int k0 = blockIdx.x;
     const int2 cut = __ldcg(&p.cut[k0]);
@@ -537,8 +538,7 @@ cudaError_t launch_rw(const PagedParams& p, int grid, cudaStream_t stream) {
     auto* f = paged_kernel<D, RW>;
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), smem);
     if (e != cudaSuccess) return e;
-    f<<<grid, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(f, dim3((unsigned)grid), kThreads, smem, stream, p);
 }
 template <int D>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {
@@ -559,17 +559,9 @@ cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t strea
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.rows + kMergeWarps - 1) / kMergeWarps));
-    cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return p.c.d == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, p, rows_pad)
-                       : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, p, rows_pad);
+    const dim3 blocks((unsigned)grid, (unsigned)((p.rows + kMergeWarps - 1) / kMergeWarps));
+    return p.c.d == 64 ? launch_dependent(paged_merge_kernel<64>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad)
+                       : launch_dependent(paged_merge_kernel<128>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad);
 }
 
 }  // namespace attn

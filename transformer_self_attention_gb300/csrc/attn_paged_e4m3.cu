@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
             *reinterpret_cast<uint4*>(smem + C::kOffZero + 16 * i) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     fence_barrier_init();
+    wait_for_kernel_before();
     int busy;
     const unsigned W = paged_prefix<kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.Hkv;
     const PagedCuts cuts(W, busy * p.Hkv, gridDim.x, shape);
@@ -568,8 +569,7 @@ cudaError_t launch_rp(const PagedParams& p, int grid, cudaStream_t stream) {
     auto* f = paged_e4m3_kernel<D, RP>;
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), Cfg<D, RP>::kSmem);
     if (e != cudaSuccess) return e;
-    f<<<grid, Cfg<D, RP>::kThreads, Cfg<D, RP>::kSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(f, dim3((unsigned)grid), Cfg<D, RP>::kThreads, Cfg<D, RP>::kSmem, stream, p);
 }
 template <int D>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {

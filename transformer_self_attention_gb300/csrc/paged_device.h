@@ -15,6 +15,24 @@ struct Walk {
     int len, seen;     // its visible positions: [seen, len)
 };
 
+// A launch that may begin while the kernel before it in the stream still runs; the kernel waits for that one
+// (griddepcontrol.wait) before it reads or writes global memory.
+template <class K, class... A>
+cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Key blocks of sequence b (0 for a length that is not followed).
 template <int KEYS>
 __device__ __forceinline__ int paged_blocks_of(const PagedParams& p, int n, int& lo) {
