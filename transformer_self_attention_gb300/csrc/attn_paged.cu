@@ -507,17 +507,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
             f = t.x == ninf ? t.y : ex2(t.x - M);
             L += t.x == ninf ? t.y : t.y * f;
         }
+        // sixteen parts' loads at a time: a round trip to L2 is most of what this kernel takes
         const int n = min(32, k1 - kk + 1);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
-            const float* src = p.part_o + at(kk + i) * D;
-            if constexpr (D == 128) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-                v[0] += fi * y.x; v[1] += fi * y.y; v[2] += fi * y.z; v[3] += fi * y.w;
-            } else {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                v[0] += fi * y.x; v[1] += fi * y.y;
+        for (int i0 = 0; i0 < n; i0 += 16) {
+            float y[16][kVec];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (i0 + i >= n) continue;
+                const float* src = p.part_o + at(kk + i0 + i) * D;
+                if constexpr (D == 128) {
+                    const float4 t = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                    y[i][0] = t.x; y[i][1] = t.y; y[i][kVec - 2] = t.z; y[i][kVec - 1] = t.w;
+                } else {
+                    const float2 t = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                    y[i][0] = t.x; y[i][1] = t.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float fi = __shfl_sync(0xFFFFFFFFu, f, (i0 + i) % 32);
+                if (i0 + i >= n) continue;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[j] += fi * y[i][j];
             }
         }
     }
