@@ -65,10 +65,11 @@ def values(pages, scales):
     return x
 
 
-def make_pool(lens, Hkv, page, d, store, seed=0, spare=2, k_scale=1.0, window_first=None):
+def make_pool(lens, Hkv, page, d, store, seed=0, spare=2, k_scale=1.0, window_first=None, v_spread=0.0):
     """(pages, scales, table, n_pages): CPU tensors; K and V of every position normal, every slot behind a length
     and every free page poisoned (NaN), unneeded table entries out of range.  window_first[b]: positions before it
-    are poisoned too, their whole pages released (entries out of range)."""
+    are poisoned too, their whole pages released (entries out of range).  v_spread: the value rows' sizes vary by
+    e^(v_spread N(0, 1))."""
     g = torch.Generator().manual_seed(seed)
     need = [-(-n // page) for n in lens]
     n_pages = sum(need) + spare
@@ -88,6 +89,8 @@ def make_pool(lens, Hkv, page, d, store, seed=0, spare=2, k_scale=1.0, window_fi
             table[b, i] = p
             x[p, :, :, lo:hi] = torch.randn((Hkv, 2, hi - lo, d), generator=g)
             x[p, :, 0, lo:hi] *= k_scale
+            if v_spread:
+                x[p, :, 1, lo:hi] *= torch.exp(v_spread * torch.randn((Hkv, hi - lo, 1), generator=g))
     if store == "bf16":
         return x.to(torch.bfloat16), None, table, n_pages
     codes, e = quantise(x)
@@ -136,7 +139,31 @@ def decode(Q, vals, table, page, lens, scale, kind, window):
     return O.view(*shape, d), L.view(shape), A.view(*shape, d), E.view(shape)
 
 
-def check_decode(O, LSE, ref, d):
+def coarse_weights(Q, vals, factors, table, page, lens, scale):
+    """The second part of the weights' rounding over E4M3 pages, per row [B, Hq, S_q] (causal): a weight of one of 128
+    positions is also off by 2^-22 of their largest weight times their largest value factor, times codes up to 448."""
+    B, Hq, S_q, d = Q.shape
+    Hkv = vals.shape[1]
+    q = Q.double().cpu().view(B, Hkv, Hq // Hkv, S_q, d)
+    out = torch.zeros(q.shape[:-1], dtype=torch.float64)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        K, _ = dense(vals, table, page, b, n)
+        j = torch.arange(n)
+        f = factors[table[b].long()[j // page], :, 1, j % page].transpose(0, 1)  # [Hkv, n]
+        for i in range(S_q):
+            hi = n - S_q + i + 1
+            if hi <= 0:
+                continue
+            p = torch.softmax(torch.einsum("hgd,hjd->hgj", q[b, :, :, i], K[:, :hi]) * scale, -1)
+            for t in range(0, n, 128):
+                if t < hi:
+                    out[b, :, :, i] += 128 * 448 * 2.0 ** -22 * p[:, :, t:t + 128].amax(-1) * f[:, t:t + 128].amax(-1)[:, None]
+    return out.view(B, Hq, S_q)
+
+
+def check_decode(O, LSE, ref, d, more=None):
     """Elementwise bounds.  Scores: a float32 sum of d products, off by d 2^-24 of their absolute sum at most; exp2's
     argument and result a few 2^-23 of |score| log2 e and of itself, and the weights' float32 sum (errors of the same
     kind, in the mean) under 2^-19; so a weight is off by r = E (d + 8) 2^-23 + 2^-19 relative.  Weights are rounded
@@ -149,6 +176,8 @@ def check_decode(O, LSE, ref, d):
     assert bool((O[~seen] == 0).all())
     assert bool(torch.isfinite(O).all()) and bool(torch.isfinite(LSE[seen]).all())
     bound = O_ref.abs() * 2.0 ** -8 + A * (2.0 ** -8 + 2 * r[..., None]) * (1 + 2.0 ** -7)
+    if more is not None:
+        bound = bound + more[..., None]
     bad = (O - O_ref).abs() - bound
     assert float(bad.max()) <= 0, f"O off by {float((O - O_ref).abs().max()):.3e}, {float(bad.max()):.3e} past its bound"
     off = (LSE - L_ref)[seen].abs() - (r[seen] + L_ref[seen].abs() * 2.0 ** -22)

@@ -100,6 +100,85 @@ def test_long_sequence():
     _decode([20000], 8, 1, 1, 128, 128, "e4m3")
 
 
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [32, 80, 96, 128, 256, 1024])
+def test_page_sizes(store, page):
+    """Boxes of 16 to 128 positions, pages inside a tile, of a tile and of many."""
+    _decode([1, 300, 1500], 8, 2, 1, 128, page, store)
+    _decode([77, 513], 4, 2, 3, 64, page, store, WINDOW, 200)
+
+
+@pytest.mark.parametrize("rows", [4, 16, 32, 64])
+def test_spread_value_factors_and_a_dominant_key(rows):
+    """Value rows of very different sizes, and one key that takes most of the weight: the small weights behind it must
+    not be lost (both rounding terms of the E4M3 weights)."""
+    lens, page, d = [1700, 257], 64, 128
+    pages, scales, table, n = pu.make_pool(lens, 1, page, d, "e4m3", seed=9, v_spread=2.0)
+    factors = torch.exp2(scales.transpose(2, 3).reshape(n, 1, 2, page).double() - 127)
+    factors[scales.transpose(2, 3).reshape(n, 1, 2, page) == 255] = 0
+    g = torch.Generator().manual_seed(3)
+    Q = torch.randn((2, rows, 1, d), generator=g).to(torch.bfloat16)
+    vals = pu.values(pages, scales)
+    for b in range(2):  # position 5 of each sequence: a key along the first query
+        k = (Q[b, 0, 0].float() * 0.9)[None]
+        codes, e = pu.quantise(k)
+        p = int(table[b, 0])
+        pages.view(torch.uint8)[p, :, 0, 5] = codes
+        scales[p, :, 0, 0, 5] = e
+    vals = pu.values(pages, scales)
+    cache = tsa.PagedCache(n, 1, page, d, dtype="e4m3", pages=pages.cuda(), scales=scales.cuda())
+    O, LSE = tsa.PagedDecodeAttention(2, rows, 1, 1, d)(Q.cuda(), cache, table.cuda(),
+                                                        torch.tensor(lens, dtype=torch.int32).cuda())
+    scale = 1 / math.sqrt(d)
+    more = pu.coarse_weights(Q, vals, factors, table, page, lens, scale)
+    pu.check_decode(O, LSE, pu.decode(Q, vals, table, page, lens, scale, CAUSAL, 0), d, more)
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_a_query_that_is_not_finite_stays_in_its_row(store, bad):
+    lens = [300, 20]
+    cache, vals, table = _cache(lens, 2, 16, 64, store, seed=2)
+    Q = torch.randn((2, 6, 2, 64), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    plan = tsa.PagedDecodeAttention(2, 6, 2, 2, 64)
+    tab, ln = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    want = plan(Q.cuda(), cache, tab, ln)
+    Q[0, 4, 1, 7] = bad
+    O, LSE = plan(Q.cuda(), cache, tab, ln)
+    keep = torch.ones((2, 6, 2), dtype=torch.bool)
+    keep[0, 4, 1] = False
+    assert torch.equal(O.cpu()[keep], want[0].cpu()[keep]) and torch.equal(LSE.cpu()[keep], want[1].cpu()[keep])
+    assert not bool(torch.isfinite(O[0, 4, 1].float()).any())
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_offsets_beyond_32_bits(store):
+    """A pool of more than 4 GiB whose sequence sits at its end."""
+    d, Hkv, page = 128, 4, 64
+    row = 2 * d if store == "bf16" else d
+    n = (4 << 30) // (Hkv * 2 * page * row) + 50
+    cache = tsa.PagedCache(n, Hkv, page, d, dtype=store)
+    assert cache.pages.numel() * cache.pages.element_size() > 2 ** 32
+    lens = [100, 90]
+    table = torch.tensor([[n - 1, n - 4], [n - 2, 1]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(1)
+    K, V = (torch.randn((2, Hkv, 100, d), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    tab, ln = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    cache.write(K, V, tab, ln, new_len=ln)
+    Kd, Vd = cache.read(tab, ln, length=100)
+    if store == "bf16":
+        assert torch.equal(Kd[0], K[0]) and torch.equal(Vd[1, :, :90], V[1, :, :90])
+    used = sorted(set(table.flatten().tolist()))
+    small = {p: i for i, p in enumerate(used)}
+    pages = cache.pages.view(torch.uint8)[used].cpu().view(cache.pages.dtype)
+    vals = pu.values(pages, None if cache.scales is None else cache.scales[used])
+    local = torch.tensor([[small[int(p)] for p in r] for r in table], dtype=torch.int32)
+    Q = torch.randn((2, 8, 1, d), generator=g).to(torch.bfloat16).cuda()
+    O, LSE = tsa.PagedDecodeAttention(2, 8, Hkv, 1, d)(Q, cache, tab, ln)
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+    pu.check_decode(O, LSE, pu.decode(Q, vals, local, page, lens, 1 / math.sqrt(d), CAUSAL, 0), d)
+
+
 def test_every_code_is_read_exactly():
     """One position, so O is its value row and each of the 256 codes and many exponents come through to bf16."""
     d = 128
@@ -365,6 +444,22 @@ def test_negative_length_is_reported_by_the_decode():
         torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda"), cache,
         torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([-1], dtype=torch.int32).cuda())
     assert cache.poll_device_error() == (tsa.ATTN_ERR_INVALID_ARG, tsa.CACHE_ERR_POSITION)
+
+
+def test_expanded_inputs_and_dimensions_of_one():
+    """Broadcast inputs are read as they are; the strides of dimensions of one do not matter."""
+    cache = tsa.PagedCache(3, 2, 16, 64)
+    K = torch.randn((1, 1, 4, 64), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    tab = torch.tensor([[0], [1]], dtype=torch.int32).cuda()
+    ln = torch.full((2,), 4, dtype=torch.int32, device="cuda")
+    cache.write(K.expand(2, 2, 4, 64), K.expand(2, 2, 4, 64), tab, ln)
+    Kd, Vd = cache.read(tab, ln, length=4)
+    assert torch.equal(Kd, K.expand(2, 2, 4, 64)) and torch.equal(Vd, Kd)
+    odd = torch.as_strided(K[0, 0, :1].clone(), (1, 1, 1, 64), (3, 5, 7, 1))
+    cache.write(odd.expand(2, 2, 1, 64), odd.expand(2, 2, 1, 64), tab, ln)
+    assert torch.equal(cache.read(tab, ln, first=3, length=1)[0], odd.expand(2, 2, 1, 64))
+    with pytest.raises(ValueError):
+        cache.read(tab, ln, K=Kd[:, :1].expand(2, 2, 4, 64), V=Vd)
 
 
 def test_refusals():

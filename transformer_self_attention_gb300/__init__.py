@@ -549,14 +549,24 @@ def _need_torch():
     return torch
 
 
-def _rows(name, t, shape, dtype, device):
+def _rows(name, t, shape, dtype, device, out=False):
     """attn_rows of a tensor view [B, H, S, d] (shape: a tuple) whose last dimension is contiguous, on CUDA device
-    number `device`."""
+    number `device`; out: it is written, so its rows must not be one another."""
     if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{device}")
     sb, sh, ss, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    B, H, S, _ = shape
+    # the stride of a dimension of one may be anything
+    if B == 1:
+        sb = 0
+    if H == 1:
+        sh = 0
+    if S == 1:
+        ss = 0
+    if out and ((B > 1 and not sb) or (H > 1 and not sh) or (S > 1 and not ss)):
+        raise ValueError(f"{name} is written and must not be an expanded tensor")
     return attn_rows(t.data_ptr(), sb, sh, ss)
 
 
@@ -647,7 +657,7 @@ class RotaryPositions:
             Q_out = torch.empty(shape, dtype=dtype, device=Q.device)
             qo = _new_rows(Q_out, Hq, S, d)
         else:
-            qo = _rows("Q_out", Q_out, shape, dtype, device)
+            qo = _rows("Q_out", Q_out, shape, dtype, device, True)
         Hk, k, ko = 0, None, None
         if K is not None:
             if K.dim() != 4 or K.shape[1] < 1:
@@ -659,7 +669,7 @@ class RotaryPositions:
                 K_out = torch.empty(shape, dtype=dtype, device=Q.device)
                 ko = _new_rows(K_out, Hk, S, d)
             else:
-                ko = _rows("K_out", K_out, shape, dtype, device)
+                ko = _rows("K_out", K_out, shape, dtype, device, True)
         pos, pb, ps = None, 0, 0
         if positions is not None:
             if positions.dtype is not torch.int32 or positions.get_device() != device \
@@ -765,7 +775,7 @@ class PagedCache:
                 Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
                 qo = _new_rows(Q_out, Hq, S, d)
             else:
-                qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device)
+                qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device, True)
         new = None if new_len is None else _int32("new_len", new_len, (B,), device)
         if B:
             st = _call(device, stream, _lib.attn_cache_write,
@@ -791,8 +801,8 @@ class PagedCache:
                     K = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
                 if V is None:
                     V = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-        k = _rows("K", K, shape, torch.bfloat16, self._device)
-        v = _rows("V", V, shape, torch.bfloat16, self._device)
+        k = _rows("K", K, shape, torch.bfloat16, self._device, True)
+        v = _rows("V", V, shape, torch.bfloat16, self._device, True)
         if B:
             st = _call(self._device, stream, _lib.attn_cache_read, (self.handle, B, int(length), int(first), k, v, *table),
                        (K, V, page_table, cache_len, self.pages, self.scales))

@@ -403,8 +403,14 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
     if (S_q < 1 || (dtype != ATTN_BF16 && dtype != ATTN_FP8_E4M3) || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
     const int w = kind == ATTN_MASK_CAUSAL_SLIDING ? window : -1;
     const attn::PagedShape shape = attn::paged_shape(d, dtype == ATTN_FP8_E4M3);
-    std::vector<unsigned> cost(B + 1, 0);
-    std::vector<int> n(B);
+    std::vector<unsigned> cost;
+    std::vector<int> n;
+    try {
+        cost.assign(B + 1, 0);
+        n.assign(B, 0);
+    } catch (...) {
+        return ATTN_ERR_OOM;
+    }
     unsigned units = 0;
     for (int b = 0; b < B; ++b) {
         int lo, hi;
