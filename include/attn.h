@@ -695,10 +695,10 @@ attn_status attn_cache_destroy(attn_cache_handle h);
  * positions no row's window reaches, are never used, whatever they hold.  With S_q > 1, an infinity or a NaN
  * in a position that only some rows of a sequence see may reach the other rows of the same kv head.
  *
- * Rounding: scores, sums and outputs are float32 until O is rounded.  Weights are rounded to eight significant bits for
- * the second product (over E4M3 pages also to 2^-22 of the largest weight times the largest value factor among 128
- * positions); their sums, and LSE, are not.  Over E4M3 pages queries enter with all their bits, down to 2^-22 of a row's
- * largest element.
+ * Rounding: scores, sums and outputs are float32 until O is rounded.  Weights are rounded to 16 significant bits
+ * for the second product over bf16 pages (to eight with more than 32 rows to a kv head), to eight over E4M3 pages (and
+ * there to 2^-22 of the largest weight times the largest value factor among 128 positions); their sums, and LSE, are not.
+ * Over E4M3 pages queries enter with all their bits, down to 2^-22 of a row's largest element.
  *
  * A handle owns the partial results of sequences that are split over the grid; it must not be used by
  * two calls in flight at once, captured graphs included.  Distinct handles are independent.
@@ -730,7 +730,8 @@ attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas);
 attn_status attn_paged_destroy(attn_paged_handle h);
 
 /*
- * attn_paged_split_host -- how attn_paged_forward cuts its work over a grid of CTAs, on the host only.
+ * attn_paged_split_host -- how attn_paged_forward cuts its work over a grid of CTAs, on the host only.  (Over E4M3
+ * pages with more than 32 rows to a kv head it takes each head's rows in two blocks: twice Hkv units a sequence.)
  * Each part is 8 ints: CTA, sequence, kv head, first key block, one past the last, key blocks of the unit,
  * first and last CTA that hold blocks of the unit.  parts may be NULL with cap = 0 to query *n_parts.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_OOM.

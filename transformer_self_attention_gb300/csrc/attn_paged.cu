@@ -17,8 +17,10 @@
 // arrive instead, 19 parts of 32 rows took 15 of a call's 44 us.)
 //
 // The products are m16n8k16 with fp32 accumulation: at the measured copy bandwidth an SM takes in 24 bytes a clock, 12
-// elements, 188 multiply-adds at 16 rows of the 1024 these products do a clock.  P is rounded to bf16 for the second
-// product (2^-8 of a weight at most); its sum is taken before.
+// elements, 188 multiply-adds at 16 rows of the 1024 these products do a clock.  Up to 32 rows a weight enters the
+// second product as the sum of two bf16 numbers (2^-16 of it at most is lost; 1.5% of the time at 8 rows, 141 us for 904
+// MB), above that, where these products are the limit, as one (2^-8; two would take 143 us for 452 MB at 64 rows
+// against 113).  The weights' sum is taken before.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -124,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     fence_barrier_init();
     wait_for_kernel_before();
     int busy;
-    const unsigned W = paged_prefix<C::kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * Hkv;
-    const PagedCuts cuts(W, busy * Hkv, gridDim.x, shape);
+    const unsigned W = paged_prefix<C::kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.units;
+    const PagedCuts cuts(W, busy * p.units, gridDim.x, shape);
     // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
@@ -358,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
             }
             const float base[2] = {m[0] == ninf ? 0.f : m[0], m[1] == ninf ? 0.f : m[1]};
             {
-                uint32_t pf[C::kBoxes][4];
+                constexpr bool kTwoParts = RW <= 2;
+                uint32_t pf[C::kBoxes][4], pl[C::kBoxes][4];
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
@@ -366,8 +369,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
                         s[j][i] = ex2(s[j][i] - base[i >> 1]);
                         l[i >> 1] += s[j][i];
                     }
-                    pf[j / 2][2 * (j % 2)] = pack_bf16x2(s[j][0], s[j][1]);
-                    pf[j / 2][2 * (j % 2) + 1] = pack_bf16x2(s[j][2], s[j][3]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t h = pack_bf16x2(s[j][2 * r], s[j][2 * r + 1]);
+                        pf[j / 2][2 * (j % 2) + r] = h;
+                        if (kTwoParts)
+                            pl[j / 2][2 * (j % 2) + r] = pack_bf16x2(s[j][2 * r] - __uint_as_float(h << 16),
+                                                                     s[j][2 * r + 1] - __uint_as_float(h & 0xFFFF0000u));
+                    }
                 }
 #pragma unroll
                 for (int bx = 0; bx < C::kBoxes; ++bx) {
@@ -379,6 +388,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
                                      (chunk ^ (row & 7)) * 16);
                         mma_bf16(acc[2 * c2], pf[bx], r[0], r[1]);
                         mma_bf16(acc[2 * c2 + 1], pf[bx], r[2], r[3]);
+                        if (kTwoParts) {
+                            mma_bf16(acc[2 * c2], pl[bx], r[0], r[1]);
+                            mma_bf16(acc[2 * c2 + 1], pl[bx], r[2], r[3]);
+                        }
                     }
                 }
             }
@@ -484,8 +497,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     const int row = blockIdx.y * kMergeWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
     const int k0 = blockIdx.x;
     const int2 cut = __ldcg(&p.cut[k0]);
-    if (cut.x < 0 || row >= p.rows) return;
-    const int unit = cut.x, k1 = cut.y;
+    if (cut.x < 0) return;
+    const int blocks = p.units / p.Hkv, head = cut.x / blocks, row_block = cut.x - head * blocks, k1 = cut.y;
+    const int out_row = row_block * rows_pad + row;
+    if (row >= rows_pad || out_row >= p.rows) return;
+    const long long out = (long long)head * p.rows + out_row;
     const float ninf = __int_as_float(0xFF800000);
     auto at = [&](int k) { return (long long)(2 * k + (k == k0)) * rows_pad + row; };
     float M, L = 0.f;
@@ -535,11 +551,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.o) + ((long long)unit * p.rows + row) * D) +
-                  lane * (D / 64);
+    uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.o) + out * D) + lane * (D / 64);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) o[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    if (p.lse && lane == 0) p.lse[(long long)unit * p.rows + row] = (M + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && lane == 0) p.lse[out] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 template <int D, int RW>
@@ -562,7 +577,10 @@ cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-int paged_rows_pad(int rows, bool e4m3) { return e4m3 && rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int paged_rows_pad(int rows, bool e4m3) {
+    return e4m3 && rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || e4m3 ? 32 : 64;
+}
+int paged_row_blocks(int rows, bool e4m3) { return e4m3 && rows > 32 ? 2 : 1; }
 int paged_ctas_per_sm(int rows, bool e4m3) { return !e4m3 || rows <= 16 ? 2 : 1; }
 
 cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t stream) {
@@ -570,7 +588,7 @@ cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t strea
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream) {
-    const dim3 blocks((unsigned)grid, (unsigned)((p.rows + kMergeWarps - 1) / kMergeWarps));
+    const dim3 blocks((unsigned)grid, (unsigned)((std::min(p.rows, rows_pad) + kMergeWarps - 1) / kMergeWarps));
     return p.c.d == 64 ? launch_dependent(paged_merge_kernel<64>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad)
                        : launch_dependent(paged_merge_kernel<128>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad);
 }

@@ -44,11 +44,11 @@ constexpr int kMostStages = 8;
 
 template <int RP>
 struct Shared {
-    static constexpr int kGroups = RP <= 8 ? 1 : 2, kThreads = 128 * kGroups + 64;
+    static constexpr int kGroups = RP / 8, kThreads = 128 * kGroups + 64;
     unsigned cost[kPagedMaxBatch + 4];
     unsigned long long full[kMostStages], empty[kMostStages], s_full[2], s_free[2], p_full, d_full, q_full;
     alignas(16) float top[2][4][RP];  // a tile's row maxima, by warp
-    alignas(16) float factor[2][2][4];  // and its largest value exponent, by group and warp
+    alignas(16) float factor[2][kGroups][4];  // and its largest value exponent, by group and warp
     float qs[RP];                     // what a row's product is multiplied by, 2^up * scale * log2 e
     float sum[4][RP];
     int last[RP], first[RP];          // the positions a row sees
@@ -62,7 +62,7 @@ struct Cfg {
     static constexpr int kN = 2 * RP;
     static constexpr int kCtas = RP <= 16 ? 2 : 1;
     static constexpr int kGroups = Shared<RP>::kGroups, kThreads = Shared<RP>::kThreads;
-    static constexpr int kRows = RP / kGroups;              // of a thread
+    static constexpr int kRows = 8;                         // of a thread
     static constexpr int kTile = kKeys * D;                 // bytes of a tile's keys, or values
     static constexpr int kStage = 2 * kTile;
     static constexpr int kScale = 2 * kKeys;                // its exponents
@@ -135,29 +135,17 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch&
     }
 }
 
-// R rows of the thread's tensor-memory lane: the hi column of row c + i, and its lo column RP further on.
-template <int RP, int R>
-__device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[R], float (&lo)[R]) {
-    if constexpr (R == 8) {
-        uint32_t a[8], b[8];
-        tmem_ld8(addr, a);
-        tmem_ld8(addr + RP, b);
-        tmem_wait_ld();
+// Eight rows of the thread's tensor-memory lane: the hi columns, and the lo columns RP further on.
+template <int RP>
+__device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[8], float (&lo)[8]) {
+    uint32_t a[8], b[8];
+    tmem_ld8(addr, a);
+    tmem_ld8(addr + RP, b);
+    tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            hi[i] = __uint_as_float(a[i]);
-            lo[i] = __uint_as_float(b[i]);
-        }
-    } else {
-        uint32_t a[16], b[16];
-        tmem_ld16(addr, a);
-        tmem_ld16(addr + RP, b);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            hi[i] = __uint_as_float(a[i]);
-            lo[i] = __uint_as_float(b[i]);
-        }
+    for (int i = 0; i < 8; ++i) {
+        hi[i] = __uint_as_float(a[i]);
+        lo[i] = __uint_as_float(b[i]);
     }
 }
 
@@ -167,7 +155,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
     constexpr PagedShape shape = paged_shape(D, true);
     static_assert(shape.keys == kKeys, "a tile is a key block");
     constexpr int N = C::kN, kStages = C::kStages, kThreads = C::kThreads, kLoader = 4 * C::kGroups;
-    constexpr int kRows = C::kRows, kChunk = kRows < 16 ? kRows : 16;
+    constexpr int kRows = C::kRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Shared<RP>& sh = *reinterpret_cast<Shared<RP>*>(smem + C::kOffShared);
@@ -199,8 +187,8 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
     fence_barrier_init();
     wait_for_kernel_before();
     int busy;
-    const unsigned W = paged_prefix<kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.Hkv;
-    const PagedCuts cuts(W, busy * p.Hkv, gridDim.x, shape);
+    const unsigned W = paged_prefix<kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.units;
+    const PagedCuts cuts(W, busy * p.units, gridDim.x, shape);
     // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
@@ -243,7 +231,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                     atomicOr(p.c.err, kCacheErrPage);
                     page = 0;
                 }
-                f.unit = page * p.Hkv + w.h;
+                f.unit = page * p.Hkv + w.h / (p.units / p.Hkv);
             }
             g += 4;
         };
@@ -324,24 +312,27 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
         __syncwarp();
     } else {
         // =================================================== weights and output
-        const float ninf = __int_as_float(0xFF800000);
+        const float ninf = __int_as_float(0xFF800000), kFar = -1e30f;
         const int group = warp / 4, gwarp = warp % 4, gtid = tid % 128;
-        const int row0 = group * kRows;  // of the group's rows
+        const int row0 = group * kRows;  // of the group's rows in the block
+        const int row_blocks = p.units / p.Hkv;
         const uint32_t t_lane = (uint32_t)(gwarp * 32) << 16;
         int n = 0;
         while (w.at < w.end) {
             paged_open<kKeys>(p, shape, sh.cost, w);
             if (w.g0 >= w.g1) continue;  // overhead alone (the same for every thread)
             const int len = w.len, seen = w.seen;
+            const int head = w.h / row_blocks, block0 = (w.h - head * row_blocks) * RP, rows = min(RP, p.rows - block0);
+            const long long out0 = ((long long)w.b * p.Hkv + head) * p.rows + block0;  // the block's first row of Q and O
             // ---- the queries' two parts; a warp per row, four elements a lane
             {
-                const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + ((long long)w.b * p.Hkv + w.h) * p.rows * D;
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + out0 * D;
                 uint2 v[kRows / 4];
 #pragma unroll
                 for (int i = 0; i < kRows / 4; ++i) {
                     const int row = row0 + gwarp + 4 * i;
                     v[i] = make_uint2(0, 0);
-                    if (row < p.rows && lane < D / 4) v[i] = *reinterpret_cast<const uint2*>(q + (long long)row * D + 4 * lane);
+                    if (row < rows && lane < D / 4) v[i] = *reinterpret_cast<const uint2*>(q + (long long)row * D + 4 * lane);
                 }
 #pragma unroll
                 for (int i = 0; i < kRows / 4; ++i) {
@@ -367,9 +358,9 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                         }
                     }
                     if (lane == 0) {
-                        const int t = len - p.S_q + row % p.S_q;
+                        const int t = len - p.S_q + (block0 + row) % p.S_q;
                         sh.qs[row] = p.scale_log2 * up;
-                        sh.last[row] = row >= p.rows ? -1 : p.causal ? t : len - 1;
+                        sh.last[row] = row >= rows ? -1 : p.causal ? t : len - 1;
                         sh.first[row] = p.window < 0 ? 0 : max(0, t - p.window);
                     }
                 }
@@ -385,20 +376,17 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 acc[r] = l[r] = back[r] = 0.f;
-                m[r] = ninf;
+                m[r] = kFar;  // below every score that counts, and finite: differences with it stay numbers
             }
             // D^T of the tile before is added to the output
             auto add_values = [&](int tile) {
                 wait(smem_u32(&sh.d_full), tile & 1, watch);
                 __syncwarp();
                 tc_fence_after();
+                float hi[kRows], lo[kRows];
+                load_parts<RP>(t_d + t_lane + row0, hi, lo);
 #pragma unroll
-                for (int c = 0; c < kRows; c += kChunk) {
-                    float hi[kChunk], lo[kChunk];
-                    load_parts<RP, kChunk>(t_d + t_lane + row0 + c, hi, lo);
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) acc[c + i] = fmaf(fmaf(lo[i], 0.0625f, hi[i]), back[c + i], acc[c + i]);
-                }
+                for (int r = 0; r < kRows; ++r) acc[r] = fmaf(fmaf(lo[r], 0.0625f, hi[r]), back[r], acc[r]);
             };
             for (int g = w.g0; g < w.g1; ++g, ++n) {
                 const int st = n % kStages;
@@ -413,12 +401,11 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                 const float kf = exponent_factor(ek);
                 const float kv = inside ? (float)((int)ev - 127) : -127.f;
                 float s[kRows];
+                {
+                    float hi[kRows], lo[kRows];
+                    load_parts<RP>(tmem + (n & 1) * N + t_lane + row0, hi, lo);
 #pragma unroll
-                for (int c = 0; c < kRows; c += kChunk) {
-                    float hi[kChunk], lo[kChunk];
-                    load_parts<RP, kChunk>(tmem + (n & 1) * N + t_lane + row0 + c, hi, lo);
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) s[c + i] = fmaf(lo[i], 0.0625f, hi[i]) * (kf * sh.qs[row0 + c + i]);
+                    for (int r = 0; r < kRows; ++r) s[r] = fmaf(lo[r], 0.0625f, hi[r]) * (kf * sh.qs[row0 + r]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -461,7 +448,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
                         const float to = fmaxf(m[r], top[r]);
-                        const float fix = m[r] == ninf ? 0.f : ex2(m[r] - to);
+                        const float fix = ex2(m[r] - to);
                         acc[r] *= fix;
                         l[r] *= fix;
                         m[r] = to;
@@ -475,34 +462,21 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = r0 + i;
-                        const float base = m[r] == ninf ? 0.f : m[r];
                         // the reference first: what is left is small, and adding the exponents loses nothing
-                        const float x = s[r] - base;
-                        const float ref = top[r] == ninf ? 0.f : top[r] - base + k_top;
+                        const float x = s[r] - m[r];
+                        const float ref = fmaxf(top[r] - m[r], kFar) + k_top;  // (no score at all: far down)
                         l[r] += ex2(x);
-                        back[r] = top[r] == ninf ? 0.f : ex2(ref);
+                        back[r] = ex2(ref);
                         y[i] = ex2(x + (kv - ref));
                     }
                     split_e4m3(y[0], y[1], y[2], y[3], hi[r0 / 4], lo[r0 / 4]);
                 }
                 // column c of position t: 16 columns side by side, then the positions, then the next 16 columns
-#pragma unroll
-                for (int c = 0; c < kRows; c += kRows < 16 ? 8 : 16) {
-                    const int ch = row0 + c, cl = RP + row0 + c;
-                    const uint32_t at_h = s_p + (ch / 16) * 16 * kKeys + 16 * gtid + ch % 16;
-                    const uint32_t at_l = s_p + (cl / 16) * 16 * kKeys + 16 * gtid + cl % 16;
-                    if constexpr (kRows < 16) {
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at_h), "r"(hi[0]), "r"(hi[1]) : "memory");
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at_l), "r"(lo[0]), "r"(lo[1]) : "memory");
-                    } else {
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at_h), "r"(hi[c / 4]),
-                                     "r"(hi[c / 4 + 1]), "r"(hi[c / 4 + 2]), "r"(hi[c / 4 + 3])
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at_l), "r"(lo[c / 4]),
-                                     "r"(lo[c / 4 + 1]), "r"(lo[c / 4 + 2]), "r"(lo[c / 4 + 3])
-                                     : "memory");
-                    }
-                }
+                const uint32_t at = s_p + 16 * gtid, ch = row0, cl = RP + row0;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (ch / 16) * 16 * kKeys + ch % 16), "r"(hi[0]), "r"(hi[1])
+                             : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (cl / 16) * 16 * kKeys + cl % 16), "r"(lo[0]), "r"(lo[1])
+                             : "memory");
                 if (!inside && group == 0) {
                     // positions past the length or before the window may hold anything: weight zero times a NaN is a
                     // NaN, so their values become zero
@@ -527,23 +501,22 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
             }
             named_bar_sync(1 + group, 128);
             const bool final = w.g0 == 0 && w.g1 == w.n;
-            const long long unit = (long long)w.b * p.Hkv + w.h;
             const long long slot = (2LL * blockIdx.x + (w.g0 > 0 ? 0 : 1)) * RP;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const int row = row0 + r;
-                if (row >= p.rows) break;
+                if (row >= rows) break;
                 const float L = (sh.sum[0][row] + sh.sum[1][row]) + (sh.sum[2][row] + sh.sum[3][row]);
                 if (gtid < D) {
                     if (final)
-                        reinterpret_cast<__nv_bfloat16*>(p.o)[(unit * p.rows + row) * D + gtid] =
+                        reinterpret_cast<__nv_bfloat16*>(p.o)[(out0 + row) * D + gtid] =
                             __float2bfloat16(L == 0.f ? 0.f : acc[r] * __frcp_rn(L));
                     else
                         __stcg(p.part_o + (slot + row) * D + gtid, acc[r]);
                 }
                 if (gtid == 0) {
                     if (!final) __stcg(&p.part_ml[slot + row], make_float2(m[r], L));
-                    else if (p.lse) p.lse[unit * p.rows + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
+                    else if (p.lse) p.lse[out0 + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
                 }
             }
             if (!final && w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w);
@@ -576,8 +549,7 @@ cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {
     switch (paged_rows_pad(p.rows, true)) {
         case 8: return launch_rp<D, 8>(p, grid, stream);
         case 16: return launch_rp<D, 16>(p, grid, stream);
-        case 32: return launch_rp<D, 32>(p, grid, stream);
-        default: return launch_rp<D, 64>(p, grid, stream);
+        default: return launch_rp<D, 32>(p, grid, stream);
     }
 }
 

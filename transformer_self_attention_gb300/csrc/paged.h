@@ -55,7 +55,8 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, c
 cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged decode
-// Work units are (sequence, kv head), in that order.  A unit of n key blocks costs max(n, least) + overhead: its start,
+// Work units are (sequence, kv head), in that order (over E4M3 pages with more than 32 rows to a head, (sequence, kv head,
+// half of the rows): the second half finds its keys and values in L2).  A unit of n key blocks costs max(n, least) + overhead: its start,
 // its merge and its output cost about as much as `overhead` blocks, and a unit of few blocks is not worth cutting
 // (joining its parts costs more than the other blocks' time), so that units up to `least` all cost the same and the cuts
 // fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals, equal but for
@@ -114,14 +115,16 @@ struct PagedParams {
     float2* part_ml;      // [2 * grid][rows_pad]: the rows' reference (base 2) and sum
     int2* cut;            // [grid]: the unit that begins in a CTA and ends in a later one, and that CTA; unit -1: none
     int B, Hq, Hkv, S_q, rows;
+    int units;            // of a sequence: Hkv, times 2 where a head's rows are taken in two blocks
     int window;           // -1: none
     int causal;           // 0: every row sees every cached position
     int box_rows;         // E4M3: positions of a TMA box, a divisor of the page size
     float scale_log2;
     long long watchdog_ns;
 };
-// Rows a slot of the partial results is padded to, and the CTAs of a full grid per multiprocessor.
+// Rows a slot of the partial results is padded to, the blocks that a kv head's rows are taken in, and the CTAs of a full grid per multiprocessor.
 int paged_rows_pad(int rows, bool e4m3);
+int paged_row_blocks(int rows, bool e4m3);
 int paged_ctas_per_sm(int rows, bool e4m3);
 constexpr int kPagedMostCtasPerSm = 2;
 cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t stream);

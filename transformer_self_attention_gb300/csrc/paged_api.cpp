@@ -356,9 +356,10 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
         return ATTN_ERR_INVALID_ARG;
     const attn::PagedShape shape = attn::paged_shape(h->d, cache->e4m3);
     const long long room = (long long)max_pages * cache->c.page;
+    const int units = h->Hkv * attn::paged_row_blocks(h->Hq / h->Hkv * h->S_q, cache->e4m3);
     const long long most = shape.least + shape.overhead + room / shape.keys + 1;  // a unit's cost
     // positions, and places on the cost line, fit an int
-    if (room > (1 << 30) || most * h->B * h->Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+    if (room > (1 << 30) || most * h->B * units > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
     attn::PagedParams p{};
     p.tm = cache->map;
     p.q = Q; p.o = O; p.lse = LSE;
@@ -366,6 +367,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     p.t.pages = page_table; p.t.len = cache_len; p.t.stride = table_stride; p.t.max_pages = max_pages;
     p.part_o = h->d_part; p.part_ml = h->d_ml; p.cut = h->d_cut;
     p.B = h->B; p.Hq = h->Hq; p.Hkv = h->Hkv; p.S_q = h->S_q; p.rows = h->Hq / h->Hkv * h->S_q;
+    p.units = units;
     p.window = h->window;
     p.causal = h->kind != ATTN_MASK_FULL;
     p.scale_log2 = (float)((double)h->scale * 1.4426950408889634);
@@ -375,7 +377,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     const int grid = std::min(h->n_sm * attn::paged_ctas_per_sm(p.rows, cache->e4m3), h->grid_limit);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cache->e4m3 ? attn::launch_paged_e4m3(p, grid, st) : attn::launch_paged_bf16(p, grid, st);
-    if (e == cudaSuccess && attn::paged_may_cut((long long)h->B * h->Hkv, room, grid, shape))
+    if (e == cudaSuccess && attn::paged_may_cut((long long)h->B * units, room, grid, shape))
         e = attn::launch_paged_merge(p, grid, rows_pad, st);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

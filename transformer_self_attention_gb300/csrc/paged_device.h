@@ -9,7 +9,7 @@ namespace attn {
 // Where a warp stands in its CTA's interval of the cost line.  A stretch is the CTA's part of one unit.
 struct Walk {
     unsigned at, end;  // cost positions
-    int b, h, n;       // current unit and its key blocks
+    int b, h, n;       // current unit (sequence, and kv head or half of its rows) and its key blocks
     int g0, g1;        // the stretch's blocks [g0, g1)
     int lo;            // first key block of the sequence
     int len, seen;     // its visible positions: [seen, len)
@@ -42,7 +42,7 @@ __device__ __forceinline__ int paged_blocks_of(const PagedParams& p, int n, int&
     return hi - lo;
 }
 
-// Prefix sums of the sequences' cost of one kv head, cost[0 .. B], by all THREADS of the CTA; scan: a word per warp.
+// Prefix sums of the sequences' cost of one unit each, cost[0 .. B], by all THREADS of the CTA; scan: a word per warp.
 // Returns the sum, and in `busy` the number of sequences with keys.
 template <int KEYS, int THREADS>
 __device__ __forceinline__ unsigned paged_prefix(const PagedParams& p, PagedShape shape, unsigned* cost, unsigned* scan,
@@ -101,7 +101,7 @@ __device__ __forceinline__ Walk paged_begin(const PagedParams& p, const PagedCut
     int lo = 0, hi = p.B - 1;  // the last b whose cost begins at or before w.at
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (cost[mid] * p.Hkv <= w.at) lo = mid;
+        if (cost[mid] * p.units <= w.at) lo = mid;
         else hi = mid - 1;
     }
     w.b = lo;
@@ -112,11 +112,11 @@ __device__ __forceinline__ Walk paged_begin(const PagedParams& p, const PagedCut
 // w.at moved behind it.
 template <int KEYS>
 __device__ __forceinline__ void paged_open(const PagedParams& p, PagedShape shape, const unsigned* cost, Walk& w) {
-    while (cost[w.b + 1] * p.Hkv <= w.at) ++w.b;
+    while (cost[w.b + 1] * p.units <= w.at) ++w.b;
     w.len = p.t.len[w.b];
     w.n = paged_blocks_of<KEYS>(p, w.len, w.lo);
     w.seen = p.window < 0 ? 0 : max(0, w.len - p.S_q - p.window);
-    const unsigned into = w.at - cost[w.b] * p.Hkv, per = paged_cost(w.n, shape);
+    const unsigned into = w.at - cost[w.b] * p.units, per = paged_cost(w.n, shape);
     w.h = (int)(into / per);
     const unsigned off = into - w.h * per, to = min(per, off + (w.end - w.at));
     w.g0 = min(w.n, max(0, (int)off - (int)shape.overhead));
@@ -127,8 +127,8 @@ __device__ __forceinline__ void paged_open(const PagedParams& p, PagedShape shap
 // Records where the last part of a unit is that begins in this CTA's stretch w and is cut (one thread).
 __device__ __forceinline__ void paged_record_cut(const PagedParams& p, const PagedCuts& cuts, PagedShape shape,
                                                  const unsigned* cost, const Walk& w) {
-    const unsigned u0 = cost[w.b] * p.Hkv + w.h * paged_cost(w.n, shape) + shape.overhead;
-    p.cut[blockIdx.x] = make_int2(w.b * p.Hkv + w.h, (int)cuts.owner(u0 + w.n - 1));
+    const unsigned u0 = cost[w.b] * p.units + w.h * paged_cost(w.n, shape) + shape.overhead;
+    p.cut[blockIdx.x] = make_int2(w.b * p.units + w.h, (int)cuts.owner(u0 + w.n - 1));
 }
 
 // Four floats of magnitude at most 448 as two E4M3 numbers each, x = hi + lo / 16: hi has four significant bits, the
