@@ -107,6 +107,20 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
+// Two floats of magnitude at most 2^8 as two E4M3 numbers each, x = hi + lo / 16, by way of fp16 (2^-11 of a number; what
+// follows is exact up to lo's own rounding).
+__device__ __forceinline__ void split2_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    asm("{\n\t.reg .b32 y, h, t;\n\t.reg .b16 e, f;\n\t"
+        "cvt.rn.f16x2.f32 y, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 e, y;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, e;\n\t"
+        "mul.rn.f16x2 y, y, %4;\n\t"
+        "fma.rn.f16x2 t, h, %5, y;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 f, t;\n\t"
+        "cvt.u32.u16 %0, e;\n\tcvt.u32.u16 %1, f;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(x0), "f"(x1), "r"(0x4C004C00u), "r"(0xCC00CC00u));  // 16 and -16, twice
+}
 __device__ __forceinline__ float warp_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
         __syncwarp();
     } else {
         // =================================================== weights and output
-        const float ninf = __int_as_float(0xFF800000), kFar = -1e30f;
+        const float ninf = __int_as_float(0xFF800000);
         const int group = warp / 4, gwarp = warp % 4, gtid = tid % 128;
         const int row0 = group * kRows;  // of the group's rows in the block
         const int row_blocks = p.units / p.Hkv;
@@ -376,8 +390,9 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 acc[r] = l[r] = back[r] = 0.f;
-                m[r] = kFar;  // below every score that counts, and finite: differences with it stay numbers
+                m[r] = 0.f;
             }
+            unsigned unset = 0xFF;  // bit r: row r has seen no key yet, and m[r] is no reference
             // D^T of the tile before is added to the output
             auto add_values = [&](int tile) {
                 wait(smem_u32(&sh.d_full), tile & 1, watch);
@@ -400,12 +415,14 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                 const uint32_t ek = lds_u8(sc), ev = lds_u8(sc + 16);
                 const float kf = exponent_factor(ek);
                 const float kv = inside ? (float)((int)ev - 127) : -127.f;
-                float s[kRows];
+                // scores in base 2, less the rows' references
+                float x[kRows];
                 {
                     float hi[kRows], lo[kRows];
                     load_parts<RP>(tmem + (n & 1) * N + t_lane + row0, hi, lo);
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) s[r] = fmaf(lo[r], 0.0625f, hi[r]) * (kf * sh.qs[row0 + r]);
+                    for (int r = 0; r < kRows; ++r)
+                        x[r] = fmaf(fmaf(lo[r], 0.0625f, hi[r]), kf * sh.qs[row0 + r], -m[r]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -413,69 +430,73 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                 if (first < all_from || first + kKeys > all_to) {
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
-                        if (!inside || pos > sh.last[row0 + r] || pos < sh.first[row0 + r]) s[r] = ninf;
+                        if (!inside || pos > sh.last[row0 + r] || pos < sh.first[row0 + r]) x[r] = ninf;
                 }
                 // ---- the tile's largest score of each row, and its largest value exponent
-                const float kv_top = warp_max(kv);
-                float mine = kv_top;
+                {
+                    float t[kRows];
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const float t = warp_max(s[r]);
-                    if (lane == r) mine = t;
+                    for (int r = 0; r < kRows; ++r) t[r] = warp_max(x[r]);
+                    const float kv_top = warp_max(kv);
+                    if (lane == 0) {
+                        float4* out = reinterpret_cast<float4*>(&sh.top[n & 1][gwarp][row0]);
+                        out[0] = make_float4(t[0], t[1], t[2], t[3]);
+                        out[1] = make_float4(t[4], t[5], t[6], t[7]);
+                        sh.factor[n & 1][group][gwarp] = kv_top;
+                    }
                 }
-                if (lane < kRows) sh.top[n & 1][gwarp][row0 + lane] = mine;
-                if (lane == 0) sh.factor[n & 1][group][gwarp] = kv_top;
                 named_bar_sync(1 + group, 128);
                 if (g > w.g0) add_values(n - 1);
                 const float4 k4 = *reinterpret_cast<const float4*>(&sh.factor[n & 1][group][0]);
                 const float k_top = fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w)) - 8.f;
-                float top[kRows];
-                bool moves = false;  // the same in every thread of the group
-#pragma unroll
-                for (int r0 = 0; r0 < kRows; r0 += 4) {
-                    const float4 t0 = *reinterpret_cast<const float4*>(&sh.top[n & 1][0][row0 + r0]);
-                    const float4 t1 = *reinterpret_cast<const float4*>(&sh.top[n & 1][1][row0 + r0]);
-                    const float4 t2 = *reinterpret_cast<const float4*>(&sh.top[n & 1][2][row0 + r0]);
-                    const float4 t3 = *reinterpret_cast<const float4*>(&sh.top[n & 1][3][row0 + r0]);
-                    top[r0] = fmaxf(fmaxf(t0.x, t1.x), fmaxf(t2.x, t3.x));
-                    top[r0 + 1] = fmaxf(fmaxf(t0.y, t1.y), fmaxf(t2.y, t3.y));
-                    top[r0 + 2] = fmaxf(fmaxf(t0.z, t1.z), fmaxf(t2.z, t3.z));
-                    top[r0 + 3] = fmaxf(fmaxf(t0.w, t1.w), fmaxf(t2.w, t3.w));
-#pragma unroll
-                    for (int i = r0; i < r0 + 4; ++i) moves |= top[i] > m[i] + 16.f;
+                // what is the same for all positions is worked out once a warp, by lane r for row r, and handed round
+                float top;
+                {
+                    const int r = row0 + lane % kRows;
+                    top = fmaxf(fmaxf(sh.top[n & 1][0][r], sh.top[n & 1][1][r]),
+                                fmaxf(sh.top[n & 1][2][r], sh.top[n & 1][3][r]));
                 }
-                if (moves) {
+                // the reference moves when a score passes it by 2^16, and to a row's first score
+                const bool fresh = unset >> (lane % kRows) & 1;
+                const unsigned moved = __ballot_sync(0xFFFFFFFFu, fresh ? top > ninf : top > 16.f) & 0xFF;
+                if (moved) {
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        const float to = fmaxf(m[r], top[r]);
-                        const float fix = ex2(m[r] - to);
+                        const float by = __shfl_sync(0xFFFFFFFFu, top, r);
+                        if (!(moved >> r & 1)) continue;
+                        const float fix = unset >> r & 1 ? 0.f : ex2(-by);
+                        m[r] += by;
+                        x[r] -= by;
                         acc[r] *= fix;
                         l[r] *= fix;
-                        m[r] = to;
                     }
+                    if (moved >> (lane % kRows) & 1) top = 0.f;
+                    unset &= ~moved;
                 }
-                // ---- weights, scaled to at most 2^8
-                uint32_t hi[kRows / 4], lo[kRows / 4];
+                // weights of a tile 2^-100 below the reference count as zeros
+                const bool far = !(top > -100.f);
+                const float up_l = far ? 0.f : ex2(-top), back_l = far ? 0.f : ex2(top + k_top);
+                const float kvf = ex2(kv - k_top);
+                uint32_t hi[kRows / 2], lo[kRows / 2];
 #pragma unroll
-                for (int r0 = 0; r0 < kRows; r0 += 4) {
-                    float y[4];
+                for (int r = 0; r < kRows; r += 2) {
+                    float y[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + i;
-                        // the reference first: what is left is small, and adding the exponents loses nothing
-                        const float x = s[r] - m[r];
-                        const float ref = fmaxf(top[r] - m[r], kFar) + k_top;  // (no score at all: far down)
-                        l[r] += ex2(x);
-                        back[r] = ex2(ref);
-                        y[i] = ex2(x + (kv - ref));
+                    for (int i = 0; i < 2; ++i) {
+                        const float e = ex2(x[r + i]);
+                        l[r + i] += e;
+                        y[i] = e * __shfl_sync(0xFFFFFFFFu, up_l, r + i) * kvf;
+                        back[r + i] = __shfl_sync(0xFFFFFFFFu, back_l, r + i);
                     }
-                    split_e4m3(y[0], y[1], y[2], y[3], hi[r0 / 4], lo[r0 / 4]);
+                    split2_e4m3(y[0], y[1], hi[r / 2], lo[r / 2]);
                 }
                 // column c of position t: 16 columns side by side, then the positions, then the next 16 columns
                 const uint32_t at = s_p + 16 * gtid, ch = row0, cl = RP + row0;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (ch / 16) * 16 * kKeys + ch % 16), "r"(hi[0]), "r"(hi[1])
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (ch / 16) * 16 * kKeys + ch % 16),
+                             "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16)
                              : "memory");
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (cl / 16) * 16 * kKeys + cl % 16), "r"(lo[0]), "r"(lo[1])
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + (cl / 16) * 16 * kKeys + cl % 16),
+                             "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16)
                              : "memory");
                 if (!inside && group == 0) {
                     // positions past the length or before the window may hold anything: weight zero times a NaN is a
@@ -515,7 +536,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                         __stcg(p.part_o + (slot + row) * D + gtid, acc[r]);
                 }
                 if (gtid == 0) {
-                    if (!final) __stcg(&p.part_ml[slot + row], make_float2(m[r], L));
+                    if (!final) __stcg(&p.part_ml[slot + row], make_float2(unset >> r & 1 ? ninf : m[r], L));
                     else if (p.lse) p.lse[out0 + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
                 }
             }
