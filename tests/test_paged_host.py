@@ -98,7 +98,7 @@ def test_split_refuses_a_cost_line_beyond_31_bits():
 
 def test_short_units_are_not_cut():
     """As many CTAs as units, one whole unit each, while the grid is large enough."""
-    for lens in ([100], [1, 384, 17, 0, 90]):
+    for lens in ([100], [1, 256, 17, 0, 90]):
         n_cta, parts = tsa.attn_paged_split_host(len(lens), 8, 1, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, lens, 304)
         assert n_cta == len(parts) == 8 * sum(n > 0 for n in lens)
         assert all(p[3] == 0 and p[4] == p[5] for p in parts.tolist())

@@ -63,13 +63,15 @@ cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t 
 // one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost positions its
 // interval covers.
 // Measured, bf16 (blocks of 8 KB): overheads of 6, 10, 16 and 24 blocks give 33.0, 31.8, 29.5 and 29.0 us for 16 ragged
-// multi-query sequences of up to 16K positions and 170, 171, 167.5 and 169 us for 256 of up to 2K.
+// multi-query sequences of up to 16K positions and 170, 171, 167.5 and 169 us for 256 of up to 2K; least of 8, 12, 16 and
+// 24 give 9.3, 9.7, 5.8 and 5.8 us for one sequence of 256 positions and 10.8, 11.0, 11.1 and 12.4 for one of 4K.  E4M3
+// (tiles of 32 KB): least of 1, 2, 3 and 4 give 9.6, 6.8, 6.9 and 6.9 us, and 11.7, 12.9, 14.4 and 14.6.
 struct PagedShape {
     int keys;  // positions of a key block
     unsigned overhead, least;
 };
 __host__ __device__ constexpr PagedShape paged_shape(int d, bool e4m3) {
-    return e4m3 ? PagedShape{128, 3, 4} : PagedShape{d == 64 ? 32 : 16, 16, 24};
+    return e4m3 ? PagedShape{128, 3, 2} : PagedShape{d == 64 ? 32 : 16, 16, 16};
 }
 constexpr int kPagedMaxBatch = ATTN_DECODE_MAX_BATCH;
 
