@@ -136,17 +136,15 @@ struct Watch {
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch& w) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (n % 64 == 0) {
-            if (*w.abort) return false;
-            if ((long long)(globaltimer() - t0) > w.ns) {
-                *w.abort = 1;
-                atomicOr(w.err, kCacheErrWait);
-                return false;
-            }
+    while (!mbar_try_wait(bar, parity)) {
+        if (*w.abort) return false;
+        if ((long long)(globaltimer() - t0) > w.ns) {
+            *w.abort = 1;
+            atomicOr(w.err, kCacheErrWait);
+            return false;
         }
     }
+    return true;
 }
 
 // Eight rows of the thread's tensor-memory lane: the hi columns, and the lo columns RP further on.
