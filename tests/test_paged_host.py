@@ -96,6 +96,34 @@ def test_split_refuses_a_cost_line_beyond_31_bits():
     assert e.value.status == tsa.ATTN_ERR_UNSUPPORTED
 
 
+def test_split_of_the_widest_windows_and_lengths():
+    """Differences of positions stay within 32 bits: the widest window sees everything, also in front of position 0."""
+    for S_q in (1, 64):
+        n_cta, parts = tsa.attn_paged_split_host(2, 1, S_q, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL_SLIDING, 2 ** 31 - 1,
+                                                 [1, 100], 304)
+        assert parts[:, 5].tolist() == [1, 7] and parts[:, 3].tolist() == [0, 0]
+    n_cta, parts = tsa.attn_paged_split_host(1, 1, 1, 128, tsa.ATTN_FP8_E4M3, tsa.MASK_CAUSAL, 0, [1 << 30], 304)
+    assert n_cta == 304 and int(parts[:, 4].max()) == 1 << 23
+    for lens, status in (([(1 << 30) + 1], tsa.ATTN_ERR_UNSUPPORTED), ([-1], tsa.ATTN_ERR_INVALID_ARG)):
+        with pytest.raises(tsa.AttnError) as e:
+            tsa.attn_paged_split_host(1, 1, 1, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, lens, 304)
+        assert e.value.status == status
+    with pytest.raises(tsa.AttnError) as e:
+        tsa.attn_paged_split_host(1, 1, 65, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, [1], 304)
+    assert e.value.status == tsa.ATTN_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):  # fewer lengths than sequences
+        tsa.attn_paged_split_host(3, 1, 1, 128, tsa.ATTN_BF16, tsa.MASK_CAUSAL, 0, [1], 304)
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    for call in (lambda: tsa.RotaryPositions(64, rotary_dim=(1 << 32) + 32),
+                 lambda: tsa.attn_rope_create(64, 64, scaling=3, factor=2.0, original_len=1 << 32),
+                 lambda: tsa.attn_paged_create(1, 1, 1, 1, 64, 1.0, tsa.MASK_CAUSAL_SLIDING, 1 << 32),
+                 lambda: tsa.attn_cache_create(1, 1, (1 << 32) + 16, 64, tsa.ATTN_BF16, 16)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_short_units_are_not_cut():
     """As many CTAs as units, one whole unit each, while the grid is large enough."""
     for lens in ([100], [1, 256, 17, 0, 90]):

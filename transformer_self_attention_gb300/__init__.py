@@ -423,12 +423,20 @@ class DecodeAttention:
 
 # ---------------------------------------------------------------- rotary positions, paged cache, paged decode
 
+def _int(x) -> int:
+    """An argument of C type int, which ctypes would cut to 32 bits without a word."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{x} does not fit a C int")
+    return x
+
+
 def attn_rope_create(d, rot, layout=0, base=10000.0, scaling=0, factor=1.0, original_len=0, beta_fast=32.0,
                      beta_slow=1.0, amplitude=0.0) -> int:
     """Returns a rope handle (int; host only); raises AttnError on a non-OK status."""
     h = ctypes.c_void_p()
-    st = _lib.attn_rope_create(ctypes.byref(h), int(d), int(rot), int(layout), float(base), int(scaling),
-                               float(factor), int(original_len), float(beta_fast), float(beta_slow),
+    st = _lib.attn_rope_create(ctypes.byref(h), _int(d), _int(rot), _int(layout), float(base), _int(scaling),
+                               float(factor), _int(original_len), float(beta_fast), float(beta_slow),
                                float(amplitude))
     if st != ATTN_OK:
         raise AttnError(st, "attn_rope_create")
@@ -466,7 +474,7 @@ def attn_rope_destroy(handle: int) -> int:
 def attn_cache_create(n_pages, Hkv, page, d, dtype, pages_ptr, scales_ptr=0) -> int:
     """Returns a cache handle (int) over the given device buffers; raises AttnError."""
     h = ctypes.c_void_p()
-    st = _lib.attn_cache_create(ctypes.byref(h), int(n_pages), int(Hkv), int(page), int(d), int(dtype),
+    st = _lib.attn_cache_create(ctypes.byref(h), _int(n_pages), _int(Hkv), _int(page), _int(d), _int(dtype),
                                 pages_ptr or None, scales_ptr or None)
     if st != ATTN_OK:
         raise AttnError(st, "attn_cache_create")
@@ -499,8 +507,8 @@ def attn_cache_destroy(handle: int) -> int:
 def attn_paged_create(B, Hq, Hkv, S_q, d, scale, kind, window=0) -> int:
     """Returns a paged decode handle (int); raises AttnError on a non-OK status."""
     h = ctypes.c_void_p()
-    st = _lib.attn_paged_create(ctypes.byref(h), int(B), int(Hq), int(Hkv), int(S_q), int(d), float(scale), int(kind),
-                                int(window))
+    st = _lib.attn_paged_create(ctypes.byref(h), _int(B), _int(Hq), _int(Hkv), _int(S_q), _int(d), float(scale),
+                                _int(kind), _int(window))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_create")
     return h.value
@@ -514,7 +522,7 @@ def attn_paged_forward(handle, cache, q_ptr, table_ptr, table_stride, max_pages,
 
 
 def attn_paged_set_grid_limit(handle: int, max_ctas: int) -> int:
-    return _lib.attn_paged_set_grid_limit(handle, int(max_ctas))
+    return _lib.attn_paged_set_grid_limit(handle, _int(max_ctas))
 
 
 def attn_paged_destroy(handle: int) -> int:
@@ -524,10 +532,12 @@ def attn_paged_destroy(handle: int) -> int:
 def attn_paged_split_host(B, Hkv, S_q, d, dtype, kind, window, cache_len, grid):
     """Host-only split of the paged decode: (n_cta, int32 [parts, 8]: CTA, sequence, kv head, first key block,
     one past the last, key blocks of the unit, first and last CTA of the unit).  Raises AttnError."""
-    lens, _ = _int_array(cache_len)
+    lens, n_lens = _int_array(cache_len)
+    if n_lens != B:
+        raise ValueError(f"cache_len must have {B} entries")
     n_cta, n = ctypes.c_int(0), ctypes.c_int(0)
-    args = (int(B), int(Hkv), int(S_q), int(d), int(dtype), int(kind), int(window),
-            ctypes.cast(lens, ctypes.c_void_p), int(grid))
+    args = (_int(B), _int(Hkv), _int(S_q), _int(d), _int(dtype), _int(kind), _int(window),
+            ctypes.cast(lens, ctypes.c_void_p), _int(grid))
     st = _lib.attn_paged_split_host(*args, ctypes.byref(n_cta), None, 0, ctypes.byref(n))
     parts = np.zeros((max(n.value, 1), 8), dtype=np.int32)
     if st == ATTN_OK:
@@ -649,8 +659,8 @@ class RotaryPositions:
     def _apply(self, fn, name, Q, K, positions, Q_out, K_out, stream):
         dtype, device, shape = Q.dtype, Q.get_device(), Q.shape
         if (dtype is not torch.bfloat16 and dtype is not torch.float32) or len(shape) != 4 or shape[3] != self.d \
-                or device < 0:
-            raise ValueError(f"Q must be a CUDA bfloat16 or float32 tensor [B, Hq, S, {self.d}]")
+                or shape[1] < 1 or device < 0:
+            raise ValueError(f"Q must be a CUDA bfloat16 or float32 tensor [B, Hq, S, {self.d}], Hq > 0")
         B, Hq, S, d = shape
         q = _rows("Q", Q, shape, dtype, device)
         if Q_out is None:
@@ -677,7 +687,7 @@ class RotaryPositions:
                 raise ValueError(f"positions must be an int32 tensor of shape {(B, S)} or {(S,)} on {Q.device}")
             pos = positions.data_ptr()
             pb, ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
-        if B * S * Hq:
+        if B * S:
             st = _call(device, stream, fn, (self.handle, ATTN_BF16 if dtype is torch.bfloat16 else ATTN_F32, B, S, Hq, q,
                                             qo, Hk, k, ko, pos, pb, ps), (Q, K, positions, Q_out, K_out))
             if st != ATTN_OK:
@@ -760,8 +770,8 @@ class PagedCache:
         shape = (B, Hkv, S, d)
         k = _rows("K", K, shape, torch.bfloat16, device)
         v = _rows("V", V, shape, torch.bfloat16, device)
-        if rope is not None and rope.d != d:
-            raise ValueError("rope is for another head width")
+        if rope is not None and (rope.d != d or not rope.handle):
+            raise ValueError("rope is for another head width, or closed")
         Hq, q, qo = 0, None, None
         if Q is not None:
             if rope is None:
@@ -804,8 +814,8 @@ class PagedCache:
         k = _rows("K", K, shape, torch.bfloat16, self._device, True)
         v = _rows("V", V, shape, torch.bfloat16, self._device, True)
         if B:
-            st = _call(self._device, stream, _lib.attn_cache_read, (self.handle, B, int(length), int(first), k, v, *table),
-                       (K, V, page_table, cache_len, self.pages, self.scales))
+            st = _call(self._device, stream, _lib.attn_cache_read,
+                       (self.handle, B, int(length), _int(first), k, v, *table), (K, V, page_table, cache_len, self.pages, self.scales))
             if st != ATTN_OK:
                 raise AttnError(st, "attn_cache_read")
         return K, V

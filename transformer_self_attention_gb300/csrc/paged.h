@@ -56,12 +56,12 @@ cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t 
 
 // ---------------------------------------------------------------- paged decode
 // Work units are (sequence, kv head), in that order (over E4M3 pages with more than 32 rows to a head, (sequence, kv head,
-// half of the rows): the second half finds its keys and values in L2).  A unit of n key blocks costs max(n, least) + overhead: its start,
-// its merge and its output cost about as much as `overhead` blocks, and a unit of few blocks is not worth cutting
-// (joining its parts costs more than the other blocks' time), so that units up to `least` all cost the same and the cuts
-// fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals, equal but for
-// one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost positions its
-// interval covers.
+// half of the rows): the second half finds its keys and values in L2).  A unit of n key blocks costs max(n, least) +
+// overhead: its start, its merge and its output cost about as much as `overhead` blocks, and a unit of few blocks is not
+// worth cutting (joining its parts costs more than the other blocks' time), so that units up to `least` all cost the same
+// and the cuts fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals, equal
+// but for one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost positions
+// its interval covers.
 // Measured, bf16 (blocks of 8 KB): overheads of 6, 10, 16 and 24 blocks give 33.0, 31.8, 29.5 and 29.0 us for 16 ragged
 // multi-query sequences of up to 16K positions and 170, 171, 167.5 and 169 us for 256 of up to 2K; least of 8, 12, 16 and
 // 24 give 9.3, 9.7, 5.8 and 5.8 us for one sequence of 256 positions and 10.8, 11.0, 11.1 and 12.4 for one of 4K.  E4M3
@@ -74,6 +74,7 @@ __host__ __device__ constexpr PagedShape paged_shape(int d, bool e4m3) {
     return e4m3 ? PagedShape{128, 3, 2} : PagedShape{d == 64 ? 32 : 16, 16, 16};
 }
 constexpr int kPagedMaxBatch = ATTN_DECODE_MAX_BATCH;
+constexpr int kPagedMostPositions = 1 << 30;  // of a sequence; windows are cut to it
 
 // Key blocks [lo, hi) of `keys` positions that some row of a sequence of length n can see.
 __host__ __device__ inline void paged_blocks(int n, int S_q, int window, int keys, int& lo, int& hi) {
@@ -124,7 +125,8 @@ struct PagedParams {
     float scale_log2;
     long long watchdog_ns;
 };
-// Rows a slot of the partial results is padded to, the blocks that a kv head's rows are taken in, and the CTAs of a full grid per multiprocessor.
+// Rows a slot of the partial results is padded to, the blocks that a kv head's rows are taken in, and the CTAs of a full
+// grid per multiprocessor.
 int paged_rows_pad(int rows, bool e4m3);
 int paged_row_blocks(int rows, bool e4m3);
 int paged_ctas_per_sm(int rows, bool e4m3);

@@ -145,6 +145,11 @@ attn_status validate_paged(int B, int Hq, int Hkv, int S_q, attn_mask_kind kind,
     return ATTN_OK;
 }
 
+// A window of 2^30 sees every position there can be; with more, a difference of positions would pass 32 bits.
+int window_of(attn_mask_kind kind, int window) {
+    return kind == ATTN_MASK_CAUSAL_SLIDING ? std::min(window, attn::kPagedMostPositions) : -1;
+}
+
 void free_paged(attn_paged_plan* h) {
     if (!h) return;
     if (h->d_part) cudaFree(h->d_part);
@@ -329,7 +334,7 @@ attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, in
     attn_paged_plan* h = new (std::nothrow) attn_paged_plan();
     if (!h) return ATTN_ERR_OOM;
     h->B = B; h->Hq = Hq; h->Hkv = Hkv; h->S_q = S_q; h->d = d; h->kind = kind; h->scale = scale;
-    h->window = kind == ATTN_MASK_CAUSAL_SLIDING ? window : -1;
+    h->window = window_of(kind, window);
     auto fail = [&](cudaError_t e) {
         free_paged(h);
         return e == cudaErrorMemoryAllocation ? ATTN_ERR_OOM : ATTN_ERR_CUDA;
@@ -359,7 +364,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     const int units = h->Hkv * attn::paged_row_blocks(h->Hq / h->Hkv * h->S_q, cache->e4m3);
     const long long most = shape.least + shape.overhead + room / shape.keys + 1;  // a unit's cost
     // positions, and places on the cost line, fit an int
-    if (room > (1 << 30) || most * h->B * units > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+    if (room > attn::kPagedMostPositions || most * h->B * units > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
     attn::PagedParams p{};
     p.tm = cache->map;
     p.q = Q; p.o = O; p.lse = LSE;
@@ -400,10 +405,10 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
                                   int* n_parts) {
     if (!cache_len || !n_cta || !n_parts || grid < 1 || (cap > 0 && !parts))
         return ATTN_ERR_INVALID_ARG;
-    const attn_status vs = validate_paged(B, Hkv, Hkv, 1, kind, window);
+    const attn_status vs = validate_paged(B, Hkv, Hkv, S_q, kind, window);
     if (vs != ATTN_OK) return vs;
-    if (S_q < 1 || (dtype != ATTN_BF16 && dtype != ATTN_FP8_E4M3) || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
-    const int w = kind == ATTN_MASK_CAUSAL_SLIDING ? window : -1;
+    if ((dtype != ATTN_BF16 && dtype != ATTN_FP8_E4M3) || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
+    const int w = window_of(kind, window);
     const attn::PagedShape shape = attn::paged_shape(d, dtype == ATTN_FP8_E4M3);
     std::vector<unsigned> cost;
     std::vector<int> n;
@@ -417,6 +422,7 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
     for (int b = 0; b < B; ++b) {
         int lo, hi;
         if (cache_len[b] < 0) return ATTN_ERR_INVALID_ARG;
+        if (cache_len[b] > attn::kPagedMostPositions) return ATTN_ERR_UNSUPPORTED;
         attn::paged_blocks(cache_len[b], S_q, w, shape.keys, lo, hi);
         n[b] = hi - lo;
         if (n[b]) units += Hkv;
