@@ -323,6 +323,21 @@ def test_written_rows_that_are_not_finite_read_back_as_nan():
     assert bool(torch.isfinite(Kd[0, 0, 0]).all()) and bool(torch.isfinite(Vd[0, 0, :2]).all())
 
 
+@pytest.mark.parametrize("rot", [0, 64])
+def test_a_bf16_cache_holds_infinities_as_they_are(rot):
+    """Keys that are not rotated, elements behind the rotated ones and values are copied bit by bit."""
+    cache = tsa.PagedCache(1, 2, 16, 128)
+    K = torch.randn((1, 2, 5, 128), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    K[0, 0, 2, 70], K[0, 1, 4, 127], K[0, 1, 0, 100] = math.inf, -math.inf, -0.0
+    V = K.flip(3).contiguous()
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([5], dtype=torch.int32).cuda()
+    cache.write(K.cuda(), V.cuda(), table, lens, rope=tsa.RotaryPositions(128, rot) if rot else None)
+    Kd, Vd = cache.read(table, lens, length=5)
+    assert torch.equal(Vd.cpu().view(torch.int16), V.view(torch.int16))
+    assert torch.equal(Kd.cpu()[..., rot:].contiguous().view(torch.int16), K[..., rot:].contiguous().view(torch.int16))
+    assert bool(torch.isfinite(Kd[..., :rot]).all())
+
+
 @pytest.mark.parametrize("power", [-130, -126, -100, 0, 100, 118])
 def test_row_sizes(power):
     """Rows from the smallest to the largest bf16 magnitudes, and the 448 border."""
@@ -394,6 +409,78 @@ def test_generation_steps_as_they_are_used(store):
     # each is within its rounding bounds of the exact result: two roundings of weights and of O each
     assert float((Od.float() - O[live].float()).abs().max()) <= 4 * 2.0 ** -8 * float(Vd.float().abs().max())
     assert float((Ld - LSE[live]).abs().max()) <= 1e-5
+
+
+def test_one_plan_over_both_cache_types_and_changing_lengths():
+    """What a call leaves in the plan's workspace (cut units, partial results) does not reach the next one."""
+    Hq, Hkv, d, page = 12, 2, 64, 32
+    plan = tsa.PagedDecodeAttention(3, Hq, Hkv, 2, d)
+    Q = torch.randn((3, Hq, 2, d), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    for i, (lens, grid) in enumerate((([3000, 9, 1200], 304), ([40, 40, 40], 304), ([0, 0, 0], 304), ([1, 5000, 0], 5),
+                                      ([2, 2, 700], 304))):
+        plan.set_grid_limit(grid)
+        for store in ("bf16", "e4m3"):
+            cache, vals, table = _cache(lens, Hkv, page, d, store, seed=20 + i)
+            O, LSE = plan(Q, cache, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+            pu.check_decode(O, LSE, pu.decode(Q, vals, table, page, lens, 1 / math.sqrt(d), CAUSAL, 0), d)
+            assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [(1 << 30) - 1, 1 << 30, 2 ** 31 - 1])
+def test_a_window_beyond_every_position(store, window):
+    """The widest windows see what no window does, also with lengths below the number of rows."""
+    lens = [0, 1, 2, 40, 700]
+    cache, vals, table = _cache(lens, 2, 16, 64, store, seed=5)
+    Q = torch.randn((5, 4, 4, 64), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    tab, ln = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    want = tsa.PagedDecodeAttention(5, 4, 2, 4, 64)(Q, cache, tab, ln)
+    got = tsa.PagedDecodeAttention(5, 4, 2, 4, 64, kind=WINDOW, window=window)(Q, cache, tab, ln)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_captured_behind_copies_and_another_stream(store):
+    """In a graph the decode stands behind a copy of its lengths and behind a write from a second stream, and two calls of
+    one plan stand behind one another; the replay sees what both left."""
+    lens = [900, 33]
+    cache, vals, table = _cache(lens, 2, 16, 128, store, seed=11)
+    new = torch.tensor(lens, dtype=torch.int32).cuda()
+    tab, ln = table.cuda(), torch.zeros(2, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(2)
+    Q = torch.randn((2, 2, 8, 1, 128), generator=g).to(torch.bfloat16).cuda()
+    K = torch.randn((2, 2, 1, 128), generator=g).to(torch.bfloat16).cuda()
+    plan = tsa.PagedDecodeAttention(2, 8, 2, 1, 128)
+    O, LSE = torch.empty_like(Q), torch.empty((2, 2, 8, 1), device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        ln.copy_(new)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            cache.write(K, K, tab, ln)
+        main.wait_stream(side)
+        for i in range(2):
+            plan(Q[i], cache, tab, ln, O=O[i], LSE=LSE[i])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for shorter in (0, 20):
+        new.sub_(shorter)
+        ln.zero_()
+        O.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        n = new.tolist()
+        vals = pu.values(cache.pages, cache.scales)
+        for i in range(2):
+            pu.check_decode(O[i], LSE[i], pu.decode(Q[i], vals, table, 16, n, 1 / math.sqrt(128), CAUSAL, 0), 128)
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
 
 
 def test_two_plans_on_two_streams():
@@ -484,6 +571,11 @@ def test_refusals():
            lambda: tsa.PagedDecodeAttention(2, 4, 2, 1, 96), lambda: tsa.PagedDecodeAttention(2, 4, 2, 0, 64),
            lambda: tsa.PagedDecodeAttention(2, 4, 2, 1, 64, kind=tsa.MASK_SLIDING),
            lambda: tsa.PagedDecodeAttention(2, 4, 2, 1, 64, kind=WINDOW, window=-1)]
+    closed = tsa.RotaryPositions(64)
+    closed.close()
+    bad += [lambda: cache.write(K, K, tab, ln, rope=closed), lambda: cache.read(tab, ln, first=1 << 32, length=3),
+            lambda: tsa.PagedDecodeAttention(2, 4, 2, 1, 64, kind=WINDOW, window=1 << 32),
+            lambda: tsa.PagedDecodeAttention((1 << 32) + 2, 4, 2, 1, 64)]
     for call in bad:
         with pytest.raises((ValueError, tsa.AttnError)):
             call()

@@ -120,6 +120,26 @@ def test_gradient_against_differences(layout):
             assert abs(float(lhs - rhs)) <= float(size) * 2.0 ** -18
 
 
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 64), ("half", 64, 26), ("interleaved", 128, 64),
+                                          ("interleaved", 64, 26)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_elements_that_are_not_finite_stay_in_their_pair(layout, d, rot, bad):
+    """One in a pair makes that pair not finite; one behind the rotated elements is copied, and touches nothing else."""
+    Q, K = _pair(1, 2, 1, 6, d, torch.bfloat16, packed=False, seed=9)
+    Q[0, 0, 2, rot + 1] = bad
+    Q[0, 1, 3, d - 2] = bad
+    Q[0, 1, 4, 2] = bad  # of the pair (2, 2 + rot / 2), or (2, 3)
+    rope = tsa.RotaryPositions(d, rot, layout=layout)
+    for got in (rope(Q, K)[0], rope.backward(Q, K)[0]):
+        odd = ~torch.isfinite(got)
+        want = torch.zeros_like(odd)
+        want[0, 0, 2, rot + 1] = want[0, 1, 3, d - 2] = True
+        want[0, 1, 4, 2] = want[0, 1, 4, 2 + rot // 2 if layout == "half" else 3] = True
+        assert torch.equal(odd, want)
+        kept = got[..., rot:]
+        assert torch.equal(torch.nan_to_num(kept, nan=7.0), torch.nan_to_num(Q[..., rot:], nan=7.0))
+
+
 def test_empty_and_other_stream():
     rope = tsa.RotaryPositions(64)
     q = torch.empty((2, 3, 0, 64), dtype=torch.bfloat16, device="cuda")
@@ -163,6 +183,8 @@ def test_refusals():
         rope(Q, positions=torch.zeros((2, 8), dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
         rope(Q, positions=torch.zeros((2, 7), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):  # no query heads
+        rope(Q[:, :0], Q)
     odd = torch.zeros(2 * 4 * 8 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(2, 4, 8, 64)
     with pytest.raises(tsa.AttnError) as e:  # rows off the 16-byte grid
         rope(odd)

@@ -34,8 +34,6 @@ struct RopeParams {
     int warp_rows;  // no row spans two warps
 };
 
-// STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
-// memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
 // Orders the shared-memory accesses of a row's threads.
 __device__ __forceinline__ void row_sync(int warp_rows) {
     if (warp_rows) __syncwarp();
@@ -46,8 +44,9 @@ __device__ __forceinline__ void row_sync(int warp_rows) {
 // turned, so that loads are always under way.
 // STAGED: pairs of halves whose second half does not start on an 8-element boundary.  The row goes through shared
 // memory, where the pairs are picked element by element; global accesses stay 16 bytes wide.
+// Three blocks of bf16 rows a multiprocessor: with two, 8K tokens of 64 heads take 51.4 us for 45.2.
 template <class T, bool HALVES, bool STAGED, int U>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 3 : 2)) rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ uint32_t stage[];
     __shared__ float2 turns[kThreads * 8];  // rows of a block * rot / 2 at most
     __shared__ unsigned long long step[kRopeMaxPairs];
@@ -86,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     __syncthreads();
     float c[8], sn[8];
+    const int live_pairs = rope_live_pairs(u, p.t.rot);
     rope_lane_turns(turns + min(slot / p.hb, p.tb - 1) * pairs, u, p.t.rot, c, sn);
     for (int h0 = h_first; h0 < h_last; h0 += U * p.hb) {
         float run[U][16];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                         x[2 * e] = (float)row_t[i0];
                         x[2 * e + 1] = (float)row_t[i1];
                     }
-                    rope_turn(x, c, sn);
+                    rope_turn<false>(x, c, sn, live_pairs);
                 }
                 row_sync(p.warp_rows);
                 if (on)
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                                             row[kWords * u + e + 3]);
                 continue;
             } else {
-                rope_turn_runs<HALVES>(run[i], c, sn);
+                rope_turn<HALVES>(run[i], c, sn, live_pairs);
             }
             if (!row_live) continue;
             const RopeRows& r = h < p.Hq ? p.q : p.k;

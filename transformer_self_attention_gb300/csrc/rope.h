@@ -51,13 +51,21 @@ __device__ __forceinline__ void rope_pair_index(bool halves, int rot, int q, int
     i0 = turned ? q : 2 * q;
     i1 = turned ? q + rot / 2 : 2 * q + 1;
 }
-// x = the lane's pairs (x[2e], x[2e + 1]).
-__device__ __forceinline__ void rope_turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+// How many of a lane's eight pairs are rotated (the first ones).  The others keep their elements: a turn by nothing would
+// make a NaN of the partner of an infinity.
+__device__ __forceinline__ int rope_live_pairs(int u, int rot) { return min(8, max(0, rot / 2 - 8 * u)); }
+// Turns a lane's pairs: neighbours in x, or (HALVES) across its two runs x[0 .. 7] and x[8 .. 15], where `live` is 0 or 8.
+// Pairs that are not rotated come with c = 1 and s = 0.
+template <bool HALVES>
+__device__ __forceinline__ void rope_turn(float (&x)[16], const float (&c)[8], const float (&s)[8], int live) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1];
-        x[2 * e] = a * c[e] - b * s[e];
-        x[2 * e + 1] = a * s[e] + b * c[e];
+        const int i0 = HALVES ? e : 2 * e, i1 = HALVES ? 8 + e : 2 * e + 1;
+        const bool on = live > (HALVES ? 0 : e);
+        const float a = x[i0], b = x[i1];
+        const float bs = on ? b * s[e] : 0.f, as = on ? a * s[e] : -0.f;
+        x[i0] = a * c[e] - bs;
+        x[i1] = b * c[e] + as;
     }
 }
 // Eight neighbouring elements as they are in memory, and as float.
@@ -91,12 +99,6 @@ __device__ __forceinline__ void widen8(const Raw8<float>& r, float* x) {
     x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
     x[4] = r.w.x; x[5] = r.w.y; x[6] = r.w.z; x[7] = r.w.w;
 }
-template <class T>
-__device__ __forceinline__ void load8(const T* p, float* x) {
-    Raw8<T> r;
-    fetch8(p, r);
-    widen8(r, x);
-}
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -109,24 +111,12 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-// Turns the pairs of a lane's two runs x[0 .. 7], x[8 .. 15]: across the runs (pairs of halves), or inside them.  Lanes
-// behind the rotated elements have c = 1, s = 0, for which the pairing does not matter.
-template <bool HALVES>
-__device__ __forceinline__ void rope_turn_runs(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int i0 = HALVES ? e : 2 * e, i1 = HALVES ? 8 + e : 2 * e + 1;
-        const float a = x[i0], b = x[i1];
-        x[i0] = a * c[e] - b * s[e];
-        x[i1] = a * s[e] + b * c[e];
-    }
-}
 // The lane's cosines and sines from a table of its token's pairs, times amp.
 __device__ __forceinline__ void rope_lane_turns(const float2* table, int u, int rot, float (&c)[8], float (&s)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int q = 8 * u + e;
-        const float2 t = 2 * q < rot ? table[q] : make_float2(1.f, 0.f);
+        const float2 t = 2 * q < rot ? table[q] : make_float2(1.f, 0.f);  // (the table ends there)
         c[e] = t.x;
         s[e] = t.y;
     }
