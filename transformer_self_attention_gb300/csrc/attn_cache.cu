@@ -9,9 +9,10 @@
 // exponent byte 255: it reads back as NaN throughout.
 //
 // Bound by memory: each row is read once and written once.  d / 16 lanes hold a row, 16 elements each (attn_rope.cu),
-// and a warp takes one token after another, two rows a lane: 5.3K tokens of 8 heads to E4M3, keys rotated, take 14.1 us
-// (3.1 TB/s; the smaller the chunk, the more the first loads' latency counts), 48K tokens of 8 heads to bf16 74 us (5.4
-// TB/s, 79% of the measured copy rate).  Blocks whose warps shared their tokens by way of shared memory were no faster.
+// and a warp takes one token after another, two rows a lane: 5.3K tokens of 8 heads to E4M3, keys rotated, take 13.7 us
+// (3.2 TB/s; the smaller the chunk, the more the first loads' latency counts), 48K tokens of 8 heads to bf16 68 us (5.8
+// TB/s, 86% of the measured copy rate) and to E4M3 75 us (instructions: 0.7 a clock).  Blocks whose warps shared their
+// tokens by way of shared memory were no faster.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,7 +25,9 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteBlocks = 2;  // of the write kernel per multiprocessor
+// Of the write kernel, which hides its loads behind its arithmetic: five blocks of 128 threads (96 registers a thread) a
+// multiprocessor take 68 us for 48K bf16 tokens, four 74.
+constexpr int kWriteThreads = 128, kWriteBlocks = 5;
 
 __device__ __forceinline__ float exponent_factor(int e) {  // 2^(e - 127); NaN for 255
     return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FFFFFFFu : (uint32_t)e << 23);
@@ -97,23 +100,24 @@ __device__ __forceinline__ void turn_row(float (&run)[16], float* row, int rot, 
 }
 
 // HALVES: the rotated pairs are (p, p + rot / 2), otherwise neighbours.  STAGED: pairs of halves off the 8-element grid.
+// QUERIES: there may be some (without, fewer registers).
 // A thread takes two rows at a time: two queries, or a head's key and value.  (One row at a time, with its kind and place
 // found anew, took 300 instructions a row and 103 us for 49K tokens of 8 heads, 4 TB/s.)
-template <int D, bool E4M3, bool HALVES, bool STAGED>
-__global__ void __launch_bounds__(kThreads, kWriteBlocks) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
-    constexpr int LANES = D / 16, SLOTS = 32 / LANES, WARPS = kThreads / 32;
+template <int D, bool E4M3, bool HALVES, bool STAGED, bool QUERIES>
+__global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
+    constexpr int LANES = D / 16, SLOTS = 32 / LANES, WARPS = kWriteThreads / 32;
     __shared__ float2 turns[WARPS][D / 2];
     __shared__ unsigned long long step[D / 2];
     __shared__ float stage[STAGED ? WARPS * SLOTS * (D + 1) : 1];
     const CacheWriteParams& p = a.p;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, u = lane % LANES, slot = lane / LANES;
-    const int pairs = p.rope.rot / 2, live = rope_live_pairs(u, p.rope.rot), q_items = (p.Hq + 1) / 2;
+    const int pairs = p.rope.rot / 2, live = rope_live_pairs(u, p.rope.rot), q_items = QUERIES ? (p.Hq + 1) / 2 : 0;
     int off_a = 16 * u, off_b = 16 * u + 8;
     if (!STAGED) rope_runs(HALVES, p.rope.rot, u, off_a, off_b);
     typedef const __nv_bfloat16* Src;
 
-    // A warp takes one token's items (a chunk of them where there are few tokens) after another; what the next step needs is
-    // always on its way.
+    // A warp takes one token's items (a chunk of them where there are few tokens) after another; what the next step needs
+    // is always on its way.
     struct Job {
         int token, b, i, fresh, item, end;  // item: the lane's next; end: behind the chunk
         int pos, entry, slot;               // position (-1: padding), its page-table entry and slot
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, kWriteBlocks) cache_write_kernel(con
     Raw8<__nv_bfloat16> raw[2][2] = {};
     auto fetch = [&](const Job& j, int item) {
         if (item >= j.end || j.i >= j.fresh) return;  // rows of padding are not read
-        const bool query = item < q_items;
+        const bool query = QUERIES && item < q_items;
         const int h = query ? 2 * item : item - q_items;
         const RopeRows& r = query ? p.q : p.k;
         const Src r0 = reinterpret_cast<Src>(r.src) + (j.b * r.sb + j.i * r.ss + h * r.sh);
@@ -205,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, kWriteBlocks) cache_write_kernel(con
             const bool last = !__any_sync(0xFFFFFFFFu, item + SLOTS < now.end);
             if (!last) fetch(now, item + SLOTS);
             else if (more) fetch(next, next.item);
-            const bool query = item < q_items;
+            const bool query = QUERIES && item < q_items;
             float* const row = stage + (STAGED ? (warp * SLOTS + slot) * (D + 1) : 0);
             turn_row<HALVES, STAGED>(run[0], row, p.rope.rot, u, c, sn, live);
             float second[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) second[e] = run[1][e];
-            turn_row<HALVES, STAGED>(second, row, p.rope.rot, u, c, sn, live);
+            if (QUERIES) turn_row<HALVES, STAGED>(second, row, p.rope.rot, u, c, sn, live);
             float big[2] = {0.f, 0.f};
             if (E4M3) {
 #pragma unroll
@@ -341,7 +345,7 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     a.by_S = Divisor(p.S);
     a.by_page = Divisor(p.c.page);
     // a warp takes all items of a token unless that leaves multiprocessors without their warps
-    const int slots = 32 / (D / 16), rounds = (a.items + slots - 1) / slots, warps = kThreads / 32;
+    const int slots = 32 / (D / 16), rounds = (a.items + slots - 1) / slots, warps = kWriteThreads / 32;
     const long long want = (long long)kWriteBlocks * warps * n_sm;
     const int split = (int)std::min<long long>(rounds, std::max<long long>(1, (want + a.tokens - 1) / a.tokens));
     a.items_chunk = (rounds + split - 1) / split * slots;
@@ -349,10 +353,14 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     a.by_chunks = Divisor(a.chunks);
     const long long blocks = ((long long)a.tokens * a.chunks + warps - 1) / warps;
     const unsigned grid = (unsigned)std::min<long long>(blocks, (long long)kWriteBlocks * n_sm);
-    auto go = [&](auto* f) { f<<<grid, kThreads, 0, stream>>>(a); };
-    if (p.rope.interleaved) go(cache_write_kernel<D, E4M3, false, false>);
-    else if (p.rope.rot % 16 != 0) go(cache_write_kernel<D, E4M3, true, true>);
-    else go(cache_write_kernel<D, E4M3, true, false>);
+    auto go = [&](auto* f) { f<<<grid, kWriteThreads, 0, stream>>>(a); };
+    const bool q = p.Hq > 0;
+    if (p.rope.interleaved)
+        q ? go(cache_write_kernel<D, E4M3, false, false, true>) : go(cache_write_kernel<D, E4M3, false, false, false>);
+    else if (p.rope.rot % 16 != 0)
+        go(cache_write_kernel<D, E4M3, true, true, true>);
+    else
+        q ? go(cache_write_kernel<D, E4M3, true, false, true>) : go(cache_write_kernel<D, E4M3, true, false, false>);
     return cudaGetLastError();
 }
 
