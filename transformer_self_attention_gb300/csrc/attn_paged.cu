@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
-    if (tid == 0) p.cut[blockIdx.x] = make_int2(-1, 0);
+    if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;
     Walk w = paged_begin(p, cuts, sh.cost);
     const uint32_t ring_smem0 = smem_u32(ring_base);
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
             if (!final) __stcg(&p.part_ml[slot * kRowsPad + tid], v);
             else if (p.lse) p.lse[(long long)unit * p.rows + tid] = (v.x + log2f(v.y)) * 0.6931471805599453f;
         }
-        if (!final && w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w);
+        if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);
         named_bar_sync(1, 32 * kWarps);  // sh.ml and sh.red are free again
     }
     // after a wait that ran out, copies of this ring may still be on their way: wait for them, with a limit
@@ -487,70 +487,86 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     }
 }
 
-// Joins the parts of the unit that begins in decode CTA blockIdx.x and ends in a later one: O = sum_k 2^(m_k - M) O_k / L
-// with M = max m_k, L = sum_k 2^(m_k - M) l_k.  A warp per row.  The first part is in its CTA's second slot (the unit
-// begins inside the interval), the others in their CTA's first.
+// Joins the parts of one cut unit: O = sum_k 2^(m_k - M) O_k / L with M = max m_k, L = sum_k 2^(m_k - M) l_k.  The first
+// part is in its CTA's second slot (the unit begins inside the interval), the others in their CTA's first.  SPLIT warps a
+// row, a stretch of the parts each: four where there are few units, so of many parts each, else one.  What counts is the
+// chain of round trips to L2 (what is cut; then maxima, sums and parts together).  16 sequences of 19 parts of 32 rows:
+// 26.6 us a decode step, 29.4 with one warp a row that reads the parts behind the maxima.
 constexpr int kMergeWarps = 8;
-template <int D>
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedParams p, int rows_pad) {
+    constexpr int kVec = D / 32, kBatch = SPLIT == 1 ? 16 : 8, kRows = kMergeWarps / SPLIT;
+    __shared__ float sums[SPLIT == 1 ? 1 : kMergeWarps][SPLIT == 1 ? 1 : D];
+    __shared__ float weights[SPLIT == 1 ? 1 : kMergeWarps];
     wait_for_kernel_before();
-    const int row = blockIdx.y * kMergeWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int k0 = blockIdx.x;
-    const int2 cut = __ldcg(&p.cut[k0]);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % SPLIT;
+    const int row = blockIdx.y * kRows + warp / SPLIT;
+    const int2 cut = __ldcg(&p.cut[blockIdx.x]);
     if (cut.x < 0) return;
-    const int blocks = p.units / p.Hkv, head = cut.x / blocks, row_block = cut.x - head * blocks, k1 = cut.y;
+    const int unit = p.by_unit ? (int)blockIdx.x : cut.x, k0 = p.by_unit ? cut.x : (int)blockIdx.x;
+    const int blocks = p.units / p.Hkv, head = unit / blocks, row_block = unit - head * blocks;
     const int out_row = row_block * rows_pad + row;
-    if (row >= rows_pad || out_row >= p.rows) return;
-    const long long out = (long long)head * p.rows + out_row;
+    const bool live = row < rows_pad && out_row < p.rows;
+    if (SPLIT == 1 && !live) return;
+    const int n = live ? cut.y - k0 + 1 : 0, lo = n * share / SPLIT, hi = n * (share + 1) / SPLIT;  // parts of the warp
     const float ninf = __int_as_float(0xFF800000);
-    auto at = [&](int k) { return (long long)(2 * k + (k == k0)) * rows_pad + row; };
-    float M, L = 0.f;
-    constexpr int kVec = D / 32;
-    float v[kVec];
+    auto at = [&](int i) { return (long long)(2 * (k0 + i) + (i == 0)) * rows_pad + row; };
+    float y[kBatch][kVec];
+    auto load = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (first + i >= hi) continue;
+            const float* src = p.part_o + at(first + i) * D;
+            if constexpr (D == 128) {
+                const float4 t = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                y[i][0] = t.x; y[i][1] = t.y; y[i][kVec - 2] = t.z; y[i][kVec - 1] = t.w;
+            } else {
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                y[i][0] = t.x; y[i][1] = t.y;
+            }
+        }
+    };
+    load(lo);
+    float M = ninf, L = 0.f, v[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = 0.f;
-    // the first 32 parts' maxima and sums stay in registers: mostly there are no more
-    const float2 t0 = k0 + lane <= k1 ? __ldcg(&p.part_ml[at(k0 + lane)]) : make_float2(ninf, 0.f);
-    M = t0.x;
-    for (int k = k0 + 32 + lane; k <= k1; k += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(k)]).x);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(i)]).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    for (int kk = k0; kk <= k1; kk += 32) {
+    for (int first = lo; first < hi; first += kBatch) {
+        if (first > lo) load(first);
         float f = 0.f;
-        if (kk + lane <= k1) {
-            const float2 t = kk == k0 ? t0 : __ldcg(&p.part_ml[at(kk + lane)]);
+        if (lane < kBatch && first + lane < hi) {
+            const float2 t = __ldcg(&p.part_ml[at(first + lane)]);
             // a part without a maximum has seen nothing (sum 0), or only NaN
             f = t.x == ninf ? t.y : ex2(t.x - M);
             L += t.x == ninf ? t.y : t.y * f;
         }
-        // sixteen parts' loads at a time: a round trip to L2 is most of what this kernel takes
-        const int n = min(32, k1 - kk + 1);
-        for (int i0 = 0; i0 < n; i0 += 16) {
-            float y[16][kVec];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (i0 + i >= n) continue;
-                const float* src = p.part_o + at(kk + i0 + i) * D;
-                if constexpr (D == 128) {
-                    const float4 t = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-                    y[i][0] = t.x; y[i][1] = t.y; y[i][kVec - 2] = t.z; y[i][kVec - 1] = t.w;
-                } else {
-                    const float2 t = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                    y[i][0] = t.x; y[i][1] = t.y;
-                }
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+            if (first + i >= hi) continue;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float fi = __shfl_sync(0xFFFFFFFFu, f, (i0 + i) % 32);
-                if (i0 + i >= n) continue;
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) v[j] += fi * y[i][j];
-            }
+            for (int j = 0; j < kVec; ++j) v[j] += fi * y[i][j];
         }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) sums[warp][kVec * lane + j] = v[j];
+        if (lane == 0) weights[warp] = L;
+        __syncthreads();
+        if (share || !live) return;
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w) {
+            L += weights[warp + w];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] += sums[warp + w][kVec * lane + j];
+        }
+    }
     const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long long out = (long long)head * p.rows + out_row;
     uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.o) + out * D) + lane * (D / 64);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) o[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
@@ -588,9 +604,11 @@ cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t strea
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream) {
-    const dim3 blocks((unsigned)grid, (unsigned)((std::min(p.rows, rows_pad) + kMergeWarps - 1) / kMergeWarps));
-    return p.c.d == 64 ? launch_dependent(paged_merge_kernel<64>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad)
-                       : launch_dependent(paged_merge_kernel<128>, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad);
+    const int split = p.by_unit ? 4 : 1, per = kMergeWarps / split, rows = std::min(p.rows, rows_pad);
+    const dim3 blocks((unsigned)(p.by_unit ? p.B * p.units : grid), (unsigned)((rows + per - 1) / per));
+    auto go = [&](auto* f) { return launch_dependent(f, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad); };
+    if (p.c.d == 64) return p.by_unit ? go(paged_merge_kernel<64, 4>) : go(paged_merge_kernel<64, 1>);
+    return p.by_unit ? go(paged_merge_kernel<128, 4>) : go(paged_merge_kernel<128, 1>);
 }
 
 }  // namespace attn

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
     // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
-    if (tid == 0) p.cut[blockIdx.x] = make_int2(-1, 0);
+    if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;
     if (warp == 0) {
         tmem_alloc(smem_u32(&sh.tmem), C::kCols);
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                     else if (p.lse) p.lse[out0 + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
                 }
             }
-            if (!final && w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w);
+            if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);
             // before sh.sum, the queries and the row bounds are written again
             named_bar_sync(1 + group, 128);
         }

@@ -116,7 +116,11 @@ struct PagedParams {
     PageTable t;
     float* part_o;        // [2 * grid][rows_pad][d] unscaled sums, two slots per CTA: its first and its last stretch
     float2* part_ml;      // [2 * grid][rows_pad]: the rows' reference (base 2) and sum
-    int2* cut;            // [grid]: the unit that begins in a CTA and ends in a later one, and that CTA; unit -1: none
+    // Where the joining kernel finds the cut units.  By unit, where there are no more of them than CTAs: the first and the
+    // last CTA that hold parts of it; otherwise by CTA: the unit that begins in it and ends in a later one, and that one.
+    // x = -1: none.
+    int2* cut;
+    int by_unit;
     int B, Hq, Hkv, S_q, rows;
     int units;            // of a sequence: Hkv, times 2 where a head's rows are taken in two blocks
     int window;           // -1: none

@@ -380,6 +380,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     p.box_rows = cache->box_rows;
     const int rows_pad = attn::paged_rows_pad(p.rows, cache->e4m3);
     const int grid = std::min(h->n_sm * attn::paged_ctas_per_sm(p.rows, cache->e4m3), h->grid_limit);
+    p.by_unit = (long long)h->B * units <= grid;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cache->e4m3 ? attn::launch_paged_e4m3(p, grid, st) : attn::launch_paged_bf16(p, grid, st);
     if (e == cudaSuccess && attn::paged_may_cut((long long)h->B * units, room, grid, shape))

@@ -81,13 +81,15 @@ __device__ __forceinline__ unsigned paged_prefix(const PagedParams& p, PagedShap
     return carry;
 }
 
-// The CTA's share of the sequences without keys: rows of zeros, LSE -inf.
+// The CTA's share of the sequences without keys: rows of zeros, LSE -inf, nothing to join.
 template <int D, int THREADS>
 __device__ __forceinline__ void paged_empty_rows(const PagedParams& p, const unsigned* cost) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (cost[b + 1] != cost[b]) continue;
         uint4* o = reinterpret_cast<uint4*>(p.o) + (long long)b * p.Hq * p.S_q * (D / 8);
         for (int i = threadIdx.x; i < p.Hq * p.S_q * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
+        if (p.by_unit)
+            for (int i = threadIdx.x; i < p.units; i += THREADS) p.cut[b * p.units + i] = make_int2(-1, 0);
         if (p.lse)
             for (int i = threadIdx.x; i < p.Hq * p.S_q; i += THREADS)
                 p.lse[(long long)b * p.Hq * p.S_q + i] = __int_as_float(0xFF800000);
@@ -124,11 +126,18 @@ __device__ __forceinline__ void paged_open(const PagedParams& p, PagedShape shap
     w.at += to - off;
 }
 
-// Records where the last part of a unit is that begins in this CTA's stretch w and is cut (one thread).
+// Records a unit for the joining kernel (one thread, of the CTA w in which the unit begins; final: it also ends there).
 __device__ __forceinline__ void paged_record_cut(const PagedParams& p, const PagedCuts& cuts, PagedShape shape,
-                                                 const unsigned* cost, const Walk& w) {
+                                                 const unsigned* cost, const Walk& w, bool final) {
+    const int unit = w.b * p.units + w.h;
+    if (final) {
+        if (p.by_unit) p.cut[unit] = make_int2(-1, 0);
+        return;
+    }
     const unsigned u0 = cost[w.b] * p.units + w.h * paged_cost(w.n, shape) + shape.overhead;
-    p.cut[blockIdx.x] = make_int2(w.b * p.units + w.h, (int)cuts.owner(u0 + w.n - 1));
+    const int last = (int)cuts.owner(u0 + w.n - 1);
+    if (p.by_unit) p.cut[unit] = make_int2((int)blockIdx.x, last);
+    else p.cut[blockIdx.x] = make_int2(unit, last);
 }
 
 // Four floats of magnitude at most 448 as two E4M3 numbers each, x = hi + lo / 16: hi has four significant bits, the
