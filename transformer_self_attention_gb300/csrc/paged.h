@@ -62,10 +62,11 @@ cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t 
 // and the cuts fall between them.  Sequences without keys cost nothing.  The cost line [0, W) is cut into C intervals, equal
 // but for one, one per CTA.  Inside a unit the blocks follow the overhead; a CTA takes the blocks whose cost positions
 // its interval covers.
-// Measured, bf16 (blocks of 8 KB): overheads of 6, 10, 16 and 24 blocks give 33.0, 31.8, 29.5 and 29.0 us for 16 ragged
-// multi-query sequences of up to 16K positions and 170, 171, 167.5 and 169 us for 256 of up to 2K; least of 8, 12, 16 and
+// Measured, bf16 (blocks of 8 KB): overheads of 10, 16, 22 and 30 blocks give 28.1, 27.1, 26.7 and 27.8 us for 16 ragged
+// multi-query sequences of up to 16K positions and 169, 167, 168 and 169 us for 256 of up to 2K; least of 8, 12, 16 and
 // 24 give 9.3, 9.7, 5.8 and 5.8 us for one sequence of 256 positions and 10.8, 11.0, 11.1 and 12.4 for one of 4K.  E4M3
-// (tiles of 32 KB): least of 1, 2, 3 and 4 give 9.6, 6.8, 6.9 and 6.9 us, and 11.7, 12.9, 14.4 and 14.6.
+// (tiles of 32 KB): overheads of 2, 3, 4 and 6 tiles give 27.9, 27.6, 27.7 and 28.1 us for 8 sequences of 1K to 8K, and
+// least of 1, 2, 3 and 4 give 9.6, 6.8, 6.9 and 6.9 us, and 11.7, 12.9, 14.4 and 14.6, for the two sequences above.
 struct PagedShape {
     int keys;  // positions of a key block
     unsigned overhead, least;
