@@ -311,6 +311,53 @@ def test_write_and_read_back(store, d, rot, layout, S, Hq):
     assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
 
 
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,rot,layout,Hq", [(128, 128, "half", 0), (128, 96, "interleaved", 5), (64, 26, "half", 4)])
+def test_more_tokens_than_the_grid_takes_at_once(store, d, rot, layout, Hq):
+    """Prompts of thousands of tokens, ragged, appended behind others: every row against the definition."""
+    lens, news, Hkv, page = [4100, 3500, 2900, 17], [4100, 3000, 2900, 0], 3, 80
+    B, S = len(lens), max(news)
+    need = [-(-n // page) for n in lens]
+    g = torch.Generator().manual_seed(31)
+    order = torch.randperm(sum(need), generator=g).to(torch.int32)
+    table = torch.full((B, max(need)), -1, dtype=torch.int32)
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    cache = tsa.PagedCache(sum(need), Hkv, page, d, dtype=store)
+    qkv = torch.randn((B, S, Hq + 2 * Hkv, d), generator=g).to(torch.bfloat16).cuda()
+    Q, K, V = (qkv[:, :, lo:hi].transpose(1, 2) for lo, hi in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    rope = tsa.RotaryPositions(d, rot, layout=layout)
+    tab, ln, nw = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), torch.tensor(news, dtype=torch.int32).cuda()
+    Qr = cache.write(K, V, tab, ln, new_len=nw, rope=rope, Q=Q if Hq else None)
+    Kd, Vd = cache.read(tab, ln, length=max(lens))
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+    f, amp = pu.frequencies(rot)
+    for b, n in enumerate(news):
+        if not n:
+            continue
+        pos = (lens[b] - n + torch.arange(n))[None]
+        k_ref, k_size = pu.rotate(K[b:b + 1, :, :n], pos, rot, layout, f, amp)
+        k, v = Kd[b:b + 1, :, lens[b] - n:lens[b]].double().cpu(), Vd[b:b + 1, :, lens[b] - n:lens[b]].double().cpu()
+        v_ref = V[b:b + 1, :, :n].double().cpu()
+        if store == "bf16":
+            assert torch.equal(v, v_ref)
+            bound = pu.rope_bound(k_ref, k_size, torch.bfloat16)
+        else:
+            codes, e = pu.quantise(v_ref.float())
+            assert torch.equal(v, codes.view(torch.float8_e4m3fn).double() * torch.exp2(e.double() - 127)[..., None])
+            # half a step of a code, 2^-4, or of the smallest ones, 2^-10 of the factor, which is below 2^-7 of the row's
+            # largest (224 2^k < max): 2^-17 of that
+            bound = k_ref.abs() * 2.0 ** -4 + k_ref.abs().amax(-1, keepdim=True) * 2.0 ** -17 + k_size * 2.0 ** -19
+        assert float(((k - k_ref).abs() - bound).max()) <= 0
+        if Hq:
+            q_ref, q_size = pu.rotate(Q[b:b + 1, :, :n], pos, rot, layout, f, amp)
+            off = (Qr[b:b + 1, :, :n].double().cpu() - q_ref).abs() - pu.rope_bound(q_ref, q_size, torch.bfloat16)
+            assert float(off.max()) <= 0
+    if Hq:
+        for b, n in enumerate(news):
+            assert bool((Qr[b, :, n:] == 0).all())
+
+
 def test_written_rows_that_are_not_finite_read_back_as_nan():
     cache = tsa.PagedCache(2, 1, 16, 64, dtype="e4m3")
     K = torch.randn((1, 1, 3, 64), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
