@@ -489,9 +489,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
 
 // Joins the parts of one cut unit: O = sum_k 2^(m_k - M) O_k / L with M = max m_k, L = sum_k 2^(m_k - M) l_k.  The first
 // part is in its CTA's second slot (the unit begins inside the interval), the others in their CTA's first.  SPLIT warps a
-// row, a stretch of the parts each: four where there are few units, so of many parts each, else one.  What counts is the
-// chain of round trips to L2 (what is cut; then maxima, sums and parts together).  16 sequences of 19 parts of 32 rows:
-// 26.6 us a decode step, 29.4 with one warp a row that reads the parts behind the maxima.
+// row, a stretch of the parts each: four where a unit has eight parts or more, two from three parts on, else one.  What
+// counts is the chain of round trips to L2 (what is cut; then maxima, sums and parts together), and that the blocks fit
+// on the chip at once.  16 sequences of 19 parts of 32 rows: 26.6 us a decode step, 29.4 with one warp a row that reads
+// the parts behind the maxima; 64 units of 5 parts of 16 rows: 26.5 us with two warps a row, 27.6 with four.
 constexpr int kMergeWarps = 8;
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedParams p, int rows_pad) {
@@ -604,11 +605,15 @@ cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t strea
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream) {
-    const int split = p.by_unit ? 4 : 1, per = kMergeWarps / split, rows = std::min(p.rows, rows_pad);
-    const dim3 blocks((unsigned)(p.by_unit ? p.B * p.units : grid), (unsigned)((rows + per - 1) / per));
+    const int units = p.by_unit ? p.B * p.units : grid, parts = grid / units, rows = std::min(p.rows, rows_pad);
+    const int split = parts >= 8 ? 4 : parts >= 3 ? 2 : 1, per = kMergeWarps / split;
+    const dim3 blocks((unsigned)units, (unsigned)((rows + per - 1) / per));
     auto go = [&](auto* f) { return launch_dependent(f, blocks, 32 * kMergeWarps, 0, stream, p, rows_pad); };
-    if (p.c.d == 64) return p.by_unit ? go(paged_merge_kernel<64, 4>) : go(paged_merge_kernel<64, 1>);
-    return p.by_unit ? go(paged_merge_kernel<128, 4>) : go(paged_merge_kernel<128, 1>);
+    if (p.c.d == 64)
+        return split == 4 ? go(paged_merge_kernel<64, 4>)
+                          : split == 2 ? go(paged_merge_kernel<64, 2>) : go(paged_merge_kernel<64, 1>);
+    return split == 4 ? go(paged_merge_kernel<128, 4>)
+                      : split == 2 ? go(paged_merge_kernel<128, 2>) : go(paged_merge_kernel<128, 1>);
 }
 
 }  // namespace attn

@@ -206,17 +206,17 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
     if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;
-    if (warp == 0) {
-        tmem_alloc(smem_u32(&sh.tmem), C::kCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sh.tmem, t_d = tmem + 2 * N;
     const Watch watch{&sh.abort, p.c.err, p.watchdog_ns};
     Walk w = paged_begin(p, cuts, sh.cost);
 
+    // The tensor memory's address, once it is allocated: called once by the computing warps and the allocating one, which
+    // nobody waits for before (the loads are on their way and the queries written by then).
+    auto tmem_ready = [&]() {
+        tc_fence_before();
+        named_bar_sync(1 + C::kGroups, kThreads - 32);
+        tc_fence_after();
+        return *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    };
     if (warp == kLoader) {
         // =================================================== loads: a batch of four tiles, eight lanes each
         int g = 0, st = 0, n = 0;
@@ -275,6 +275,9 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
         }
     } else if (warp == kLoader + 1) {
         // =================================================== products (lane 0)
+        tmem_alloc(smem_u32(&sh.tmem), C::kCols);
+        tmem_relinquish();
+        const uint32_t tmem = tmem_ready(), t_d = tmem + 2 * N;
         if (lane == 0) {
             constexpr uint32_t idesc_s = idesc_e4m3_f32(kKeys, N, false);
             // V: elements of d contiguous; P: columns contiguous, 16 bytes to a position
@@ -329,6 +332,8 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
         const int row0 = group * kRows;  // of the group's rows in the block
         const int row_blocks = p.units / p.Hkv;
         const uint32_t t_lane = (uint32_t)(gwarp * 32) << 16;
+        constexpr uint32_t kNone = 0xFFFFFFFFu;
+        uint32_t tmem = kNone;
         int n = 0;
         while (w.at < w.end) {
             paged_open<kKeys>(p, shape, sh.cost, w);
@@ -381,6 +386,8 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
                 if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
                 named_bar_sync(1 + group, 128);
             }
+            if (tmem == kNone) tmem = tmem_ready();
+            const uint32_t t_d = tmem + 2 * N;
             // positions every real row sees need no test: [all_from, all_to)
             const int all_to = p.causal ? len - p.S_q + 1 : len;
             const int all_from = p.window < 0 ? 0 : max(0, len - 1 - p.window);
@@ -542,6 +549,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
             // before sh.sum, the queries and the row bounds are written again
             named_bar_sync(1 + group, 128);
         }
+        if (tmem == kNone) tmem_ready();
     }
     // after a wait that ran out, copies and products may still be under way: wait for them, with a limit
     __syncthreads();
@@ -550,9 +558,9 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
         while (globaltimer() - t0 < 10000000ULL) __nanosleep(1000);
         __syncthreads();
     }
-    if (warp == 0) {
+    if (warp == kLoader + 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kCols);
+        tmem_dealloc(sh.tmem, C::kCols);
     }
 }
 
