@@ -699,6 +699,8 @@ attn_status attn_cache_destroy(attn_cache_handle h);
  * for the second product over bf16 pages (to eight with more than 32 rows to a kv head), to eight over E4M3 pages (and
  * there to 2^-22 of the largest weight times the largest value factor among 128 positions); their sums, and LSE, are not.
  * Over E4M3 pages queries enter with all their bits, down to 2^-22 of a row's largest element.
+ * Sums are taken before they are divided, over weights of at most 2^16: a row overflows where 2^16 times the sum of its
+ * values' magnitudes passes the float32 range.
  *
  * A handle owns the partial results of sequences that are split over the grid; it must not be used by
  * two calls in flight at once, captured graphs included.  Distinct handles are independent.
