@@ -9,16 +9,15 @@
 // exponent byte 255: it reads back as NaN throughout.
 //
 // Bound by memory: each row is read once and written once.  d / 16 lanes hold a row, 16 elements each (attn_rope.cu),
-// and a warp takes one token after another, two rows a lane: 5.3K tokens of 8 heads to E4M3, keys rotated, take 13.7 us
-// (3.2 TB/s; the smaller the chunk, the more the first loads' latency counts), 48K tokens of 8 heads to bf16 68 us (5.8
+// and a warp takes one token after another, two rows a lane: 5.3K tokens of 8 heads to E4M3, keys rotated, take 14 us
+// (3.1 TB/s; the smaller the chunk, the more the first loads' latency counts), 48K tokens of 8 heads to bf16 68 us (5.8
 // TB/s, 86% of the measured copy rate) and to E4M3 75 us (instructions: 0.7 a clock).  Blocks whose warps shared their
 // tokens by way of shared memory were no faster.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "paged.h"
-#include "sm103_ptx.h"
+#include "paged_device.h"
 
 namespace attn {
 
@@ -165,6 +164,8 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kerne
             fetch8(r1 + 8, raw[1][1]);
         }
     };
+    wait_for_kernel_before();
+    let_kernel_behind_in();
     // (the frequencies lie in the parameters, where 32 different words take 32 reads)
     if ((int)threadIdx.x < pairs) step[threadIdx.x] = p.rope.step[threadIdx.x];
     __syncthreads();
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kerne
 }
 
 // Readback: each D / 16 threads take one (position, kv head, K or V) row.  Many small blocks hide the three dependent loads
-// (length, page, row): 32K ragged positions of 8 heads, E4M3, take 26.6 us, 74% of the measured copy rate; two and four
+// (length, page, row): 32K ragged positions of 8 heads, E4M3, take 26.1 us, 75% of the measured copy rate; two and four
 // heads a thread with all loads first take 29.0 and 29.8.  Rows at or past the length are left as they are.  E4M3 codes
 // become fp16 (exact), then times 2^k, which bf16 holds exactly.
 template <int D, bool E4M3>
@@ -286,6 +287,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     constexpr int LANES = D / 16, ROWS = kThreads / LANES;
     const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const int s = blockIdx.x * ROWS + slot, b = blockIdx.z;
+    wait_for_kernel_before();
+    let_kernel_behind_in();
     if (s >= p.S) return;
     const long long pos = (long long)p.first + s;
     const int len = p.t.len[b];
@@ -353,15 +356,12 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     a.by_chunks = Divisor(a.chunks);
     const long long blocks = ((long long)a.tokens * a.chunks + warps - 1) / warps;
     const unsigned grid = (unsigned)std::min<long long>(blocks, (long long)kWriteBlocks * n_sm);
-    auto go = [&](auto* f) { f<<<grid, kWriteThreads, 0, stream>>>(a); };
+    auto go = [&](auto* f) { return launch_dependent(f, dim3(grid), kWriteThreads, 0, stream, a); };
     const bool q = p.Hq > 0;
     if (p.rope.interleaved)
-        q ? go(cache_write_kernel<D, E4M3, false, false, true>) : go(cache_write_kernel<D, E4M3, false, false, false>);
-    else if (p.rope.rot % 16 != 0)
-        go(cache_write_kernel<D, E4M3, true, true, true>);
-    else
-        q ? go(cache_write_kernel<D, E4M3, true, false, true>) : go(cache_write_kernel<D, E4M3, true, false, false>);
-    return cudaGetLastError();
+        return q ? go(cache_write_kernel<D, E4M3, false, false, true>) : go(cache_write_kernel<D, E4M3, false, false, false>);
+    if (p.rope.rot % 16 != 0) return go(cache_write_kernel<D, E4M3, true, true, true>);
+    return q ? go(cache_write_kernel<D, E4M3, true, false, true>) : go(cache_write_kernel<D, E4M3, true, false, false>);
 }
 
 template <int D, bool E4M3>
@@ -369,8 +369,7 @@ cudaError_t read_d(const CacheReadParams& p, cudaStream_t stream) {
     const int rows = kThreads / (D / 16);
     const unsigned gx = (unsigned)((p.S + rows - 1) / rows);
     const dim3 grid(gx, (unsigned)std::min(p.c.Hkv, 65535), (unsigned)p.B);
-    cache_read_kernel<D, E4M3><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(cache_read_kernel<D, E4M3>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace

@@ -128,8 +128,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     int busy;
     const unsigned W = paged_prefix<C::kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.units;
     const PagedCuts cuts(W, busy * p.units, gridDim.x, shape);
-    // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_kernel_behind_in();
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
     if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;
@@ -500,6 +499,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     __shared__ float sums[SPLIT == 1 ? 1 : kMergeWarps][SPLIT == 1 ? 1 : D];
     __shared__ float weights[SPLIT == 1 ? 1 : kMergeWarps];
     wait_for_kernel_before();
+    let_kernel_behind_in();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % SPLIT;
     const int row = blockIdx.y * kRows + warp / SPLIT;
     const int2 cut = __ldcg(&p.cut[blockIdx.x]);

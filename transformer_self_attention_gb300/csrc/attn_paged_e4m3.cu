@@ -201,8 +201,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) page
     int busy;
     const unsigned W = paged_prefix<kKeys, kThreads>(p, shape, sh.cost, sh.scan, busy) * p.units;
     const PagedCuts cuts(W, busy * p.units, gridDim.x, shape);
-    // the joining kernel may be scheduled from here on: it waits for this grid before it reads anything
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_kernel_behind_in();
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
     if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;

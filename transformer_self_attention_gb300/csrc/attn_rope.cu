@@ -12,8 +12,7 @@
 
 #include <algorithm>
 
-#include "paged.h"
-#include "rope.h"
+#include "paged_device.h"
 
 namespace attn {
 
@@ -70,6 +69,8 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 3 : 2)) rope_kerne
             fetch8(in + off_b, raw[i][1]);
         }
     };
+    wait_for_kernel_before();
+    let_kernel_behind_in();
     fetch(h_first);
     // (the frequencies lie in the parameters, where 32 different words take 32 reads)
     const int pairs = p.t.rot / 2;
@@ -201,11 +202,11 @@ cudaError_t launch_rope(const RopeTable& t, const RopeRows& q, const RopeRows& k
     const dim3 grid((unsigned)blocks_x, (unsigned)((p.H + p.heads_block - 1) / p.heads_block));
     const bool staged = !t.interleaved && t.rot % 16 != 0;
     const size_t smem = staged ? (size_t)rows * (d * (f32 ? 4 : 2) + 4) : 0;
-    auto go = [&](auto* f) { f<<<grid, kThreads, smem, stream>>>(p); };
-    if (staged) f32 ? go(rope_kernel<float, true, true, 1>) : go(rope_kernel<__nv_bfloat16, true, true, 1>);
-    else if (t.interleaved) f32 ? go(rope_kernel<float, false, false, 2>) : go(rope_kernel<__nv_bfloat16, false, false, 2>);
-    else f32 ? go(rope_kernel<float, true, false, 2>) : go(rope_kernel<__nv_bfloat16, true, false, 2>);
-    return cudaGetLastError();
+    auto go = [&](auto* f) { return launch_dependent(f, grid, kThreads, (int)smem, stream, p); };
+    if (staged) return f32 ? go(rope_kernel<float, true, true, 1>) : go(rope_kernel<__nv_bfloat16, true, true, 1>);
+    if (t.interleaved)
+        return f32 ? go(rope_kernel<float, false, false, 2>) : go(rope_kernel<__nv_bfloat16, false, false, 2>);
+    return f32 ? go(rope_kernel<float, true, false, 2>) : go(rope_kernel<__nv_bfloat16, true, false, 2>);
 }
 
 }  // namespace attn

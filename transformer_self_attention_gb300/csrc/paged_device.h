@@ -32,6 +32,8 @@ cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, int smem, cudaSt
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on (in all CTAs) the kernel behind may be brought in; it waits for the end of this one.
+__device__ __forceinline__ void let_kernel_behind_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Key blocks of sequence b (0 for a length that is not followed).
 template <int KEYS>
