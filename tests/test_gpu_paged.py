@@ -530,6 +530,48 @@ def test_captured_behind_copies_and_another_stream(store):
     assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
 
 
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_calls_behind_one_another_need_no_synchronisation(store):
+    """Each call reads what the one before wrote, and writes what the one before that read, in the same few buffers: the
+    same bits with and without waiting for each."""
+    B, Hq, Hkv, d, page, room = 5, 16, 2, 128, 32, 1600
+    g = torch.Generator().manual_seed(17)
+    base = torch.randn((B, Hq + 2 * Hkv, 1, d), generator=g).to(torch.bfloat16).cuda()
+    table = torch.randperm(B * room // page, generator=g).to(torch.int32).view(B, room // page).cuda()
+    start = torch.tensor([1500, 0, 700, 31, 32], dtype=torch.int32).cuda()
+    rope = tsa.RotaryPositions(d)
+
+    def run(wait):
+        cache = tsa.PagedCache(B * room // page, Hkv, page, d, dtype=store)
+        plan = tsa.PagedDecodeAttention(B, Hq, Hkv, 1, d)
+        x, lens = base.clone(), start.clone()
+        Q, K, V = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        Qr, O = (torch.empty((B, Hq, 1, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        LSE = torch.empty((B, Hq, 1), device="cuda")
+        for _ in range(40):
+            lens.add_(1)
+            wait()
+            cache.write(K, V, table, lens, rope=rope, Q=Q, Q_out=Qr)
+            wait()
+            plan(Qr, cache, table, lens, O=O, LSE=LSE)
+            wait()
+            cache.read(table, lens, K=K, V=V)  # the first position's rows become the next step's
+            wait()
+            rope(K, O, positions=lens[:, None], Q_out=K, K_out=Q)
+            wait()
+            rope.backward(Q, positions=lens[:, None], dQ=Q)
+            wait()
+        torch.cuda.synchronize()
+        assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+        return x, O, LSE, cache.pages.view(torch.uint8).clone()
+
+    want = run(torch.cuda.synchronize)
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+
+
 def test_two_plans_on_two_streams():
     lens = [700, 90, 1300]
     cache, vals, table = _cache(lens, 2, 16, 128, "bf16", seed=6)
