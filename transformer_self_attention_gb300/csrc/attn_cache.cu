@@ -361,7 +361,8 @@ cudaError_t write_d(const CacheWriteParams& p, int n_sm, cudaStream_t stream) {
     if (p.rope.interleaved)
         return q ? go(cache_write_kernel<D, E4M3, false, false, true>) : go(cache_write_kernel<D, E4M3, false, false, false>);
     if (p.rope.rot % 16 != 0) return go(cache_write_kernel<D, E4M3, true, true, true>);
-    return q ? go(cache_write_kernel<D, E4M3, true, false, true>) : go(cache_write_kernel<D, E4M3, true, false, false>);
+    return q ? go(cache_write_kernel<D, E4M3, true, false, true>)
+             : go(cache_write_kernel<D, E4M3, true, false, false>);
 }
 
 template <int D, bool E4M3>

@@ -162,7 +162,8 @@ __device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[8], float 
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1)) paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
+    paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
     using C = Cfg<D, RP>;
     constexpr PagedShape shape = paged_shape(D, true);
     static_assert(shape.keys == kKeys, "a tile is a key block");
