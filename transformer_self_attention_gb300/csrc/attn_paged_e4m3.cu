@@ -518,32 +518,54 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
             }
             add_values(n - 1);
             tc_fence_before();
-            // ---- the rows' sums over the threads, and the stretch's result
+            // ---- the rows' sums over the threads, and the stretch's result.  The warp's sums, eight at once: each step halves
+            // the rows that a lane still holds, until the lanes 4 r .. 4 r + 3 hold row r.
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int step = 0; step < 3; ++step) {
+                const int o = 16 >> step, half = kRows / 2 >> step;
+                const bool up = lane & o;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-                if (lane == 0) sh.sum[gwarp][row0 + r] = l[r];
+                for (int i = 0; i < half; ++i) {
+                    const float give = up ? l[i] : l[i + half], keep = up ? l[i + half] : l[i];
+                    l[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                }
             }
+            l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 2);
+            l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 1);
+            if (lane % 4 == 0) sh.sum[gwarp][row0 + lane / 4] = l[0];
             named_bar_sync(1 + group, 128);
             const bool final = w.g0 == 0 && w.g1 == w.n;
             const long long slot = (2LL * blockIdx.x + (w.g0 > 0 ? 0 : 1)) * RP;
+            // lane r works out what belongs to row r, for all threads
+            const int mine = lane % kRows, my_row = row0 + mine;
+            const float L = (sh.sum[0][my_row] + sh.sum[1][my_row]) + (sh.sum[2][my_row] + sh.sum[3][my_row]);
+            const float inv = __frcp_rn(L);
+            const unsigned none = __ballot_sync(0xFFFFFFFFu, L == 0.f);  // bit r: the row has seen nothing
+            float out[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                const int row = row0 + r;
-                if (row >= rows) break;
-                const float L = (sh.sum[0][row] + sh.sum[1][row]) + (sh.sum[2][row] + sh.sum[3][row]);
-                if (gtid < D) {
-                    if (final)
-                        reinterpret_cast<__nv_bfloat16*>(p.o)[(out0 + row) * D + gtid] =
-                            __float2bfloat16(L == 0.f ? 0.f : acc[r] * __frcp_rn(L));
-                    else
-                        __stcg(p.part_o + (slot + row) * D + gtid, acc[r]);
+                const float by = __shfl_sync(0xFFFFFFFFu, inv, r);
+                out[r] = !final ? acc[r] : none >> r & 1 ? 0.f : acc[r] * by;
+            }
+            if (gtid < D) {
+                if (final) {
+                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.o) + (out0 + row0) * D + gtid;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (row0 + r < rows) o[r * D] = __float2bfloat16(out[r]);
+                } else {
+                    float* o = p.part_o + (slot + row0) * D + gtid;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (row0 + r < rows) __stcg(o + r * D, out[r]);
                 }
-                if (gtid == 0) {
-                    if (!final) __stcg(&p.part_ml[slot + row], make_float2(unset >> r & 1 ? ninf : m[r], L));
-                    else if (p.lse) p.lse[out0 + row] = (m[r] + log2f(L)) * 0.6931471805599453f;
-                }
+            }
+            if (gtid < kRows && my_row < rows) {
+                float ref = m[0];
+#pragma unroll
+                for (int r = 1; r < kRows; ++r) ref = mine == r ? m[r] : ref;
+                if (!final) __stcg(&p.part_ml[slot + my_row], make_float2(unset >> mine & 1 ? ninf : ref, L));
+                else if (p.lse) p.lse[out0 + my_row] = (ref + log2f(L)) * 0.6931471805599453f;
             }
             if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);
             // before sh.sum, the queries and the row bounds are written again
