@@ -49,9 +49,10 @@ struct Shared {
     unsigned long long full[kMostStages], empty[kMostStages], s_full[2], s_free[2], p_full, d_full, q_full;
     alignas(16) float top[2][4][RP];  // a tile's row maxima, by warp
     alignas(16) float factor[2][kGroups][4];  // and its largest value exponent, by group and warp
-    float qs[RP];                     // what a row's product is multiplied by, 2^up * scale * log2 e
+    alignas(16) float qs[RP];         // what a row's product is multiplied by, 2^up * scale * log2 e
+    alignas(16) int last[RP];         // the positions a row sees
+    alignas(16) int first[RP];
     float sum[4][RP];
-    int last[RP], first[RP];          // the positions a row sees
     unsigned scan[kThreads / 32];
     uint32_t tmem;
     int abort;
@@ -426,16 +427,27 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
                     float hi[kRows], lo[kRows];
                     load_parts<RP>(tmem + (n & 1) * N + t_lane + row0, hi, lo);
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r)
-                        x[r] = fmaf(fmaf(lo[r], 0.0625f, hi[r]), kf * sh.qs[row0 + r], -m[r]);
+                    for (int r = 0; r < kRows; r += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(&sh.qs[row0 + r]);
+                        x[r] = fmaf(fmaf(lo[r], 0.0625f, hi[r]), kf * q.x, -m[r]);
+                        x[r + 1] = fmaf(fmaf(lo[r + 1], 0.0625f, hi[r + 1]), kf * q.y, -m[r + 1]);
+                        x[r + 2] = fmaf(fmaf(lo[r + 2], 0.0625f, hi[r + 2]), kf * q.z, -m[r + 2]);
+                        x[r + 3] = fmaf(fmaf(lo[r + 3], 0.0625f, hi[r + 3]), kf * q.w, -m[r + 3]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[n & 1]));
                 if (first < all_from || first + kKeys > all_to) {
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r)
-                        if (!inside || pos > sh.last[row0 + r] || pos < sh.first[row0 + r]) x[r] = ninf;
+                    for (int r = 0; r < kRows; r += 4) {  // (without branches: each would cost a wait for shared memory)
+                        const int4 to = *reinterpret_cast<const int4*>(&sh.last[row0 + r]);
+                        const int4 from = *reinterpret_cast<const int4*>(&sh.first[row0 + r]);
+                        x[r] = !inside | (pos > to.x) | (pos < from.x) ? ninf : x[r];
+                        x[r + 1] = !inside | (pos > to.y) | (pos < from.y) ? ninf : x[r + 1];
+                        x[r + 2] = !inside | (pos > to.z) | (pos < from.z) ? ninf : x[r + 2];
+                        x[r + 3] = !inside | (pos > to.w) | (pos < from.w) ? ninf : x[r + 3];
+                    }
                 }
                 // ---- the tile's largest score of each row, and its largest value exponent
                 {
@@ -467,8 +479,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
                 if (moved) {
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        const float by = __shfl_sync(0xFFFFFFFFu, top, r);
-                        if (!(moved >> r & 1)) continue;
+                        const float by = moved >> r & 1 ? __shfl_sync(0xFFFFFFFFu, top, r) : 0.f;
                         const float fix = unset >> r & 1 ? 0.f : ex2(-by);
                         m[r] += by;
                         x[r] -= by;
