@@ -728,6 +728,14 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
 /* attn_paged_set_grid_limit -- test hook, as attn_decode_set_grid_limit. */
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas);
 
+/* attn_paged_set_watchdog -- test hook for the failure-detection path, as attn_set_watchdog.
+ *   limit_ns : wall-clock limit of every bounded wait inside the kernels (default 2e9 ns).
+ *   withhold : 0 = normal; n > 0 = a loading warp with n key blocks to load behind one another (n up to 32) stops in
+ *              front of the n-th, so that the wait for it runs out: bit 4 of the cache's error word is set, and the
+ *              kernel waits for its copies and returns (the outputs of the call are then undefined).
+ * Errors: ATTN_ERR_INVALID_ARG (limit_ns <= 0, withhold < 0). */
+attn_status attn_paged_set_watchdog(attn_paged_handle h, long long limit_ns, int withhold);
+
 /* attn_paged_destroy -- free the handle (synchronises the device first); NULL is ignored. */
 attn_status attn_paged_destroy(attn_paged_handle h);
 

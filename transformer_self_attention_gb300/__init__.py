@@ -37,7 +37,7 @@ EXPORTED = ("attn_create", "attn_forward", "attn_destroy", "attn_status_string",
             "attn_rope_create", "attn_rope_frequencies", "attn_rope_forward", "attn_rope_backward",
             "attn_rope_destroy", "attn_cache_create", "attn_cache_write", "attn_cache_read",
             "attn_cache_poll_device_error", "attn_cache_destroy", "attn_paged_create", "attn_paged_forward",
-            "attn_paged_set_grid_limit", "attn_paged_destroy", "attn_paged_split_host")
+            "attn_paged_set_grid_limit", "attn_paged_set_watchdog", "attn_paged_destroy", "attn_paged_split_host")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DECODE_MAX_BATCH = 1024
 DECODE_MAX_ROWS = 64
@@ -131,7 +131,8 @@ def _load():
                        ("attn_cache_poll_device_error", [P, ctypes.POINTER(I)]), ("attn_cache_destroy", [P]),
                        ("attn_paged_create", [ctypes.POINTER(P), I, I, I, I, I, F, I, I]),
                        ("attn_paged_forward", [P, P, P, P, LL, I, P, P, P, P]),
-                       ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_destroy", [P]),
+                       ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_set_watchdog", [P, LL, I]),
+                       ("attn_paged_destroy", [P]),
                        ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, ctypes.POINTER(I), P, I,
                                                   ctypes.POINTER(I)])):
         getattr(lib, name).argtypes = args
@@ -525,6 +526,10 @@ def attn_paged_set_grid_limit(handle: int, max_ctas: int) -> int:
     return _lib.attn_paged_set_grid_limit(handle, _int(max_ctas))
 
 
+def attn_paged_set_watchdog(handle: int, limit_ns: int, withhold: int = 0) -> int:
+    return _lib.attn_paged_set_watchdog(handle, int(limit_ns), _int(withhold))
+
+
 def attn_paged_destroy(handle: int) -> int:
     return _lib.attn_paged_destroy(handle)
 
@@ -883,6 +888,13 @@ class PagedDecodeAttention:
         st = attn_paged_set_grid_limit(self.handle, max_ctas)
         if st != ATTN_OK:
             raise AttnError(st, "attn_paged_set_grid_limit")
+
+    def set_watchdog(self, limit_ns: int, withhold: int = 0):
+        """Test hook: the limit of every bounded wait; with withhold = n > 0 a loading warp with n key blocks to load
+        behind one another stops in front of the n-th."""
+        st = attn_paged_set_watchdog(self.handle, limit_ns, withhold)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_paged_set_watchdog")
 
 
 # ---------------------------------------------------------------- torch convenience

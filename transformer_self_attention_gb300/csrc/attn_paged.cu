@@ -99,6 +99,7 @@ struct Shared {
     float2 ml[kWarps * 16];
     unsigned long long full[12 * kWarps], empty[12 * kWarps];
     unsigned scan[2 * kWarps];
+    int abort;
 };
 static_assert(offsetof(Shared, red) % 16 == 0 && offsetof(Shared, full) % 8 == 0 && offsetof(Shared, ml) % 8 == 0 &&
                   alignof(Shared) == 16 && Red<8>::kPitch * 8 <= Red<16>::kPitch * 16,
@@ -122,7 +123,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
         mbar_init(smem_u32(&sh.full[tid]), 1);
         mbar_init(smem_u32(&sh.empty[tid]), RW);
     }
-    if (tid == 0) prefetch_tmap(&p.tm);
+    if (tid == 0) {
+        prefetch_tmap(&p.tm);
+        sh.abort = 0;
+    }
     fence_barrier_init();
     wait_for_kernel_before();
     int busy;
@@ -132,14 +136,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     if (busy < p.B) paged_empty_rows<D, kThreads>(p, sh.cost);
     if (tid == 0 && !p.by_unit) p.cut[blockIdx.x] = make_int2(-1, 0);
     if (blockIdx.x >= cuts.C || W == 0) return;
+    const Watch watch{&sh.abort, p.c.err, p.watchdog_ns};
     Walk w = paged_begin(p, cuts, sh.cost);
     const uint32_t ring_smem0 = smem_u32(ring_base);
+    // The end of every warp: all meet behind their last copy, and after a wait that ran out those still on their way are
+    // waited for before the CTA gives its shared memory up.
+    auto finish = [&]() {
+        named_bar_sync(2, kThreads);
+        if (*watch.abort) drain();
+    };
 
     // =================================================== the loading warps: one for each ring
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         const int ring = warp - kWarps;
-        if (ring >= kRings) return;
+        if (ring >= kRings) {
+            finish();
+            return;
+        }
         const uint32_t dst0 = ring_smem0 + ring * kStages * C::kBlockBytes;
         const uint32_t full0 = smem_u32(&sh.full[ring * kStages]), empty0 = smem_u32(&sh.empty[ring * kStages]);
         int g = 0;  // next block of the ring in the stretch
@@ -181,14 +195,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
         while (now.n) {
             fetch(then);
             for (int i = 0; i < now.n; ++i) {
-                bool stop = false;
-                if (!mbar_try_wait(empty0 + 8 * fill, parity)) {
-                    const uint64_t t0 = globaltimer();
-                    while (!stop && !mbar_try_wait(empty0 + 8 * fill, parity))
-                        stop = (long long)(globaltimer() - t0) > 2 * p.watchdog_ns;
+                if (!__all_sync(0xFFFFFFFFu, i + 1 != p.withhold && wait(empty0 + 8 * fill, parity, watch))) {
+                    then.n = 0;
+                    break;
                 }
-                // the computing warps have stopped (their own wait ran out and is recorded): stop as well
-                if (__any_sync(0xFFFFFFFFu, stop)) return;
                 const uint32_t bar = full0 + 8 * fill;
                 int unit[C::kBoxes], slot[C::kBoxes], boxes = 0;
 #pragma unroll
@@ -212,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
             }
             now = then;
         }
+        finish();
         return;
     }
 
@@ -223,7 +234,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
     const uint32_t full = smem_u32(&sh.full[ring * kStages]), empty = smem_u32(&sh.empty[ring * kStages]);
     const float ninf = __int_as_float(0xFF800000);
     constexpr int kTiles = C::kKeys / 8;  // score tiles of a block
-    bool dead = false;  // a wait ran out: nothing more is waited for, and the outputs are undefined
+    // A wait ran out: the warp takes no further block and frees no place, so that its loading warp stops too; it goes on
+    // to the ends of the stretches, where the warps meet.  The outputs are undefined.
+    bool dead = false;
     int stage = 0;
     uint32_t phase = 0;
     while (w.at < w.end) {
@@ -260,20 +273,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
         for (int j = 0; j < D / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
         float m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
 
-        for (int g = w.g0 + ring; g < w.g1; g += kRings) {
+        for (int g = w.g0 + ring; g < w.g1 && !dead; g += kRings) {
             const int first = (w.lo + g) * C::kKeys;
             const uint32_t buf = ring_smem + stage * C::kBlockBytes;
-            if (!dead && !mbar_try_wait(full + 8 * stage, phase)) {
-                const uint64_t t0 = globaltimer();
-                while (!mbar_try_wait(full + 8 * stage, phase)) {
-                    if ((long long)(globaltimer() - t0) > p.watchdog_ns) {
-                        dead = true;
-                        atomicOr(p.c.err, kCacheErrWait);
-                        break;
-                    }
-                }
+            if (!__all_sync(0xFFFFFFFFu, wait(full + 8 * stage, phase, watch))) {
+                dead = true;
+                break;
             }
-            __syncwarp();
             if (first + C::kKeys > len || first < seen) {
                 // positions past the length or before the window may hold anything: weight zero times a NaN is a
                 // NaN, so their values become zero (their scores are masked below)
@@ -479,11 +485,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
         if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);
         named_bar_sync(1, 32 * kWarps);  // sh.ml and sh.red are free again
     }
-    // after a wait that ran out, copies of this ring may still be on their way: wait for them, with a limit
-    if (dead) {
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 10000000ULL) __nanosleep(1000);
-    }
+    finish();
 }
 
 // Joins the parts of one cut unit: O = sum_k 2^(m_k - M) O_k / L with M = max m_k, L = sum_k 2^(m_k - M) l_k.  The first

@@ -128,26 +128,6 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
-// A wait with a limit; after one has run out every wait of the CTA returns at once and its outputs are undefined.
-struct Watch {
-    volatile int* abort;
-    int* err;
-    long long ns;
-};
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch& w) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*w.abort) return false;
-        if ((long long)(globaltimer() - t0) > w.ns) {
-            *w.abort = 1;
-            atomicOr(w.err, kCacheErrWait);
-            return false;
-        }
-    }
-    return true;
-}
-
 // Eight rows of the thread's tensor-memory lane: the hi columns, and the lo columns RP further on.
 template <int RP>
 __device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[8], float (&lo)[8]) {
@@ -254,6 +234,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
         while (now.tiles && ok) {
             for (int i = 0; i < now.tiles; ++i, ++n) {
                 if (n >= kStages) ok = wait(empty(st), (n / kStages - 1) & 1, watch);
+                if (n + 1 == p.withhold) ok = false;
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -584,11 +565,10 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
         }
         if (tmem == kNone) tmem_ready();
     }
-    // after a wait that ran out, copies and products may still be under way: wait for them, with a limit
+    // all warps meet behind their last copy and product
     __syncthreads();
     if (sh.abort) {
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 10000000ULL) __nanosleep(1000);
+        drain();
         __syncthreads();
     }
     if (warp == kLoader + 1) {

@@ -129,6 +129,7 @@ struct PagedParams {
     int box_rows;         // E4M3: positions of a TMA box, a divisor of the page size
     float scale_log2;
     long long watchdog_ns;
+    int withhold;  // test hook: a loading warp stops in front of the withhold-th key block of a batch (0: never)
 };
 // Rows a slot of the partial results is padded to, the blocks that a kv head's rows are taken in, and the CTAs of a full
 // grid per multiprocessor.

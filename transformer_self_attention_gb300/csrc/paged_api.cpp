@@ -34,6 +34,7 @@ struct attn_paged_plan {
     int device = 0, n_sm = 0;
     int grid_limit = 1 << 30;
     long long watchdog_ns = 2000000000LL;
+    int withhold = 0;
     float scale = 0.f;
     float* d_part = nullptr;
     float2* d_ml = nullptr;
@@ -377,6 +378,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     p.causal = h->kind != ATTN_MASK_FULL;
     p.scale_log2 = (float)((double)h->scale * 1.4426950408889634);
     p.watchdog_ns = h->watchdog_ns;
+    p.withhold = h->withhold;
     p.box_rows = cache->box_rows;
     const int rows_pad = attn::paged_rows_pad(p.rows, cache->e4m3);
     const int grid = std::min(h->n_sm * attn::paged_ctas_per_sm(p.rows, cache->e4m3), h->grid_limit);
@@ -391,6 +393,13 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas) {
     if (!h || max_ctas < 1) return ATTN_ERR_INVALID_ARG;
     h->grid_limit = max_ctas;
+    return ATTN_OK;
+}
+
+attn_status attn_paged_set_watchdog(attn_paged_handle h, long long limit_ns, int withhold) {
+    if (!h || limit_ns <= 0 || withhold < 0) return ATTN_ERR_INVALID_ARG;
+    h->watchdog_ns = limit_ns;
+    h->withhold = withhold;
     return ATTN_OK;
 }
 

@@ -35,6 +35,33 @@ __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddep
 // From here on (in all CTAs) the kernel behind may be brought in; it waits for the end of this one.
 __device__ __forceinline__ void let_kernel_behind_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A wait with a limit.  Once one has run out, those of the CTA that are not satisfied return false as well; a loading warp
+// then starts no further copies, and the outputs are undefined.
+struct Watch {
+    volatile int* abort;  // of the CTA, in shared memory
+    int* err;
+    long long ns;
+};
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Watch& w) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*w.abort) return false;
+        if ((long long)(ptx::globaltimer() - t0) > w.ns) {
+            *w.abort = 1;
+            atomicOr(w.err, kCacheErrWait);
+            return false;
+        }
+    }
+    return true;
+}
+// After an abort, when no warp starts a copy or a product any more: 10 ms for those that are still under way, which write
+// shared memory that the next CTA may own.
+__device__ __forceinline__ void drain() {
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 10000000ULL) __nanosleep(1000);
+}
+
 // Key blocks of sequence b (0 for a length that is not followed).
 template <int KEYS>
 __device__ __forceinline__ int paged_blocks_of(const PagedParams& p, int n, int& lo) {
