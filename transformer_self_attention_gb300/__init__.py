@@ -585,6 +585,19 @@ def _rows(name, t, shape, dtype, device, out=False):
     return attn_rows(t.data_ptr(), sb, sh, ss)
 
 
+def _new(shape, dtype, device, stream, zero=False):
+    """A tensor for the results of a call on `stream` (None: the current one).  It comes from that stream's own memory,
+    which work still pending on the current stream does not touch, and is reported to the allocator as used by the
+    current stream too, where the caller goes on with it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _new_rows(t, H, S, d):
     """attn_rows of a tensor [B, H, S, d] allocated here."""
     return attn_rows(t.data_ptr(), H * S * d, S * d, d)
@@ -669,7 +682,7 @@ class RotaryPositions:
         B, Hq, S, d = shape
         q = _rows("Q", Q, shape, dtype, device)
         if Q_out is None:
-            Q_out = torch.empty(shape, dtype=dtype, device=Q.device)
+            Q_out = _new(shape, dtype, Q.device, stream)
             qo = _new_rows(Q_out, Hq, S, d)
         else:
             qo = _rows("Q_out", Q_out, shape, dtype, device, True)
@@ -681,7 +694,7 @@ class RotaryPositions:
             shape = (B, Hk, S, d)
             k = _rows("K", K, shape, dtype, device)
             if K_out is None:
-                K_out = torch.empty(shape, dtype=dtype, device=Q.device)
+                K_out = _new(shape, dtype, Q.device, stream)
                 ko = _new_rows(K_out, Hk, S, d)
             else:
                 ko = _rows("K_out", K_out, shape, dtype, device, True)
@@ -787,7 +800,7 @@ class PagedCache:
             shape = (B, Hq, S, d)
             q = _rows("Q", Q, shape, torch.bfloat16, device)
             if Q_out is None:
-                Q_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+                Q_out = _new(shape, torch.bfloat16, self.device, stream)
                 qo = _new_rows(Q_out, Hq, S, d)
             else:
                 qo = _rows("Q_out", Q_out, shape, torch.bfloat16, device, True)
@@ -810,12 +823,11 @@ class PagedCache:
                 raise ValueError("give length, or the tensors to fill")
             length = (K if K is not None else V).shape[2]
         shape = (B, Hkv, int(length), d)
-        if K is None or V is None:
-            with torch.cuda.stream(stream):  # a new tensor's zeros come before the rows
-                if K is None:
-                    K = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-                if V is None:
-                    V = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        # (a new tensor's zeros come before the rows: they are written on the same stream)
+        if K is None:
+            K = _new(shape, torch.bfloat16, self.device, stream, zero=True)
+        if V is None:
+            V = _new(shape, torch.bfloat16, self.device, stream, zero=True)
         k = _rows("K", K, shape, torch.bfloat16, self._device, True)
         v = _rows("V", V, shape, torch.bfloat16, self._device, True)
         if B:
@@ -873,9 +885,9 @@ class PagedDecodeAttention:
                                                    or t.shape != want or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {want} on {self.device}")
         if O is None:
-            O = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            O = _new(shape, torch.bfloat16, self.device, stream)
         if LSE is None and want_lse:
-            LSE = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
+            LSE = _new(shape[:3], torch.float32, self.device, stream)
         st = _call(self._device, stream, _lib.attn_paged_forward,
                    (self.handle, cache.handle, Q.data_ptr(), *table, O.data_ptr(), None if LSE is None else LSE.data_ptr()),
                    (Q, O, LSE, page_table, cache_len, cache.pages, cache.scales))
