@@ -657,6 +657,7 @@ attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int 
  *             keys, rounded once.
  *   Hq, Q, Q_out : bf16 rows [B, Hq, S_new, d] of the same tokens' queries, rotated in the same launch
  *             (Hq = 0: none); padding rows of Q_out are zeros.  Q_out may be Q itself.
+ * S_new = 0 is accepted and does nothing; the rows are then not looked at.
  * Rows of one call must go to different slots: of two rows for one slot, which values and which
  * exponent remain is unspecified.
  * Errors: ATTN_ERR_INVALID_ARG (pointers, strides, sizes, a rope of another head width, a current device
@@ -669,7 +670,7 @@ attn_status attn_cache_write(attn_cache_handle h, int B, int S_new, const attn_r
 
 /*
  * attn_cache_read -- the positions first .. first + S - 1 of every sequence as dense bf16 rows
- * K, V [B, Hkv, S, d]; rows at or past cache_len[b] are left as they were.  E4M3 rows come back exactly
+ * K, V [B, Hkv, S, d]; rows at or past cache_len[b] are left as they were (S = 0 does nothing).  E4M3 rows come back exactly
  * (a code times a power of two is a bf16 number, up to 2^127).  Errors: as attn_cache_write.
  */
 attn_status attn_cache_read(attn_cache_handle h, int B, int S, int first, const attn_rows* K, const attn_rows* V,

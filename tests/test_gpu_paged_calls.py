@@ -1,0 +1,25 @@
+"""Calls of the paged cache at the edges of what its documentation allows."""
+import pytest
+import torch
+
+import transformer_self_attention_gb300 as tsa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,rot", [(0, 0), (0, 64), (6, 64)])
+def test_an_append_of_no_rows_does_nothing(store, Hq, rot):
+    cache = tsa.PagedCache(3, 2, 16, 64, dtype=store)
+    before = cache.pages.view(torch.uint8).fill_(0x11).clone()
+    table, lens = torch.zeros((2, 1), dtype=torch.int32).cuda(), torch.tensor([5, 0], dtype=torch.int32).cuda()
+    K = torch.empty((2, 2, 0, 64), dtype=torch.bfloat16, device="cuda")
+    Q = torch.empty((2, Hq, 0, 64), dtype=torch.bfloat16, device="cuda") if Hq else None
+    out = cache.write(K, K, table, lens, rope=tsa.RotaryPositions(64, rot) if rot else None, Q=Q)
+    assert out is None if Q is None else out.shape == Q.shape
+    if Q is not None:  # and into an output that is given
+        assert cache.write(K, K, table, lens, rope=tsa.RotaryPositions(64, rot), Q=Q, Q_out=Q) is Q
+    Kd, Vd = cache.read(table, lens, length=0)
+    assert Kd.shape == Vd.shape == (2, 2, 0, 64)
+    assert torch.equal(cache.pages.view(torch.uint8), before)
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)

@@ -269,9 +269,9 @@ attn_status attn_cache_write(attn_cache_handle h, int B, int S_new, const attn_r
                              const attn_rows* Q_out, void* stream) {
     if (!h || B < 1 || S_new < 0 || Hq < 0 || Hq > (1 << 20)) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len) || !aligned(new_len, 4)) return ATTN_ERR_INVALID_ARG;
-    if (Hq > 0 && (!rows_ok(Q, 2) || !rows_ok(Q_out, 2))) return ATTN_ERR_INVALID_ARG;
     if (rope && rope->d != h->c.d) return ATTN_ERR_INVALID_ARG;
-    if (S_new == 0) return ATTN_OK;
+    if (S_new == 0) return ATTN_OK;  // (rows of nothing need no data)
+    if (Hq > 0 && (!rows_ok(Q, 2) || !rows_ok(Q_out, 2))) return ATTN_ERR_INVALID_ARG;
     if (!rows_ok(K, 2) || !rows_ok(V, 2)) return ATTN_ERR_INVALID_ARG;
     if (B > ATTN_DECODE_MAX_BATCH || (long long)B * S_new > (1LL << 30)) return ATTN_ERR_UNSUPPORTED;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
