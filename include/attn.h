@@ -560,8 +560,8 @@ attn_status attn_decode_schedule_host(int B, int Hkv, int S_q, int S_cap, attn_m
  *                     with r = original_len f_p / (2 pi) the turns of the pair within the
  *                     original context; amplitude 0.1 ln s + 1.
  * ("Transformer 演进与变体" (ai.icyfenix.cn), the sections on RoPE, NTK and YaRN.)
- * Angles are exact to 2^-65 turns per position, so far positions lose nothing; the cosines and
- * sines and the products are float32, and the result is rounded once.
+ * The frequencies are float64, known to 2^-53 turns per position (2^-33 turns at position 2^20); whole turns are
+ * taken off exactly.  The cosines and sines and the products are float32, and the result is rounded once.
  */
 typedef enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 } attn_rope_layout;
 typedef enum { ATTN_ROPE_PLAIN = 0, ATTN_ROPE_LINEAR = 1, ATTN_ROPE_NTK = 2, ATTN_ROPE_YARN = 3 } attn_rope_scaling;
