@@ -23,3 +23,18 @@ def test_an_append_of_no_rows_does_nothing(store, Hq, rot):
     assert Kd.shape == Vd.shape == (2, 2, 0, 64)
     assert torch.equal(cache.pages.view(torch.uint8), before)
     assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+
+
+def test_an_error_behind_a_poll_on_another_stream_is_recorded():
+    """A new cache's first call, and a call directly behind a poll that cleared the word, on a stream that waits for no
+    other: the clearing is done by then."""
+    side = torch.cuda.Stream()
+    K = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    bad, lens = torch.tensor([[9]], dtype=torch.int32).cuda(), torch.ones(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        cache = tsa.PagedCache(1, 1, 16, 64)  # (its pages' zeros may still be pending: the call writes none)
+        for _ in range(5):
+            cache.write(K, K, bad, lens, stream=side)
+            assert cache.poll_device_error() == (tsa.ATTN_ERR_INVALID_ARG, tsa.CACHE_ERR_PAGE)
+        assert cache.poll_device_error() == (tsa.ATTN_OK, 0)

@@ -105,6 +105,12 @@ attn::RopeRows rows_of(const attn_rows* src, const attn_rows* dst) {
     return r;
 }
 
+// The error word set to zero, by the time the call returns: the caller's next launch may be on a stream that does not wait
+// for the one this runs on, and what it records must not be wiped out.
+bool clear_error(int* err) {
+    return cudaMemset(err, 0, sizeof(int)) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
+}
+
 bool on_device(int device) {
     int dev = -1;
     return cudaGetDevice(&dev) == cudaSuccess && dev == device;
@@ -255,7 +261,7 @@ attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int 
         return fail(ATTN_ERR_CUDA);
     const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->c.err), sizeof(int));
     if (e != cudaSuccess) return fail(e == cudaErrorMemoryAllocation ? ATTN_ERR_OOM : ATTN_ERR_CUDA);
-    if (cudaMemset(h->c.err, 0, sizeof(int)) != cudaSuccess) return fail(ATTN_ERR_CUDA);
+    if (!clear_error(h->c.err)) return fail(ATTN_ERR_CUDA);
     // the largest power of two that divides the page, up to a decode tile
     while (h->box_rows < 128 && page % (2 * h->box_rows) == 0) h->box_rows *= 2;
     if (!(h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows) : encode_bf16(&h->map, h->c))) return fail(ATTN_ERR_CUDA);
@@ -312,7 +318,7 @@ attn_status attn_cache_poll_device_error(attn_cache_handle h, int* code) {
     *code = 0;
     if (cudaDeviceSynchronize() != cudaSuccess) return ATTN_ERR_CUDA;
     if (cudaMemcpy(code, h->c.err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (*code != 0 && cudaMemset(h->c.err, 0, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (*code != 0 && !clear_error(h->c.err)) return ATTN_ERR_CUDA;
     return *code == 0 ? ATTN_OK : *code & attn::kCacheErrWait ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_ERR_INVALID_ARG;
 }
 
