@@ -38,3 +38,26 @@ def test_an_error_behind_a_poll_on_another_stream_is_recorded():
             cache.write(K, K, bad, lens, stream=side)
             assert cache.poll_device_error() == (tsa.ATTN_ERR_INVALID_ARG, tsa.CACHE_ERR_PAGE)
         assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_a_new_caches_zeros_come_before_the_first_write_on_another_stream(store):
+    """The stream that allocates the pages is held up; the write runs on one that does not wait for it."""
+    made, side = torch.cuda.Stream(), torch.cuda.Stream()
+    K = torch.randn((1, 2, 40, 64), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    table = torch.arange(40, dtype=torch.int32)[None, -3:].contiguous().cuda()
+    lens = torch.tensor([40], dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(made):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        cache = tsa.PagedCache(40, 2, 16, 64, dtype=store)
+    cache.write(K, K, table, lens, stream=side)
+    torch.cuda.synchronize()
+    Kd, Vd = cache.read(table, lens, length=40)
+    if store == "bf16":
+        assert torch.equal(Kd, K) and torch.equal(Vd, K)
+    else:  # half a step of a code, or of the smallest ones, 2^-10 of a factor that is below 2^-7 of the row's largest
+        x = K.double()
+        bound = x.abs() * 2.0 ** -4 + x.abs().amax(-1, keepdim=True) * 2.0 ** -17
+        assert float(((Kd.double() - x).abs() - bound).max()) <= 0 and torch.equal(Kd, Vd)
+    assert bool((cache.pages.view(torch.uint8)[:37] == 0).all())

@@ -733,6 +733,7 @@ class PagedCache:
         if min(self.shape) < 1 or page % 16:
             raise ValueError("n_pages, Hkv and d must be positive, page a positive multiple of 16")
         want = (n_pages, Hkv, 2, page, d)
+        made = pages is None or (dtype == "e4m3" and scales is None)
         if pages is None:
             pages = torch.zeros(want, dtype=torch.uint8 if dtype == "e4m3" else tdt,
                                 device=device or torch.device("cuda", torch.cuda.current_device()))
@@ -750,6 +751,8 @@ class PagedCache:
         elif scales is not None:
             raise ValueError("a bf16 cache has no scales")
         self.pages, self.scales = pages, scales
+        if made:  # the zeros are there before the first call, on whatever stream that is
+            torch.cuda.current_stream(self.device).synchronize()
         with torch.cuda.device(self.device):
             self.handle = attn_cache_create(n_pages, Hkv, page, d, code, pages.data_ptr(),
                                             0 if scales is None else scales.data_ptr())
