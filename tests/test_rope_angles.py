@@ -66,3 +66,24 @@ def test_far_positions(layout, kw):
     size[..., first] = size[..., second] = (a.abs() + b.abs()) * amp
     far = torch.tensor(pos, dtype=torch.float64).abs()[:, None] * (2 * float(PI) * 2.0 ** -53)
     assert float(((y - want).abs() - pu.rope_bound(want, size, torch.float32) - size * far).max()) <= 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_cosines_and_sines_are_float32_ones(layout):
+    """Rows of pairs (1, 0) come back as (cos t, sin t).  Each is off by an ulp at most (CUDA's bound for sincospif; an ulp
+    is at most 2^-23 of the number) and by the angle's own error times the other one: t is brought to at most an eighth of
+    a turn exactly, a float32 number of half turns there is rounded by 2^-27 and cut by 2^-33 of one, and the frequencies
+    (theirs and the reference's) and the reference's product add less than 1e-11 rad at these positions."""
+    d, S = 256, 4096
+    x = torch.zeros((1, 1, S, d))
+    i = torch.arange(d // 2)
+    first, second = (i, i + d // 2) if layout == "half" else (2 * i, 2 * i + 1)
+    x[..., first] = 1.0
+    y = tsa.RotaryPositions(d, layout=layout)(x.cuda()).double().cpu()[0, 0]
+    f, _ = pu.frequencies(d)
+    t = torch.arange(S, dtype=torch.float64)[:, None] * f
+    cos, sin = torch.cos(t), torch.sin(t)
+    turn = float(PI) * (2.0 ** -27 + 2.0 ** -33) + 1e-11
+    for got, want, other in ((y[:, first], cos, sin), (y[:, second], sin, cos)):
+        assert float(((got - want).abs() - other.abs() * turn - want.abs() * 2.0 ** -23).max()) <= 0

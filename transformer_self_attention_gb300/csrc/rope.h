@@ -31,12 +31,19 @@ struct RopeRows {  // rows of d contiguous elements; strides in elements
 };
 
 #ifdef __CUDACC__
-// cos and sin of the phase of one pair.  The top 32 bits of the phase, as a signed number, are the angle in
-// turns times 2^32 (off by 1.5e-9 rad); sincospif is accurate to about an ulp for every argument.
+// cos and sin of the phase of one pair.  The nearest quarter of a turn is taken off in integers, so that a float32 number
+// of half turns holds the rest, an eighth of a turn at most, to 2^-27 (2.3e-8 rad; the cut to 32 bits adds 4e-10);
+// sincospif is accurate to an ulp.  (The whole angle as one float32 number would be off by up to 9e-8 rad.)
 __device__ __forceinline__ void rope_cos_sin(int position, unsigned long long step, float& c, float& s) {
     const unsigned long long phase = (unsigned long long)(long long)position * step;
-    const float half_turns = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(half_turns, &s, &c);
+    const unsigned quarter = ((unsigned)(phase >> 32) + 0x20000000u) >> 30;
+    const int rest = (int)(unsigned)(phase >> 30);  // the bits below the quarters, as a signed number of 2^-33 half turns
+    float c0, s0;
+    sincospif((float)rest * 1.1641532182693481e-10f, &s0, &c0);
+    c = quarter & 1 ? s0 : c0;
+    s = quarter & 1 ? c0 : s0;
+    c = __uint_as_float(__float_as_uint(c) ^ ((quarter + 1) << 30 & 0x80000000u));
+    s = __uint_as_float(__float_as_uint(s) ^ (quarter << 30 & 0x80000000u));
 }
 
 // The 16 elements a lane holds, as two runs of 8 (a, b), and where the runs start in the row.  Lane u of the d / 16
