@@ -671,7 +671,8 @@ attn_status attn_cache_write(attn_cache_handle h, int B, int S_new, const attn_r
 /*
  * attn_cache_read -- the positions first .. first + S - 1 of every sequence as dense bf16 rows
  * K, V [B, Hkv, S, d]; rows at or past cache_len[b] are left as they were (S = 0 does nothing).  E4M3 rows come back exactly
- * (a code times a power of two is a bf16 number, up to 2^127).  Errors: as attn_cache_write.
+ * (a code times a power of two is a bf16 number; but of a row with magnitudes of 1.9375 * 2^127 and more those are
+ * rounded up to 2^128 and come back as infinities).  Errors: as attn_cache_write.
  */
 attn_status attn_cache_read(attn_cache_handle h, int B, int S, int first, const attn_rows* K, const attn_rows* V,
                             const int* page_table, long long table_stride, int max_pages, const int* cache_len,
@@ -692,9 +693,10 @@ attn_status attn_cache_destroy(attn_cache_handle h);
  * attn_decode_forward's operation over a paged cache: S_q new rows per sequence, row i at position
  * t = cache_len[b] - S_q + i, its own key and value already written.  Masks, layouts of Q, O and LSE and
  * limits are those of the decode entry points; lengths are on the device and may be 0.  A row that sees no
- * key (an empty sequence, or t < 0) gives O = 0 and LSE = -inf.  Positions at or past the length, and
- * positions no row's window reaches, are never used, whatever they hold.  With S_q > 1, an infinity or a NaN
- * in a position that only some rows of a sequence see may reach the other rows of the same kv head.
+ * key (an empty sequence, or under the causal masks t < 0) gives O = 0 and LSE = -inf.  Positions at or past the
+ * length, and positions no row's window reaches, are never used, whatever they hold.  With S_q > 1, an infinity or a
+ * NaN in a position that only some rows of a sequence see may reach the other rows of the same kv head.  An infinity
+ * among the values that a row sees makes that element of its O an infinity or a NaN.
  *
  * Rounding: scores, sums and outputs are float32 until O is rounded.  Weights are rounded to 16 significant bits
  * for the second product over bf16 pages (to eight with more than 32 rows to a kv head), to eight over E4M3 pages (and

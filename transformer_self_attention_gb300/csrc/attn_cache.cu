@@ -9,10 +9,10 @@
 // exponent byte 255: it reads back as NaN throughout.
 //
 // Bound by memory: each row is read once and written once.  d / 16 lanes hold a row, 16 elements each (attn_rope.cu),
-// and a warp takes one token after another, two rows a lane: 5.3K tokens of 8 heads to E4M3, keys rotated, take 14 us
-// (3.1 TB/s; the smaller the chunk, the more the first loads' latency counts), 48K tokens of 8 heads to bf16 68 us (5.8
-// TB/s, 86% of the measured copy rate) and to E4M3 75 us (instructions: 0.7 a clock).  Blocks whose warps shared their
-// tokens by way of shared memory were no faster.
+// and a warp takes one token after another, two rows a lane: 7.1K tokens of 8 heads to E4M3, keys rotated, take 15 us
+// (2.9 TB/s; the smaller the chunk, the more the first loads' latency counts), 50.6K tokens of 8 heads to bf16 72 us (5.7
+// TB/s, 85% of the measured copy rate) and to E4M3 81 us (3.9 TB/s; instructions: 0.7 a clock).  Blocks whose warps shared
+// their tokens by way of shared memory were no faster.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Of the write kernel, which hides its loads behind its arithmetic: five blocks of 128 threads (96 registers a thread) a
-// multiprocessor take 68 us for 48K bf16 tokens, four 74.
+// multiprocessor took 68 us for 48.5K bf16 tokens, four 74.
 constexpr int kWriteThreads = 128, kWriteBlocks = 5;
 
 __device__ __forceinline__ float exponent_factor(int e) {  // 2^(e - 127); NaN for 255
@@ -101,7 +101,7 @@ __device__ __forceinline__ void turn_row(float (&run)[16], float* row, int rot, 
 // HALVES: the rotated pairs are (p, p + rot / 2), otherwise neighbours.  STAGED: pairs of halves off the 8-element grid.
 // QUERIES: there may be some (without, fewer registers).
 // A thread takes two rows at a time: two queries, or a head's key and value.  (One row at a time, with its kind and place
-// found anew, took 300 instructions a row and 103 us for 49K tokens of 8 heads, 4 TB/s.)
+// found anew, took 300 instructions a row and 103 us for 48.5K tokens of 8 heads, 4 TB/s.)
 template <int D, bool E4M3, bool HALVES, bool STAGED, bool QUERIES>
 __global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kernel(const __grid_constant__ WriteLaunch a) {
     constexpr int LANES = D / 16, SLOTS = 32 / LANES, WARPS = kWriteThreads / 32;
@@ -279,8 +279,9 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kerne
 }
 
 // Readback: each D / 16 threads take one (position, kv head, K or V) row.  Many small blocks hide the three dependent loads
-// (length, page, row): 32K ragged positions of 8 heads, E4M3, take 26.1 us, 75% of the measured copy rate; two and four
-// heads a thread with all loads first take 29.0 and 29.8.  Rows at or past the length are left as they are.  E4M3 codes
+// (length, page, row): 21.6K ragged positions of 8 heads, E4M3 (133 MB), take 26.0 us, 75% of the measured copy rate (bf16,
+// 177 MB, 28.8 us, 91%); two and four heads a thread with all loads first took 29.0 and 29.8.  Rows at or past the length
+// are left as they are.  E4M3 codes
 // become fp16 (exact), then times 2^k, which bf16 holds exactly.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheReadParams p) {

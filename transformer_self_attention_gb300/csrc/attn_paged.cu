@@ -12,15 +12,15 @@
 // of its own in shared memory, filled by a loading warp with one TMA box per 16 positions (keys and values of a head in
 // one box, so that pages of any multiple of 16 work).  The warps share nothing until the stretch ends: each holds its own
 // running maximum, sum and output tile (16 rows x d, fp32 registers).  Then their results are added through shared
-// memory.  A unit cut between CTAs is joined by a second kernel, launched as a programmatic dependent, a warp per row;
-// it adds the parts in their order, so that a result does not depend on who finishes first.  (Joined by the last CTA to
+// memory.  A unit cut between CTAs is joined by a second kernel, launched as a programmatic dependent, one to four warps
+// a row; it adds the parts in their order, so that a result does not depend on who finishes first.  (Joined by the last CTA to
 // arrive instead, 19 parts of 32 rows took 15 of a call's 44 us.)
 //
 // The products are m16n8k16 with fp32 accumulation: at the measured copy bandwidth an SM takes in 24 bytes a clock, 12
 // elements, 188 multiply-adds at 16 rows of the 1024 these products do a clock.  Up to 32 rows a weight enters the
 // second product as the sum of two bf16 numbers (2^-16 of it at most is lost; 1.5% of the time at 8 rows, 141 us for 904
-// MB), above that, where these products are the limit, as one (2^-8; two would take 143 us for 452 MB at 64 rows
-// against 113).  The weights' sum is taken before.
+// MB), above that, where these products are the limit, as one (2^-8; two took 143 us for 452 MB at 64 rows
+// against 110).  The weights' sum is taken before.
 #include <cuda_bf16.h>
 
 #include <algorithm>
