@@ -728,6 +728,16 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
                                long long table_stride, int max_pages, const int* cache_len, void* O, float* LSE,
                                void* stream);
 
+/*
+ * attn_paged_forward_heads -- attn_paged_forward with a page table of its own for each kv head: position j of sequence b
+ * and head g is slot j % page of the page page_table[b * table_stride + g * head_stride + j / page].  Positions, masks and
+ * windows are those of the tables.  (What attn_bounds_select writes is such a table.)  Errors as attn_paged_forward, and
+ * ATTN_ERR_INVALID_ARG for a negative head_stride.
+ */
+attn_status attn_paged_forward_heads(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
+                                     long long table_stride, long long head_stride, int max_pages, const int* cache_len,
+                                     void* O, float* LSE, void* stream);
+
 /* attn_paged_set_grid_limit -- test hook, as attn_decode_set_grid_limit. */
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas);
 
@@ -751,6 +761,54 @@ attn_status attn_paged_destroy(attn_paged_handle h);
  */
 attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dtype, attn_mask_kind kind, int window,
                                   const int* cache_len, int grid, int* n_cta, int* parts, int cap, int* n_parts);
+
+/*
+ * ---------------------------------------------------------------- attention over selected pages
+ * New rows attend to the pages that a cheap score selects for their sequence and kv head: bounds of the pages' keys are
+ * kept beside the cache, attn_bounds_select writes a page table for each head, and attn_paged_forward_heads attends
+ * over that.
+ *
+ * The bounds of a page and head, over its positions inside a sequence, are the smallest and the largest key element lo_c
+ * and hi_c of every channel, in 8 bits: with k = min { k >= -126 : max_c max(|lo_c|, |hi_c|) <= 127 * 2^k },
+ *   codes     : int8 [n_pages, Hkv, 2, d], floor(lo_c 2^-k) at index 0 and ceil(hi_c 2^-k) at index 1;
+ *   exponents : uint8 [n_pages, Hkv], k + 127; 255 (and codes 0) where a key of the page is not finite.
+ * The score of a page for a kv head's rows (the heads of its group times the new rows): with the queries rounded to
+ * nearest whole numbers r of at most 127 times one power of two for all of the rows, the smallest that serves,
+ *   2^k max over rows sum_c max(r_c lo_c, r_c hi_c),
+ * in exact arithmetic: no product of a rounded query with a key of the page is larger.  A page with exponent 255 has
+ * the score +infinity.  Queries that are not finite make all scores of their sequence and head equal.
+ *
+ * Both calls run on the cache's device and need no workspace; codes and exponents are the caller's.
+ */
+
+/*
+ * attn_bounds_update -- compute the bounds of the pages that hold the last new_len[b] positions of each sequence (those
+ * pages' other positions count too); other pages' bounds are left as they were.
+ *   codes, exponents : device, as above; codes 16-byte aligned.
+ *   new_len : int32 device [B], or NULL: all positions.  More than cache_len[b] counts as that.
+ * A page that appears twice with different lengths gets the bounds of one of them.
+ * Errors: as attn_cache_write (ATTN_ERR_UNSUPPORTED also for max_pages * page > 2^30).  Lengths and page numbers that are
+ * not followed are recorded in the cache's error word.
+ */
+attn_status attn_bounds_update(attn_cache_handle h, void* codes, void* exponents, int B, const int* page_table,
+                               long long table_stride, int max_pages, const int* cache_len, const int* new_len,
+                               void* stream);
+
+/*
+ * attn_bounds_select -- for each sequence and kv head, choose `keep` of its pages: the first `sinks`, the last `recent`,
+ * and between them those of the largest scores (of equal scores the first).  Sequences of at most `keep` pages keep all.
+ *   Q         : bf16 [B, Hq, S_q, d], contiguous, 16-byte aligned; limits as attn_paged_create.
+ *   keep      : sinks + recent at least.   sinks : >= 0.
+ *   recent    : at least 1 + ceil((S_q - 1) / page), so that the new rows' own positions are among the chosen.
+ *   out_table : int32 device [B, Hkv, keep]: the chosen entries of the page table in their order, then -1.
+ *   out_len   : int32 device [B]: the positions in the chosen pages (the same for every head, as only the last page is
+ *               not full).  Neither may be an input.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (rows, or max_pages or keep above 49152), ATTN_ERR_CUDA.
+ */
+attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const void* exponents, int B, int Hq, int S_q,
+                               const void* Q, const int* page_table, long long table_stride, int max_pages,
+                               const int* cache_len, int keep, int sinks, int recent, int* out_table, int* out_len,
+                               void* stream);
 
 #ifdef __cplusplus
 }

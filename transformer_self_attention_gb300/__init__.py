@@ -37,7 +37,8 @@ EXPORTED = ("attn_create", "attn_forward", "attn_destroy", "attn_status_string",
             "attn_rope_create", "attn_rope_frequencies", "attn_rope_forward", "attn_rope_backward",
             "attn_rope_destroy", "attn_cache_create", "attn_cache_write", "attn_cache_read",
             "attn_cache_poll_device_error", "attn_cache_destroy", "attn_paged_create", "attn_paged_forward",
-            "attn_paged_set_grid_limit", "attn_paged_set_watchdog", "attn_paged_destroy", "attn_paged_split_host")
+            "attn_paged_set_grid_limit", "attn_paged_set_watchdog", "attn_paged_destroy", "attn_paged_split_host",
+            "attn_paged_forward_heads", "attn_bounds_update", "attn_bounds_select")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DECODE_MAX_BATCH = 1024
 DECODE_MAX_ROWS = 64
@@ -131,6 +132,9 @@ def _load():
                        ("attn_cache_poll_device_error", [P, ctypes.POINTER(I)]), ("attn_cache_destroy", [P]),
                        ("attn_paged_create", [ctypes.POINTER(P), I, I, I, I, I, F, I, I]),
                        ("attn_paged_forward", [P, P, P, P, LL, I, P, P, P, P]),
+                       ("attn_paged_forward_heads", [P, P, P, P, LL, LL, I, P, P, P, P]),
+                       ("attn_bounds_update", [P, P, P, I, P, LL, I, P, P, P]),
+                       ("attn_bounds_select", [P, P, P, I, I, I, P, P, LL, I, P, I, I, I, P, P, P]),
                        ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_set_watchdog", [P, LL, I]),
                        ("attn_paged_destroy", [P]),
                        ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, ctypes.POINTER(I), P, I,
@@ -522,6 +526,28 @@ def attn_paged_forward(handle, cache, q_ptr, table_ptr, table_stride, max_pages,
                                    lse_ptr or None, stream or None)
 
 
+def attn_paged_forward_heads(handle, cache, q_ptr, table_ptr, table_stride, head_stride, max_pages, len_ptr, o_ptr,
+                             lse_ptr=0, stream=0) -> int:
+    """attn_paged_forward with a page table of its own for each kv head; returns the status."""
+    return _lib.attn_paged_forward_heads(handle, cache, q_ptr, table_ptr, table_stride, head_stride, max_pages, len_ptr,
+                                         o_ptr, lse_ptr or None, stream or None)
+
+
+def attn_bounds_update(cache, codes_ptr, exponents_ptr, B, table_ptr, table_stride, max_pages, len_ptr, new_ptr=0,
+                       stream=0) -> int:
+    """Bounds of the keys of the pages that changed; returns the status."""
+    return _lib.attn_bounds_update(cache, codes_ptr, exponents_ptr, B, table_ptr, table_stride, max_pages, len_ptr,
+                                   new_ptr or None, stream or None)
+
+
+def attn_bounds_select(cache, codes_ptr, exponents_ptr, B, Hq, S_q, q_ptr, table_ptr, table_stride, max_pages, len_ptr,
+                       keep, sinks, recent, out_table_ptr, out_len_ptr, stream=0) -> int:
+    """Page tables of the pages with the largest scores; returns the status."""
+    return _lib.attn_bounds_select(cache, codes_ptr, exponents_ptr, B, Hq, S_q, q_ptr, table_ptr, table_stride, max_pages,
+                                   len_ptr, _int(keep), _int(sinks), _int(recent), out_table_ptr, out_len_ptr,
+                                   stream or None)
+
+
 def attn_paged_set_grid_limit(handle: int, max_ctas: int) -> int:
     return _lib.attn_paged_set_grid_limit(handle, _int(max_ctas))
 
@@ -851,6 +877,7 @@ class PagedDecodeAttention:
 
     Q: [B, Hq, S_q, d] bf16; row i of sequence b sits at position cache_len[b] - S_q + i, its own key and value
     already written.  Returns (O like Q, LSE float32 [B, Hq, S_q]); a row that sees no key gives zeros and -inf.
+    page_table: [B, max_pages], or [B, Hkv, max_pages] with a table of its own for each kv head (PageBounds.select).
     """
 
     def __init__(self, B, Hq, Hkv, S_q, d, scale=None, kind=MASK_CAUSAL, window=0, device=None):
@@ -877,10 +904,14 @@ class PagedDecodeAttention:
             pass
 
     def __call__(self, Q, cache, page_table, cache_len, O=None, LSE=None, stream=None, want_lse=True):
-        B, Hq, _, S_q, d = self.shape
-        rows, table = cache._table(page_table, cache_len)
+        B, Hq, Hkv, S_q, d = self.shape
+        heads = page_table.dim() == 3
+        if heads and page_table.shape[1] != Hkv:
+            raise ValueError(f"page_table must have a row for each of {Hkv} kv heads")
+        rows, table = cache._table(page_table[:, 0] if heads else page_table, cache_len)
         if rows != B:
             raise ValueError(f"page_table must have {B} rows")
+        table = (*table[:2], page_table.stride(1) if heads and Hkv > 1 else 0, *table[2:])
         shape = (B, Hq, S_q, d)
         for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
                                   ("LSE", LSE, shape[:3], torch.float32)):
@@ -891,7 +922,7 @@ class PagedDecodeAttention:
             O = _new(shape, torch.bfloat16, self.device, stream)
         if LSE is None and want_lse:
             LSE = _new(shape[:3], torch.float32, self.device, stream)
-        st = _call(self._device, stream, _lib.attn_paged_forward,
+        st = _call(self._device, stream, _lib.attn_paged_forward_heads,
                    (self.handle, cache.handle, Q.data_ptr(), *table, O.data_ptr(), None if LSE is None else LSE.data_ptr()),
                    (Q, O, LSE, page_table, cache_len, cache.pages, cache.scales))
         if st != ATTN_OK:
@@ -910,6 +941,78 @@ class PagedDecodeAttention:
         st = attn_paged_set_watchdog(self.handle, limit_ns, withhold)
         if st != ATTN_OK:
             raise AttnError(st, "attn_paged_set_watchdog")
+
+
+class PageBounds:
+    """Bounds of the keys of a PagedCache's pages, and the pages that they select (``attn_bounds_*``).
+
+    codes: int8 [n_pages, Hkv, 2, d], the smallest and the largest key element of each channel; exponents: uint8
+    [n_pages, Hkv], the biased exponent of their power of two.  Both are allocated (zeroed) unless given, and stay the
+    caller's to use.  A generation step over the selected pages:
+
+        cache.write(K, V, page_table, cache_len, ...)
+        bounds.update(page_table, cache_len, new_len)
+        O, LSE = step(Q, cache, *bounds.select(Q, page_table, cache_len, keep=32))
+    """
+
+    def __init__(self, cache, codes=None, exponents=None):
+        _need_torch()
+        n_pages, Hkv, _, d = cache.shape
+        made = codes is None or exponents is None
+        self.cache, self._device = cache, cache._device
+        self.codes = self._buffer("codes", codes, (n_pages, Hkv, 2, d), torch.int8)
+        self.exponents = self._buffer("exponents", exponents, (n_pages, Hkv), torch.uint8)
+        if made:  # the zeros are there before the first call, on whatever stream that is
+            torch.cuda.current_stream(cache.device).synchronize()
+
+    def _buffer(self, name, t, shape, dtype):
+        if t is None:
+            return torch.zeros(shape, dtype=dtype, device=self.cache.device)
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != self._device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.cache.device}")
+        return t
+
+    def update(self, page_table, cache_len, new_len=None, stream=None):
+        """Recompute the bounds of the pages that hold the last new_len[b] (int32 CUDA [B]; default: all) positions
+        of each sequence."""
+        cache = self.cache
+        B, table = cache._table(page_table, cache_len)
+        new = None if new_len is None else _int32("new_len", new_len, (B,), self._device)
+        if B:
+            st = _call(self._device, stream, _lib.attn_bounds_update,
+                       (cache.handle, self.codes.data_ptr(), self.exponents.data_ptr(), B, *table, new),
+                       (page_table, cache_len, new_len, self.codes, self.exponents, cache.pages, cache.scales))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_bounds_update")
+
+    def select(self, Q, page_table, cache_len, keep, sinks=1, recent=1, table=None, length=None, stream=None):
+        """For each sequence and kv head the first ``sinks`` pages, the last ``recent``, and those of the largest
+        scores for Q [B, Hq, S_q, d] between them, ``keep`` in all.  Returns (table, length), int32 [B, Hkv, keep] and
+        [B], for PagedDecodeAttention; table[b, h] has -1 behind the chosen pages."""
+        cache = self.cache
+        _, Hkv, page, d = cache.shape
+        B, tab = cache._table(page_table, cache_len)
+        if (Q.dim() != 4 or Q.shape[0] != B or Q.shape[3] != d or Q.shape[1] < 1 or Q.shape[1] % Hkv or Q.shape[2] < 1
+                or Q.dtype is not torch.bfloat16 or Q.get_device() != self._device or not Q.is_contiguous()):
+            raise ValueError(f"Q must be a contiguous bfloat16 tensor [{B}, Hq, S_q, {d}] on {cache.device}, Hq a "
+                             f"multiple of {Hkv}, S_q at least 1")
+        keep, sinks, recent = _int(keep), _int(sinks), _int(recent)
+        least = 1 - (1 - Q.shape[2]) // page
+        if sinks < 0 or recent < least or keep < sinks + recent:
+            raise ValueError(f"recent must be at least {least}, sinks at least 0, keep at least sinks + recent")
+        if table is None:
+            table = _new((B, Hkv, keep), torch.int32, cache.device, stream)
+        if length is None:
+            length = _new((B,), torch.int32, cache.device, stream)
+        if B:
+            st = _call(self._device, stream, _lib.attn_bounds_select,
+                       (cache.handle, self.codes.data_ptr(), self.exponents.data_ptr(), B, Q.shape[1], Q.shape[2],
+                        Q.data_ptr(), *tab, keep, sinks, recent, _int32("table", table, (B, Hkv, keep), self._device),
+                        _int32("length", length, (B,), self._device)),
+                       (Q, page_table, cache_len, table, length, self.codes, self.exponents))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_bounds_select")
+        return table, length
 
 
 # ---------------------------------------------------------------- torch convenience

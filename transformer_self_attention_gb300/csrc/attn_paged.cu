@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
                 if (lane >= f.n || pos >= w.len || pos + 16 <= w.seen) continue;
                 const int index = (unsigned)pos / (unsigned)p.c.page;
                 f.slot[k] = pos - index * p.c.page;
-                int page = p.t.pages[w.b * p.t.stride + index];
+                int page = p.t.pages[w.b * p.t.stride + w.h * p.t.head_stride + index];
                 if (page < 0 || page >= p.c.n_pages) {
                     atomicOr(p.c.err, kCacheErrPage);
                     page = 0;

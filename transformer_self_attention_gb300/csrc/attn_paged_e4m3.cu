@@ -219,12 +219,13 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
             if (lane / 8 < f.tiles && 16 * part % box == 0 && pos < w.len && pos + box > w.seen) {
                 const int index = (unsigned)pos / (unsigned)p.c.page;
                 f.slot = pos - index * p.c.page;
-                int page = p.t.pages[w.b * p.t.stride + index];
+                const int head = w.h / (p.units / p.Hkv);
+                int page = p.t.pages[w.b * p.t.stride + head * p.t.head_stride + index];
                 if (page < 0 || page >= p.c.n_pages) {
                     atomicOr(p.c.err, kCacheErrPage);
                     page = 0;
                 }
-                f.unit = page * p.Hkv + w.h / (p.units / p.Hkv);
+                f.unit = page * p.Hkv + head;
             }
             g += 4;
         };

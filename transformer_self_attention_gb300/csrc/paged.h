@@ -32,10 +32,11 @@ struct CacheView {
     int* err = nullptr;
 };
 struct PageTable {
-    const int* pages = nullptr;  // [B, max_pages], row stride `stride`
+    const int* pages = nullptr;  // [B, max_pages], row stride `stride`; decode: also one for each kv head, head_stride apart
     const int* len = nullptr;    // [B]
     long long stride = 0;
     int max_pages = 0;
+    long long head_stride = 0;
 };
 struct CacheWriteParams {
     CacheView c;
@@ -53,6 +54,32 @@ struct CacheReadParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, bool e4m3, int n_sm, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheReadParams& p, bool e4m3, cudaStream_t stream);
+
+// ---------------------------------------------------------------- page bounds
+// Of page g and head h, over its positions that are inside a sequence: codes[g][h][0] and [1], the smallest and the largest
+// key element of every channel as 8-bit whole numbers times 2^(exps[g][h] - 127), rounded outwards; exps 255: a key is not
+// finite.
+struct BoundsParams {
+    CacheView c;
+    PageTable t;
+    int8_t* codes;
+    uint8_t* exps;
+    const int* new_len;  // [B], or null: all positions
+    int B;
+};
+struct SelectParams {
+    CacheView c;
+    PageTable t;
+    const int8_t* codes;
+    const uint8_t* exps;
+    const void* q;  // [B, Hq, S_q, d] bf16
+    int B, Hkv, rows, keep, sinks, recent;
+    int* out_table;  // [B, Hkv, keep]
+    int* out_len;    // [B]
+};
+constexpr int kSelectMostPages = 48 << 10;  // of a sequence: a word for each in shared memory
+cudaError_t launch_bounds_update(const BoundsParams& p, bool e4m3, int n_sm, cudaStream_t stream);
+cudaError_t launch_bounds_select(const SelectParams& p, int n_sm, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged decode
 // Work units are (sequence, kv head), in that order (over E4M3 pages with more than 32 rows to a head, (sequence, kv head,

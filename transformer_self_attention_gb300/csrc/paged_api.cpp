@@ -13,21 +13,7 @@
 #include "attn.h"
 #include "device_once.h"
 #include "paged.h"
-
-struct attn_rope_plan {
-    attn::RopeTable t;
-    double freq[attn::kRopeMaxPairs] = {};
-    double amplitude = 1.0;
-    int d = 0;
-};
-
-struct attn_cache_plan {
-    attn::CacheView c;
-    CUtensorMap map{};
-    bool e4m3 = false;
-    int box_rows = 16;
-    int device = 0, n_sm = 0;
-};
+#include "paged_host.h"
 
 struct attn_paged_plan {
     int B = 0, Hq = 0, Hkv = 0, S_q = 0, d = 0, kind = 0, window = 0;
@@ -40,6 +26,12 @@ struct attn_paged_plan {
     float2* d_ml = nullptr;
     int2* d_cut = nullptr;
 };
+
+using attn::aligned;
+using attn::on_device;
+using attn::table_ok;
+using attn::validate_paged;
+using attn::window_of;
 
 namespace {
 
@@ -84,8 +76,6 @@ bool encode_e4m3(CUtensorMap* map, const attn::CacheView& c, int rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 // Rows of `el`-byte elements: the first one and every stride on 16-byte boundaries.
 bool rows_ok(const attn_rows* r, int el) {
     const long long unit = 16 / el;
@@ -111,11 +101,6 @@ bool clear_error(int* err) {
     return cudaMemset(err, 0, sizeof(int)) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
 }
 
-bool on_device(int device) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == device;
-}
-
 attn_status rope_apply(attn_rope_handle h, attn_dtype dtype, int B, int S, int Hq, const attn_rows* Q,
                        const attn_rows* Q_out, int Hk, const attn_rows* K, const attn_rows* K_out,
                        const int* positions, long long pos_stride_b, long long pos_stride_s, bool inverse,
@@ -134,27 +119,6 @@ attn_status rope_apply(attn_rope_handle h, attn_dtype dtype, int B, int S, int H
                                             Hk, B, S, h->d, positions, pos_stride_b, pos_stride_s, inverse,
                                             dtype == ATTN_F32, n_sm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
-bool table_ok(const int* page_table, long long stride, int max_pages, const int* cache_len) {
-    return page_table && aligned(page_table, 4) && cache_len && aligned(cache_len, 4) && max_pages >= 1 &&
-           max_pages <= (1 << 26) && stride >= 0;
-}
-
-attn_status validate_paged(int B, int Hq, int Hkv, int S_q, attn_mask_kind kind, int window) {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S_q < 1) return ATTN_ERR_INVALID_ARG;
-    if ((int)kind < ATTN_MASK_FULL || (int)kind > ATTN_MASK_LOCAL_GLOBAL) return ATTN_ERR_INVALID_ARG;
-    if (kind != ATTN_MASK_FULL && kind != ATTN_MASK_CAUSAL && kind != ATTN_MASK_CAUSAL_SLIDING)
-        return ATTN_ERR_UNSUPPORTED;
-    if (kind == ATTN_MASK_CAUSAL_SLIDING && window < 0) return ATTN_ERR_INVALID_ARG;
-    if (B > ATTN_DECODE_MAX_BATCH || (long)(Hq / Hkv) * S_q > ATTN_DECODE_MAX_ROWS || Hkv > (1 << 16))
-        return ATTN_ERR_UNSUPPORTED;
-    return ATTN_OK;
-}
-
-// A window of 2^30 sees every position there can be; with more, a difference of positions would pass 32 bits.
-int window_of(attn_mask_kind kind, int window) {
-    return kind == ATTN_MASK_CAUSAL_SLIDING ? std::min(window, attn::kPagedMostPositions) : -1;
 }
 
 void free_paged(attn_paged_plan* h) {
@@ -362,6 +326,13 @@ attn_status attn_paged_create(attn_paged_handle* out, int B, int Hq, int Hkv, in
 attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
                                long long table_stride, int max_pages, const int* cache_len, void* O, float* LSE,
                                void* stream) {
+    return attn_paged_forward_heads(h, cache, Q, page_table, table_stride, 0, max_pages, cache_len, O, LSE, stream);
+}
+
+attn_status attn_paged_forward_heads(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
+                                     long long table_stride, long long head_stride, int max_pages, const int* cache_len,
+                                     void* O, float* LSE, void* stream) {
+    if (head_stride < 0) return ATTN_ERR_INVALID_ARG;
     if (!h || !cache || !Q || !O || !aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4)) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (cache->c.Hkv != h->Hkv || cache->c.d != h->d || cache->device != h->device || !on_device(h->device))
@@ -377,6 +348,7 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
     p.q = Q; p.o = O; p.lse = LSE;
     p.c = cache->c;
     p.t.pages = page_table; p.t.len = cache_len; p.t.stride = table_stride; p.t.max_pages = max_pages;
+    p.t.head_stride = head_stride;
     p.part_o = h->d_part; p.part_ml = h->d_ml; p.cut = h->d_cut;
     p.B = h->B; p.Hq = h->Hq; p.Hkv = h->Hkv; p.S_q = h->S_q; p.rows = h->Hq / h->Hkv * h->S_q;
     p.units = units;
