@@ -810,6 +810,51 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
                                const int* cache_len, int keep, int sinks, int recent, int* out_table, int* out_len,
                                void* stream);
 
+/*
+ * ---------------------------------------------------------------- attention weights of cached positions
+ * The attention weight that every cached position has received, summed over the rows of a kv head and over steps, and
+ * eviction of the positions that received least.  ("第 8 章 现代大模型架构" (theaiera.top), the sections on the KV cache's
+ * size.)
+ *
+ *   weights : float32 [n_pages, Hkv, page], a number for every slot and kv head of the cache, the caller's.
+ *
+ * Pages of the sequences of one call must be distinct.  Both calls run on the cache's device and need no workspace.
+ */
+
+/*
+ * attn_weights_accumulate -- after a decode step over the cache, for every position j < cache_len[b] and kv head:
+ *   W_j <- decay W_j + sum over the rows i that see j of exp(scale q_i . k_j - LSE_i),
+ * where W_j counts as 0 for the step's own positions, j >= cache_len[b] - S_q, whatever it holds.
+ *   Q, LSE : the step's queries, bf16 [B, Hq, S_q, d], contiguous, 16-byte aligned, and its logarithms of sums, float32
+ *            [B, Hq, S_q]; rows with LSE = -inf (no visible key) add nothing.
+ *   scale, kind, window : the step's, as attn_paged_create.
+ *   decay  : 0 .. 1.
+ * Sums are float32; a sum has a fixed order.  Slots at or past the lengths are left as they were.
+ * Errors: as attn_paged_forward, ATTN_ERR_UNSUPPORTED above B * Hkv * max_pages * page of about 2^35.
+ */
+attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, int Hq, int S_q, const void* Q,
+                                    const float* LSE, float scale, attn_mask_kind kind, int window, float decay,
+                                    const int* page_table, long long table_stride, int max_pages, const int* cache_len,
+                                    void* stream);
+
+/*
+ * attn_weights_evict -- cut every sequence of n = cache_len[b] > keep + recent positions down to that many: for each kv
+ * head the `keep` positions of largest weight among the first n - recent (of equal weights the first; a NaN counts as the
+ * largest), and the last `recent`.  Their keys, values, row factors and weights become positions 0, 1, .. in their order;
+ * the rotation of a key stays that of its old position.  Shorter sequences keep all.
+ *   to_table : where the kept rows go: int32 device [B][to_max_pages], row stride to_stride, of pages that hold nothing
+ *              of this call's sequences (what was there stays); with room for min(keep + recent, max_pages * page) positions.  NULL: they
+ *              move within their own pages; slots behind the new lengths are left as they were, and the pages behind them
+ *              are free.
+ *   out_len  : int32 device [B], min(n, keep + recent).   kept : int32 device [B, Hkv, keep + recent], the old positions of
+ *              the new ones, then -1.  Neither may be an input.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.  A sequence whose length is not followed counts as
+ * empty, rows whose page is out of range are not moved; both are recorded in the cache's error word.
+ */
+attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const int* page_table, long long table_stride,
+                               int max_pages, const int* cache_len, int keep, int recent, const int* to_table,
+                               long long to_stride, int to_max_pages, int* out_len, int* kept, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,3 +81,55 @@ def decode_chosen(Q, vals, table, page, lens, chosen, scale):
             short.append(n - (-(-n // page) - len(c)) * page)
         outs.append(pu.decode(Q[:, h * group:(h + 1) * group], vals[:, h:h + 1], tab, page, short, scale, 1, 0))
     return tuple(torch.cat([o[i] for o in outs], dim=1) for i in range(4))
+
+
+def weigh(Q, LSE, W, vals, table, page, lens, scale, kind, window, decay):
+    """W [n_pages, Hkv, page] after a step (float64), and a bound on its float32 errors."""
+    B, Hq, S_q, d = Q.shape
+    Hkv = vals.shape[1]
+    out, bound = W.double().clone(), torch.zeros(W.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        K, _ = pu.dense(vals, table, page, b, n)  # [Hkv, n, d]
+        q = Q[b].double().view(Hkv, -1, S_q, d)
+        lse = LSE[b].double().view(Hkv, -1, S_q)
+        j = torch.arange(n)
+        p, slot = table[b].long()[j // page].clamp(0, W.shape[0] - 1), j % page
+        new = out[p, :, slot].T * decay  # [Hkv, n]
+        new[:, max(0, n - S_q):] = 0
+        err = new.abs() * 2.0 ** -24
+        for i in range(S_q):
+            t = n - S_q + i
+            hi = n if kind == 0 else t + 1
+            lo = max(0, t - window) if kind == 3 else 0
+            if hi <= lo:
+                continue
+            s = torch.einsum("hgd,hjd->hgj", q[:, :, i], K[:, lo:hi]) * scale
+            big = torch.einsum("hgd,hjd->hgj", q[:, :, i].abs(), K[:, lo:hi].abs()) * scale
+            x = lse[:, :, i, None]
+            live = x > -math.inf
+            w = torch.where(live, torch.exp(s - torch.where(live, x, torch.zeros_like(x))), torch.zeros_like(s))
+            # float32 sums of d products and the exponent's rounding: d + 8 half steps of what they are made of;
+            # exp2 two more, and the sum over the rows one each
+            r = (big * (d + 8) + torch.where(live, x.abs(), torch.zeros_like(x)) * 2) * 2.0 ** -23 + (2 + Hq * S_q) * 2.0 ** -24
+            new[:, lo:hi] += w.sum(1)
+            err[:, lo:hi] += (w * r).sum(1)
+        out[p, :, slot] = new.T
+        bound[p, :, slot] = err.T + out[p, :, slot].abs() * 2.0 ** -23
+    return out, bound
+
+
+def evict(W, table, page, lens, keep, recent):
+    """Old positions [B][Hkv] of the positions that stay."""
+    out = []
+    for b, n in enumerate(lens):
+        rows = []
+        for h in range(W.shape[1]):
+            old = max(0, n - recent)
+            w = [float(W[int(table[b, i // page]), h, i % page]) for i in range(old)]
+            key = [-math.inf if math.isnan(x) else -x for x in w]
+            nan_first = sorted(range(old), key=lambda i: (not math.isnan(w[i]), key[i], i))
+            rows.append(sorted(nan_first[:keep]) + list(range(old, n)) if n > keep + recent else list(range(n)))
+        out.append(rows)
+    return out

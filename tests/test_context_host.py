@@ -40,3 +40,22 @@ def test_selection_arguments_are_refused():
         bounds.select(Q, table, lens, keep=2 ** 40)
     with pytest.raises(ValueError):
         tsa.PageBounds(_fake_cache(), codes=torch.zeros((8, 2, 2, 64), dtype=torch.uint8))
+
+
+def test_weights_arguments_are_refused():
+    assert tsa.attn_weights_accumulate(0, 16, 1, 1, 1, 16, 16, 1.0, 1, 0, 1.0, 16, 1, 1, 16) == BAD
+    assert tsa.attn_weights_evict(0, 16, 1, 16, 1, 1, 16, 4, 1, 0, 0, 0, 32, 32) == BAD
+    weights = tsa.PageWeights(_fake_cache(), weights=torch.zeros((8, 2, 16)))
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    Q, LSE = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16), torch.zeros((1, 4, 1))
+    for q, lse in ((Q.float(), LSE), (Q[:, :3], LSE[:, :3]), (Q, LSE[:, :2]), (Q, LSE.double()), (Q[..., :32], LSE),
+                   (Q.expand(2, 4, 1, 64), LSE)):
+        with pytest.raises(ValueError):
+            weights.accumulate(q, lse, table, lens)
+    for kw in (dict(keep=-1), dict(keep=0), dict(keep=4, recent=-1), dict(keep=2 ** 31),
+               dict(keep=40, to_table=torch.zeros((1, 2), dtype=torch.int32)),
+               dict(keep=4, to_table=torch.zeros((2, 4), dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            weights.evict(table, lens, **kw)
+    with pytest.raises(ValueError):
+        tsa.PageWeights(_fake_cache(), weights=torch.zeros((8, 16)))

@@ -38,7 +38,8 @@ EXPORTED = ("attn_create", "attn_forward", "attn_destroy", "attn_status_string",
             "attn_rope_destroy", "attn_cache_create", "attn_cache_write", "attn_cache_read",
             "attn_cache_poll_device_error", "attn_cache_destroy", "attn_paged_create", "attn_paged_forward",
             "attn_paged_set_grid_limit", "attn_paged_set_watchdog", "attn_paged_destroy", "attn_paged_split_host",
-            "attn_paged_forward_heads", "attn_bounds_update", "attn_bounds_select")
+            "attn_paged_forward_heads", "attn_bounds_update", "attn_bounds_select",
+            "attn_weights_accumulate", "attn_weights_evict")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DECODE_MAX_BATCH = 1024
 DECODE_MAX_ROWS = 64
@@ -135,6 +136,8 @@ def _load():
                        ("attn_paged_forward_heads", [P, P, P, P, LL, LL, I, P, P, P, P]),
                        ("attn_bounds_update", [P, P, P, I, P, LL, I, P, P, P]),
                        ("attn_bounds_select", [P, P, P, I, I, I, P, P, LL, I, P, I, I, I, P, P, P]),
+                       ("attn_weights_accumulate", [P, P, I, I, I, P, P, F, I, I, F, P, LL, I, P, P]),
+                       ("attn_weights_evict", [P, P, I, P, LL, I, P, I, I, P, LL, I, P, P, P]),
                        ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_set_watchdog", [P, LL, I]),
                        ("attn_paged_destroy", [P]),
                        ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, ctypes.POINTER(I), P, I,
@@ -545,6 +548,22 @@ def attn_bounds_select(cache, codes_ptr, exponents_ptr, B, Hq, S_q, q_ptr, table
     """Page tables of the pages with the largest scores; returns the status."""
     return _lib.attn_bounds_select(cache, codes_ptr, exponents_ptr, B, Hq, S_q, q_ptr, table_ptr, table_stride, max_pages,
                                    len_ptr, _int(keep), _int(sinks), _int(recent), out_table_ptr, out_len_ptr,
+                                   stream or None)
+
+
+def attn_weights_accumulate(cache, weights_ptr, B, Hq, S_q, q_ptr, lse_ptr, scale, kind, window, decay, table_ptr,
+                            table_stride, max_pages, len_ptr, stream=0) -> int:
+    """Add a step's attention weights to the positions'; returns the status."""
+    return _lib.attn_weights_accumulate(cache, weights_ptr, B, Hq, S_q, q_ptr, lse_ptr, float(scale), _int(kind),
+                                        _int(window), float(decay), table_ptr, table_stride, max_pages, len_ptr,
+                                        stream or None)
+
+
+def attn_weights_evict(cache, weights_ptr, B, table_ptr, table_stride, max_pages, len_ptr, keep, recent, to_ptr,
+                       to_stride, to_max_pages, out_len_ptr, kept_ptr, stream=0) -> int:
+    """Cut sequences down to their heaviest and latest positions; returns the status."""
+    return _lib.attn_weights_evict(cache, weights_ptr, B, table_ptr, table_stride, max_pages, len_ptr, _int(keep),
+                                   _int(recent), to_ptr or None, to_stride, to_max_pages, out_len_ptr, kept_ptr,
                                    stream or None)
 
 
@@ -1011,8 +1030,89 @@ class PageBounds:
                         _int32("length", length, (B,), self._device)),
                        (Q, page_table, cache_len, table, length, self.codes, self.exponents))
             if st != ATTN_OK:
-                raise AttnError(st, "attn_bounds_select")
+                raise AttnError(st, "attn_bounds_select",
+            "attn_weights_accumulate", "attn_weights_evict")
         return table, length
+
+
+class PageWeights:
+    """The attention weight that each position of a PagedCache has received (``attn_weights_*``).
+
+    weights: float32 [n_pages, Hkv, page], allocated (zeroed) unless given; the caller's to use.  Generation with a
+    bounded cache:
+
+        O, LSE = step(Q, cache, page_table, cache_len)
+        weights.accumulate(Q, LSE, page_table, cache_len)
+        cache_len, kept = weights.evict(page_table, cache_len, keep=1024, recent=256)
+
+    A kept key stays rotated by its old position: rotate new rows by positions of your own (RotaryPositions) before
+    they are written, once positions and places in the cache differ.
+    """
+
+    def __init__(self, cache, weights=None):
+        _need_torch()
+        n_pages, Hkv, page, _ = cache.shape
+        self.cache, self._device = cache, cache._device
+        shape = (n_pages, Hkv, page)
+        if weights is None:
+            weights = torch.zeros(shape, dtype=torch.float32, device=cache.device)
+            torch.cuda.current_stream(cache.device).synchronize()  # they are there before the first call on any stream
+        if (weights.shape != shape or weights.dtype is not torch.float32 or weights.get_device() != self._device
+                or not weights.is_contiguous()):
+            raise ValueError(f"weights must be a contiguous float32 tensor of shape {shape} on {cache.device}")
+        self.weights = weights
+
+    def accumulate(self, Q, LSE, page_table, cache_len, scale=None, kind=MASK_CAUSAL, window=0, decay=1.0, stream=None):
+        """Multiply the weights of all positions by decay and add those of a decode step: Q [B, Hq, S_q, d] bf16 and
+        LSE [B, Hq, S_q] float32 as PagedDecodeAttention took and gave them, its scale, kind and window."""
+        cache = self.cache
+        _, Hkv, _, d = cache.shape
+        B, table = cache._table(page_table, cache_len)
+        if (Q.dim() != 4 or Q.shape[0] != B or Q.shape[3] != d or Q.shape[1] < 1 or Q.shape[1] % Hkv or Q.shape[2] < 1
+                or Q.dtype is not torch.bfloat16 or Q.get_device() != self._device or not Q.is_contiguous()):
+            raise ValueError(f"Q must be a contiguous bfloat16 tensor [{B}, Hq, S_q, {d}] on {cache.device}, Hq a "
+                             f"multiple of {Hkv}, S_q at least 1")
+        if (LSE.shape != Q.shape[:3] or LSE.dtype is not torch.float32 or LSE.get_device() != self._device
+                or not LSE.is_contiguous()):
+            raise ValueError(f"LSE must be a contiguous float32 tensor of shape {tuple(Q.shape[:3])} on {cache.device}")
+        if B:
+            st = _call(self._device, stream, _lib.attn_weights_accumulate,
+                       (cache.handle, self.weights.data_ptr(), B, Q.shape[1], Q.shape[2], Q.data_ptr(), LSE.data_ptr(),
+                        float(scale) if scale is not None else d ** -0.5, _int(kind), _int(window), float(decay), *table),
+                       (Q, LSE, page_table, cache_len, self.weights, cache.pages, cache.scales))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_weights_accumulate")
+
+    def evict(self, page_table, cache_len, keep, recent=0, to_table=None, length=None, kept=None, stream=None):
+        """Cut every sequence down to keep + recent positions: for each kv head the heaviest among all but the last
+        ``recent``, and those.  They move to the front of the pages of to_table (int32 CUDA [B, pages], pages that hold
+        nothing of these sequences), or of their own.  Returns (length, kept): the new lengths, int32 [B], and the old
+        positions of the new ones, int32 [B, Hkv, keep + recent], -1 behind them."""
+        cache = self.cache
+        B, table = cache._table(page_table, cache_len)
+        keep, recent = _int(keep), _int(recent)
+        if keep < 0 or recent < 0 or keep + recent < 1:
+            raise ValueError("keep and recent must not be negative, nor both zero")
+        to = (None, 0, 0)
+        if to_table is not None:
+            rows, to = cache._table(to_table, cache_len)
+            if rows != B:
+                raise ValueError(f"to_table must have {B} rows")
+            if to[2] * cache.shape[2] < min(keep + recent, table[2] * cache.shape[2]):
+                raise ValueError("to_table has too few pages for the positions that stay")
+        shape = (B, cache.shape[1], keep + recent)
+        if length is None:
+            length = _new((B,), torch.int32, cache.device, stream)
+        if kept is None:
+            kept = _new(shape, torch.int32, cache.device, stream)
+        if B:
+            st = _call(self._device, stream, _lib.attn_weights_evict,
+                       (cache.handle, self.weights.data_ptr(), B, *table, keep, recent, *to[:3],
+                        _int32("length", length, (B,), self._device), _int32("kept", kept, shape, self._device)),
+                       (page_table, cache_len, to_table, length, kept, self.weights, cache.pages, cache.scales))
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_weights_evict")
+        return length, kept
 
 
 # ---------------------------------------------------------------- torch convenience

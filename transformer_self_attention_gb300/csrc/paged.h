@@ -169,4 +169,27 @@ cudaError_t launch_paged_e4m3(const PagedParams& p, int grid, cudaStream_t strea
 // Joins the parts of cut units; enqueued behind either as a programmatic dependent.
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream);
 
+// ---------------------------------------------------------------- attention weights of positions
+struct WeighParams {
+    PagedParams g;     // q, c, t, B, Hq, Hkv, S_q, rows, units, causal, scale_log2; window: of the blocks that are walked
+    const float* lse;  // [B, Hq, S_q]
+    float* w;          // [n_pages, Hkv, page]
+    float decay;
+    int window;        // of the mask, -1: none
+};
+struct EvictParams {
+    CacheView c;
+    PageTable t;
+    float* w;
+    const int* to;  // table of the pages that rows move to
+    long long to_stride;
+    int* out_len;   // [B]
+    int* kept;      // [B, Hkv, keep + recent]
+    int B, keep, recent, in_place;
+    int cached;     // weights of a head that fit in shared memory
+};
+constexpr int kEvictCached = 48 << 10;
+cudaError_t launch_weigh(const WeighParams& p, bool e4m3, int n_sm, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, bool e4m3, cudaStream_t stream);
+
 }  // namespace attn
