@@ -855,6 +855,51 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
                                int max_pages, const int* cache_len, int keep, int recent, const int* to_table,
                                long long to_stride, int to_max_pages, int* out_len, int* kept, void* stream);
 
+/*
+ * ---------------------------------------------------------------- shared prefixes
+ * A decode step for a batch whose sequences share long prefixes (a system prompt, a document, samples of one prompt), each
+ * prefix's keys and values read once for all of its sequences.  Row i of sequence b attends to the prefix_len[g] positions
+ * of its prefix g = prefix_of[b], and behind them to the positions of its own: as attn_paged_forward over a
+ * sequence of the prefix's positions followed by its own, with ATTN_MASK_FULL or ATTN_MASK_CAUSAL (S_q new rows, the last of
+ * the own positions).  Prefixes and own positions are pages of one cache; either may end inside a page.
+ *
+ * Rounding: over the prefix scores and sums are float32, weights are rounded to bf16 (2^-9 of a weight) for the second
+ * product, after their sum is taken; over the own positions as in attn_paged_forward.  Parts are joined in float32,
+ * and O is rounded once.  What is said there of infinities and of queries that are not finite holds here.
+ *
+ * A handle owns the parts' memory; it must not be used by two calls in flight at once, captured graphs included.
+ */
+typedef struct attn_prefix_plan* attn_prefix_handle;
+
+/* attn_prefix_create -- arguments and errors as attn_paged_create (the sliding kinds are ATTN_ERR_UNSUPPORTED). */
+attn_status attn_prefix_create(attn_prefix_handle* out, int B, int Hq, int Hkv, int S_q, int d, float scale,
+                               attn_mask_kind kind);
+
+/*
+ * attn_prefix_forward -- enqueue one step over `cache` on `stream`: three kernels.
+ *   prefix_table, prefix_len : int32 device [n_prefix][prefix_max_pages], row stride prefix_stride, and [n_prefix].  A
+ *                              length may be 0, and a prefix may have no sequence.
+ *   n_prefix  : 1 .. ATTN_DECODE_MAX_BATCH.
+ *   prefix_of : int32 device [B], the prefix of every sequence or -1 for none; NULL: all have the only one.
+ *   page_table, cache_len : of the own positions, as attn_paged_forward; a length may be 0.
+ *   Q, O, LSE : as attn_paged_forward.  A row that sees nothing gives O = 0 and LSE = -inf.
+ * Errors: as attn_paged_forward; ATTN_ERR_UNSUPPORTED also where n_prefix and the tables' sizes pass 32-bit numbers of
+ * 128-position tiles.  Lengths, page numbers and prefix numbers that are not followed are recorded in the cache's error
+ * word (a prefix number outside -1 .. n_prefix - 1 as a position; its sequence has none then).
+ */
+attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, const void* Q, const int* prefix_table,
+                                long long prefix_stride, int prefix_max_pages, const int* prefix_len, int n_prefix,
+                                const int* prefix_of, const int* page_table, long long table_stride, int max_pages,
+                                const int* cache_len, void* O, float* LSE, void* stream);
+
+/* attn_prefix_set_grid_limit, attn_prefix_set_watchdog -- test hooks, as for a paged decode handle (withhold: a
+ * loading warp stops in front of its n-th tile of a prefix too). */
+attn_status attn_prefix_set_grid_limit(attn_prefix_handle h, int max_ctas);
+attn_status attn_prefix_set_watchdog(attn_prefix_handle h, long long limit_ns, int withhold);
+
+/* attn_prefix_destroy -- free the handle (synchronises the device first); NULL is ignored. */
+attn_status attn_prefix_destroy(attn_prefix_handle h);
+
 #ifdef __cplusplus
 }
 #endif

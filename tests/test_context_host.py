@@ -59,3 +59,20 @@ def test_weights_arguments_are_refused():
             weights.evict(table, lens, **kw)
     with pytest.raises(ValueError):
         tsa.PageWeights(_fake_cache(), weights=torch.zeros((8, 16)))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(kind=tsa.MASK_CAUSAL_SLIDING), tsa.ATTN_ERR_UNSUPPORTED), (dict(kind=tsa.MASK_SLIDING), tsa.ATTN_ERR_UNSUPPORTED),
+    (dict(kind=9), BAD), (dict(B=0), BAD), (dict(Hq=3), BAD), (dict(S_q=0), BAD), (dict(scale=0.0), BAD),
+    (dict(scale=float("inf")), BAD), (dict(d=96), tsa.ATTN_ERR_UNSUPPORTED), (dict(B=1025), tsa.ATTN_ERR_UNSUPPORTED),
+    (dict(S_q=33), tsa.ATTN_ERR_UNSUPPORTED)])
+def test_prefix_create_refuses(kw, status):
+    with pytest.raises(tsa.AttnError) as e:
+        tsa.attn_prefix_create(**{**dict(B=2, Hq=4, Hkv=2, S_q=1, d=64, scale=0.1, kind=tsa.MASK_CAUSAL), **kw})
+    assert e.value.status == status
+
+
+def test_prefix_arguments_are_refused():
+    assert tsa.attn_prefix_forward(0, 0, 16, 16, 1, 1, 16, 1, 0, 16, 1, 1, 16, 16) == BAD
+    assert tsa.attn_prefix_set_grid_limit(0, 1) == BAD and tsa.attn_prefix_set_watchdog(0, 1) == BAD
+    assert tsa.attn_prefix_destroy(0) == tsa.ATTN_OK

@@ -39,7 +39,9 @@ EXPORTED = ("attn_create", "attn_forward", "attn_destroy", "attn_status_string",
             "attn_cache_poll_device_error", "attn_cache_destroy", "attn_paged_create", "attn_paged_forward",
             "attn_paged_set_grid_limit", "attn_paged_set_watchdog", "attn_paged_destroy", "attn_paged_split_host",
             "attn_paged_forward_heads", "attn_bounds_update", "attn_bounds_select",
-            "attn_weights_accumulate", "attn_weights_evict")
+            "attn_weights_accumulate", "attn_weights_evict",
+            "attn_prefix_create", "attn_prefix_forward", "attn_prefix_set_grid_limit", "attn_prefix_set_watchdog",
+            "attn_prefix_destroy")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DECODE_MAX_BATCH = 1024
 DECODE_MAX_ROWS = 64
@@ -138,6 +140,10 @@ def _load():
                        ("attn_bounds_select", [P, P, P, I, I, I, P, P, LL, I, P, I, I, I, P, P, P]),
                        ("attn_weights_accumulate", [P, P, I, I, I, P, P, F, I, I, F, P, LL, I, P, P]),
                        ("attn_weights_evict", [P, P, I, P, LL, I, P, I, I, P, LL, I, P, P, P]),
+                       ("attn_prefix_create", [ctypes.POINTER(P), I, I, I, I, I, F, I]),
+                       ("attn_prefix_forward", [P, P, P, P, LL, I, P, I, P, P, LL, I, P, P, P, P]),
+                       ("attn_prefix_set_grid_limit", [P, I]), ("attn_prefix_set_watchdog", [P, LL, I]),
+                       ("attn_prefix_destroy", [P]),
                        ("attn_paged_set_grid_limit", [P, I]), ("attn_paged_set_watchdog", [P, LL, I]),
                        ("attn_paged_destroy", [P]),
                        ("attn_paged_split_host", [I, I, I, I, I, I, I, P, I, ctypes.POINTER(I), P, I,
@@ -567,6 +573,35 @@ def attn_weights_evict(cache, weights_ptr, B, table_ptr, table_stride, max_pages
                                    stream or None)
 
 
+def attn_prefix_create(B, Hq, Hkv, S_q, d, scale, kind) -> int:
+    """Returns a shared-prefix decode handle (int); raises AttnError on a non-OK status."""
+    h = ctypes.c_void_p()
+    st = _lib.attn_prefix_create(ctypes.byref(h), _int(B), _int(Hq), _int(Hkv), _int(S_q), _int(d), float(scale), _int(kind))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_prefix_create")
+    return h.value
+
+
+def attn_prefix_forward(handle, cache, q_ptr, prefix_ptr, prefix_stride, prefix_max_pages, prefix_len_ptr, n_prefix,
+                        prefix_of_ptr, table_ptr, table_stride, max_pages, len_ptr, o_ptr, lse_ptr=0, stream=0) -> int:
+    """Enqueue one decode step over shared prefixes and own positions; returns the status."""
+    return _lib.attn_prefix_forward(handle, cache, q_ptr, prefix_ptr, prefix_stride, prefix_max_pages, prefix_len_ptr,
+                                    _int(n_prefix), prefix_of_ptr or None, table_ptr, table_stride, max_pages, len_ptr,
+                                    o_ptr, lse_ptr or None, stream or None)
+
+
+def attn_prefix_set_grid_limit(handle: int, max_ctas: int) -> int:
+    return _lib.attn_prefix_set_grid_limit(handle, _int(max_ctas))
+
+
+def attn_prefix_set_watchdog(handle: int, limit_ns: int, withhold: int = 0) -> int:
+    return _lib.attn_prefix_set_watchdog(handle, int(limit_ns), _int(withhold))
+
+
+def attn_prefix_destroy(handle: int) -> int:
+    return _lib.attn_prefix_destroy(handle)
+
+
 def attn_paged_set_grid_limit(handle: int, max_ctas: int) -> int:
     return _lib.attn_paged_set_grid_limit(handle, _int(max_ctas))
 
@@ -962,6 +997,82 @@ class PagedDecodeAttention:
             raise AttnError(st, "attn_paged_set_watchdog")
 
 
+class SharedPrefixAttention:
+    """A decode plan over a PagedCache for a batch whose sequences share long prefixes (``attn_prefix_*``), each prefix
+    read once for all of its sequences.
+
+    Q: [B, Hq, S_q, d] bf16.  Sequence b attends to the prefix_len[g] positions of its prefix g = prefix_of[b], and
+    behind them to its own cache_len[b], of which the last S_q are the new rows'.  kind: MASK_CAUSAL or MASK_FULL.
+    Returns (O like Q, LSE float32 [B, Hq, S_q]); a row that sees no key gives zeros and -inf.
+    """
+
+    def __init__(self, B, Hq, Hkv, S_q, d, scale=None, kind=MASK_CAUSAL, device=None):
+        import math
+        _need_torch()
+        self.shape = (int(B), int(Hq), int(Hkv), int(S_q), int(d))
+        self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(d)
+        self.kind = int(kind)
+        with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+            self._device = torch.cuda.current_device()
+            self.device = torch.device("cuda", self._device)
+            self.handle = attn_prefix_create(B, Hq, Hkv, S_q, d, self.scale, self.kind)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            with torch.cuda.device(self.device):
+                attn_prefix_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __call__(self, Q, cache, prefix_table, prefix_len, page_table, cache_len, prefix_of=None, O=None, LSE=None,
+                 stream=None, want_lse=True):
+        """prefix_table: int32 CUDA [n_prefix, pages]; prefix_len: int32 CUDA [n_prefix]; prefix_of: int32 CUDA [B], -1
+        for none (default: the only prefix); page_table [B, max_pages] and cache_len [B]: the sequences' own pages."""
+        B, Hq, _, S_q, d = self.shape
+        n_prefix, prefix = cache._table(prefix_table, prefix_len)
+        rows, table = cache._table(page_table, cache_len)
+        if rows != B:
+            raise ValueError(f"page_table must have {B} rows")
+        if n_prefix < 1 or (prefix_of is None and n_prefix != 1):
+            raise ValueError("give at least one prefix, and prefix_of if there are several")
+        of = None if prefix_of is None else _int32("prefix_of", prefix_of, (B,), self._device)
+        shape = (B, Hq, S_q, d)
+        for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
+                                  ("LSE", LSE, shape[:3], torch.float32)):
+            if (t is not None or name == "Q") and (t.dtype is not dt or t.get_device() != self._device
+                                                   or t.shape != want or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {want} on {self.device}")
+        if O is None:
+            O = _new(shape, torch.bfloat16, self.device, stream)
+        if LSE is None and want_lse:
+            LSE = _new(shape[:3], torch.float32, self.device, stream)
+        st = _call(self._device, stream, _lib.attn_prefix_forward,
+                   (self.handle, cache.handle, Q.data_ptr(), *prefix, n_prefix, of, *table, O.data_ptr(),
+                    None if LSE is None else LSE.data_ptr()),
+                   (Q, O, LSE, prefix_table, prefix_len, prefix_of, page_table, cache_len, cache.pages, cache.scales))
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_prefix_forward")
+        return O, LSE
+
+    def set_grid_limit(self, max_ctas: int):
+        """Test hook: at most max_ctas CTAs per launch (long shares on small problems)."""
+        st = attn_prefix_set_grid_limit(self.handle, max_ctas)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_prefix_set_grid_limit")
+
+    def set_watchdog(self, limit_ns: int, withhold: int = 0):
+        """Test hook: the limit of every bounded wait; with withhold = n > 0 a loading warp stops in front of the n-th
+        tile or key block that it would load."""
+        st = attn_prefix_set_watchdog(self.handle, limit_ns, withhold)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_prefix_set_watchdog")
+
+
 class PageBounds:
     """Bounds of the keys of a PagedCache's pages, and the pages that they select (``attn_bounds_*``).
 
@@ -1031,7 +1142,9 @@ class PageBounds:
                        (Q, page_table, cache_len, table, length, self.codes, self.exponents))
             if st != ATTN_OK:
                 raise AttnError(st, "attn_bounds_select",
-            "attn_weights_accumulate", "attn_weights_evict")
+            "attn_weights_accumulate", "attn_weights_evict",
+            "attn_prefix_create", "attn_prefix_forward", "attn_prefix_set_grid_limit", "attn_prefix_set_watchdog",
+            "attn_prefix_destroy")
         return table, length
 
 

@@ -18,7 +18,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["attn_api.cpp", "schedule.cpp", "attn_fwd_tc.cu", "attn_fwd_f32.cu", "attn_noalloc.cu", "decode_api.cpp",
            "attn_decode.cu", "attn_bwd.cu", "paged_api.cpp", "attn_rope.cu", "attn_cache.cu", "attn_paged.cu", "attn_paged_e4m3.cu",
-           "context_api.cpp", "attn_bounds.cu", "attn_weights.cu"]
+           "context_api.cpp", "attn_bounds.cu", "attn_weights.cu", "attn_prefix.cu"]
 HEADERS = [os.path.join(INCLUDE, "attn.h")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")]
 
 

@@ -463,7 +463,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
                             &sh.red[((g * RW + row / ROWS) * ROWS + row % ROWS) * PITCH + c4]);
                         v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
                     }
-                    if (final) {
+                    if (final && p.whole_o) {
+                        __stcg(reinterpret_cast<float4*>(p.whole_o + ((long long)unit * p.rows + row) * D + c0 + c4), v);
+                    } else if (final) {
                         const float L = row_ml(row).y;
                         const float inv = L == 0.f ? 0.f : 1.f / L;
                         const uint2 o = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
@@ -480,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const __gri
         if (tid < p.rows) {
             const float2 v = row_ml(tid);
             if (!final) __stcg(&p.part_ml[slot * kRowsPad + tid], v);
+            else if (p.whole_o) __stcg(&p.whole_ml[(long long)unit * p.rows + tid], v);
             else if (p.lse) p.lse[(long long)unit * p.rows + tid] = (v.x + log2f(v.y)) * 0.6931471805599453f;
         }
         if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);

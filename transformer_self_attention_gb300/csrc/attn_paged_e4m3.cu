@@ -538,10 +538,15 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const float by = __shfl_sync(0xFFFFFFFFu, inv, r);
-                out[r] = !final ? acc[r] : none >> r & 1 ? 0.f : acc[r] * by;
+                out[r] = !final || p.whole_o ? acc[r] : none >> r & 1 ? 0.f : acc[r] * by;
             }
             if (gtid < D) {
-                if (final) {
+                if (final && p.whole_o) {
+                    float* o = p.whole_o + (out0 + row0) * D + gtid;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (row0 + r < rows) __stcg(o + r * D, out[r]);
+                } else if (final) {
                     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.o) + (out0 + row0) * D + gtid;
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
@@ -557,7 +562,9 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
                 float ref = m[0];
 #pragma unroll
                 for (int r = 1; r < kRows; ++r) ref = mine == r ? m[r] : ref;
-                if (!final) __stcg(&p.part_ml[slot + my_row], make_float2(unset >> mine & 1 ? ninf : ref, L));
+                const float2 ml = make_float2(unset >> mine & 1 ? ninf : ref, L);
+                if (!final) __stcg(&p.part_ml[slot + my_row], ml);
+                else if (p.whole_o) __stcg(&p.whole_ml[out0 + my_row], ml);
                 else if (p.lse) p.lse[out0 + my_row] = (ref + log2f(L)) * 0.6931471805599453f;
             }
             if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);

@@ -1,0 +1,740 @@
+// Decode attention for a batch whose sequences share long prefixes, each prefix's keys and values read once for all of its
+// sequences.
+//
+//     O_i = sum_j softmax_j(scale q_i . k_j) v_j   over the prefix of row i's sequence, then the positions of its own.
+//
+// Three kernels.  The first attends to the prefixes: the rows of all members of a prefix, for one kv head, are the rows of
+// a matrix, and a tile of 128 of them meets tiles of 128 positions,
+//     S [128 x 128] = Q K^T,   O [128 x d] += P V,   P = 2^(scale' S - m),
+// with tcgen05.mma: S and O in tensor memory, P written over S as bf16 (weights of at most 2^8 relative to a reference m
+// that moves only when a score passes it by 2^8; their sum is taken in float32 before they are rounded).  The decode
+// kernels (attn_paged.cu, attn_paged_e4m3.cu) attend to the own positions and leave unscaled sums in float32.  The
+// third joins the parts of every row: O = sum_k 2^(m_k - M) O_k / L, M = max m_k, L = sum_k 2^(m_k - M) l_k.
+//
+// Bound by the products and the exponentials where a prefix has many rows, by memory below about 150 rows: 4 flops a
+// row and element read, against about 280 flops a byte.  Work is cut over a grid of two CTAs a multiprocessor as in
+// the decode kernels: units (prefix, kv head, tile of rows) end to end on a line of cost, equal shares of it.  Two CTAs
+// share a multiprocessor, so that one's products run under the other's exponentials.
+//
+//   warps 0-3: one thread a row: the queries to shared memory, weights, the row's part to global memory
+//   bf16 pages: a warp for the TMA loads, boxes of 16 to 128 positions with 128 bytes of each row
+//   E4M3 pages: four warps that load codes, widen them (code * 2^k is a bf16 number) and write the tiles themselves
+//   last warp: one thread issues the products
+#include <cuda_bf16.h>
+
+#include <cstddef>
+
+#include "device_once.h"
+#include "paged_device.h"
+
+namespace attn {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kTile = 128;  // rows of a unit, and positions of a tile
+constexpr PagedShape kShape{kTile, 2, 2};
+
+template <bool E4M3>
+struct Roles {
+    static constexpr int kLoad = 4, kLoaders = E4M3 ? 4 : 1, kMma = kLoad + kLoaders, kThreads = 32 * (kMma + 1);
+};
+struct Shared {
+    unsigned cost[kPagedMaxBatch + 1];        // of the prefixes before g
+    unsigned short members[kPagedMaxBatch + 1];  // sequences of the prefixes before g
+    unsigned short order[kPagedMaxBatch];     // sequences by prefix
+    unsigned short rank[kPagedMaxBatch];      // a sequence's place among those of its prefix
+    unsigned count[kPagedMaxBatch];           // sequences of prefix g
+    unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full, p_half, p_full, o_full, q_full;
+    unsigned scan[2][12];
+    uint32_t tmem;
+    int abort;
+};
+template <int D>
+struct Cfg {
+    static constexpr int kStages = D == 64 ? 2 : 1;
+    static constexpr int kParts = D / 64;           // of a row, 128 bytes each
+    static constexpr int kPart = kTile * 128;
+    static constexpr int kBytes = kParts * kPart;   // of a tile of queries, keys or values
+    static constexpr int kOffK = kBytes, kOffV = kOffK + kStages * kBytes, kOffShared = kOffV + kStages * kBytes;
+    static constexpr int kSmem = 1024 + kOffShared + (int)sizeof(Shared);
+    static constexpr uint32_t kCols = 256, kColO = 128;
+    static_assert(kSmem <= 115712, "two CTAs per multiprocessor");
+};
+constexpr float kRescale = 8.f;  // log2 of how far a score may pass the reference
+
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int part, int kv,
+                                             int unit) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slot), "r"(part), "r"(kv), "r"(unit), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ int prefix_length(const PrefixParams& p, int g) {
+    const int n = p.t.len[g];
+    return n < 0 || n > p.t.max_pages * p.c.page ? 0 : n;
+}
+__device__ __forceinline__ int prefix_of(const PrefixParams& p, int b) {
+    if (!p.of) return 0;
+    const int g = p.of[b];
+    return g < 0 || g >= p.G ? -1 : g;
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+
+// Members by prefix and costs, by all threads; CTA 0 leaves them for the joining kernel.  Returns the line's length and,
+// in `units`, how many units there are.
+template <int THREADS>
+__device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& sh, int& units) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    for (int g = tid; g < p.G; g += THREADS) sh.count[g] = p.of ? 0 : p.B;
+    __syncthreads();
+    if (p.of && warp == 0) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            const int g = b < p.B ? prefix_of(p, b) : -1;
+            if (blockIdx.x == 0 && b < p.B && g < 0 && p.of[b] != -1) atomicOr(p.c.err, kCacheErrPosition);
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, g);
+            if (g >= 0) {
+                const unsigned before = sh.count[g];
+                sh.rank[b] = (unsigned short)(before + __popc(same & ((1u << lane) - 1)));
+                __syncwarp(same);
+                if ((same >> lane) == 1u) sh.count[g] = before + __popc(same);  // the last of them
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    unsigned carry_c = 0, carry_m = 0;
+    int own_units = 0;
+    if (tid == 0) {
+        sh.cost[0] = 0;
+        sh.members[0] = 0;
+    }
+    for (int g0 = 0; g0 < p.G; g0 += THREADS) {
+        const int g = g0 + tid;
+        unsigned c = 0, m = 0;
+        if (g < p.G) {
+            const int n = tiles_of(prefix_length(p, g));
+            if (blockIdx.x == 0 && p.t.len[g] != prefix_length(p, g)) atomicOr(p.c.err, kCacheErrPosition);
+            m = sh.count[g];
+            const int per = p.Hkv * (((int)m * p.rows + kTile - 1) / kTile);
+            c = per * paged_cost(n, kShape);
+            if (n) own_units += per;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const unsigned y = __shfl_up_sync(0xFFFFFFFFu, c, o), z = __shfl_up_sync(0xFFFFFFFFu, m, o);
+            if (lane >= o) {
+                c += y;
+                m += z;
+            }
+        }
+        if (lane == 31) {
+            sh.scan[0][warp] = c;
+            sh.scan[1][warp] = m;
+        }
+        __syncthreads();
+        unsigned all_c = carry_c, all_m = carry_m;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) {
+                c += sh.scan[0][w];
+                m += sh.scan[1][w];
+            }
+            all_c += sh.scan[0][w];
+            all_m += sh.scan[1][w];
+        }
+        if (g < p.G) {
+            sh.cost[g + 1] = carry_c + c;
+            sh.members[g + 1] = (unsigned short)(carry_m + m);
+        }
+        carry_c = all_c;
+        carry_m = all_m;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int o = 16; o; o /= 2) own_units += __shfl_xor_sync(0xFFFFFFFFu, own_units, o);
+    if (lane == 0) sh.scan[0][warp] = own_units;
+    for (int b = tid; b < p.B; b += THREADS) {
+        const int g = prefix_of(p, b), r = p.of ? sh.rank[b] : b;
+        if (g >= 0) sh.order[sh.members[g] + r] = (unsigned short)b;
+        if (blockIdx.x == 0) p.place[b] = g < 0 ? make_int2(-1, 0) : make_int2(g, r);
+    }
+    __syncthreads();
+    units = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) units += sh.scan[0][w];
+    if (blockIdx.x == 0) {
+        for (int g = tid; g < p.G; g += THREADS)
+            p.groups[g] = make_int4((int)sh.cost[g], sh.members[g], sh.members[g + 1] - sh.members[g],
+                                    tiles_of(prefix_length(p, g)));
+        if (tid == 0) p.groups[p.G] = make_int4((int)carry_c, units, 0, 0);
+    }
+    return carry_c;
+}
+
+// A CTA's part of a unit: tiles [g0, g1) of prefix g for rows of kv head h, from row `row0` of the prefix's rows on.
+struct Stretch {
+    unsigned at, end;
+    int g, h, row0, rows, len, g0, g1;
+};
+__device__ __forceinline__ Stretch stretch_begin(const PrefixParams& p, const PagedCuts& cuts, const Shared& sh) {
+    Stretch s{};
+    s.at = cuts.begin(blockIdx.x);
+    s.end = cuts.begin(blockIdx.x + 1);
+    int lo = 0, hi = p.G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (sh.cost[mid] <= s.at) lo = mid;
+        else hi = mid - 1;
+    }
+    s.g = lo;
+    return s;
+}
+__device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared& sh, Stretch& s) {
+    while (sh.cost[s.g + 1] <= s.at) ++s.g;
+    s.len = prefix_length(p, s.g);
+    const int n = tiles_of(s.len), all = (sh.members[s.g + 1] - sh.members[s.g]) * p.rows;
+    const unsigned per = paged_cost(n, kShape), into = s.at - sh.cost[s.g];
+    const int unit = (int)(into / per), blocks = (all + kTile - 1) / kTile;
+    const unsigned off = into - unit * per, to = min(per, off + (s.end - s.at));
+    s.h = unit / blocks;
+    s.row0 = (unit - s.h * blocks) * kTile;
+    s.rows = min(kTile, all - s.row0);
+    s.g0 = min(n, max(0, (int)off - (int)kShape.overhead));
+    s.g1 = min(n, max(0, (int)to - (int)kShape.overhead));
+    s.at += to - off;
+}
+
+// Largest of a row's scores; columns from `live` on do not count.
+template <bool MASKED>
+__device__ __forceinline__ float row_max(uint32_t t_s, int live) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = __int_as_float(0xFF800000);
+#pragma unroll
+    for (int c0 = 0; c0 < kTile; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(t_s + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float a = MASKED && c0 + e >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[e]);
+            const float b = MASKED && c0 + e + 1 >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[e + 1]);
+            m[(e >> 1) & 3] = fmax3(m[(e >> 1) & 3], a, b);
+        }
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Weights 2^(s scale - ref) as bf16 over the scores; returns their sum.  The first half (64 positions) is announced as soon
+// as it is written.
+template <bool MASKED>
+__device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale, float ref, uint32_t bar_half) {
+    const float2 scale2 = make_float2(scale, scale), nref = make_float2(-ref, -ref);
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c0 = 0; c0 < kTile; c0 += 32) {
+        uint32_t r[32], pk[16];
+        tmem_ld32(t_s + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float a = MASKED && c0 + 2 * e >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[2 * e]);
+            const float b = MASKED && c0 + 2 * e + 1 >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[2 * e + 1]);
+            const float2 x = __ffma2_rn(make_float2(a, b), scale2, nref);
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            if (e % 2) sum1 = __fadd2_rn(sum1, y);
+            else sum0 = __fadd2_rn(sum0, y);
+            pk[e] = pack_bf16x2(y.x, y.y);
+        }
+        tmem_st16(t_s + c0 / 2, pk);  // over columns that this thread has read
+        if (c0 == 32) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar_half);
+        }
+    }
+    return (sum0.x + sum0.y) + (sum1.x + sum1.y);
+}
+
+// 16 codes as bf16 numbers times a power of two (exact), two 16-byte pieces.
+__device__ __forceinline__ void widen16(const uint4& v, float f, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t h2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w[i / 2] >> 16 * (i % 2))));
+        float a, b;
+        asm("{.reg .f16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h2));
+        o[i] = pack_bf16x2(a * f, b * f);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const __grid_constant__ PrefixParams p) {
+    using C = Cfg<D>;
+    using R = Roles<E4M3>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffShared);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t s_q = smem_u32(smem), s_k = s_q + C::kOffK, s_v = s_q + C::kOffV;
+    if (tid == 0) {
+        prefetch_tmap(&p.tm);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sh.k_full[i]), E4M3 ? 4 : 1);
+            mbar_init(smem_u32(&sh.v_full[i]), E4M3 ? 4 : 1);
+            mbar_init(smem_u32(&sh.k_empty[i]), 1);
+            mbar_init(smem_u32(&sh.v_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.s_full), 1);
+        mbar_init(smem_u32(&sh.p_half), 128);
+        mbar_init(smem_u32(&sh.p_full), 128);
+        mbar_init(smem_u32(&sh.o_full), 1);
+        mbar_init(smem_u32(&sh.q_full), 4);
+        sh.abort = 0;
+    }
+    fence_barrier_init();
+    wait_for_kernel_before();
+    int units;
+    const unsigned W = prefix_plan<R::kThreads>(p, sh, units);
+    const PagedCuts cuts(W, units, gridDim.x, kShape);
+    let_kernel_behind_in();
+    if (blockIdx.x >= cuts.C || W == 0) return;
+    if (warp == R::kMma) {
+        tmem_alloc(smem_u32(&sh.tmem), C::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    const Watch watch{&sh.abort, p.c.err, p.watchdog_ns};
+    Stretch s = stretch_begin(p, cuts, sh);
+
+    if (warp < 4) {
+        // =================================================== rows
+        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + C::kColO;
+        int n = 0, stretch = 0;
+        while (s.at < s.end) {
+            stretch_open(p, sh, s);
+            if (s.g0 >= s.g1) continue;
+            // ---- the queries, 16-byte pieces of rows in the layout of the products (128-byte swizzle)
+            constexpr int kLanes = D / 8;
+            for (int i = tid; i < kTile * kLanes; i += 128) {
+                const int row = i / kLanes, c = i % kLanes;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < s.rows) {
+                    const int x = s.row0 + row, member = x / p.rows;
+                    const long long b = sh.order[sh.members[s.g] + member];
+                    v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) +
+                                                        ((b * p.Hkv + s.h) * p.rows + (x - member * p.rows)) * D + 8 * c);
+                }
+                *reinterpret_cast<uint4*>(smem + (c / 8) * C::kPart + row * 128 + ((c % 8) ^ (row & 7)) * 16) = v;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+            float m = __int_as_float(0xFF800000), l = 0.f;
+            for (int g = s.g0; g < s.g1; ++g, ++n) {
+                const int live = s.len - g * kTile;
+                wait(smem_u32(&sh.s_full), n & 1, watch);
+                __syncwarp();
+                tc_fence_after();
+                const float top = (live >= kTile ? row_max<false>(t_s, live) : row_max<true>(t_s, live)) * p.scale_log2;
+                // the reference moves, for all rows of the warp together, when a score passes it by 2^8 (the values of the
+                // tile before are added by now: these scores were issued behind them)
+                if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
+                    const float to = fmaxf(m, top);
+                    const float fix = to == m ? 1.f : ex2(m - to);
+                    m = to;
+                    l *= fix;
+                    if (g > s.g0) {
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t r[32];
+                            tmem_ld32(t_o + c0, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fix);
+                            tmem_st32(t_o + c0, r);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float ref = m == __int_as_float(0xFF800000) ? 0.f : m;
+                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, smem_u32(&sh.p_half))
+                                   : row_weights<true>(t_s, live, p.scale_log2, ref, smem_u32(&sh.p_half));
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full));
+            }
+            // ---- the row's part: unscaled sums, reference and sum of weights
+            wait(smem_u32(&sh.o_full), stretch & 1, watch);
+            __syncwarp();
+            tc_fence_after();
+            ++stretch;
+            const int all = (sh.members[s.g + 1] - sh.members[s.g]) * p.rows;
+            const long long at = (long long)p.Hkv * p.rows * sh.members[s.g] + (long long)s.h * all + s.row0 + tid +
+                                 (long long)kTile * blockIdx.x;
+            float* o = p.part_o + at * D;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(t_o + c0, r);
+                tmem_wait_ld();
+                if (tid < s.rows) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + c0 + e), "r"(r[e]),
+                                     "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]), "r"(r[e + 5]), "r"(r[e + 6]),
+                                     "r"(r[e + 7])
+                                     : "memory");
+                }
+            }
+            if (tid < s.rows) p.part_ml[at] = make_float2(m, l);
+            tc_fence_before();
+        }
+    } else if (warp < R::kMma && !E4M3) {
+        // =================================================== loads, a box or more to a lane
+        const int box = p.box_rows, copies = kTile / box * C::kParts;  // of a tile of keys, at most 16
+        const int mine = lane / C::kParts * box, part = lane % C::kParts;
+        int n = 0;
+        bool ok = true;
+        while (s.at < s.end && ok) {
+            stretch_open(p, sh, s);
+            auto page_at = [&](int g) {
+                const int pos = g * kTile + mine;
+                if (lane >= copies || g >= s.g1 || pos >= s.len) return -1;
+                int page = p.t.pages[s.g * p.t.stride + (unsigned)pos / (unsigned)p.c.page];
+                if (page < 0 || page >= p.c.n_pages) {
+                    atomicOr(p.c.err, kCacheErrPage);
+                    page = 0;
+                }
+                return page;
+            };
+            int page = page_at(s.g0);
+            for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
+                const int st = n % kStages, next = page_at(g + 1);
+                const bool need = page >= 0;
+                const int slot = (int)((unsigned)(g * kTile + mine) % (unsigned)p.c.page), unit = page * p.Hkv + s.h;
+                const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, need)) * box * 128;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t full = smem_u32(kv ? &sh.v_full[st] : &sh.k_full[st]);
+                    if (ok && n >= kStages)
+                        ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (n / kStages - 1) & 1, watch);
+                    if (n + 1 == p.withhold) ok = false;
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (need)
+                        tma_load_box((kv ? s_v : s_k) + st * C::kBytes + part * C::kPart + mine * 128, &p.tm, full, slot, part,
+                                     kv, unit);
+                }
+                page = next;
+            }
+        }
+    } else if (warp < R::kMma) {
+        // =================================================== E4M3: codes to tiles of bf16 numbers
+        constexpr int kLanes = D / 16, kRows = 128 / kLanes, kEach = kTile / kRows;  // lanes of a row, rows at once
+        const int ltid = tid - 32 * R::kLoad, r0 = ltid / kLanes, c = ltid % kLanes;
+        int n = 0;
+        bool ok = true;
+        struct Codes {
+            uint4 v[kEach];
+            uint32_t e[kEach];  // exponent byte; 0 beside codes of zeros where there is nothing
+        };
+        while (s.at < s.end && ok) {
+            stretch_open(p, sh, s);
+            // lane i < 8 of every warp: the page of positions 16 i .. of the tile
+            auto page_at = [&](int g) {
+                const int pos = g * kTile + 16 * lane;
+                if (lane >= 8 || g >= s.g1 || pos >= s.len) return -1;
+                int page = p.t.pages[s.g * p.t.stride + (unsigned)pos / (unsigned)p.c.page];
+                if (page < 0 || page >= p.c.n_pages) {
+                    atomicOr(p.c.err, kCacheErrPage);
+                    page = 0;
+                }
+                return page;
+            };
+            auto fetch = [&](int g, int pages, int kv, Codes& f) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int row = i * kRows + r0, pos = g * kTile + row;
+                    const int page = __shfl_sync(0xFFFFFFFFu, pages, row / 16);
+                    f.v[i] = make_uint4(0, 0, 0, 0);
+                    f.e[i] = 0;
+                    if (pos >= s.len) continue;
+                    const int slot = (int)((unsigned)pos % (unsigned)p.c.page);
+                    const long long unit = (long long)page * p.Hkv + s.h;
+                    f.v[i] = *reinterpret_cast<const uint4*>(p.c.pages + ((unit * 2 + kv) * p.c.page + slot) * D + 16 * c);
+                    f.e[i] = p.c.scales[(unit * (p.c.page / 16) + slot / 16) * 32 + 16 * kv + slot % 16];
+                }
+            };
+            auto put = [&](const Codes& f, uint32_t dst) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int row = i * kRows + r0;
+                    // 2^(e - 127); 255 goes with NaN codes
+                    const float factor = __uint_as_float(max(f.e[i] << 23, 0x00400000u));
+                    uint4 lo, hi;
+                    widen16(f.v[i], factor, lo, hi);
+                    const uint32_t at = dst + (c / 4) * C::kPart + row * 128;
+                    const int x = 2 * (c % 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x ^ (row & 7)) * 16)), "r"(lo.x),
+                                 "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((x + 1) ^ (row & 7)) * 16)), "r"(hi.x),
+                                 "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                                 : "memory");
+                }
+            };
+            auto give = [&](unsigned long long* full) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(full));
+            };
+            if (s.g0 >= s.g1) continue;
+            Codes a, b;
+            int pages = page_at(s.g0);
+            fetch(s.g0, pages, 0, a);
+            for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
+                const int st = n % kStages;
+                fetch(g, pages, 1, b);
+                pages = page_at(g + 1);
+                if (n >= kStages) ok = wait(smem_u32(&sh.k_empty[st]), (n / kStages - 1) & 1, watch);
+                if (n + 1 == p.withhold) ok = false;
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                put(a, s_k + st * C::kBytes);
+                give(&sh.k_full[st]);
+                if (g + 1 < s.g1) fetch(g + 1, pages, 0, a);
+                if (n >= kStages) ok = wait(smem_u32(&sh.v_empty[st]), (n / kStages - 1) & 1, watch);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                put(b, s_v + st * C::kBytes);
+                give(&sh.v_full[st]);
+            }
+        }
+    } else {
+        // =================================================== products (lane 0; all lanes clear values past the end)
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false), idesc_o = idesc_bf16_f32(kTile, D, true);
+        int n = 0, stretch = 0;
+        bool ok = true;
+        auto scores = [&](int m) {
+            const int st = m % kStages;
+            ok = ok && wait(smem_u32(&sh.k_full[st]), (m / kStages) & 1, watch);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) return;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * C::kPart + (k % 4) * 32;
+                    mma_ss(tmem, sdesc_sw128(s_q + off, 16, 1024), sdesc_sw128(s_k + st * C::kBytes + off, 16, 1024), idesc_s,
+                           k > 0);
+                }
+                mma_commit(smem_u32(&sh.s_full));
+                mma_commit(smem_u32(&sh.k_empty[st]));
+            }
+        };
+        while (s.at < s.end && ok) {
+            stretch_open(p, sh, s);
+            if (s.g0 >= s.g1) continue;
+            ok = __all_sync(0xFFFFFFFFu, wait(smem_u32(&sh.q_full), stretch & 1, watch));
+            ++stretch;
+            for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
+                // (the scores' columns hold the weights of the tile before; its product with the values, issued before,
+                // has read them by the time these are written)
+                scores(n);
+                const int st = n % kStages;
+                ok = ok && wait(smem_u32(&sh.v_full[st]), (n / kStages) & 1, watch);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                const uint32_t v = s_v + st * C::kBytes;
+                if (!E4M3 && (g + 1) * kTile > s.len) {
+                    // positions past the end may hold anything: weight zero times a NaN is a NaN
+                    const int live = s.len - g * kTile;
+                    for (int i = lane; i < (kTile - live) * 8 * C::kParts; i += 32) {
+                        const int row = live + i / (8 * C::kParts), x = i % (8 * C::kParts);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + (x / 8) * C::kPart + row * 128 +
+                                                                                      (x % 8) * 16),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && wait(smem_u32(half ? &sh.p_full : &sh.p_half), n & 1, watch);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 4 * half; k < 4 * half + 4; ++k)
+                            mma_ts(tmem + C::kColO, tmem + 8 * k, sdesc_sw128(v + k * 16 * 128, C::kPart, 1024), idesc_o,
+                                   g > s.g0 || k > 0);
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    mma_commit(smem_u32(&sh.v_empty[st]));
+                    if (g + 1 == s.g1) mma_commit(smem_u32(&sh.o_full));
+                }
+                __syncwarp();
+            }
+        }
+    }
+    // all warps meet behind their last copy and product
+    __syncthreads();
+    if (sh.abort) {
+        drain();
+        __syncthreads();
+    }
+    if (warp == R::kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+}
+
+// Joins a row's parts, a warp to a row: those of its prefix, from the CTAs that held tiles of its unit, and those of its
+// own positions.
+constexpr int kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PrefixParams p,
+                                                               const __grid_constant__ JoinParams own) {
+    constexpr int kVec = D / 32, kBatch = 8;
+    wait_for_kernel_before();
+    let_kernel_behind_in();
+    const int lane = threadIdx.x % 32;
+    const long long out = (long long)blockIdx.x * kJoinWarps + threadIdx.x / 32;  // row of O
+    if (out >= (long long)p.B * p.Hkv * p.rows) return;
+    const int head = (int)(out / p.rows), r = (int)(out - (long long)head * p.rows), b = head / p.Hkv, h = head - b * p.Hkv;
+    const float ninf = __int_as_float(0xFF800000);
+    // the prefix's parts
+    int n1 = 0, c0 = 0;
+    long long base = 0;
+    const int2 place = __ldcg(&p.place[b]);
+    if (place.x >= 0) {
+        const int4 g = __ldcg(&p.groups[place.x]), total = __ldcg(&p.groups[p.G]);
+        const int all = g.z * p.rows, x = place.y * p.rows + r, blocks = (all + kTile - 1) / kTile;
+        if (g.w > 0) {
+            const PagedCuts cuts((unsigned)total.x, (unsigned)total.y, own.prefix_grid, kShape);
+            const unsigned u0 = (unsigned)g.x + (h * blocks + x / kTile) * paged_cost(g.w, kShape) + kShape.overhead;
+            c0 = (int)cuts.owner(u0);
+            n1 = (int)cuts.owner(u0 + g.w - 1) - c0 + 1;
+            base = (long long)p.Hkv * p.rows * g.y + (long long)h * all + x;
+        }
+    }
+    // and its own
+    const int row_block = r / own.rows_pad, unit = head * own.row_blocks + row_block;
+    const int2 cut = __ldcg(&own.cut[unit]);
+    const int n = n1 + (cut.x < 0 ? 1 : cut.y - cut.x + 1);
+    auto find = [&](int i, const float*& o, float2& ml) {
+        long long at;
+        if (i < n1) {
+            at = base + (long long)kTile * (c0 + i);
+            o = p.part_o + at * D;
+            ml = __ldcg(&p.part_ml[at]);
+        } else if (cut.x < 0) {
+            o = own.whole_o + out * D;
+            ml = __ldcg(&own.whole_ml[out]);
+        } else {
+            at = (long long)(2 * (cut.x + i - n1) + (i == n1)) * own.rows_pad + (r - row_block * own.rows_pad);
+            o = own.part_o + at * D;
+            ml = __ldcg(&own.part_ml[at]);
+        }
+    };
+    float M = ninf, L = 0.f, v[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const float* o = nullptr;
+        float2 ml = make_float2(ninf, 0.f);
+        if (i0 + lane < n) find(i0 + lane, o, ml);
+        float top = ml.x;
+#pragma unroll
+        for (int k = 16; k; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+        const float to = fmaxf(M, top);
+        const float fix = M == to ? 1.f : ex2(M - to);
+        M = to;
+        L *= fix;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] *= fix;
+        // a part without a reference has seen nothing (sum 0: its output is not looked at), or only NaN
+        const float f = ml.x == ninf ? ml.y : ex2(ml.x - M);
+        L += ml.x == ninf ? ml.y : ml.y * f;
+        const int m = min(32, n - i0);
+        for (int k0 = 0; k0 < m; k0 += kBatch) {
+            float y[kBatch][kVec];
+            float w[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int who = min(k0 + k, 31);
+                const float* src = reinterpret_cast<const float*>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(o), who));
+                w[k] = __shfl_sync(0xFFFFFFFFu, f, who);
+                if (k0 + k >= m) w[k] = 0.f;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) y[k][j] = 0.f;
+                if (w[k] != 0.f) {
+                    if constexpr (D == 128) {
+                        const float4 t = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                        y[k][0] = t.x; y[k][1] = t.y; y[k][kVec - 2] = t.z; y[k][kVec - 1] = t.w;
+                    } else {
+                        const float2 t = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                        y[k][0] = t.x; y[k][1] = t.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[j] = fmaf(w[k], y[k][j], v[j]);
+        }
+    }
+#pragma unroll
+    for (int k = 16; k; k /= 2) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(own.o) + out * D) + lane * (D / 64);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) dst[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+    if (own.lse && lane == 0) own.lse[out] = (M + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(const PrefixParams& p, bool e4m3, int grid, cudaStream_t stream) {
+    auto go = [&](auto* f, int threads, int smem) {
+        const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), smem);
+        return e != cudaSuccess ? e : launch_dependent(f, dim3((unsigned)grid), threads, smem, stream, p);
+    };
+    if (p.c.d == 64)
+        return e4m3 ? go(prefix_kernel<64, true>, Roles<true>::kThreads, Cfg<64>::kSmem)
+                    : go(prefix_kernel<64, false>, Roles<false>::kThreads, Cfg<64>::kSmem);
+    return e4m3 ? go(prefix_kernel<128, true>, Roles<true>::kThreads, Cfg<128>::kSmem)
+                : go(prefix_kernel<128, false>, Roles<false>::kThreads, Cfg<128>::kSmem);
+}
+
+cudaError_t launch_join(const PrefixParams& p, const JoinParams& own, cudaStream_t stream) {
+    const long long rows = (long long)p.B * p.Hkv * p.rows;
+    const dim3 grid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+    return p.c.d == 64 ? launch_dependent(join_kernel<64>, grid, 32 * kJoinWarps, 0, stream, p, own)
+                       : launch_dependent(join_kernel<128>, grid, 32 * kJoinWarps, 0, stream, p, own);
+}
+
+}  // namespace attn

@@ -1,14 +1,24 @@
 // Host implementation of the entry points of include/attn.h for long contexts over a paged cache: page bounds and
-// selection, attention weights and eviction.
+// selection, attention weights and eviction, shared prefixes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
 
 #include "attn.h"
 #include "paged.h"
 #include "paged_host.h"
+
+struct attn_prefix_plan {
+    attn_paged_plan* step = nullptr;  // of the own positions
+    attn::OwnParts own;
+    float* part_o = nullptr;
+    float2* part_ml = nullptr;
+    int4* groups = nullptr;
+    int2* place = nullptr;
+};
 
 using attn::aligned;
 using attn::on_device;
@@ -140,6 +150,107 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
     p.B = B; p.keep = keep; p.recent = recent;
     p.in_place = !to_table;
     return done(attn::launch_evict(p, h->e4m3, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_prefix_create(attn_prefix_handle* out, int B, int Hq, int Hkv, int S_q, int d, float scale,
+                               attn_mask_kind kind) {
+    if (!out) return ATTN_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (kind != ATTN_MASK_FULL && kind != ATTN_MASK_CAUSAL)
+        return (int)kind < ATTN_MASK_FULL || (int)kind > ATTN_MASK_LOCAL_GLOBAL ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
+    attn_prefix_plan* h = new (std::nothrow) attn_prefix_plan();
+    if (!h) return ATTN_ERR_OOM;
+    attn_status st = attn_paged_create(&h->step, B, Hq, Hkv, S_q, d, scale, kind, 0);
+    if (st != ATTN_OK) {
+        delete h;
+        return st;
+    }
+    const size_t rows = (size_t)B * Hq * S_q;
+    const size_t parts = rows + (size_t)attn::kPrefixTile * attn::kPrefixCtasPerSm * h->step->n_sm;
+    auto get = [&](auto& p, size_t n) {
+        if (st != ATTN_OK) return;
+        const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), n * sizeof(*p));
+        if (e != cudaSuccess) st = e == cudaErrorMemoryAllocation ? ATTN_ERR_OOM : ATTN_ERR_CUDA;
+    };
+    get(h->own.whole_o, rows * d);
+    get(h->own.whole_ml, rows);
+    get(h->own.cut, (size_t)B * Hkv * 2);
+    get(h->part_o, parts * d);
+    get(h->part_ml, parts);
+    get(h->groups, ATTN_DECODE_MAX_BATCH + 1);
+    get(h->place, B);
+    if (st != ATTN_OK) {
+        attn_prefix_destroy(h);
+        return st;
+    }
+    *out = h;
+    return ATTN_OK;
+}
+
+attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, const void* Q, const int* prefix_table,
+                                long long prefix_stride, int prefix_max_pages, const int* prefix_len, int n_prefix,
+                                const int* prefix_of, const int* page_table, long long table_stride, int max_pages,
+                                const int* cache_len, void* O, float* LSE, void* stream) {
+    if (!h || !cache) return ATTN_ERR_INVALID_ARG;
+    if (!table_ok(prefix_table, prefix_stride, prefix_max_pages, prefix_len) || n_prefix < 1 || !aligned(prefix_of, 4) ||
+        (!prefix_of && n_prefix != 1))
+        return ATTN_ERR_INVALID_ARG;
+    if (!table_ok(page_table, table_stride, max_pages, cache_len) || !Q || !aligned(Q, 16) || !O || !aligned(O, 16) ||
+        !aligned(LSE, 4))
+        return ATTN_ERR_INVALID_ARG;
+    attn_paged_plan* s = h->step;
+    if (cache->c.Hkv != s->Hkv || cache->c.d != s->d || cache->device != s->device || !on_device(s->device))
+        return ATTN_ERR_INVALID_ARG;
+    const int rows = s->Hq / s->Hkv * s->S_q;
+    if (n_prefix > ATTN_DECODE_MAX_BATCH || !room_ok(cache, prefix_max_pages) || !room_ok(cache, max_pages))
+        return ATTN_ERR_UNSUPPORTED;
+    // the line of cost fits an int: every unit, and every prefix's last one
+    const long long tiles = (long long)prefix_max_pages * cache->c.page / attn::kPrefixTile + 8;
+    if (tiles * s->Hkv * ((long long)n_prefix + (long long)s->B * rows / attn::kPrefixTile) > 0x7FFFFFFFLL)
+        return ATTN_ERR_UNSUPPORTED;
+    attn::PrefixParams p{};
+    p.tm = cache->rows_map;
+    p.c = cache->c;
+    p.t = table_of(prefix_table, prefix_stride, prefix_max_pages, prefix_len);
+    p.of = prefix_of;
+    p.q = Q;
+    p.B = s->B; p.G = n_prefix; p.Hkv = s->Hkv; p.rows = rows;
+    p.box_rows = cache->box_rows;
+    p.part_o = h->part_o; p.part_ml = h->part_ml; p.groups = h->groups; p.place = h->place;
+    p.scale_log2 = (float)((double)s->scale * 1.4426950408889634);
+    p.watchdog_ns = s->watchdog_ns;
+    p.withhold = s->withhold;
+    const int grid = std::min(s->n_sm * attn::kPrefixCtasPerSm, s->grid_limit);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (attn::launch_prefix(p, cache->e4m3, grid, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    attn::OwnParts own = h->own;
+    const attn_status r = attn::paged_step(s, cache, Q, page_table, table_stride, 0, max_pages, cache_len, O, LSE, &own, stream);
+    if (r != ATTN_OK) return r;
+    attn::JoinParams j{};
+    j.whole_o = own.whole_o; j.whole_ml = own.whole_ml;
+    j.part_o = s->d_part; j.part_ml = s->d_ml; j.cut = own.cut;
+    j.rows_pad = own.rows_pad; j.row_blocks = own.row_blocks;
+    j.prefix_grid = grid;
+    j.o = O; j.lse = LSE;
+    return done(attn::launch_join(p, j, st));
+}
+
+attn_status attn_prefix_set_grid_limit(attn_prefix_handle h, int max_ctas) {
+    return h ? attn_paged_set_grid_limit(h->step, max_ctas) : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status attn_prefix_set_watchdog(attn_prefix_handle h, long long limit_ns, int withhold) {
+    return h ? attn_paged_set_watchdog(h->step, limit_ns, withhold) : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status attn_prefix_destroy(attn_prefix_handle h) {
+    if (!h) return ATTN_OK;
+    const attn_status st = attn_paged_destroy(h->step);  // (synchronises the device)
+    for (void* p : {(void*)h->own.whole_o, (void*)h->own.whole_ml, (void*)h->own.cut, (void*)h->part_o, (void*)h->part_ml,
+                    (void*)h->groups, (void*)h->place})
+        if (p) cudaFree(p);
+    delete h;
+    return st;
 }
 
 }  // extern "C"

@@ -149,6 +149,9 @@ struct PagedParams {
     // x = -1: none.
     int2* cut;
     int by_unit;
+    // Not null: units that are not cut leave unscaled sums too, [B, Hq, S_q, d] and [B, Hq, S_q], instead of O and LSE.
+    float* whole_o;
+    float2* whole_ml;
     int B, Hq, Hkv, S_q, rows;
     int units;            // of a sequence: Hkv, times 2 where a head's rows are taken in two blocks
     int window;           // -1: none
@@ -168,6 +171,40 @@ cudaError_t launch_paged_bf16(const PagedParams& p, int grid, cudaStream_t strea
 cudaError_t launch_paged_e4m3(const PagedParams& p, int grid, cudaStream_t stream);
 // Joins the parts of cut units; enqueued behind either as a programmatic dependent.
 cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cudaStream_t stream);
+
+// ---------------------------------------------------------------- shared prefixes
+struct PrefixParams {
+    CUtensorMap tm;  // bf16 pages: boxes of box_rows positions and 128 bytes of a row
+    CacheView c;
+    PageTable t;     // of the prefixes, [G, max_pages] and [G]
+    const int* of;   // [B]: the prefix of a sequence, -1: none; null: the only one
+    const void* q;   // [B, Hq, S_q, d] bf16
+    int B, G, Hkv, rows, box_rows;
+    // Parts: that of CTA c for row x of the rows of prefix g and kv head h is number
+    //   Hkv * rows * (sequences of the prefixes before g) + h * (rows of the prefix) + x + 128 c,
+    // so that no two meet: along the line of work either the CTA or the unit moves on.
+    float* part_o;    // [.][d]
+    float2* part_ml;  // [.]: reference (base 2) and sum
+    int4* groups;     // [G + 1]: cost of the prefixes before, their sequences, sequences of this one, its tiles; last: the
+                      // whole cost, and the units
+    int2* place;      // [B]: prefix and place among its sequences
+    float scale_log2;
+    long long watchdog_ns;
+    int withhold;
+};
+struct JoinParams {  // of the own positions, as PagedParams; prefix_grid: the first kernel's CTAs
+    const float* whole_o;
+    const float2* whole_ml;
+    const float* part_o;
+    const float2* part_ml;
+    const int2* cut;
+    int rows_pad, row_blocks, prefix_grid;
+    void* o;
+    float* lse;
+};
+constexpr int kPrefixTile = 128, kPrefixCtasPerSm = 2;
+cudaError_t launch_prefix(const PrefixParams& p, bool e4m3, int grid, cudaStream_t stream);
+cudaError_t launch_join(const PrefixParams& p, const JoinParams& own, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention weights of positions
 struct WeighParams {

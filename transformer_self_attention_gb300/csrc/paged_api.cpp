@@ -15,18 +15,6 @@
 #include "paged.h"
 #include "paged_host.h"
 
-struct attn_paged_plan {
-    int B = 0, Hq = 0, Hkv = 0, S_q = 0, d = 0, kind = 0, window = 0;
-    int device = 0, n_sm = 0;
-    int grid_limit = 1 << 30;
-    long long watchdog_ns = 2000000000LL;
-    int withhold = 0;
-    float scale = 0.f;
-    float* d_part = nullptr;
-    float2* d_ml = nullptr;
-    int2* d_cut = nullptr;
-};
-
 using attn::aligned;
 using attn::on_device;
 using attn::table_ok;
@@ -50,14 +38,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // bf16 pages as {row part, slots, parts of a row, K / V, page * Hkv + head}: a row comes in parts of 128 bytes, one box
-// holds 16 positions' keys and values of one head.
-bool encode_bf16(CUtensorMap* map, const attn::CacheView& c) {
+// holds 16 positions' keys and values of one head; not `whole`: `slots` positions, 128 bytes of their keys or values.
+bool encode_bf16(CUtensorMap* map, const attn::CacheView& c, int slots = 16, bool whole = true) {
     auto enc = encoder();
     if (!enc) return false;
     const int row = c.d * 2, parts = row / 128;
     cuuint64_t dims[5] = {64, (cuuint64_t)c.page, (cuuint64_t)parts, 2, (cuuint64_t)c.n_pages * c.Hkv};
     cuuint64_t strides[4] = {(cuuint64_t)row, 128, (cuuint64_t)c.page * row, (cuuint64_t)2 * c.page * row};
-    cuuint32_t box[5] = {64, 16, (cuuint32_t)parts, 2, 1};
+    cuuint32_t box[5] = {64, (cuuint32_t)slots, whole ? (cuuint32_t)parts : 1, whole ? 2u : 1u, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c.pages, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -228,7 +216,9 @@ attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int 
     if (!clear_error(h->c.err)) return fail(ATTN_ERR_CUDA);
     // the largest power of two that divides the page, up to a decode tile
     while (h->box_rows < 128 && page % (2 * h->box_rows) == 0) h->box_rows *= 2;
-    if (!(h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows) : encode_bf16(&h->map, h->c))) return fail(ATTN_ERR_CUDA);
+    if (!(h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows)
+                  : encode_bf16(&h->map, h->c) && encode_bf16(&h->rows_map, h->c, h->box_rows, false)))
+        return fail(ATTN_ERR_CUDA);
     *out = h;
     return ATTN_OK;
 }
@@ -332,6 +322,14 @@ attn_status attn_paged_forward(attn_paged_handle h, attn_cache_handle cache, con
 attn_status attn_paged_forward_heads(attn_paged_handle h, attn_cache_handle cache, const void* Q, const int* page_table,
                                      long long table_stride, long long head_stride, int max_pages, const int* cache_len,
                                      void* O, float* LSE, void* stream) {
+    return attn::paged_step(h, cache, Q, page_table, table_stride, head_stride, max_pages, cache_len, O, LSE, nullptr, stream);
+}
+
+}  // extern "C"
+
+attn_status attn::paged_step(attn_paged_plan* h, attn_cache_plan* cache, const void* Q, const int* page_table,
+                             long long table_stride, long long head_stride, int max_pages, const int* cache_len, void* O,
+                             float* LSE, attn::OwnParts* own, void* stream) {
     if (head_stride < 0) return ATTN_ERR_INVALID_ARG;
     if (!h || !cache || !Q || !O || !aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4)) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
@@ -360,13 +358,22 @@ attn_status attn_paged_forward_heads(attn_paged_handle h, attn_cache_handle cach
     p.box_rows = cache->box_rows;
     const int rows_pad = attn::paged_rows_pad(p.rows, cache->e4m3);
     const int grid = std::min(h->n_sm * attn::paged_ctas_per_sm(p.rows, cache->e4m3), h->grid_limit);
-    p.by_unit = (long long)h->B * units <= grid;
+    p.by_unit = own || (long long)h->B * units <= grid;
+    if (own) {
+        p.cut = own->cut;
+        p.whole_o = own->whole_o;
+        p.whole_ml = own->whole_ml;
+        own->rows_pad = rows_pad;
+        own->row_blocks = units / h->Hkv;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cache->e4m3 ? attn::launch_paged_e4m3(p, grid, st) : attn::launch_paged_bf16(p, grid, st);
-    if (e == cudaSuccess && attn::paged_may_cut((long long)h->B * units, room, grid, shape))
+    if (e == cudaSuccess && !own && attn::paged_may_cut((long long)h->B * units, room, grid, shape))
         e = attn::launch_paged_merge(p, grid, rows_pad, st);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
+
+extern "C" {
 
 attn_status attn_paged_set_grid_limit(attn_paged_handle h, int max_ctas) {
     if (!h || max_ctas < 1) return ATTN_ERR_INVALID_ARG;

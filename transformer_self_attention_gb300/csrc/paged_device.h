@@ -115,10 +115,15 @@ template <int D, int THREADS>
 __device__ __forceinline__ void paged_empty_rows(const PagedParams& p, const unsigned* cost) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (cost[b + 1] != cost[b]) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.o) + (long long)b * p.Hq * p.S_q * (D / 8);
-        for (int i = threadIdx.x; i < p.Hq * p.S_q * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
         if (p.by_unit)
             for (int i = threadIdx.x; i < p.units; i += THREADS) p.cut[b * p.units + i] = make_int2(-1, 0);
+        if (p.whole_o) {
+            for (int i = threadIdx.x; i < p.Hq * p.S_q; i += THREADS)
+                p.whole_ml[(long long)b * p.Hq * p.S_q + i] = make_float2(__int_as_float(0xFF800000), 0.f);
+            continue;
+        }
+        uint4* o = reinterpret_cast<uint4*>(p.o) + (long long)b * p.Hq * p.S_q * (D / 8);
+        for (int i = threadIdx.x; i < p.Hq * p.S_q * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
         if (p.lse)
             for (int i = threadIdx.x; i < p.Hq * p.S_q; i += THREADS)
                 p.lse[(long long)b * p.Hq * p.S_q + i] = __int_as_float(0xFF800000);

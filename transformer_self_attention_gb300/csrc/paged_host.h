@@ -21,12 +21,38 @@ struct attn_rope_plan {
 struct attn_cache_plan {
     attn::CacheView c;
     CUtensorMap map{};
+    CUtensorMap rows_map{};  // bf16: boxes of box_rows positions, 128 bytes of their keys or values
     bool e4m3 = false;
     int box_rows = 16;
     int device = 0, n_sm = 0;
 };
 
+struct attn_paged_plan {
+    int B = 0, Hq = 0, Hkv = 0, S_q = 0, d = 0, kind = 0, window = 0;
+    int device = 0, n_sm = 0;
+    int grid_limit = 1 << 30;
+    long long watchdog_ns = 2000000000LL;
+    int withhold = 0;
+    float scale = 0.f;
+    float* d_part = nullptr;
+    float2* d_ml = nullptr;
+    int2* d_cut = nullptr;
+};
+
 namespace attn {
+
+// A decode step that leaves its parts to be joined by somebody else: where they go (cut: [B * units], by unit), and, filled
+// in by the step, how they lie there.
+struct OwnParts {
+    float* whole_o = nullptr;
+    float2* whole_ml = nullptr;
+    int2* cut = nullptr;
+    int rows_pad = 0, row_blocks = 0;
+};
+// attn_paged_forward_heads, or with `own` the part of it before the joining of cut units.
+attn_status paged_step(attn_paged_plan* h, attn_cache_plan* cache, const void* Q, const int* page_table,
+                       long long table_stride, long long head_stride, int max_pages, const int* cache_len, void* O,
+                       float* LSE, OwnParts* own, void* stream);
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
