@@ -816,7 +816,8 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
  * eviction of the positions that received least.  ("第 8 章 现代大模型架构" (theaiera.top), the sections on the KV cache's
  * size.)
  *
- *   weights : float32 [n_pages, Hkv, page], a number for every slot and kv head of the cache, the caller's.
+ *   weights : float32 [n_pages, Hkv, page], a number for every slot and kv head of the cache, the
+ *             caller's; 16-byte aligned.
  *
  * Pages of the sequences of one call must be distinct.  Both calls run on the cache's device and need no workspace.
  */

@@ -12,9 +12,12 @@
 //
 // Update: bound by memory, the changed pages' keys read once (and by latency where one page a sequence changes).  A warp
 // takes a page and head; its lanes hold 16 bytes of a row each, several rows at once, eight loads under way.
-// Select: a cluster of one to eight blocks for each sequence and kv head, four lanes to a page (each takes a quarter of the
-// channels: 16 channels an instruction would need four dp4a of a product, which the scores' 2 d bytes a page are worth).
-// Scores go to the first block's shared memory, which then finds the largest (select.h).
+// Select: a cluster of one to eight blocks for each sequence and kv head.  With the negative and the positive parts of a
+// query behind one another, a score is one product of 2 d whole numbers, lo first, then hi: m16n8k32 products of 8-bit numbers with
+// the rows as the first operand and eight pages as the second.  (This GPU's rate for them is low, and is enough:
+// 16 rows of 131K pages and heads took 33 us with four lanes to a page and dp4a.)  A lane's 16 bytes of a page are those
+// that it would hold of two steps; the queries are permuted to match.  Scores go to the first block's shared memory, which
+// then finds the largest (select.h).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,16 +36,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kUpdateThreads = 256;
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t y;
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
@@ -105,47 +98,55 @@ struct RowBounds<false> {
         }
     }
 };
+// Codes become bf16 numbers: a code's exponent and mantissa, moved to where a bf16 number has them, stand for 2^-120 of it
+// (subnormal codes become subnormal numbers), so that two multiplications by powers of two give the row's elements, as exactly
+// as a bf16 number can (beyond 2^128: infinities).  (By way of fp16 and float32 numbers 235 MB took 88 us.)
 template <>
 struct RowBounds<true> {
     static constexpr int kChannels = 16;
-    float lo[16], hi[16];
+    uint32_t lo[8], hi[8];
+    uint32_t nan;
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            lo[i] = __uint_as_float(0x7F800000u);
-            hi[i] = __uint_as_float(0xFF800000u);
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = 0x7F807F80u;
+            hi[i] = 0xFF80FF80u;
         }
+        nan = 0;
     }
     __device__ __forceinline__ void take(const uint4& v, uint32_t e) {
-        // 2^(e - 127), or NaN for 255
-        const float f = e == 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(max(e << 23, 0x00400000u));
+        // 2^(e - 127) as a bf16 number, twice; for 255 a NaN
+        const uint32_t f = (e == 255 ? 0x7FFFu : e == 0 ? 0x0040u : e << 7) * 0x10001u;
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w[i / 2] >> 16 * (i % 2))));
-            float a, b;
-            asm("{.reg .f16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h2));
-            a *= f;
-            b *= f;
-            lo[2 * i] = min_nan(lo[2 * i], a);
-            hi[2 * i] = max_nan(hi[2 * i], a);
-            lo[2 * i + 1] = min_nan(lo[2 * i + 1], b);
-            hi[2 * i + 1] = max_nan(hi[2 * i + 1], b);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = __byte_perm(w[i], 0, 0x1404), b = __byte_perm(w[i], 0, 0x3424);
+            uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x7B807B80u));  // 2^120
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x7B807B80u));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(f));
+            nan |= ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a NaN code: 127 carries into the top bit
+            lo[2 * i] = min2_nan(lo[2 * i], x);
+            hi[2 * i] = max2_nan(hi[2 * i], x);
+            lo[2 * i + 1] = min2_nan(lo[2 * i + 1], y);
+            hi[2 * i + 1] = max2_nan(hi[2 * i + 1], y);
         }
     }
     __device__ __forceinline__ void join(int o) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            lo[i] = min_nan(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
-            hi[i] = max_nan(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = min2_nan(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
+            hi[i] = max2_nan(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
         }
     }
     __device__ __forceinline__ void get(float* l, float* h) const {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            l[i] = lo[i];
-            h[i] = hi[i];
+        for (int i = 0; i < 8; ++i) {
+            l[2 * i] = nan ? __int_as_float(0x7FFFFFFF) : __uint_as_float(lo[i] << 16);
+            l[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
+            h[2 * i] = __uint_as_float(hi[i] << 16);
+            h[2 * i + 1] = __uint_as_float(hi[i] & 0xFFFF0000u);
         }
     }
 };
@@ -271,14 +272,22 @@ __global__ void __launch_bounds__(kUpdateThreads) update_kernel(const __grid_con
 // ---------------------------------------------------------------------------------------------- selection
 constexpr int kSelectThreads = 512;
 
+constexpr int kSelectWarps = kSelectThreads / 32;
 template <int D>
 struct SelectMemory {
-    alignas(16) int8_t q[ATTN_DECODE_MAX_ROWS][2][D];  // negative and positive parts
+    static constexpr int kPitch = 2 * D + 16;  // rows begin 16 bytes of banks apart
+    alignas(16) int8_t q[ATTN_DECODE_MAX_ROWS][kPitch];  // negative parts, positive parts
     SelectShared<kSelectThreads> sel;
-    unsigned big[kSelectThreads / 32];
+    unsigned big[kSelectWarps];
 };
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-template <int D>
+template <int D, int RT>  // RT: row tiles of 16, at most (the last may be short)
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams p) {
     __shared__ SelectMemory<D> sh;
     extern __shared__ uint32_t keys[];  // of the first block of the cluster: a page each
@@ -286,11 +295,30 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int unit = blockIdx.x / blocks, b = unit / p.Hkv, h = unit - b * p.Hkv, page = p.c.page;
+    const int quad = lane / 4, pair = lane % 4;
     wait_for_kernel_before();
     let_kernel_behind_in();
+    // the loads that do not wait for one another first: queries, length, the warp's first pages
+    const int* row = p.t.pages + b * p.t.stride;
+    const uint4* q = reinterpret_cast<const uint4*>(p.q) + (long long)unit * p.rows * (D / 8);
+    constexpr int kPieces = (RT * 2 * D + kSelectThreads - 1) / kSelectThreads;  // 16-byte pieces of the queries, a thread's
+    uint4 v[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int i = tid + k * kSelectThreads;
+        v[k] = i < p.rows * (D / 8) ? q[i] : make_uint4(0, 0, 0, 0);
+    }
+    constexpr int kAtOnce = RT == 1 ? 2 : 1;  // tiles of eight pages under way
+    const int stride = blocks * kSelectWarps * 8 * kAtOnce, lo = p.sinks;
+    int i0 = (rank * kSelectWarps + warp) * 8 * kAtOnce;
+    int g[kAtOnce];
+    auto pages_at = [&](int at) {  // (entries that no position needs may hold anything, and are not used)
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) g[x] = row[min(lo + at + 8 * x + quad, p.t.max_pages - 1)];
+    };
+    pages_at(i0);
     const int len = sequence_length(p.t, page, b, p.c.err, tid == 0 && h == 0 && rank == 0);
     const int n = (unsigned)(len + page - 1) / (unsigned)page;
-    const int* row = p.t.pages + b * p.t.stride;
     int* out = p.out_table + (long long)unit * p.keep;
     if (h == 0 && rank == 0 && tid == 0) p.out_len[b] = n > p.keep ? len - (n - p.keep) * page : len;
     if (n <= p.keep) {  // (the whole cluster)
@@ -298,92 +326,121 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             for (int i = tid; i < p.keep; i += kSelectThreads) out[i] = i < n ? row[i] : -1;
         return;
     }
-    const int lo = p.sinks, m = n - p.recent - lo, K = p.keep - p.recent - lo;  // m > K >= 0
+    const int m = n - p.recent - lo, K = p.keep - p.recent - lo;  // m > K >= 0
     if (rank == 0) {
         for (int i = tid; i < lo; i += kSelectThreads) out[i] = row[i];
         for (int i = tid; i < p.recent; i += kSelectThreads) out[lo + K + i] = row[n - p.recent + i];
     }
     if (K == 0) return;
-    // the queries as whole numbers of one power of two
-    const uint4* q = reinterpret_cast<const uint4*>(p.q) + (long long)unit * p.rows * (D / 8);
+    constexpr int kChunks = D / 32;  // 16-byte pieces of a lane and page
+    uint4 c[kAtOnce][kChunks];
+    uint32_t e[kAtOnce];
+    auto codes_of = [&](int at) {
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const bool live = at + 8 * x + quad < m, ok = live && g[x] >= 0 && g[x] < p.c.n_pages;
+            const long long place = (long long)(ok ? g[x] : 0) * p.Hkv + h;
+            const uint4* src = reinterpret_cast<const uint4*>(p.codes + place * 2 * D) + pair;
+            e[x] = p.exps[place];
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) c[x][j] = src[4 * j];
+            if (live && !ok) g[x] = -1;  // told below
+            else g[x] = 0;
+        }
+    };
+    codes_of(i0);
+    // ---- the queries as whole numbers of one power of two: negative and positive parts
     uint32_t big = 0;  // as bits of a bf16
-    for (int i = tid; i < p.rows * (D / 8); i += kSelectThreads) {
-        const uint4 v = q[i];
-        uint32_t t = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const uint32_t t = __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
+                                    __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu));
         big = max(big, max(t & 0xFFFFu, t >> 16));
     }
     big = __reduce_max_sync(0xFFFFFFFFu, big);
     if (lane == 0) sh.big[warp] = big;
     __syncthreads();
-    big = __reduce_max_sync(0xFFFFFFFFu, sh.big[lane % (kSelectThreads / 32)]);
+    big = __reduce_max_sync(0xFFFFFFFFu, sh.big[lane % kSelectWarps]);
     const bool bad = big >= 0x7F80u;  // queries that are not finite choose the first pages
     const float f = bad ? 0.f : exp2_of(-power_of(big << 16));
-    for (int i = tid; i < p.rows * (D / 8); i += kSelectThreads) {
-        const uint4 v = q[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int tiles = (p.rows + 15) / 16;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {  // (rows up to the end of the last tile: zeros)
+        const int i = tid + k * kSelectThreads, r = i / (D / 8), at = i % (D / 8);
+        if (r >= 16 * tiles) continue;
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
         uint32_t neg[2] = {0, 0}, pos[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-            const int c = bad ? 0 : __float2int_rn(x * f);
-            neg[j / 4] |= (uint32_t)(min(c, 0) & 0xFF) << 8 * (j % 4);
-            pos[j / 4] |= (uint32_t)max(c, 0) << 8 * (j % 4);
+            const int y = bad ? 0 : __float2int_rn(x * f);
+            neg[j / 4] |= (uint32_t)(min(y, 0) & 0xFF) << 8 * (j % 4);
+            pos[j / 4] |= (uint32_t)max(y, 0) << 8 * (j % 4);
         }
-        const int r = i / (D / 8), c = i % (D / 8);
-        *reinterpret_cast<uint2*>(&sh.q[r][0][8 * c]) = make_uint2(neg[0], neg[1]);
-        *reinterpret_cast<uint2*>(&sh.q[r][1][8 * c]) = make_uint2(pos[0], pos[1]);
+        *reinterpret_cast<uint2*>(&sh.q[r][8 * at]) = make_uint2(neg[0], neg[1]);
+        *reinterpret_cast<uint2*>(&sh.q[r][D + 8 * at]) = make_uint2(pos[0], pos[1]);
     }
     if (blocks > 1) cluster.sync();  // (all blocks of the cluster are there)
     else __syncthreads();
     uint32_t* first_keys = blocks > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-    constexpr int kPages = kSelectThreads / 4, kChunks = D / 64;  // 16-byte chunks of a lane and row
-    const int quarter = lane % 4;
-    for (int i0 = rank * kPages; i0 < m; i0 += blocks * kPages) {
-        const int i = i0 + tid / 4;
-        uint32_t c[2][4 * kChunks];
-        int e = 0;
-        if (i < m) {
-            const int g = row[lo + i];
-            const bool ok = g >= 0 && g < p.c.n_pages;
-            if (!ok && h == 0 && quarter == 0) atomicOr(p.c.err, kCacheErrPage);
-            const long long at = (long long)(ok ? g : 0) * p.Hkv + h;
-            const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
-            e = p.exps[at];
+    uint4 qa[RT == 1 ? kChunks : 1], qb[RT == 1 ? kChunks : 1];  // rows quad and quad + 8
+    if constexpr (RT == 1) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+        for (int j = 0; j < kChunks; ++j) {
+            qa[j] = *reinterpret_cast<const uint4*>(&sh.q[quad][16 * (4 * j + pair)]);
+            qb[j] = *reinterpret_cast<const uint4*>(&sh.q[quad + 8][16 * (4 * j + pair)]);
+        }
+    }
+    for (; i0 < m; i0 += stride) {
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x)
+            if (g[x] < 0 && h == 0 && pair == 0) atomicOr(p.c.err, kCacheErrPage);
+        if (i0 + stride < m) pages_at(i0 + stride);
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            int best[2] = {-(1 << 30), -(1 << 30)};  // of the lane's rows, for pages 2 pair and 2 pair + 1
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                if (r >= tiles) break;
+                int s[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < kChunks; ++j) {
-                    const uint4 v = src[s * (D / 16) + 4 * j + quarter];
-                    c[s][4 * j] = v.x; c[s][4 * j + 1] = v.y; c[s][4 * j + 2] = v.z; c[s][4 * j + 3] = v.w;
+                    uint4 a, b;
+                    if constexpr (RT == 1) {
+                        a = qa[j];
+                        b = qb[j];
+                    } else {
+                        a = *reinterpret_cast<const uint4*>(&sh.q[16 * r + quad][16 * (4 * j + pair)]);
+                        b = *reinterpret_cast<const uint4*>(&sh.q[16 * r + quad + 8][16 * (4 * j + pair)]);
+                    }
+                    mma_s8(s, a.x, b.x, a.y, b.y, c[x][j].x, c[x][j].y);
+                    mma_s8(s, a.z, b.z, a.w, b.w, c[x][j].z, c[x][j].w);
                 }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4 * kChunks; ++j) c[0][j] = c[1][j] = 0;
-        }
-        int best = -(1 << 30);
-        for (int r = 0; r < p.rows; ++r) {
-            int sum = 0;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int j = 0; j < kChunks; ++j) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(&sh.q[r][s][16 * (4 * j + quarter)]);
-                    sum = __dp4a((int)v.x, (int)c[s][4 * j], sum);
-                    sum = __dp4a((int)v.y, (int)c[s][4 * j + 1], sum);
-                    sum = __dp4a((int)v.z, (int)c[s][4 * j + 2], sum);
-                    sum = __dp4a((int)v.w, (int)c[s][4 * j + 3], sum);
+                if (16 * r + quad < p.rows) {
+                    best[0] = max(best[0], s[0]);
+                    best[1] = max(best[1], s[1]);
                 }
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            best = max(best, sum);
+                if (16 * r + quad + 8 < p.rows) {
+                    best[0] = max(best[0], s[2]);
+                    best[1] = max(best[1], s[3]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) best[k] = max(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], o));
+                const uint32_t ek = __shfl_sync(0xFFFFFFFFu, e[x], 4 * (2 * pair + k));
+                const int i = i0 + 8 * x + 2 * pair + k;
+                if (quad == k && i < m)
+                    first_keys[i] = ek == 255 ? 0xFF800000u : ordered((float)best[k] * __uint_as_float(ek << 23));
+            }
         }
-        if (i < m && quarter == 0)
-            first_keys[i] = e == 255 ? 0xFF800000u : ordered((float)best * __uint_as_float((uint32_t)e << 23));
+        if (i0 + stride < m) codes_of(i0 + stride);
     }
     if (blocks > 1) cluster.sync();
     else __syncthreads();
     if (rank) return;
-    select_largest<kSelectThreads>(m, K, sh.sel, [&](int i) { return keys[i]; },
+    select_largest<kSelectThreads, 4>(m, K, sh.sel, [&](int i) { return keys[i]; },
                                    [&](int place, int i) { out[lo + place] = row[lo + i]; });
 }
 
@@ -418,13 +475,14 @@ cudaError_t launch_bounds_update(const BoundsParams& p, bool e4m3, int n_sm, cud
 cudaError_t launch_bounds_select(const SelectParams& p, int n_sm, cudaStream_t stream) {
     const int units = p.B * p.Hkv;
     int cluster = 1;  // more blocks while they would be idle and a block has several rounds of pages
-    while (cluster < 8 && 2LL * cluster * units <= 2LL * n_sm && p.t.max_pages > cluster * (kSelectThreads / 4)) cluster *= 2;
+    while (cluster < 8 && 2LL * cluster * units <= 2LL * n_sm && p.t.max_pages > cluster * 16 * kSelectWarps) cluster *= 2;
     const int smem = 4 * p.t.max_pages;
     auto go = [&](auto* f) {
         const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), 4 * kSelectMostPages);
         return e != cudaSuccess ? e : launch_cluster(f, units * cluster, cluster, kSelectThreads, smem, stream, p);
     };
-    return p.c.d == 64 ? go(select_kernel<64>) : go(select_kernel<128>);
+    if (p.c.d == 64) return p.rows <= 16 ? go(select_kernel<64, 1>) : go(select_kernel<64, 4>);
+    return p.rows <= 16 ? go(select_kernel<128, 1>) : go(select_kernel<128, 4>);
 }
 
 }  // namespace attn

@@ -12,14 +12,19 @@
 // third joins the parts of every row: O = sum_k 2^(m_k - M) O_k / L, M = max m_k, L = sum_k 2^(m_k - M) l_k.
 //
 // Bound by the products and the exponentials where a prefix has many rows, by memory below about 150 rows: 4 flops a
-// row and element read, against about 280 flops a byte.  Work is cut over a grid of two CTAs a multiprocessor as in
-// the decode kernels: units (prefix, kv head, tile of rows) end to end on a line of cost, equal shares of it.  Two CTAs
-// share a multiprocessor, so that one's products run under the other's exponentials.
+// row and element read, against about 280 flops a byte.  Work is cut over one CTA a multiprocessor as in the decode
+// kernels: units (prefix, kv head, up to 256 of the rows) end to end on a line of cost, equal shares of it.
 //
-//   warps 0-3: one thread a row: the queries to shared memory, weights, the row's part to global memory
+// A CTA has two streams of scores -> weights -> output, so that one's products run under the other's exponentials.  With
+// more than 128 rows the streams are two tiles of rows against the same positions (each tile of keys and values is
+// loaded once for 256 rows), with up to 128 they are the same rows against the even and the odd tiles of positions, two
+// parts to be joined.
+//
+//   warps 0-3, 4-7: a stream each, one thread a row: the queries to shared memory, weights, the row's part to global memory
 //   bf16 pages: a warp for the TMA loads, boxes of 16 to 128 positions with 128 bytes of each row
 //   E4M3 pages: four warps that load codes, widen them (code * 2^k is a bf16 number) and write the tiles themselves
-//   last warp: one thread issues the products
+//   last two warps: a stream each, one thread issues its products (one thread for both left gaps between them: a wait
+//   that is already over costs it 130 cycles, four of them to 1030 cycles of products)
 #include <cuda_bf16.h>
 
 #include <cstddef>
@@ -33,12 +38,14 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kTile = 128;  // rows of a unit, and positions of a tile
-constexpr PagedShape kShape{kTile, 2, 2};
+constexpr int kTile = 128;         // rows of a stream, and positions of a tile
+constexpr int kRows = 2 * kTile;   // of a unit, at most
+// Costs are counted in products of a tile of rows with a tile of positions.
+constexpr PagedShape kShape{kTile, 4, 4};
 
 template <bool E4M3>
 struct Roles {
-    static constexpr int kLoad = 4, kLoaders = E4M3 ? 4 : 1, kMma = kLoad + kLoaders, kThreads = 32 * (kMma + 1);
+    static constexpr int kLoad = 8, kLoaders = E4M3 ? 4 : 1, kMma = kLoad + kLoaders, kThreads = 32 * (kMma + 2);
 };
 struct Shared {
     unsigned cost[kPagedMaxBatch + 1];        // of the prefixes before g
@@ -46,21 +53,21 @@ struct Shared {
     unsigned short order[kPagedMaxBatch];     // sequences by prefix
     unsigned short rank[kPagedMaxBatch];      // a sequence's place among those of its prefix
     unsigned count[kPagedMaxBatch];           // sequences of prefix g
-    unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full, p_half, p_full, o_full, q_full;
-    unsigned scan[2][12];
+    unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], q_full;
+    unsigned scan[2][16];
     uint32_t tmem;
     int abort;
 };
 template <int D>
 struct Cfg {
-    static constexpr int kStages = D == 64 ? 2 : 1;
+    static constexpr int kStages = 2;
     static constexpr int kParts = D / 64;           // of a row, 128 bytes each
     static constexpr int kPart = kTile * 128;
     static constexpr int kBytes = kParts * kPart;   // of a tile of queries, keys or values
-    static constexpr int kOffK = kBytes, kOffV = kOffK + kStages * kBytes, kOffShared = kOffV + kStages * kBytes;
+    static constexpr int kOffK = 2 * kBytes, kOffV = kOffK + kStages * kBytes, kOffShared = kOffV + kStages * kBytes;
     static constexpr int kSmem = 1024 + kOffShared + (int)sizeof(Shared);
-    static constexpr uint32_t kCols = 256, kColO = 128;
-    static_assert(kSmem <= 115712, "two CTAs per multiprocessor");
+    static constexpr uint32_t kCols = 512, kColO = 256;  // scores of the streams at 0 and 128, outputs at 256 and 384
+    static_assert(kSmem <= 232448, "shared memory");
 };
 constexpr float kRescale = 8.f;  // log2 of how far a score may pass the reference
 
@@ -83,6 +90,18 @@ __device__ __forceinline__ int prefix_of(const PrefixParams& p, int b) {
     return g < 0 || g >= p.G ? -1 : g;
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+// Units of one prefix and kv head: `whole` of 256 rows, and one of the rest (up to 128 rows cost half).
+struct HeadCost {
+    int whole, rest;           // units of 256 rows; rows of the last one, 0: none
+    unsigned per, last;        // their costs
+    __device__ __forceinline__ HeadCost(int rows, int tiles) {
+        whole = rows / kRows;
+        rest = rows - whole * kRows;
+        per = paged_cost(2 * tiles, kShape);
+        last = rest == 0 ? 0 : rest > kTile ? per : paged_cost(tiles, kShape);
+    }
+    __device__ __forceinline__ unsigned sum() const { return whole * per + last; }
+};
 
 // Members by prefix and costs, by all threads; CTA 0 leaves them for the joining kernel.  Returns the line's length and,
 // in `units`, how many units there are.
@@ -120,9 +139,9 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
             const int n = tiles_of(prefix_length(p, g));
             if (blockIdx.x == 0 && p.t.len[g] != prefix_length(p, g)) atomicOr(p.c.err, kCacheErrPosition);
             m = sh.count[g];
-            const int per = p.Hkv * (((int)m * p.rows + kTile - 1) / kTile);
-            c = per * paged_cost(n, kShape);
-            if (n) own_units += per;
+            const HeadCost head((int)m * p.rows, n);
+            c = p.Hkv * head.sum();
+            if (n) own_units += p.Hkv * (head.whole + (head.rest > 0));
         }
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -180,6 +199,10 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
 struct Stretch {
     unsigned at, end;
     int g, h, row0, rows, len, g0, g1;
+    __device__ __forceinline__ bool two() const { return rows > kTile; }  // tiles of rows; else the streams share the positions
+    // Tiles of a stream, and its i-th.
+    __device__ __forceinline__ int steps(int stream) const { return two() ? g1 - g0 : (g1 - g0 + 1 - stream) / 2; }
+    __device__ __forceinline__ int tile(int stream, int i) const { return g0 + (two() ? i : 2 * i + stream); }
 };
 __device__ __forceinline__ Stretch stretch_begin(const PrefixParams& p, const PagedCuts& cuts, const Shared& sh) {
     Stretch s{};
@@ -198,14 +221,18 @@ __device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared
     while (sh.cost[s.g + 1] <= s.at) ++s.g;
     s.len = prefix_length(p, s.g);
     const int n = tiles_of(s.len), all = (sh.members[s.g + 1] - sh.members[s.g]) * p.rows;
-    const unsigned per = paged_cost(n, kShape), into = s.at - sh.cost[s.g];
-    const int unit = (int)(into / per), blocks = (all + kTile - 1) / kTile;
-    const unsigned off = into - unit * per, to = min(per, off + (s.end - s.at));
-    s.h = unit / blocks;
-    s.row0 = (unit - s.h * blocks) * kTile;
-    s.rows = min(kTile, all - s.row0);
-    s.g0 = min(n, max(0, (int)off - (int)kShape.overhead));
-    s.g1 = min(n, max(0, (int)to - (int)kShape.overhead));
+    const HeadCost head(all, n);
+    const unsigned into = s.at - sh.cost[s.g], sum = head.sum();
+    s.h = (int)(into / sum);
+    const unsigned in_head = into - s.h * sum;
+    const int unit = min(head.whole, (int)(in_head / head.per));
+    const unsigned off = in_head - unit * head.per, per = unit < head.whole ? head.per : head.last;
+    const unsigned to = min(per, off + (s.end - s.at));
+    s.row0 = unit * kRows;
+    s.rows = min(kRows, all - s.row0);
+    const int w = s.two() ? 2 : 1;
+    s.g0 = min(n, max(0, (int)off - (int)kShape.overhead) / w);
+    s.g1 = min(n, max(0, (int)to - (int)kShape.overhead) / w);
     s.at += to - off;
 }
 
@@ -277,7 +304,7 @@ __device__ __forceinline__ void widen16(const uint4& v, float f, uint4& lo, uint
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
     using C = Cfg<D>;
     using R = Roles<E4M3>;
     constexpr int kStages = C::kStages;
@@ -291,14 +318,16 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sh.k_full[i]), E4M3 ? 4 : 1);
             mbar_init(smem_u32(&sh.v_full[i]), E4M3 ? 4 : 1);
-            mbar_init(smem_u32(&sh.k_empty[i]), 1);
-            mbar_init(smem_u32(&sh.v_empty[i]), 1);
+            mbar_init(smem_u32(&sh.k_empty[i]), 2);
+            mbar_init(smem_u32(&sh.v_empty[i]), 2);
         }
-        mbar_init(smem_u32(&sh.s_full), 1);
-        mbar_init(smem_u32(&sh.p_half), 128);
-        mbar_init(smem_u32(&sh.p_full), 128);
-        mbar_init(smem_u32(&sh.o_full), 1);
-        mbar_init(smem_u32(&sh.q_full), 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.p_half[i]), 128);
+            mbar_init(smem_u32(&sh.p_full[i]), 128);
+            mbar_init(smem_u32(&sh.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.q_full), 8);
         sh.abort = 0;
     }
     fence_barrier_init();
@@ -319,33 +348,51 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
     const Watch watch{&sh.abort, p.c.err, p.watchdog_ns};
     Stretch s = stretch_begin(p, cuts, sh);
 
-    if (warp < 4) {
+    if (warp < 8) {
         // =================================================== rows
-        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + C::kColO;
-        int n = 0, stretch = 0;
+        const int stream = warp / 4, row = tid % 128;
+        const uint32_t t_lane = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+        const uint32_t t_s = t_lane + stream * kTile, t_o = t_lane + C::kColO + stream * kTile;
+        const uint32_t s_full = smem_u32(&sh.s_full[stream]), p_half = smem_u32(&sh.p_half[stream]);
+        const uint32_t p_full = smem_u32(&sh.p_full[stream]), o_full = smem_u32(&sh.o_full[stream]);
+        const float ninf = __int_as_float(0xFF800000);
+        int n = 0, stretch = 0, tiles = 0;  // the stream's tiles and stretches, all tiles of the stretches before
         while (s.at < s.end) {
             stretch_open(p, sh, s);
             if (s.g0 >= s.g1) continue;
-            // ---- the queries, 16-byte pieces of rows in the layout of the products (128-byte swizzle)
-            constexpr int kLanes = D / 8;
-            for (int i = tid; i < kTile * kLanes; i += 128) {
-                const int row = i / kLanes, c = i % kLanes;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < s.rows) {
-                    const int x = s.row0 + row, member = x / p.rows;
-                    const long long b = sh.order[sh.members[s.g] + member];
-                    v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) +
-                                                        ((b * p.Hkv + s.h) * p.rows + (x - member * p.rows)) * D + 8 * c);
+            // ---- the queries, 16-byte pieces of rows in the layout of the products (128-byte swizzle), once both streams
+            // are through with those before
+            named_bar_sync(1, 256);
+            constexpr int kLanes = D / 8, kAtOnce = 256 / kLanes, kBatch = kTile / kAtOnce;  // rows at once; a stream's rounds
+            const int members0 = sh.members[s.g];
+            for (int r0 = tid / kLanes; r0 < (s.two() ? 2 : 1) * kTile; r0 += kTile) {
+                const int c = tid % kLanes;
+                uint4 v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * kAtOnce;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (r >= s.rows) continue;
+                    const int x = s.row0 + r, member = x / p.rows;
+                    const long long b = sh.order[members0 + member];
+                    v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) +
+                                                           ((b * p.Hkv + s.h) * p.rows + (x - member * p.rows)) * D + 8 * c);
                 }
-                *reinterpret_cast<uint4*>(smem + (c / 8) * C::kPart + row * 128 + ((c % 8) ^ (row & 7)) * 16) = v;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * kAtOnce;
+                    *reinterpret_cast<uint4*>(smem + (r / kTile) * C::kBytes + (c / 8) * C::kPart + (r % kTile) * 128 +
+                                              ((c % 8) ^ (r & 7)) * 16) = v[k];
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-            float m = __int_as_float(0xFF800000), l = 0.f;
-            for (int g = s.g0; g < s.g1; ++g, ++n) {
-                const int live = s.len - g * kTile;
-                wait(smem_u32(&sh.s_full), n & 1, watch);
+            const int steps = s.steps(stream);
+            float m = ninf, l = 0.f;
+            for (int i = 0; i < steps; ++i, ++n) {
+                const int live = s.len - s.tile(stream, i) * kTile;
+                wait(s_full, n & 1, watch);
                 __syncwarp();
                 tc_fence_after();
                 const float top = (live >= kTile ? row_max<false>(t_s, live) : row_max<true>(t_s, live)) * p.scale_log2;
@@ -356,7 +403,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
                     const float fix = to == m ? 1.f : ex2(m - to);
                     m = to;
                     l *= fix;
-                    if (g > s.g0) {
+                    if (i > 0) {
 #pragma unroll
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t r[32];
@@ -369,28 +416,47 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
                         tmem_wait_st();
                     }
                 }
-                const float ref = m == __int_as_float(0xFF800000) ? 0.f : m;
-                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, smem_u32(&sh.p_half))
-                                   : row_weights<true>(t_s, live, p.scale_log2, ref, smem_u32(&sh.p_half));
+                if (!E4M3 && live < kTile) {
+                    // positions past the end may hold anything: weight zero times a NaN is a NaN, so their values become
+                    // zero (by either stream: neither waits for the other)
+                    const int t = tiles + s.tile(stream, i) - s.g0, st = t % kStages;
+                    wait(smem_u32(&sh.v_full[st]), (t / kStages) & 1, watch);
+                    if (row >= live)
+#pragma unroll
+                        for (int x = 0; x < 8 * C::kParts; ++x)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             s_v + st * C::kBytes + (x / 8) * C::kPart + row * 128 + (x % 8) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const float ref = m == ninf ? 0.f : m;
+                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, p_half)
+                                   : row_weights<true>(t_s, live, p.scale_log2, ref, p_half);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full));
+                mbar_arrive(p_full);
             }
+            tiles += s.g1 - s.g0;
             // ---- the row's part: unscaled sums, reference and sum of weights
-            wait(smem_u32(&sh.o_full), stretch & 1, watch);
+            const bool mine = s.two() ? stream * kTile + row < s.rows : row < s.rows;
+            const int all = (sh.members[s.g + 1] - members0) * p.rows;
+            const long long at = 2 * ((long long)p.Hkv * p.rows * members0 + (long long)s.h * all + s.row0) +
+                                 stream * (s.two() ? kTile : s.rows) + row + (long long)kRows * blockIdx.x;
+            if (mine) p.part_ml[at] = make_float2(m, l);
+            if (steps == 0) continue;
+            wait(o_full, stretch & 1, watch);
             __syncwarp();
             tc_fence_after();
             ++stretch;
-            const int all = (sh.members[s.g + 1] - sh.members[s.g]) * p.rows;
-            const long long at = (long long)p.Hkv * p.rows * sh.members[s.g] + (long long)s.h * all + s.row0 + tid +
-                                 (long long)kTile * blockIdx.x;
             float* o = p.part_o + at * D;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t r[32];
                 tmem_ld32(t_o + c0, r);
                 tmem_wait_ld();
-                if (tid < s.rows) {
+                if (mine) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + c0 + e), "r"(r[e]),
@@ -399,7 +465,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
                                      : "memory");
                 }
             }
-            if (tid < s.rows) p.part_ml[at] = make_float2(m, l);
             tc_fence_before();
         }
     } else if (warp < R::kMma && !E4M3) {
@@ -532,72 +597,66 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 2) prefix_kernel(const 
             }
         }
     } else {
-        // =================================================== products (lane 0; all lanes clear values past the end)
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false), idesc_o = idesc_bf16_f32(kTile, D, true);
-        int n = 0, stretch = 0;
-        bool ok = true;
-        auto scores = [&](int m) {
-            const int st = m % kStages;
-            ok = ok && wait(smem_u32(&sh.k_full[st]), (m / kStages) & 1, watch);
-            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) return;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * C::kPart + (k % 4) * 32;
-                    mma_ss(tmem, sdesc_sw128(s_q + off, 16, 1024), sdesc_sw128(s_k + st * C::kBytes + off, 16, 1024), idesc_s,
-                           k > 0);
-                }
-                mma_commit(smem_u32(&sh.s_full));
-                mma_commit(smem_u32(&sh.k_empty[st]));
-            }
-        };
-        while (s.at < s.end && ok) {
-            stretch_open(p, sh, s);
-            if (s.g0 >= s.g1) continue;
-            ok = __all_sync(0xFFFFFFFFu, wait(smem_u32(&sh.q_full), stretch & 1, watch));
-            ++stretch;
-            for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
-                // (the scores' columns hold the weights of the tile before; its product with the values, issued before,
-                // has read them by the time these are written)
-                scores(n);
-                const int st = n % kStages;
-                ok = ok && wait(smem_u32(&sh.v_full[st]), (n / kStages) & 1, watch);
-                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-                const uint32_t v = s_v + st * C::kBytes;
-                if (!E4M3 && (g + 1) * kTile > s.len) {
-                    // positions past the end may hold anything: weight zero times a NaN is a NaN
-                    const int live = s.len - g * kTile;
-                    for (int i = lane; i < (kTile - live) * 8 * C::kParts; i += 32) {
-                        const int row = live + i / (8 * C::kParts), x = i % (8 * C::kParts);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + (x / 8) * C::kPart + row * 128 +
-                                                                                      (x % 8) * 16),
-                                     "r"(0)
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = ok && wait(smem_u32(half ? &sh.p_full : &sh.p_half), n & 1, watch);
-                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        // =================================================== products of a stream (lane 0)
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false), idesc_o = idesc_bf16_f32(kTile, D, true);
+            const int stream = warp - R::kMma;
+            const uint32_t t_s = tmem + stream * kTile, t_o = tmem + C::kColO + stream * kTile;
+            const uint32_t s_full = smem_u32(&sh.s_full[stream]), p_half = smem_u32(&sh.p_half[stream]);
+            const uint32_t p_full = smem_u32(&sh.p_full[stream]), k_full = smem_u32(sh.k_full), v_full = smem_u32(sh.v_full);
+            const uint32_t k_empty = smem_u32(sh.k_empty), v_empty = smem_u32(sh.v_empty);
+            int n = 0, stretch = 0, done = 0;  // all tiles of the stretches before; the stream's
+            bool ok = true;
+            while (s.at < s.end && ok) {
+                stretch_open(p, sh, s);
+                if (s.g0 >= s.g1) continue;
+                const bool two = s.two();
+                const int steps = s.steps(stream);
+                const uint32_t q = s_q + (two ? stream * C::kBytes : 0);
+                ok = wait(smem_u32(&sh.q_full), stretch++ & 1, watch);
+                // scores of tile t; their columns hold the weights of the tile before, whose product with the values, issued
+                // earlier, has read them by the time they are written
+                auto scores = [&](int t) {
+                    const int st = t % kStages;
+                    if (!(ok = ok && wait(k_full + 8 * st, (t / kStages) & 1, watch))) return;
                     tc_fence_after();
-                    if (lane == 0) {
+                    const uint32_t k0 = s_k + st * C::kBytes;
 #pragma unroll
-                        for (int k = 4 * half; k < 4 * half + 4; ++k)
-                            mma_ts(tmem + C::kColO, tmem + 8 * k, sdesc_sw128(v + k * 16 * 128, C::kPart, 1024), idesc_o,
-                                   g > s.g0 || k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k / 4) * C::kPart + (k % 4) * 32;
+                        mma_ss(t_s, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k0 + off, 16, 1024), idesc_s, k > 0);
                     }
+                    mma_commit(s_full);
+                    mma_commit(k_empty + 8 * st);
+                    if (!two) mma_commit(k_empty + 8 * st);  // for the other stream, which does not look at it
+                };
+                int t = two ? n : n + stream;
+                if (steps > 0) scores(t);
+                for (int i = 0; i < steps && ok; ++i) {
+                    const int st = t % kStages;
+                    const uint32_t v = s_v + st * C::kBytes;
+                    ok = wait(v_full + 8 * st, (t / kStages) & 1, watch) && wait(p_half, done & 1, watch);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(t_o, t_s + 8 * k, sdesc_sw128(v + k * 16 * 128, C::kPart, 1024), idesc_o, i > 0 || k > 0);
+                    if (!(ok = wait(p_full, done & 1, watch))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 4; k < 8; ++k)
+                        mma_ts(t_o, t_s + 8 * k, sdesc_sw128(v + k * 16 * 128, C::kPart, 1024), idesc_o, 1u);
+                    ++done;
+                    mma_commit(v_empty + 8 * st);
+                    if (!two) mma_commit(v_empty + 8 * st);
+                    t += two ? 1 : 2;
+                    if (i + 1 < steps) scores(t);
+                    else mma_commit(smem_u32(&sh.o_full[stream]));
                 }
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(smem_u32(&sh.v_empty[st]));
-                    if (g + 1 == s.g1) mma_commit(smem_u32(&sh.o_full));
-                }
-                __syncwarp();
+                n += s.g1 - s.g0;
             }
         }
+        __syncwarp();
     }
     // all warps meet behind their last copy and product
     __syncthreads();
@@ -626,18 +685,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int head = (int)(out / p.rows), r = (int)(out - (long long)head * p.rows), b = head / p.Hkv, h = head - b * p.Hkv;
     const float ninf = __int_as_float(0xFF800000);
     // the prefix's parts
-    int n1 = 0, c0 = 0;
+    int n1 = 0, c0 = 0, streams = 1, step = 0;
     long long base = 0;
     const int2 place = __ldcg(&p.place[b]);
     if (place.x >= 0) {
         const int4 g = __ldcg(&p.groups[place.x]), total = __ldcg(&p.groups[p.G]);
-        const int all = g.z * p.rows, x = place.y * p.rows + r, blocks = (all + kTile - 1) / kTile;
+        const int all = g.z * p.rows, x = place.y * p.rows + r;
         if (g.w > 0) {
             const PagedCuts cuts((unsigned)total.x, (unsigned)total.y, own.prefix_grid, kShape);
-            const unsigned u0 = (unsigned)g.x + (h * blocks + x / kTile) * paged_cost(g.w, kShape) + kShape.overhead;
-            c0 = (int)cuts.owner(u0);
-            n1 = (int)cuts.owner(u0 + g.w - 1) - c0 + 1;
-            base = (long long)p.Hkv * p.rows * g.y + (long long)h * all + x;
+            const HeadCost head(all, g.w);
+            const int unit = x / kRows, rows = min(kRows, all - unit * kRows), w = rows > kTile ? 2 : 1;
+            const unsigned u0 = (unsigned)g.x + h * head.sum() + unit * head.per + kShape.overhead;
+            // a tile is the CTA's that its last product's cost belongs to
+            c0 = (int)cuts.owner(u0 + w - 1);
+            streams = w == 2 ? 1 : 2;
+            n1 = ((int)cuts.owner(u0 + w * g.w - 1) - c0 + 1) * streams;
+            base = 2 * ((long long)p.Hkv * p.rows * g.y + (long long)h * all + unit * kRows) + x - unit * kRows;
+            step = rows;
         }
     }
     // and its own
@@ -647,7 +711,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     auto find = [&](int i, const float*& o, float2& ml) {
         long long at;
         if (i < n1) {
-            at = base + (long long)kTile * (c0 + i);
+            at = base + (long long)kRows * (c0 + i / streams) + i % streams * step;
             o = p.part_o + at * D;
             ml = __ldcg(&p.part_ml[at]);
         } else if (cut.x < 0) {

@@ -5,9 +5,10 @@
 // (positions of the step itself begin at 0).  Bound by memory: the keys are read once, W is read and written; 2 d flops a
 // row and element.  The split of the work over the CTAs is the decode's (paged.h), by blocks of 16 positions; inside a
 // stretch they go to the warps in turn, and nothing is shared, so that a position's sum has one owner and one order.
-// The products are m16n8k16 with the rows as the first operand.  A lane's piece of a key is 16 bytes as they lie in
-// memory, loaded to registers without a detour by shared memory: the order of a row's elements in the sum is free, so that
-// the queries are permuted to match (a lane's 16 bytes are the elements that it would hold of two steps).
+// Each warp has a ring of its own in shared memory and fills it itself: a TMA box of 16 keys, their W and exponents, a few
+// blocks ahead.  The products are m16n8k16 with the rows as the first operand.  A lane's piece of a key is 16 bytes as they
+// lie in memory: the order of a row's elements in the sum is free, so that the queries are permuted to match (a
+// lane's 16 bytes are the elements that it would hold of two steps, or four of codes).
 //
 // Eviction: of each sequence and kv head the `keep` positions of largest W among all but the last `recent`, and those,
 // moved to the front in their order.  One block finds the chosen positions of a head (select.h); then rows are
@@ -33,148 +34,288 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKeys = 16;  // of a block
 constexpr PagedShape kShape{kKeys, 8, 32};
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-// Four E4M3 codes as two pairs of bf16 numbers (exact).
-__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    uint32_t h0, h1;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(w >> 16)));
-    float a, b;
-    asm("{.reg .f16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h0));
-    lo = pack_bf16x2(a, b);
-    asm("{.reg .f16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h1));
-    hi = pack_bf16x2(a, b);
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
-// A lane's loads of one block: its pieces of the keys quad and quad + 8, and (E4M3) their exponents.
+// Four E4M3 codes as two pairs of fp16 numbers (exact).
+__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+}
+// Two bf16 numbers times a power of two, as fp16 numbers.
+__device__ __forceinline__ uint32_t to_f16(uint32_t w, float scale) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(__uint_as_float(w & 0xFFFF0000u) * scale), "f"(__uint_as_float(w << 16) * scale));
+    return y;
+}
+
+// A place of a warp's ring: 16 positions' keys (swizzled by the TMA load), their W, and (E4M3) their exponents.
 template <int D, bool E4M3>
-struct Piece {
-    static constexpr int kLoads = D * (E4M3 ? 1 : 2) / 64;  // of a key
-    uint4 k[2][kLoads];
-    uint32_t e[2];
-    float old;  // W of the lane's position
+struct Place {
+    static constexpr int kRow = D * (E4M3 ? 1 : 2);        // bytes of a key
+    static constexpr int kSwizzled = kRow < 128 ? kRow : 128;  // a row comes in parts of so many bytes
+    static constexpr int kBytes = kKeys * kRow;
+    static constexpr int kSide = 128, kOffE = 64;          // beside the rings: W, and the exponents behind them
+    static_assert(kBytes % 1024 == 0, "swizzled by address");
+};
+template <int D, bool E4M3, int RT>
+struct WeighCfg {
+    using P = Place<D, E4M3>;
+    static constexpr int kCtas = RT == 4 ? 1 : 2;
+    static constexpr int kFrag = RT == 1 ? 0 : RT * (D / 16) * 512;  // the queries as the products take them
+    static constexpr int kRoom = (kCtas == 2 ? 113 : 225) * 1024 - 1024 - 6 * 1024 - kFrag;
+    static constexpr int kFit = kRoom / (kWarps * (P::kBytes + P::kSide));
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr int kOffSide = kStages * kWarps * P::kBytes, kOffFrag = kOffSide + kStages * kWarps * P::kSide;
+    static constexpr int kSmem = 1024 + kOffFrag + kFrag;
+    static_assert(kStages >= 2, "a ring");
 };
 
 template <int D, bool E4M3, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) weigh_kernel(const __grid_constant__ WeighParams wp) {
+__global__ void __launch_bounds__(kThreads, (WeighCfg<D, E4M3, RT>::kCtas)) weigh_kernel(const __grid_constant__ WeighParams wp) {
+    using C = WeighCfg<D, E4M3, RT>;
+    using P = Place<D, E4M3>;
     const PagedParams& p = wp.g;
     constexpr int kSteps = D / 16;  // products of a key tile and row tile
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
     __shared__ unsigned cost[kPagedMaxBatch + 4];
     __shared__ unsigned scan[kWarps];
-    __shared__ uint4 frag[RT == 1 ? 1 : RT * kSteps * 32];  // the queries as the products take them, a step's four words
+    __shared__ unsigned long long full[kWarps][kStages];
+    __shared__ int abort_;
+    uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint4* const frag = reinterpret_cast<uint4*>(smem + C::kOffFrag);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int quad = lane / 4, pair = lane % 4, Hkv = p.Hkv, S_q = p.S_q;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * P::kBytes;
+    const uint32_t sides = smem_u32(smem) + C::kOffSide + warp * kStages * P::kSide;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    if (tid == 0) {
+        prefetch_tmap(&p.tm);
+        abort_ = 0;
+    }
+    fence_barrier_init();
     wait_for_kernel_before();
     int busy;
     const unsigned W = paged_prefix<kKeys, kThreads>(p, kShape, cost, scan, busy) * p.units;
     const PagedCuts cuts(W, busy * p.units, gridDim.x, kShape);
     let_kernel_behind_in();
     if (blockIdx.x >= cuts.C || W == 0) return;
+    const Watch watch{&abort_, p.c.err, p.watchdog_ns};
     Walk w = paged_begin(p, cuts, cost);
     const float log2e = 1.4426950408889634f;
+    int filled = 0, taken = 0;  // blocks of the warp so far
+    bool ok = true;
     while (w.at < w.end) {
         paged_open<kKeys>(p, kShape, cost, w);
         if (w.g0 >= w.g1) continue;
         const int len = w.len;
-        // a step's words of row tile r: rows quad and quad + 8 alternate
+        const int n_mine = ok ? (w.g1 - w.g0 - warp + kWarps - 1) / kWarps : 0;
+        // positions that a row of the sequence sees begin here; older blocks only fade
+        const int seen = wp.window < 0 ? 0 : max(0, len - S_q - wp.window);
+        auto block_of = [&](int i) { return w.lo + w.g0 + warp + i * kWarps; };
+        // ---- loads, the warp's own, kStages blocks ahead.  Lane j has the page of the batch's j-th block, and the place in it.
+        int pages = -1, slots = 0;       // of the blocks that are loaded next
+        int pages_now = -1, slots_now = 0;  // of those that are worked on
+        auto look_up = [&](int i0) {
+            pages = -1;
+            if (i0 + lane < n_mine) {
+                const unsigned pos = (unsigned)block_of(i0 + lane) * kKeys, index = pos / (unsigned)p.c.page;
+                slots = (int)(pos - index * p.c.page);
+                pages = p.t.pages[w.b * p.t.stride + index];
+                if (pages < 0 || pages >= p.c.n_pages) {
+                    atomicOr(p.c.err, kCacheErrPage);
+                    pages = -1;
+                }
+            }
+        };
+        auto load = [&](int i) {  // block i of the stretch; the batch of its page is the current one
+            const int page = max(0, __shfl_sync(0xFFFFFFFFu, pages, i % 32)), slot = __shfl_sync(0xFFFFFFFFu, slots, i % 32);
+            if (lane == 0) {
+                const int st = filled % kStages;
+                const uint32_t dst = ring + st * P::kBytes, side = sides + st * P::kSide, bar = smem_u32(&full[warp][st]);
+                const long long unit = (long long)page * Hkv + w.h;
+                const bool keys = block_of(i) * kKeys + kKeys > seen;
+                mbar_arrive_expect_tx(bar, 4 * kKeys + (keys ? kKeys * P::kRow + (E4M3 ? 16 : 0) : 0));
+                bulk_load(side, wp.w + unit * p.c.page + slot, 4 * kKeys, bar);
+                if (keys) {
+                    if constexpr (E4M3) {
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                            "l"(reinterpret_cast<uint64_t>(&p.tm)), "r"(0), "r"(slot), "r"(0), "r"((int)unit), "r"(bar)
+                            : "memory");
+                        bulk_load(side + P::kOffE, p.c.scales + (unit * (p.c.page / 16) + slot / 16) * 32, 16, bar);
+                    } else {
+                        asm volatile(
+                            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+                            "l"(reinterpret_cast<uint64_t>(&p.tm)), "r"(0), "r"(slot), "r"(0), "r"(0), "r"((int)unit), "r"(bar)
+                            : "memory");
+                    }
+                }
+            }
+            ++filled;
+        };
+        look_up(0);
+        pages_now = pages;
+        slots_now = slots;
+        for (int i = 0; i < min(kStages - 1, n_mine); ++i) load(i);
+
+        // ---- the queries.  A step's words of row tile r: rows quad and quad + 8 alternate, 4 of the lane's 8 (bf16) or 16
+        // (E4M3) neighbouring elements
         auto query_words = [&](int r, int ks) {
             const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + ((long long)w.b * Hkv + w.h) * p.rows * D;
             const int ra = 16 * r + quad, rb = ra + 8;
-            // element of the step's first word: 4 of the lane's 8 (bf16) or 16 (E4M3) neighbouring elements
             const int at = E4M3 ? (ks / 4) * 64 + 16 * pair + 4 * (ks % 4) : (ks / 2) * 32 + 8 * pair + 4 * (ks % 2);
             const uint2 zero = make_uint2(0, 0);
             const uint2 a = ra < p.rows ? *reinterpret_cast<const uint2*>(q + (long long)ra * D + at) : zero;
             const uint2 b = rb < p.rows ? *reinterpret_cast<const uint2*>(q + (long long)rb * D + at) : zero;
             return make_uint4(a.x, b.x, a.y, b.y);
         };
+        // E4M3: codes are fp16 numbers in the products, and so are the queries, each row times a power of two that brings its
+        // largest element to 2^14 .. 2^15 (elements below 2^-28 of that lose bits, 2^-39 of it at most); `up` undoes it
+        float up[2 * RT];
         uint4 qf[RT == 1 ? kSteps : 1];
-        if constexpr (RT == 1) {
+        if constexpr (RT > 1) __syncthreads();
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) qf[ks] = query_words(0, ks);
-        } else {
-            __syncthreads();
-            for (int i = warp; i < RT * kSteps; i += kWarps) frag[i * 32 + lane] = query_words(i / kSteps, i % kSteps);
-            __syncthreads();
+        for (int r = 0; r < RT; ++r) {
+            uint4 q[kSteps];
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) q[ks] = query_words(r, ks);
+            if constexpr (E4M3) {
+                uint32_t big[2] = {0, 0};  // as bits of bf16 numbers
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) {
+                    big[0] = __vmaxu2(big[0], __vmaxu2(q[ks].x & 0x7FFF7FFFu, q[ks].z & 0x7FFF7FFFu));
+                    big[1] = __vmaxu2(big[1], __vmaxu2(q[ks].y & 0x7FFF7FFFu, q[ks].w & 0x7FFF7FFFu));
+                }
+                float down[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t t = max(big[x] & 0xFFFFu, big[x] >> 16);
+                    t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+                    t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+                    // exponent field e: the row is below 2^(e - 126), so below 2^15 times 2^(141 - e).  A row below 2^-100
+                    // is taken as zeros in part; one with an infinity or a NaN becomes NaN.
+                    const int e = max((int)(t >> 7), 27);
+                    down[x] = e == 255 ? __int_as_float(0x7FFFFFFF) : __uint_as_float((uint32_t)min(268 - e, 254) << 23);
+                    up[2 * r + x] = __uint_as_float((uint32_t)max(e - 14, 0) << 23);
+                    if (e == 255) up[2 * r + x] = 1.f;
+                }
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks)
+                    q[ks] = make_uint4(to_f16(q[ks].x, down[0]), to_f16(q[ks].y, down[1]), to_f16(q[ks].z, down[0]),
+                                       to_f16(q[ks].w, down[1]));
+            }
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                if constexpr (RT == 1) qf[ks] = q[ks];
+                else if ((r * kSteps + ks) % kWarps == warp) frag[(r * kSteps + ks) * 32 + lane] = q[ks];
+            }
         }
+        if constexpr (RT > 1) __syncthreads();
         // rows quad and quad + 8 of every row tile: what is taken off the exponent, and the positions they see
         float lse[2 * RT];
         int last[2 * RT], first_seen[2 * RT];
+        bool dead = false;  // a row of the sequence has no weights
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
             const int row = 16 * (r / 2) + 8 * (r % 2) + quad;
             const float x = row < p.rows ? wp.lse[((long long)w.b * Hkv + w.h) * p.rows + row] : 0.f;
             const int t = len - S_q + row % S_q;
-            const bool dead = row >= p.rows || x == __int_as_float(0xFF800000);
+            const bool none = x == __int_as_float(0xFF800000);
             lse[r] = x * log2e;
-            last[r] = dead ? -1 : p.causal ? t : len - 1;
+            if constexpr (E4M3) up[r] *= p.scale_log2;
+            last[r] = none || row >= p.rows ? -1 : p.causal ? t : len - 1;
             first_seen[r] = wp.window < 0 ? 0 : max(0, t - wp.window);
+            dead |= none;
         }
-        // positions that a row of the sequence sees
-        const int seen = wp.window < 0 ? 0 : max(0, len - S_q - wp.window);
+        dead = __any_sync(0xFFFFFFFFu, dead);
         const int all_to = p.causal ? len - S_q + 1 : len;
         const int all_from = wp.window < 0 ? 0 : max(0, len - 1 - wp.window);
-        bool whole = true;  // no row of the lane is without weights
-#pragma unroll
-        for (int r = 0; r < 2 * RT; ++r) whole &= last[r] >= 0;
-        whole = __all_sync(0xFFFFFFFFu, whole);
         // the lane's position of a block, after the sums over the rows: key 8 (lane / 16) + 2 pair + (lane / 8) % 2
         const int mine = 8 * (lane / 16) + 2 * pair + (lane / 8) % 2;
-        int batch = 0;  // page numbers of the warp's next 32 blocks, a lane each
-        const int n_mine = (w.g1 - w.g0 - warp + kWarps - 1) / kWarps;
-        auto block_of = [&](int i) { return w.lo + w.g0 + warp + i * kWarps; };
-        auto pages_from = [&](int i) {
-            batch = 0;
-            if (i + lane < n_mine) {
-                const unsigned pos = (unsigned)block_of(i + lane) * kKeys;
-                batch = p.t.pages[w.b * p.t.stride + pos / (unsigned)p.c.page];
-                if (batch < 0 || batch >= p.c.n_pages) {
-                    atomicOr(p.c.err, kCacheErrPage);
-                    batch = -1;
+
+        for (int i = 0; i < n_mine && ok; ++i) {
+            // the place that the block before left is filled again
+            const int ahead = i + kStages - 1;
+            if (ahead < n_mine) {
+                if (ahead % 32 == 0) {
+                    __syncwarp();
+                    look_up(ahead);
                 }
+                load(ahead);
             }
-        };
-        using P = Piece<D, E4M3>;
-        auto fetch = [&](int i, P& f) {
-            if (i % 32 == 0) pages_from(i);
-            if (i >= n_mine) return;
-            const int page = __shfl_sync(0xFFFFFFFFu, batch, i % 32);
-            const int pos = block_of(i) * kKeys, slot = pos % p.c.page;
-            const long long unit = (long long)max(page, 0) * Hkv + w.h;
-            if (pos + kKeys > seen) {  // (older positions only fade)
-                const char* src = p.c.pages + (unit * 2 * p.c.page + slot + quad) * (D * (E4M3 ? 1 : 2)) + 16 * pair;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int l = 0; l < P::kLoads; ++l)
-                        f.k[j][l] = *reinterpret_cast<const uint4*>(src + 8 * j * (D * (E4M3 ? 1 : 2)) + 64 * l);
-                if (E4M3) {  // of the keys whose products the lane gets: 2 pair and 2 pair + 1 of either tile
-                    const uint8_t* sc = p.c.scales + (unit * (p.c.page / 16) + slot / 16) * 32 + 2 * pair;
-                    f.e[0] = *reinterpret_cast<const uint16_t*>(sc);
-                    f.e[1] = *reinterpret_cast<const uint16_t*>(sc + 8);
-                }
+            if (i % 32 == 0 && i > 0) {  // (kStages <= 32: the batch that is loaded from holds this block's page too)
+                pages_now = pages;
+                slots_now = slots;
             }
-            f.old = pos + mine < len - S_q ? wp.w[unit * p.c.page + slot + mine] : 0.f;
-        };
-        auto take = [&](int i, const P& f) {
-            const int page = __shfl_sync(0xFFFFFFFFu, batch, i % 32);
-            const int pos = block_of(i) * kKeys, slot = pos % p.c.page;
+            const int st = taken % kStages;
+            const uint32_t buf = ring + st * P::kBytes, side = sides + st * P::kSide;
+            ok = __all_sync(0xFFFFFFFFu, wait(smem_u32(&full[warp][st]), (taken / kStages) & 1, watch));
+            if (!ok) break;
+            const int pos = block_of(i) * kKeys;
             float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
             if (pos + kKeys > seen) {
-                const bool check = !whole || pos < all_from || pos + kKeys > all_to;
-                float factor[2][2];
+                // a lane's pieces of the keys quad and quad + 8, 16 bytes each
+                uint4 k[2][P::kRow / 64];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t e = f.e[j] >> 8 * c & 0xFF;  // (255: NaN codes beside it)
-                        factor[j][c] = E4M3 ? p.scale_log2 * __uint_as_float(max(e << 23, 0x00400000u)) : p.scale_log2;
+                    for (int l = 0; l < P::kRow / 64; ++l) {
+                        const int row = quad + 8 * j, chunk = 4 * (l % (P::kSwizzled / 64)) + pair;
+                        const int sw = P::kSwizzled == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+                        k[j][l] = lds16(buf + (l / (P::kSwizzled / 64)) * kKeys * P::kSwizzled + row * P::kSwizzled + 16 * sw);
+                    }
+                float factor[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t e = 0;  // of the keys whose products the lane gets: 2 pair and 2 pair + 1 of either tile
+                    if (E4M3)
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e) : "r"(side + P::kOffE + 8 * j + 2 * pair) : "memory");
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)  // (255: NaN codes beside it)
+                        factor[j][c] = __uint_as_float(max((e >> 8 * c & 0xFF) << 23, 0x00400000u));
+                }
+                const bool check = dead || pos < all_from || pos + kKeys > all_to;
+                uint32_t kb[2][2 * kSteps];  // the keys as 16-bit numbers
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int l = 0; l < P::kRow / 64; ++l) {
+                        const uint32_t v[4] = {k[j][l].x, k[j][l].y, k[j][l].z, k[j][l].w};
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) widen_e4m3(v[x], kb[j][8 * l + 2 * x], kb[j][8 * l + 2 * x + 1]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) kb[j][4 * l + x] = v[x];
+                        }
                     }
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -185,31 +326,22 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) weigh_kernel(const 
                         for (int c = 0; c < 4; ++c) s[j][0][c] = s[j][1][c] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < kSteps; ++ks) {
-                        const uint4 a = RT == 1 ? qf[ks % (RT == 1 ? kSteps : 1)] : frag[(r * kSteps + ks) * 32 + lane];
+                        const uint4 a = RT == 1 ? qf[RT == 1 ? ks : 0] : frag[(r * kSteps + ks) * 32 + lane];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t b0, b1;
-                            if constexpr (E4M3) {
-                                const uint4& v = f.k[j][ks / 4];
-                                widen_e4m3(ks % 4 == 0 ? v.x : ks % 4 == 1 ? v.y : ks % 4 == 2 ? v.z : v.w, b0, b1);
-                            } else {
-                                const uint4& v = f.k[j][ks / 2];
-                                b0 = ks % 2 ? v.z : v.x;
-                                b1 = ks % 2 ? v.w : v.y;
-                            }
-                            mma_bf16(s[j][ks % 2], a.x, a.y, a.z, a.w, b0, b1);
-                        }
+                        for (int j = 0; j < 2; ++j) mma16<E4M3>(s[j][ks % 2], a, kb[j][2 * ks], kb[j][2 * ks + 1]);
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int row = 2 * r + c / 2;
-                            const float x = s[j][0][c] + s[j][1][c];
-                            float y = ex2(fmaf(x, factor[j][c % 2], -lse[row]));
+                            const float scale = E4M3 ? factor[j][c % 2] * up[row] : p.scale_log2;
+                            float y = ex2(fmaf(s[j][0][c] + s[j][1][c], scale, -lse[row]));
                             if (check) {
                                 const int at = pos + 8 * j + 2 * pair + c % 2;
                                 if (at > last[row] || at < first_seen[row]) y = 0.f;
+                            } else if (16 * (row / 2) + 8 * (row % 2) + quad >= p.rows) {
+                                y = 0.f;
                             }
                             sum[j][c % 2] += y;
                         }
@@ -226,25 +358,25 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) weigh_kernel(const 
             const bool odd = lane & 8;
             float total = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 8);
             total += __shfl_xor_sync(0xFFFFFFFFu, total, 4);
+            float old;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(side + 4 * mine) : "memory");
+            if (pos + mine >= len - S_q) old = 0.f;  // (whatever it holds)
+            const int page = __shfl_sync(0xFFFFFFFFu, pages_now, i % 32), slot = __shfl_sync(0xFFFFFFFFu, slots_now, i % 32);
             if ((lane & 4) == 0 && pos + mine < len && page >= 0)
-                wp.w[((long long)page * Hkv + w.h) * p.c.page + slot + mine] = fmaf(wp.decay, f.old, total);
-        };
-        P a, b;
-        if (n_mine > 0) fetch(0, a);
-        for (int i = 0; i < n_mine; i += 2) {
-            // (the batch of page numbers changes at multiples of 32: the block before is through by then)
-            fetch(i + 1, b);
-            take(i, a);
-            if (i + 1 < n_mine) take(i + 1, b);
-            fetch(i + 2, a);
+                wp.w[((long long)page * Hkv + w.h) * p.c.page + slot + mine] = fmaf(wp.decay, old, total);
+            ++taken;
+            __syncwarp();  // the block is read: its place may be filled again
         }
     }
+    // all warps meet behind their last copy; after a wait that ran out those on their way are waited for
+    __syncthreads();
+    if (abort_) drain();
 }
 
 // ---------------------------------------------------------------------------------------------- eviction
 constexpr int kRankThreads = 1024;
 
-__global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kRankThreads, 1) rank_kernel(const __grid_constant__ EvictParams p) {
     __shared__ SelectShared<kRankThreads> sh;
     extern __shared__ uint32_t keys[];
     const int tid = threadIdx.x, unit = blockIdx.x, b = unit / p.c.Hkv, h = unit - b * p.c.Hkv, page = p.c.page;
@@ -265,23 +397,42 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constan
         else if (i >= p.keep) kept[i] = old + i - p.keep;
     }
     if (n <= stay) return;
-    auto weight = [&](int i) {
+    const int Hkv = p.c.Hkv;
+    bool astray = false;
+    auto page_of = [&](int i, int& slot) {
         const int index = (unsigned)i / (unsigned)page;
-        const int g = row[index];
-        if (g < 0 || g >= p.c.n_pages) {
-            atomicOr(p.c.err, kCacheErrPage);
-            return 0u;
-        }
-        return ordered(p.w[((long long)g * p.c.Hkv + h) * page + (i - index * page)]);
+        slot = i - index * page;
+        return row[index];
+    };
+    auto weight_in = [&](int g, int slot) {  // (a page out of range: as light as can be)
+        const bool ok = g >= 0 && g < p.c.n_pages;
+        astray |= !ok;
+        return ok ? ordered(p.w[((long long)g * Hkv + h) * page + slot]) : 0u;
     };
     auto emit = [&](int place, int i) { kept[place] = i; };
     if (old <= p.cached) {
-        for (int i = tid; i < old; i += kRankThreads) keys[i] = weight(i);
+        constexpr int kAhead = 8;  // pages, then weights, at once
+        for (int i0 = tid; i0 < old; i0 += kAhead * kRankThreads) {
+            int g[kAhead], slot[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) g[j] = page_of(min(i0 + j * kRankThreads, old - 1), slot[j]);
+            uint32_t k[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) k[j] = weight_in(g[j], slot[j]);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j * kRankThreads < old) keys[i0 + j * kRankThreads] = k[j];
+        }
         __syncthreads();
-        select_largest<kRankThreads>(old, p.keep, sh, [&](int i) { return keys[i]; }, emit);
+        select_largest<kRankThreads, 16>(old, p.keep, sh, [&](int i) { return keys[i]; }, emit);
     } else {
-        select_largest<kRankThreads>(old, p.keep, sh, weight, emit);
+        select_largest<kRankThreads, 1>(old, p.keep, sh, [&](int i) {
+            int slot;
+            const int g = page_of(i, slot);
+            return weight_in(g, slot);
+        }, emit);
     }
+    if (astray) atomicOr(p.c.err, kCacheErrPage);
 }
 
 // A row's place in memory: [page][head][keys, values][slot].
@@ -412,12 +563,19 @@ __global__ void __launch_bounds__(kPlaceThreads) move_in_place_kernel(const __gr
 
 cudaError_t launch_weigh(const WeighParams& p, bool e4m3, int n_sm, cudaStream_t stream) {
     const int tiles = (p.g.rows + 15) / 16, rt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;
-    const int grid = n_sm * (rt == 1 ? 2 : 1);
-    auto go = [&](auto* f) { return launch_dependent(f, dim3((unsigned)grid), kThreads, 0, stream, p); };
+    auto go = [&](auto* f, int smem, int ctas) {
+        const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), smem);
+        return e != cudaSuccess ? e : launch_dependent(f, dim3((unsigned)(n_sm * ctas)), kThreads, smem, stream, p);
+    };
     auto of_rows = [&](auto d, auto type) {
         constexpr int D = decltype(d)::value;
         constexpr bool E = decltype(type)::value;
-        return rt == 1 ? go(weigh_kernel<D, E, 1>) : rt == 2 ? go(weigh_kernel<D, E, 2>) : go(weigh_kernel<D, E, 4>);
+        auto with = [&](auto t) {
+            using C = WeighCfg<D, E, decltype(t)::value>;
+            return go(weigh_kernel<D, E, decltype(t)::value>, C::kSmem, C::kCtas);
+        };
+        return rt == 1 ? with(std::integral_constant<int, 1>{})
+                       : rt == 2 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 4>{});
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

@@ -95,7 +95,7 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
                                     const float* LSE, float scale, attn_mask_kind kind, int window, float decay,
                                     const int* page_table, long long table_stride, int max_pages, const int* cache_len,
                                     void* stream) {
-    if (!h || !weights || !aligned(weights, 4) || !Q || !aligned(Q, 16) || !LSE || !aligned(LSE, 4))
+    if (!h || !weights || !aligned(weights, 16) || !Q || !aligned(Q, 16) || !LSE || !aligned(LSE, 4))
         return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f) || !(decay >= 0.f && decay <= 1.f)) return ATTN_ERR_INVALID_ARG;
@@ -106,6 +106,8 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
     if (!room_ok(h, max_pages) || most * B * h->c.Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
     attn::WeighParams p{};
+    p.g.tm = h->keys_map;
+    p.g.watchdog_ns = 2000000000LL;
     p.g.q = Q;
     p.g.c = h->c;
     p.g.t = table_of(page_table, table_stride, max_pages, cache_len);
@@ -166,7 +168,7 @@ attn_status attn_prefix_create(attn_prefix_handle* out, int B, int Hq, int Hkv, 
         return st;
     }
     const size_t rows = (size_t)B * Hq * S_q;
-    const size_t parts = rows + (size_t)attn::kPrefixTile * attn::kPrefixCtasPerSm * h->step->n_sm;
+    const size_t parts = 2 * (rows + (size_t)attn::kPrefixTile * h->step->n_sm);
     auto get = [&](auto& p, size_t n) {
         if (st != ATTN_OK) return;
         const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), n * sizeof(*p));
@@ -206,7 +208,7 @@ attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, c
         return ATTN_ERR_UNSUPPORTED;
     // the line of cost fits an int: every unit, and every prefix's last one
     const long long tiles = (long long)prefix_max_pages * cache->c.page / attn::kPrefixTile + 8;
-    if (tiles * s->Hkv * ((long long)n_prefix + (long long)s->B * rows / attn::kPrefixTile) > 0x7FFFFFFFLL)
+    if (2 * tiles * s->Hkv * ((long long)n_prefix + (long long)s->B * rows / attn::kPrefixTile) > 0x7FFFFFFFLL)
         return ATTN_ERR_UNSUPPORTED;
     attn::PrefixParams p{};
     p.tm = cache->rows_map;
@@ -220,7 +222,7 @@ attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, c
     p.scale_log2 = (float)((double)s->scale * 1.4426950408889634);
     p.watchdog_ns = s->watchdog_ns;
     p.withhold = s->withhold;
-    const int grid = std::min(s->n_sm * attn::kPrefixCtasPerSm, s->grid_limit);
+    const int grid = std::min(s->n_sm, s->grid_limit);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (attn::launch_prefix(p, cache->e4m3, grid, st) != cudaSuccess) return ATTN_ERR_CUDA;
     attn::OwnParts own = h->own;

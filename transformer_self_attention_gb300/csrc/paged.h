@@ -180,9 +180,9 @@ struct PrefixParams {
     const int* of;   // [B]: the prefix of a sequence, -1: none; null: the only one
     const void* q;   // [B, Hq, S_q, d] bf16
     int B, G, Hkv, rows, box_rows;
-    // Parts: that of CTA c for row x of the rows of prefix g and kv head h is number
-    //   Hkv * rows * (sequences of the prefixes before g) + h * (rows of the prefix) + x + 128 c,
-    // so that no two meet: along the line of work either the CTA or the unit moves on.
+    // Parts: those of CTA c for a unit of `rows` rows, which begins `before` rows into the rows of all prefixes and kv
+    // heads, are numbers 2 before + 256 c + row, or with up to 128 rows, where there are two, + stream * rows + row: along
+    // the line of work either the CTA or the unit moves on, so that no two meet.
     float* part_o;    // [.][d]
     float2* part_ml;  // [.]: reference (base 2) and sum
     int4* groups;     // [G + 1]: cost of the prefixes before, their sequences, sequences of this one, its tiles; last: the
@@ -202,7 +202,7 @@ struct JoinParams {  // of the own positions, as PagedParams; prefix_grid: the f
     void* o;
     float* lse;
 };
-constexpr int kPrefixTile = 128, kPrefixCtasPerSm = 2;
+constexpr int kPrefixTile = 128;
 cudaError_t launch_prefix(const PrefixParams& p, bool e4m3, int grid, cudaStream_t stream);
 cudaError_t launch_join(const PrefixParams& p, const JoinParams& own, cudaStream_t stream);
 

@@ -38,14 +38,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // bf16 pages as {row part, slots, parts of a row, K / V, page * Hkv + head}: a row comes in parts of 128 bytes, one box
-// holds 16 positions' keys and values of one head; not `whole`: `slots` positions, 128 bytes of their keys or values.
-bool encode_bf16(CUtensorMap* map, const attn::CacheView& c, int slots = 16, bool whole = true) {
+// holds `slots` positions' keys and values of one head, or (sides = 1) their keys or values, or one part of those.
+bool encode_bf16(CUtensorMap* map, const attn::CacheView& c, int slots, int box_parts, int sides) {
     auto enc = encoder();
     if (!enc) return false;
     const int row = c.d * 2, parts = row / 128;
     cuuint64_t dims[5] = {64, (cuuint64_t)c.page, (cuuint64_t)parts, 2, (cuuint64_t)c.n_pages * c.Hkv};
     cuuint64_t strides[4] = {(cuuint64_t)row, 128, (cuuint64_t)c.page * row, (cuuint64_t)2 * c.page * row};
-    cuuint32_t box[5] = {64, (cuuint32_t)slots, whole ? (cuuint32_t)parts : 1, whole ? 2u : 1u, 1};
+    cuuint32_t box[5] = {64, (cuuint32_t)slots, (cuuint32_t)box_parts, (cuuint32_t)sides, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c.pages, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -216,9 +216,11 @@ attn_status attn_cache_create(attn_cache_handle* out, int n_pages, int Hkv, int 
     if (!clear_error(h->c.err)) return fail(ATTN_ERR_CUDA);
     // the largest power of two that divides the page, up to a decode tile
     while (h->box_rows < 128 && page % (2 * h->box_rows) == 0) h->box_rows *= 2;
-    if (!(h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows)
-                  : encode_bf16(&h->map, h->c) && encode_bf16(&h->rows_map, h->c, h->box_rows, false)))
-        return fail(ATTN_ERR_CUDA);
+    const int parts = d * 2 / 128;
+    const bool encoded = h->e4m3 ? encode_e4m3(&h->map, h->c, h->box_rows) && encode_e4m3(&h->keys_map, h->c, 16)
+                                 : encode_bf16(&h->map, h->c, 16, parts, 2) && encode_bf16(&h->keys_map, h->c, 16, parts, 1) &&
+                                       encode_bf16(&h->rows_map, h->c, h->box_rows, 1, 1);
+    if (!encoded) return fail(ATTN_ERR_CUDA);
     *out = h;
     return ATTN_OK;
 }

@@ -21,6 +21,7 @@ struct attn_rope_plan {
 struct attn_cache_plan {
     attn::CacheView c;
     CUtensorMap map{};
+    CUtensorMap keys_map{};  // the keys of 16 positions
     CUtensorMap rows_map{};  // bf16: boxes of box_rows positions, 128 bytes of their keys or values
     bool e4m3 = false;
     int box_rows = 16;
