@@ -803,7 +803,7 @@ attn_status attn_bounds_update(attn_cache_handle h, void* codes, void* exponents
  *   out_table : int32 device [B, Hkv, keep]: the chosen entries of the page table in their order, then -1.
  *   out_len   : int32 device [B]: the positions in the chosen pages (the same for every head, as only the last page is
  *               not full).  Neither may be an input.
- * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (rows, or max_pages or keep above 49152), ATTN_ERR_CUDA.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (rows, or max_pages or keep above 40960), ATTN_ERR_CUDA.
  */
 attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const void* exponents, int B, int Hq, int S_q,
                                const void* Q, const int* page_table, long long table_stride, int max_pages,

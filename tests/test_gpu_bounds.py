@@ -90,6 +90,35 @@ def test_bounds_of_extreme_keys():
     assert bounds.exponents.cpu()[[5, 6, 8]].tolist() == [[255]] * 3
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,pages", [(16, 4), (64, 3), (144, 40)])
+def test_bounds_of_rows_of_very_different_sizes(d, page, pages):
+    """E4M3 rows whose exponents lie far apart, up to 14 apart and 15 apart; rows of zeros; a NaN code beside a usual
+    exponent; few pages (a block each) and many (a warp each)."""
+    g = torch.Generator().manual_seed(4)
+    n = pages * page
+    x = torch.randn((pages, 3, 2, page, d), generator=g)
+    x[:, 0] *= torch.exp2(torch.randint(-60, 60, (pages, 2, page, 1), generator=g).float())
+    x[:, 1] *= torch.exp2(torch.randint(0, 15, (pages, 2, page, 1), generator=g).float())
+    x[:, 2, :, 3] = 0
+    codes, e = pu.quantise(x)
+    codes[0, 1, 0, 2, 5] = 0x7F
+    codes[1, 0, 0, 3, 1] = 0xFF
+    e[2, 1, 0, :9] = torch.tensor([100, 114, 113, 101, 107, 100, 114, 109, 110], dtype=torch.uint8)
+    e[2, 1, 0, 9:] = 105
+    e[2, 2, 0, :] = 90
+    e[2, 2, 0, 4] = 105
+    e[1, 2, 1, 7] = 255  # (a value's: no matter)
+    cache = tsa.PagedCache(pages, 3, page, d, dtype="e4m3", pages=codes.view(torch.float8_e4m3fn).cuda(),
+                           scales=e.view(pages, 3, 2, page // 16, 16).transpose(2, 3).contiguous().cuda())
+    vals = pu.values(cache.pages, cache.scales)
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    bounds, before = _marked(cache)
+    bounds.update(table.cuda(), _int32([n - 1]))
+    _check_bounds(bounds, vals, table, page, [n - 1], [n - 1], before)
+    assert int(bounds.exponents[0, 1]) == 255 and int(bounds.exponents[1, 0]) == 255
+
+
 def _sparse(lens, Hq, Hkv, S_q, d, page, store, keep, sinks, recent, seed=0, poke=None, q_scale=1.0):
     cache, vals, table = _cache(lens, Hkv, page, d, store, seed=seed)
     if poke:

@@ -10,16 +10,18 @@
 // two costs nothing, so that scores are exact: the selection does not depend on an order of summation, and equal
 // scores go to the page that comes first.
 //
-// Update: bound by memory, the changed pages' keys read once (and by latency where one page a sequence changes).  A warp
-// takes a page and head; its lanes hold 16 bytes of a row each, several rows at once, eight loads under way.
+// Update: bound by memory, the changed pages' keys read once, or by latency where one page a sequence changes.  A warp takes
+// a page and head, or the whole block does where there are fewer of them than blocks; the lanes hold 16 bytes of a row
+// each, several rows at once, eight loads under way (sixteen of codes).
 // Select: a cluster of one to eight blocks for each sequence and kv head.  With the negative and the positive parts of a
-// query behind one another, a score is one product of 2 d whole numbers, lo first, then hi: m16n8k32 products of 8-bit numbers with
-// the rows as the first operand and eight pages as the second.  (This GPU's rate for them is low, and is enough:
-// 16 rows of 131K pages and heads took 33 us with four lanes to a page and dp4a.)  A lane's 16 bytes of a page are those
-// that it would hold of two steps; the queries are permuted to match.  Scores go to the first block's shared memory, which
-// then finds the largest (select.h).
+// query behind one another, a score is one product of 2 d whole numbers, lo first, then hi: m16n8k16 products of fp16 numbers,
+// which hold them exactly, as float32 holds their sums, with the rows as the first operand and eight pages as the second.
+// (Products of 8-bit whole numbers, m16n8k32, took 200 cycles each, and dp4a with four lanes to a page was no faster.)  A
+// lane's 16 bytes of a page are those that it would hold of four steps; the queries are permuted to match.  Scores go to the
+// first block's shared memory, which then finds the largest (select.h).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -59,11 +61,8 @@ __device__ __forceinline__ int sequence_length(const PageTable& t, int page, int
     return 0;
 }
 
-// A lane's channels of one row, 16 bytes, and the running bounds over rows.
-template <bool E4M3>
-struct RowBounds;
-template <>
-struct RowBounds<false> {
+// A lane's channels of one row, 16 bytes, and the running bounds over rows: bf16.
+struct RowBounds {
     static constexpr int kChannels = 8;
     uint32_t lo[4], hi[4];
     __device__ __forceinline__ void clear() {
@@ -73,22 +72,18 @@ struct RowBounds<false> {
             hi[i] = 0xFF80FF80u;
         }
     }
-    __device__ __forceinline__ void take(const uint4& v, uint32_t) {
+    __device__ __forceinline__ void take(const uint4& v, uint32_t, uint32_t) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        join(w, w);
+    }
+    __device__ __forceinline__ void join(const uint32_t* l, const uint32_t* h) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            lo[i] = min2_nan(lo[i], w[i]);
-            hi[i] = max2_nan(hi[i], w[i]);
+            lo[i] = min2_nan(lo[i], l[i]);
+            hi[i] = max2_nan(hi[i], h[i]);
         }
     }
-    __device__ __forceinline__ void join(int o) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo[i] = min2_nan(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
-            hi[i] = max2_nan(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
-        }
-    }
-    __device__ __forceinline__ void get(float* l, float* h) const {
+    __device__ __forceinline__ void get(float* l, float* h, uint32_t) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             l[2 * i] = __uint_as_float(lo[i] << 16);
@@ -98,56 +93,88 @@ struct RowBounds<false> {
         }
     }
 };
-// Codes become bf16 numbers: a code's exponent and mantissa, moved to where a bf16 number has them, stand for 2^-120 of it
-// (subnormal codes become subnormal numbers), so that two multiplications by powers of two give the row's elements, as exactly
-// as a bf16 number can (beyond 2^128: infinities).  (By way of fp16 and float32 numbers 235 MB took 88 us.)
-template <>
-struct RowBounds<true> {
+// E4M3: both bounds of a pair of channels as packed 16-bit numbers.  Where the rows' exponents lie within 14 of the largest
+// (WIDE false), codes become fp16 numbers times 2^(e - largest), exactly; otherwise bf16 numbers: a code's exponent and
+// mantissa, moved to where a bf16 number has them, stand for 2^-120 of it (subnormal codes become subnormal numbers), and two
+// multiplications by powers of two give the element, as exactly as a bf16 number can (beyond 2^128: infinities).  The second
+// form takes twice the instructions: 88 us for 235 MB.
+template <bool WIDE>
+struct CodeBounds {
     static constexpr int kChannels = 16;
     uint32_t lo[8], hi[8];
     uint32_t nan;
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            lo[i] = 0x7F807F80u;
-            hi[i] = 0xFF80FF80u;
+            lo[i] = WIDE ? 0x7F807F80u : 0x7C007C00u;
+            hi[i] = WIDE ? 0xFF80FF80u : 0xFC00FC00u;
         }
         nan = 0;
     }
-    __device__ __forceinline__ void take(const uint4& v, uint32_t e) {
-        // 2^(e - 127) as a bf16 number, twice; for 255 a NaN
-        const uint32_t f = (e == 255 ? 0x7FFFu : e == 0 ? 0x0040u : e << 7) * 0x10001u;
+    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
+        uint32_t y;
+        if constexpr (WIDE) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+        uint32_t y;
+        if constexpr (WIDE) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    __device__ __forceinline__ void take(const uint4& v, uint32_t e, uint32_t top) {
+        // 2^(e - 127) as a bf16 number, or 2^(e - top) as an fp16 number, twice (no row has 255 here)
+        const uint32_t f = (WIDE ? (e == 0 ? 0x0040u : e << 7) : e + 15 - top << 10) * 0x10001u;
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t a = __byte_perm(w[i], 0, 0x1404), b = __byte_perm(w[i], 0, 0x3424);
-            uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
-            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x7B807B80u));  // 2^120
-            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x7B807B80u));
-            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
-            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(f));
-            nan |= ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a NaN code: 127 carries into the top bit
-            lo[2 * i] = min2_nan(lo[2 * i], x);
-            hi[2 * i] = max2_nan(hi[2 * i], x);
-            lo[2 * i + 1] = min2_nan(lo[2 * i + 1], y);
-            hi[2 * i + 1] = max2_nan(hi[2 * i + 1], y);
+            uint32_t x, y;
+            if constexpr (WIDE) {
+                const uint32_t a = __byte_perm(w[i], 0, 0x1404), b = __byte_perm(w[i], 0, 0x3424);
+                x = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u);
+                y = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x7B807B80u));  // 2^120
+                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x7B807B80u));
+                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(f));
+                nan |= ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a NaN code: 127 carries into the top bit
+            } else {
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)w[i]));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)(w[i] >> 16)));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(f));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(f));
+            }
+            lo[2 * i] = least(lo[2 * i], x);
+            hi[2 * i] = most(hi[2 * i], x);
+            lo[2 * i + 1] = least(lo[2 * i + 1], y);
+            hi[2 * i + 1] = most(hi[2 * i + 1], y);
         }
     }
-    __device__ __forceinline__ void join(int o) {
+    __device__ __forceinline__ void join(const uint32_t* l, const uint32_t* h) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            lo[i] = min2_nan(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
-            hi[i] = max2_nan(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
+            lo[i] = least(lo[i], l[i]);
+            hi[i] = most(hi[i], h[i]);
         }
     }
-    __device__ __forceinline__ void get(float* l, float* h) const {
+    __device__ __forceinline__ void get(float* l, float* h, uint32_t top) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            l[2 * i] = nan ? __int_as_float(0x7FFFFFFF) : __uint_as_float(lo[i] << 16);
-            l[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
-            h[2 * i] = __uint_as_float(hi[i] << 16);
-            h[2 * i + 1] = __uint_as_float(hi[i] & 0xFFFF0000u);
+            if constexpr (WIDE) {
+                l[2 * i] = __uint_as_float(lo[i] << 16);
+                l[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
+                h[2 * i] = __uint_as_float(hi[i] << 16);
+                h[2 * i + 1] = __uint_as_float(hi[i] & 0xFFFF0000u);
+            } else {
+                const float f = __uint_as_float(max(top << 23, 0x00400000u));
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo[i]));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+                l[2 * i] = a.x * f; l[2 * i + 1] = a.y * f;
+                h[2 * i] = b.x * f; h[2 * i + 1] = b.y * f;
+            }
         }
+        if (nan) l[0] = __int_as_float(0x7FFFFFFF);
     }
 };
 
@@ -159,12 +186,100 @@ __device__ __forceinline__ void changed_pages(const BoundsParams& p, int b, bool
     lo = fresh == 0 ? hi : (unsigned)(n - fresh) / (unsigned)p.c.page;
 }
 
+// The bounds of one page and head by `share` warps (1, or all of the block, which then meet in `joint`); `part`: the warp's
+// number among them.
+template <int D, bool E4M3>
+struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
+    static constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kAhead = E4M3 ? 16 : 8;
+    static constexpr int kRound = kAhead * kAtOnce;
+    uint4 v[kAhead];
+    uint32_t e[kAhead];
+    __device__ __forceinline__ void load(const BoundsParams& p, long long unit, int rows, int r0) {
+        const int lane = threadIdx.x % 32;
+        const char* src = p.c.pages + unit * 2 * p.c.page * kRow + 16 * (lane % kLanes);
+        const uint8_t* sc = E4M3 ? p.c.scales + unit * (p.c.page / 16) * 32 : nullptr;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int row = min(r0 + i * kAtOnce + lane / kLanes, rows - 1);  // the last row again changes nothing
+            v[i] = *reinterpret_cast<const uint4*>(src + (long long)row * kRow);
+            e[i] = E4M3 ? sc[(row / 16) * 32 + row % 16] : 0;
+        }
+    }
+};
+template <int D, bool E4M3, class R>
+__device__ __forceinline__ void page_bounds(const BoundsParams& p, long long unit, int rows, uint32_t top, int part, int share,
+                                            Rows<D, E4M3>& x, uint32_t (*joint)[2][32][8]) {
+    using X = Rows<D, E4M3>;
+    constexpr int kLanes = X::kLanes, kWords = R::kChannels / 2;
+    const int lane = threadIdx.x % 32;
+    R run;
+    run.clear();
+    for (int r0 = part * X::kRound; r0 < rows;) {  // (the first rows have been loaded)
+#pragma unroll
+        for (int i = 0; i < X::kAhead; ++i) run.take(x.v[i], x.e[i], top);
+        r0 += share * X::kRound;
+        if (r0 < rows) x.load(p, unit, rows, r0);
+    }
+#pragma unroll
+    for (int o = kLanes; o < 32; o *= 2) {
+        uint32_t l[kWords], h[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            l[i] = __shfl_xor_sync(0xFFFFFFFFu, run.lo[i], o);
+            h[i] = __shfl_xor_sync(0xFFFFFFFFu, run.hi[i], o);
+        }
+        run.join(l, h);
+    }
+    if (share > 1) {
+        if (lane < kLanes)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                joint[part][0][lane][i] = run.lo[i];
+                joint[part][1][lane][i] = run.hi[i];
+            }
+        bool nan = false;
+        if constexpr (E4M3) nan = run.nan != 0;
+        nan = __syncthreads_or(nan);
+        if (part) return;
+        for (int w = 1; w < share; ++w) run.join(joint[w][0][lane % kLanes], joint[w][1][lane % kLanes]);
+        if constexpr (E4M3) run.nan = nan;
+    }
+    float l[R::kChannels], u[R::kChannels];
+    run.get(l, u, top);
+    uint32_t big = 0;  // as bits: a NaN is above an infinity
+#pragma unroll
+    for (int i = 0; i < R::kChannels; ++i)
+        big = max(big, max(__float_as_uint(l[i]) & 0x7FFFFFFFu, __float_as_uint(u[i]) & 0x7FFFFFFFu));
+    big = __reduce_max_sync(0xFFFFFFFFu, big);
+    const bool bad = big >= 0x7F800000u;
+    const int k = bad ? 0 : power_of(big);
+    if (lane < kLanes) {
+        const float f = exp2_of(-k);
+        uint32_t cl[R::kChannels / 4], cu[R::kChannels / 4];
+#pragma unroll
+        for (int i = 0; i < R::kChannels / 4; ++i) {
+            cl[i] = cu[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int a = bad ? 0 : __float2int_rd(l[4 * i + j] * f), c = bad ? 0 : __float2int_ru(u[4 * i + j] * f);
+                cl[i] |= (uint32_t)(a & 0xFF) << 8 * j;
+                cu[i] |= (uint32_t)(c & 0xFF) << 8 * j;
+            }
+        }
+        uint32_t* out = reinterpret_cast<uint32_t*>(p.codes + unit * 2 * D) + lane * (R::kChannels / 4);
+#pragma unroll
+        for (int i = 0; i < R::kChannels / 4; ++i) {
+            out[i] = cl[i];
+            out[D / 4 + i] = cu[i];
+        }
+        if (lane == 0) p.exps[unit] = (uint8_t)(bad ? 255 : k + 127);
+    }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kUpdateThreads) update_kernel(const __grid_constant__ BoundsParams p) {
-    using R = RowBounds<E4M3>;
-    constexpr int kLanes = D / R::kChannels;  // of a row
-    constexpr int kRows = 32 / kLanes;        // a warp's rows at once
-    constexpr int kAhead = 8;
+    constexpr int kWarps = kUpdateThreads / 32;
+    __shared__ uint32_t joint[kWarps][2][32][8];
     __shared__ unsigned first[kPagedMaxBatch + 1];  // changed pages of the sequences before b
     __shared__ unsigned scan[kUpdateThreads / 32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -198,8 +313,9 @@ __global__ void __launch_bounds__(kUpdateThreads) update_kernel(const __grid_con
         __syncthreads();
     }
     const long long items = (long long)carry * p.c.Hkv;
-    for (long long item = (long long)blockIdx.x * (kUpdateThreads / 32) + warp; item < items;
-         item += (long long)gridDim.x * (kUpdateThreads / 32)) {
+    const int share = items <= (long long)gridDim.x ? kWarps : 1, part = share > 1 ? warp : 0;
+    const long long step = (long long)gridDim.x * kWarps / share;
+    for (long long item = ((long long)blockIdx.x * kWarps + warp) / share; item < items; item += step) {
         const unsigned entry = (unsigned)(item / p.c.Hkv);
         const int h = (int)(item - (long long)entry * p.c.Hkv);
         int b = 0, top = p.B - 1;  // the last b with first[b] <= entry
@@ -214,82 +330,74 @@ __global__ void __launch_bounds__(kUpdateThreads) update_kernel(const __grid_con
         const int page = p.t.pages[b * p.t.stride + index];
         if (page < 0 || page >= p.c.n_pages) {
             if (lane == 0) atomicOr(p.c.err, kCacheErrPage);
-            continue;
+            continue;  // (all warps that share the page)
         }
         const long long unit = (long long)page * p.c.Hkv + h;
-        const int rows = min(p.c.page, n - index * p.c.page), r0 = lane / kLanes;
-        const char* src = p.c.pages + unit * 2 * p.c.page * (D * (E4M3 ? 1 : 2)) + 16 * (lane % kLanes);
-        const uint8_t* sc = E4M3 ? p.c.scales + unit * (p.c.page / 16) * 32 : nullptr;
-        R run;
-        run.clear();
-        for (int r = r0; r < rows + r0; r += kAhead * kRows) {  // (the same number of rounds for all lanes)
-            uint4 v[kAhead];
-            uint32_t e[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int row = min(r + i * kRows, rows - 1);  // the last row again changes nothing
-                v[i] = *reinterpret_cast<const uint4*>(src + (long long)row * (D * (E4M3 ? 1 : 2)));
-                e[i] = E4M3 ? sc[(row / 16) * 32 + row % 16] : 0;
+        const int rows = min(p.c.page, n - index * p.c.page);
+        Rows<D, E4M3> x;
+        x.load(p, unit, rows, min(part * Rows<D, E4M3>::kRound, rows - 1));
+        if constexpr (E4M3) {
+            // the largest and the smallest exponent of the rows
+            const uint8_t* sc = p.c.scales + unit * (p.c.page / 16) * 32;
+            uint32_t most = 0, least = 255;
+            for (int r = lane; r < rows; r += 32) {
+                const uint32_t e = sc[(r / 16) * 32 + r % 16];
+                most = max(most, e);
+                least = min(least, e);
             }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) run.take(v[i], e[i]);
-        }
-#pragma unroll
-        for (int o = kLanes; o < 32; o *= 2) run.join(o);
-        float l[R::kChannels], u[R::kChannels];
-        run.get(l, u);
-        uint32_t big = 0;  // as bits: a NaN is above an infinity
-#pragma unroll
-        for (int i = 0; i < R::kChannels; ++i)
-            big = max(big, max(__float_as_uint(l[i]) & 0x7FFFFFFFu, __float_as_uint(u[i]) & 0x7FFFFFFFu));
-        big = __reduce_max_sync(0xFFFFFFFFu, big);
-        const bool bad = big >= 0x7F800000u;
-        const int k = bad ? 0 : power_of(big);
-        if (lane < kLanes) {
-            const float f = exp2_of(-k);
-            uint32_t cl[R::kChannels / 4], cu[R::kChannels / 4];
-#pragma unroll
-            for (int i = 0; i < R::kChannels / 4; ++i) {
-                cl[i] = cu[i] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int a = bad ? 0 : __float2int_rd(l[4 * i + j] * f), c = bad ? 0 : __float2int_ru(u[4 * i + j] * f);
-                    cl[i] |= (uint32_t)(a & 0xFF) << 8 * j;
-                    cu[i] |= (uint32_t)(c & 0xFF) << 8 * j;
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            if (most == 255) {  // a row that is not finite
+                if (part == 0) {
+                    for (int i = lane; i < 2 * D / 4; i += 32) reinterpret_cast<uint32_t*>(p.codes + unit * 2 * D)[i] = 0;
+                    if (lane == 0) p.exps[unit] = 255;
                 }
+            } else if (most - least <= 14) {
+                page_bounds<D, true, CodeBounds<false>>(p, unit, rows, most, part, share, x, joint);
+            } else {
+                page_bounds<D, true, CodeBounds<true>>(p, unit, rows, most, part, share, x, joint);
             }
-            uint32_t* out = reinterpret_cast<uint32_t*>(p.codes + unit * 2 * D) + lane * (R::kChannels / 4);
-#pragma unroll
-            for (int i = 0; i < R::kChannels / 4; ++i) {
-                out[i] = cl[i];
-                out[D / 4 + i] = cu[i];
-            }
-            if (lane == 0) p.exps[unit] = (uint8_t)(bad ? 255 : k + 127);
+        } else {
+            page_bounds<D, false, RowBounds>(p, unit, rows, 0, part, share, x, joint);
         }
+        if (share > 1) __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------------------------------------- selection
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256, kSelectBlocks = 3;  // a multiprocessor: with 512 threads one block fitted, 24 us for 512 heads
 
 constexpr int kSelectWarps = kSelectThreads / 32;
-template <int D>
+template <int D, int RT>
 struct SelectMemory {
-    static constexpr int kPitch = 2 * D + 16;  // rows begin 16 bytes of banks apart
-    alignas(16) int8_t q[ATTN_DECODE_MAX_ROWS][kPitch];  // negative parts, positive parts
+    static constexpr int kPitch = 4 * D + 16;  // bytes; rows begin 16 bytes of banks apart
+    alignas(16) uint8_t q[RT * 16][kPitch];    // negative parts, positive parts, fp16
     SelectShared<kSelectThreads> sel;
     unsigned big[kSelectWarps];
 };
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four whole numbers of 8 bits as fp16 numbers: with the sign turned they are 0 .. 255 above -128, and 1024 + that has them as
+// its last bits.
+__device__ __forceinline__ void widen_s8(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));  // 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
 }
 
 template <int D, int RT>  // RT: row tiles of 16, at most (the last may be short)
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ SelectMemory<D> sh;
+__global__ void __launch_bounds__(kSelectThreads, RT == 1 ? kSelectBlocks : 2) select_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ SelectMemory<D, RT> sh;
     extern __shared__ uint32_t keys[];  // of the first block of the cluster: a page each
     const cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -308,15 +416,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         const int i = tid + k * kSelectThreads;
         v[k] = i < p.rows * (D / 8) ? q[i] : make_uint4(0, 0, 0, 0);
     }
-    constexpr int kAtOnce = RT == 1 ? 2 : 1;  // tiles of eight pages under way
-    const int stride = blocks * kSelectWarps * 8 * kAtOnce, lo = p.sinks;
-    int i0 = (rank * kSelectWarps + warp) * 8 * kAtOnce;
-    int g[kAtOnce];
-    auto pages_at = [&](int at) {  // (entries that no position needs may hold anything, and are not used)
-#pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) g[x] = row[min(lo + at + 8 * x + quad, p.t.max_pages - 1)];
-    };
-    pages_at(i0);
+    // a warp's round: a tile of eight pages, one for each four lanes
+    const int stride = blocks * kSelectWarps * 8, lo = p.sinks;
+    int i0 = (rank * kSelectWarps + warp) * 8;
+    auto page_at = [&](int i) { return row[min(lo + i + quad, p.t.max_pages - 1)]; };  // (beyond those in use: anything)
+    int g = page_at(i0), g1 = page_at(i0 + stride), g2 = page_at(i0 + 2 * stride);  // this round's, and the next ones'
     const int len = sequence_length(p.t, page, b, p.c.err, tid == 0 && h == 0 && rank == 0);
     const int n = (unsigned)(len + page - 1) / (unsigned)page;
     int* out = p.out_table + (long long)unit * p.keep;
@@ -333,22 +437,28 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     }
     if (K == 0) return;
     constexpr int kChunks = D / 32;  // 16-byte pieces of a lane and page
-    uint4 c[kAtOnce][kChunks];
-    uint32_t e[kAtOnce];
-    auto codes_of = [&](int at) {
-#pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const bool live = at + 8 * x + quad < m, ok = live && g[x] >= 0 && g[x] < p.c.n_pages;
-            const long long place = (long long)(ok ? g[x] : 0) * p.Hkv + h;
-            const uint4* src = reinterpret_cast<const uint4*>(p.codes + place * 2 * D) + pair;
-            e[x] = p.exps[place];
-#pragma unroll
-            for (int j = 0; j < kChunks; ++j) c[x][j] = src[4 * j];
-            if (live && !ok) g[x] = -1;  // told below
-            else g[x] = 0;
-        }
+    uint4 c[kChunks];
+    uint32_t e = 0;
+    bool astray = false;
+    auto place_of = [&](int page_no, int i) {
+        const bool live = i + quad < m, ok = live && page_no >= 0 && page_no < p.c.n_pages;
+        astray |= live && !ok;
+        return (long long)(ok ? page_no : 0) * p.Hkv + h;
     };
-    codes_of(i0);
+    auto codes_of = [&](int page_no, int i) {
+        const long long place = place_of(page_no, i);
+        const uint4* src = reinterpret_cast<const uint4*>(p.codes + place * 2 * D) + pair;
+        e = p.exps[place];
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) c[j] = src[4 * j];
+    };
+    auto to_l2 = [&](int page_no, int i) {  // (2 d bytes: a line of 128 to a lane)
+        if (i < m && pair < 2 * D / 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes + place_of(page_no, i) * 2 * D + 128 * pair));
+    };
+    codes_of(g, i0);
+    to_l2(g1, i0 + stride);
+    to_l2(g2, i0 + 2 * stride);
     // ---- the queries as whole numbers of one power of two: negative and positive parts
     uint32_t big = 0;  // as bits of a bf16
 #pragma unroll
@@ -369,78 +479,64 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         const int i = tid + k * kSelectThreads, r = i / (D / 8), at = i % (D / 8);
         if (r >= 16 * tiles) continue;
         const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t neg[2] = {0, 0}, pos[2] = {0, 0};
+        uint32_t neg[4], pos[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x = __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-            const int y = bad ? 0 : __float2int_rn(x * f);
-            neg[j / 4] |= (uint32_t)(min(y, 0) & 0xFF) << 8 * (j % 4);
-            pos[j / 4] |= (uint32_t)max(y, 0) << 8 * (j % 4);
+        for (int j = 0; j < 4; ++j) {
+            const float x = bad ? 0.f : rintf(__uint_as_float(w[j] << 16) * f);
+            const float y = bad ? 0.f : rintf(__uint_as_float(w[j] & 0xFFFF0000u) * f);
+            neg[j] = f16_pair(fminf(x, 0.f), fminf(y, 0.f));
+            pos[j] = f16_pair(fmaxf(x, 0.f), fmaxf(y, 0.f));
         }
-        *reinterpret_cast<uint2*>(&sh.q[r][8 * at]) = make_uint2(neg[0], neg[1]);
-        *reinterpret_cast<uint2*>(&sh.q[r][D + 8 * at]) = make_uint2(pos[0], pos[1]);
+        *reinterpret_cast<uint4*>(&sh.q[r][16 * at]) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+        *reinterpret_cast<uint4*>(&sh.q[r][2 * D + 16 * at]) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
     }
     if (blocks > 1) cluster.sync();  // (all blocks of the cluster are there)
     else __syncthreads();
     uint32_t* first_keys = blocks > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-    uint4 qa[RT == 1 ? kChunks : 1], qb[RT == 1 ? kChunks : 1];  // rows quad and quad + 8
-    if constexpr (RT == 1) {
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            qa[j] = *reinterpret_cast<const uint4*>(&sh.q[quad][16 * (4 * j + pair)]);
-            qb[j] = *reinterpret_cast<const uint4*>(&sh.q[quad + 8][16 * (4 * j + pair)]);
-        }
-    }
     for (; i0 < m; i0 += stride) {
+        float best[2] = {-16777216.f, -16777216.f};  // of the lane's rows, for pages 2 pair and 2 pair + 1
+#pragma unroll 1
+        for (int r = 0; r < tiles; ++r) {
+            float s[2][4];  // two chains
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x)
-            if (g[x] < 0 && h == 0 && pair == 0) atomicOr(p.c.err, kCacheErrPage);
-        if (i0 + stride < m) pages_at(i0 + stride);
+            for (int k = 0; k < 4; ++k) s[0][k] = s[1][k] = 0.f;
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            int best[2] = {-(1 << 30), -(1 << 30)};  // of the lane's rows, for pages 2 pair and 2 pair + 1
+            for (int j = 0; j < kChunks; ++j) {
+                const uint8_t* qa = &sh.q[16 * r + quad][32 * (4 * j + pair)];
+                const uint8_t* qb = &sh.q[16 * r + quad + 8][32 * (4 * j + pair)];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r >= tiles) break;
-                int s[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < kChunks; ++j) {
-                    uint4 a, b;
-                    if constexpr (RT == 1) {
-                        a = qa[j];
-                        b = qb[j];
-                    } else {
-                        a = *reinterpret_cast<const uint4*>(&sh.q[16 * r + quad][16 * (4 * j + pair)]);
-                        b = *reinterpret_cast<const uint4*>(&sh.q[16 * r + quad + 8][16 * (4 * j + pair)]);
-                    }
-                    mma_s8(s, a.x, b.x, a.y, b.y, c[x][j].x, c[x][j].y);
-                    mma_s8(s, a.z, b.z, a.w, b.w, c[x][j].z, c[x][j].w);
-                }
-                if (16 * r + quad < p.rows) {
-                    best[0] = max(best[0], s[0]);
-                    best[1] = max(best[1], s[1]);
-                }
-                if (16 * r + quad + 8 < p.rows) {
-                    best[0] = max(best[0], s[2]);
-                    best[1] = max(best[1], s[3]);
+                for (int y = 0; y < 2; ++y) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(qa + 16 * y), b = *reinterpret_cast<const uint4*>(qb + 16 * y);
+                    uint32_t b0, b1, b2, b3;
+                    widen_s8(y ? c[j].z : c[j].x, b0, b1);
+                    widen_s8(y ? c[j].w : c[j].y, b2, b3);
+                    mma_f16(s[0], a.x, b.x, a.y, b.y, b0, b1);
+                    mma_f16(s[1], a.z, b.z, a.w, b.w, b2, b3);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int o = 4; o < 32; o *= 2) best[k] = max(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], o));
-                const uint32_t ek = __shfl_sync(0xFFFFFFFFu, e[x], 4 * (2 * pair + k));
-                const int i = i0 + 8 * x + 2 * pair + k;
-                if (quad == k && i < m)
-                    first_keys[i] = ek == 255 ? 0xFF800000u : ordered((float)best[k] * __uint_as_float(ek << 23));
-            }
+            for (int k = 0; k < 4; ++k)
+                if (16 * r + quad + 8 * (k / 2) < p.rows) best[k % 2] = fmaxf(best[k % 2], s[0][k] + s[1][k]);
         }
-        if (i0 + stride < m) codes_of(i0 + stride);
+        const uint32_t mine = e;
+        if (i0 + stride < m) codes_of(g1, i0 + stride);
+        g1 = g2;
+        g2 = page_at(i0 + 3 * stride);
+        to_l2(g2, i0 + 3 * stride);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], o));
+            const uint32_t ek = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * pair + k));
+            const int i = i0 + 2 * pair + k;
+            if (quad == k && i < m) first_keys[i] = ek == 255 ? 0xFF800000u : ordered(best[k] * __uint_as_float(ek << 23));
+        }
     }
+    if (astray && h == 0) atomicOr(p.c.err, kCacheErrPage);
     if (blocks > 1) cluster.sync();
     else __syncthreads();
     if (rank) return;
-    select_largest<kSelectThreads, 4>(m, K, sh.sel, [&](int i) { return keys[i]; },
+    select_largest<kSelectThreads>(m, K, sh.sel, [&](int i) { return keys[i]; },
                                    [&](int place, int i) { out[lo + place] = row[lo + i]; });
 }
 
@@ -475,7 +571,7 @@ cudaError_t launch_bounds_update(const BoundsParams& p, bool e4m3, int n_sm, cud
 cudaError_t launch_bounds_select(const SelectParams& p, int n_sm, cudaStream_t stream) {
     const int units = p.B * p.Hkv;
     int cluster = 1;  // more blocks while they would be idle and a block has several rounds of pages
-    while (cluster < 8 && 2LL * cluster * units <= 2LL * n_sm && p.t.max_pages > cluster * 16 * kSelectWarps) cluster *= 2;
+    while (cluster < 8 && 2LL * cluster * units <= 2LL * n_sm && p.t.max_pages > cluster * 24 * kSelectWarps) cluster *= 2;
     const int smem = 4 * p.t.max_pages;
     auto go = [&](auto* f) {
         const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), 4 * kSelectMostPages);

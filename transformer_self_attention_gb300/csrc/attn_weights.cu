@@ -378,7 +378,7 @@ constexpr int kRankThreads = 1024;
 
 __global__ void __launch_bounds__(kRankThreads, 1) rank_kernel(const __grid_constant__ EvictParams p) {
     __shared__ SelectShared<kRankThreads> sh;
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     const int tid = threadIdx.x, unit = blockIdx.x, b = unit / p.c.Hkv, h = unit - b * p.c.Hkv, page = p.c.page;
     wait_for_kernel_before();
     let_kernel_behind_in();
@@ -411,22 +411,34 @@ __global__ void __launch_bounds__(kRankThreads, 1) rank_kernel(const __grid_cons
     };
     auto emit = [&](int place, int i) { kept[place] = i; };
     if (old <= p.cached) {
-        constexpr int kAhead = 8;  // pages, then weights, at once
-        for (int i0 = tid; i0 < old; i0 += kAhead * kRankThreads) {
+        // four neighbours to a thread (they are in one page: its size is a multiple of 16), pages, then weights, at once
+        constexpr int kAhead = 4;
+        for (int i0 = 4 * tid; i0 < old; i0 += 4 * kAhead * kRankThreads) {
             int g[kAhead], slot[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) g[j] = page_of(min(i0 + j * kRankThreads, old - 1), slot[j]);
-            uint32_t k[kAhead];
+            for (int j = 0; j < kAhead; ++j) g[j] = page_of(min(i0 + 4 * j * kRankThreads, (old - 1) & ~3), slot[j]);
+            float4 v[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) k[j] = weight_in(g[j], slot[j]);
+            for (int j = 0; j < kAhead; ++j) {
+                const bool ok = g[j] >= 0 && g[j] < p.c.n_pages;
+                astray |= !ok;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ok) v[j] = *reinterpret_cast<const float4*>(p.w + ((long long)g[j] * Hkv + h) * page + slot[j]);
+                else slot[j] = -1;  // as light as can be
+            }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (i0 + j * kRankThreads < old) keys[i0 + j * kRankThreads] = k[j];
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + 4 * j * kRankThreads;  // (room for the last four: the places' number is rounded up)
+                if (i < old)
+                    *reinterpret_cast<uint4*>(&keys[i]) =
+                        slot[j] < 0 ? make_uint4(0, 0, 0, 0)
+                                    : make_uint4(ordered(v[j].x), ordered(v[j].y), ordered(v[j].z), ordered(v[j].w));
+            }
         }
         __syncthreads();
-        select_largest<kRankThreads, 16>(old, p.keep, sh, [&](int i) { return keys[i]; }, emit);
+        select_largest<kRankThreads>(old, p.keep, sh, [&](int i) { return keys[i]; }, emit);
     } else {
-        select_largest<kRankThreads, 1>(old, p.keep, sh, [&](int i) {
+        select_largest<kRankThreads>(old, p.keep, sh, [&](int i) {
             int slot;
             const int g = page_of(i, slot);
             return weight_in(g, slot);

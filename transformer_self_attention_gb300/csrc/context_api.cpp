@@ -126,7 +126,7 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
 attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const int* page_table, long long table_stride,
                                int max_pages, const int* cache_len, int keep, int recent, const int* to_table,
                                long long to_stride, int to_max_pages, int* out_len, int* kept, void* stream) {
-    if (!h || !weights || !aligned(weights, 4) || B < 1) return ATTN_ERR_INVALID_ARG;
+    if (!h || !weights || !aligned(weights, 16) || B < 1) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (keep < 0 || recent < 0 || (long long)keep + recent < 1 || !out_len || !aligned(out_len, 4) || !kept ||
         !aligned(kept, 4) || out_len == cache_len || kept == page_table)

@@ -77,7 +77,7 @@ struct SelectParams {
     int* out_table;  // [B, Hkv, keep]
     int* out_len;    // [B]
 };
-constexpr int kSelectMostPages = 48 << 10;  // of a sequence: a word for each in shared memory
+constexpr int kSelectMostPages = 40 << 10;  // of a sequence: a word for each in shared memory
 cudaError_t launch_bounds_update(const BoundsParams& p, bool e4m3, int n_sm, cudaStream_t stream);
 cudaError_t launch_bounds_select(const SelectParams& p, int n_sm, cudaStream_t stream);
 
