@@ -12,7 +12,7 @@
 //
 // Update: bound by memory, the changed pages' keys read once, or by latency where one page a sequence changes.  A warp takes
 // a page and head, or the whole block does where there are fewer of them than blocks; the lanes hold 16 bytes of a row
-// each, several rows at once, eight loads under way (sixteen of codes).
+// each, several rows at once, eight loads under way.
 // Select: a cluster of one to eight blocks for each sequence and kv head.  With the negative and the positive parts of a
 // query behind one another, a score is one product of 2 d whole numbers, lo first, then hi: m16n8k16 products of fp16 numbers,
 // which hold them exactly, as float32 holds their sums, with the rows as the first operand and eight pages as the second.
@@ -37,6 +37,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kUpdateThreads = 256;
+__host__ __device__ constexpr int update_blocks(bool e4m3) { return e4m3 ? 3 : 4; }  // of a multiprocessor, all at once
 
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t y;
@@ -190,7 +191,7 @@ __device__ __forceinline__ void changed_pages(const BoundsParams& p, int b, bool
 // number among them.
 template <int D, bool E4M3>
 struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
-    static constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kAhead = E4M3 ? 16 : 8;
+    static constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kAhead = 8;
     static constexpr int kRound = kAhead * kAtOnce;
     uint4 v[kAhead];
     uint32_t e[kAhead];
@@ -198,6 +199,16 @@ struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
         const int lane = threadIdx.x % 32;
         const char* src = p.c.pages + unit * 2 * p.c.page * kRow + 16 * (lane % kLanes);
         const uint8_t* sc = E4M3 ? p.c.scales + unit * (p.c.page / 16) * 32 : nullptr;
+        if (r0 % 16 == 0 && r0 + kRound <= rows) {  // one address, and constants
+            src += (r0 + lane / kLanes) * (long long)kRow;
+            if (E4M3) sc += r0 * 2 + lane / kLanes;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                v[i] = *reinterpret_cast<const uint4*>(src + i * kAtOnce * kRow);
+                e[i] = E4M3 ? sc[i * kAtOnce / 16 * 32 + i * kAtOnce % 16] : 0;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int row = min(r0 + i * kAtOnce + lane / kLanes, rows - 1);  // the last row again changes nothing
@@ -277,7 +288,7 @@ __device__ __forceinline__ void page_bounds(const BoundsParams& p, long long uni
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kUpdateThreads) update_kernel(const __grid_constant__ BoundsParams p) {
+__global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int kWarps = kUpdateThreads / 32;
     __shared__ uint32_t joint[kWarps][2][32][8];
     __shared__ unsigned first[kPagedMaxBatch + 1];  // changed pages of the sequences before b
@@ -562,7 +573,7 @@ cudaError_t launch_cluster(K* kernel, int grid, int cluster, int threads, int sm
 
 cudaError_t launch_bounds_update(const BoundsParams& p, bool e4m3, int n_sm, cudaStream_t stream) {
     const long long items = (long long)p.B * p.t.max_pages * p.c.Hkv, warps = kUpdateThreads / 32;
-    const int grid = (int)std::min<long long>((items + warps - 1) / warps, 4LL * n_sm);
+    const int grid = (int)std::min<long long>((items + warps - 1) / warps, (long long)update_blocks(e4m3) * n_sm);
     auto go = [&](auto* f) { return launch_dependent(f, dim3((unsigned)grid), kUpdateThreads, 0, stream, p); };
     if (p.c.d == 64) return e4m3 ? go(update_kernel<64, true>) : go(update_kernel<64, false>);
     return e4m3 ? go(update_kernel<128, true>) : go(update_kernel<128, false>);

@@ -467,54 +467,74 @@ __device__ __forceinline__ long long weight_at(const EvictParams& p, RowAt r, in
     return ((long long)r.page * p.c.Hkv + h) * p.c.page + r.slot;
 }
 
-// Into other pages: 32 rows of one head to a warp, a lane looks up one row, and all lanes copy them, 512 bytes at a time.
+// Into other pages: a warp takes 32 rows of one head after another (eight where there are too few for all warps), a lane looks up one row, and all lanes copy them, 512
+// bytes at a time, eight loads under way; the next rows are looked up meanwhile.
+constexpr int kMoveBlocks = 4;  // a multiprocessor, all at once
 template <int ROWB>  // bytes of a key
-__global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ EvictParams p, int groups) {
+__global__ void __launch_bounds__(kThreads, kMoveBlocks) move_kernel(const __grid_constant__ EvictParams p, int groups, int per) {
     constexpr int kLanes = ROWB / 16, kAtOnce = 32 / kLanes, kAhead = 8;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     wait_for_kernel_before();
     let_kernel_behind_in();
-    const long long item = (long long)blockIdx.x * kWarps + warp;
-    const int unit = (int)(item / groups), first = (int)(item - (long long)unit * groups) * 32;
-    if (unit >= p.B * p.c.Hkv) return;
-    const int b = unit / p.c.Hkv, h = unit - b * p.c.Hkv, stay = p.keep + p.recent;
-    const int i = first + lane, from = i < stay ? p.kept[(long long)unit * stay + i] : -1;
-    RowAt src{-1, 0}, dst{-1, 0};
-    if (from >= 0) {
-        src = row_at(p, p.t.pages + b * p.t.stride, from);
-        dst = row_at(p, p.to + b * p.to_stride, i);
-    }
-    const bool ok = src.page >= 0 && dst.page >= 0;
-    if (!__any_sync(0xFFFFFFFFu, ok)) return;
-    if (ok) {
-        p.w[weight_at(p, dst, h)] = p.w[weight_at(p, src, h)];
-        if (p.c.scales) {
-            const uint8_t* s = p.c.scales + scale_at(p, src, h);
-            uint8_t* d = p.c.scales + scale_at(p, dst, h);
-            d[0] = s[0];
-            d[16] = s[16];
-        }
-    }
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, from >= 0));  // (the first lanes)
-    const long long side = (long long)p.c.page * ROWB;            // from a key to its value
-    // where the lane's row begins
-    const long long s0 = (((long long)src.page * p.c.Hkv + h) * 2 * p.c.page + src.slot) * ROWB;
-    const long long d0 = (((long long)dst.page * p.c.Hkv + h) * 2 * p.c.page + dst.slot) * ROWB;
+    const int items = p.B * p.c.Hkv * groups, stay = p.keep + p.recent, step = gridDim.x * kWarps;
+    const long long side = (long long)p.c.page * ROWB;  // from a key to its value
     const int sub = lane / kLanes, off = 16 * (lane % kLanes);
-    for (int r = 0; r < 2 * n; r += kAhead * kAtOnce) {  // rows: the keys, then the values, of row r / 2
-        uint4 v[kAhead];
-        long long to[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int x = r + k * kAtOnce + sub, who = min(x / 2, 31);
-            const long long s = __shfl_sync(0xFFFFFFFFu, s0, who) + (x % 2) * side + off;
-            to[k] = __shfl_sync(0xFFFFFFFFu, d0, who) + (x % 2) * side + off;
-            if (!__shfl_sync(0xFFFFFFFFu, (int)ok, who) || x >= 2 * n) to[k] = -1;
-            else v[k] = *reinterpret_cast<const uint4*>(p.c.pages + s);
+    auto kept_of = [&](int item) {
+        const int unit = item / groups, i = (item - unit * groups) * per + lane;
+        return item < items && lane < per && i < stay ? p.kept[(long long)unit * stay + i] : -1;
+    };
+    struct Where {
+        RowAt src, dst;
+        int from;
+    };
+    auto look_up = [&](int item, int from) {
+        Where w{{-1, 0}, {-1, 0}, from};
+        if (from >= 0) {
+            const int unit = item / groups, i = (item - unit * groups) * per + lane, b = unit / p.c.Hkv;
+            w.src = row_at(p, p.t.pages + b * p.t.stride, from);
+            w.dst = row_at(p, p.to + b * p.to_stride, i);
         }
+        return w;
+    };
+    int item = blockIdx.x * kWarps + warp;
+    Where now = look_up(item, kept_of(item));
+    for (; item < items; item += step) {
+        const int next_from = kept_of(item + step), h = item / groups % p.c.Hkv;
+        Where next{{-1, 0}, {-1, 0}, -1};
+        const bool ok = now.src.page >= 0 && now.dst.page >= 0;
+        if (ok) {
+            p.w[weight_at(p, now.dst, h)] = p.w[weight_at(p, now.src, h)];
+            if (p.c.scales) {
+                const uint8_t* s = p.c.scales + scale_at(p, now.src, h);
+                uint8_t* d = p.c.scales + scale_at(p, now.dst, h);
+                d[0] = s[0];
+                d[16] = s[16];
+            }
+        }
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, now.from >= 0));  // (the first lanes)
+        // where the lane's row begins; -1: it is not moved
+        const long long s0 = ok ? (((long long)now.src.page * p.c.Hkv + h) * 2 * p.c.page + now.src.slot) * ROWB : -1;
+        const long long d0 = (((long long)now.dst.page * p.c.Hkv + h) * 2 * p.c.page + now.dst.slot) * ROWB;
+        bool looked = false;
+        for (int r = 0; r < 2 * n; r += kAhead * kAtOnce) {  // rows: the keys, then the values, of row r / 2
+            uint4 v[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (to[k] >= 0) *reinterpret_cast<uint4*>(p.c.pages + to[k]) = v[k];
+            for (int k = 0; k < kAhead; ++k) {
+                const int x = r + k * kAtOnce + sub;
+                const long long s = __shfl_sync(0xFFFFFFFFu, s0, min(x / 2, 31));
+                if (s >= 0 && x < 2 * n) v[k] = *reinterpret_cast<const uint4*>(p.c.pages + s + (x % 2) * side + off);
+            }
+            if (!looked) next = look_up(item + step, next_from);
+            looked = true;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int x = r + k * kAtOnce + sub;
+                const long long s = __shfl_sync(0xFFFFFFFFu, s0, min(x / 2, 31)), d = __shfl_sync(0xFFFFFFFFu, d0, min(x / 2, 31));
+                if (s >= 0 && x < 2 * n) *reinterpret_cast<uint4*>(p.c.pages + d + (x % 2) * side + off) = v[k];
+            }
+        }
+        if (!looked) next = look_up(item + step, next_from);
+        now = next;
     }
 }
 
@@ -595,7 +615,7 @@ cudaError_t launch_weigh(const WeighParams& p, bool e4m3, int n_sm, cudaStream_t
     return e4m3 ? of_rows(D128{}, std::true_type{}) : of_rows(D128{}, std::false_type{});
 }
 
-cudaError_t launch_evict(EvictParams p, bool e4m3, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams p, bool e4m3, int n_sm, cudaStream_t stream) {
     const int units = p.B * p.c.Hkv, stay = p.keep + p.recent;
     p.cached = (int)std::min<long long>((long long)p.t.max_pages * p.c.page, kEvictCached);
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(&rank_kernel), 4 * kEvictCached);
@@ -609,9 +629,10 @@ cudaError_t launch_evict(EvictParams p, bool e4m3, cudaStream_t stream) {
         return rowb == 64 ? go(move_in_place_kernel<64>) : rowb == 128 ? go(move_in_place_kernel<128>)
                                                                        : go(move_in_place_kernel<256>);
     }
-    const int groups = (int)((std::min<long long>(stay, (long long)p.t.max_pages * p.c.page) + 31) / 32);
-    const dim3 grid((unsigned)(((long long)units * groups + kWarps - 1) / kWarps));
-    auto go = [&](auto* f) { return launch_dependent(f, grid, kThreads, 0, stream, p, groups); };
+    const int rows = (int)std::min<long long>(stay, (long long)p.t.max_pages * p.c.page), most = kMoveBlocks * n_sm;
+    const int per = (long long)units * rows >= 32LL * kWarps * most ? 32 : 8, groups = (rows + per - 1) / per;
+    const dim3 grid((unsigned)std::min<long long>(((long long)units * groups + kWarps - 1) / kWarps, most));
+    auto go = [&](auto* f) { return launch_dependent(f, grid, kThreads, 0, stream, p, groups, per); };
     return rowb == 64 ? go(move_kernel<64>) : rowb == 128 ? go(move_kernel<128>) : go(move_kernel<256>);
 }
 

@@ -138,7 +138,7 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
             return ATTN_ERR_INVALID_ARG;
     }
     if (B > ATTN_DECODE_MAX_BATCH || !room_ok(h, max_pages) || stay > attn::kPagedMostPositions ||
-        (long long)B * h->c.Hkv * ((std::min(stay, room) + 31) / 32) > 0x7FFFFFFFLL)
+        (long long)B * h->c.Hkv * ((std::min(stay, room) + 7) / 8) > (1LL << 30))
         return ATTN_ERR_UNSUPPORTED;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
     attn::EvictParams p{};
@@ -151,7 +151,7 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
     p.kept = kept;
     p.B = B; p.keep = keep; p.recent = recent;
     p.in_place = !to_table;
-    return done(attn::launch_evict(p, h->e4m3, static_cast<cudaStream_t>(stream)));
+    return done(attn::launch_evict(p, h->e4m3, h->n_sm, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_prefix_create(attn_prefix_handle* out, int B, int Hq, int Hkv, int S_q, int d, float scale,

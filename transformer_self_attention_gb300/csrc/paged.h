@@ -227,6 +227,6 @@ struct EvictParams {
 };
 constexpr int kEvictCached = 48 << 10;
 cudaError_t launch_weigh(const WeighParams& p, bool e4m3, int n_sm, cudaStream_t stream);
-cudaError_t launch_evict(EvictParams p, bool e4m3, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, bool e4m3, int n_sm, cudaStream_t stream);
 
 }  // namespace attn
