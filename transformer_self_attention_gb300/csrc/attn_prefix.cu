@@ -85,7 +85,6 @@ __device__ __forceinline__ int prefix_length(const PrefixParams& p, int g) {
     return n < 0 || n > p.t.max_pages * p.c.page ? 0 : n;
 }
 __device__ __forceinline__ int prefix_of(const PrefixParams& p, int b) {
-    if (!p.of) return 0;
     const int g = p.of[b];
     return g < 0 || g >= p.G ? -1 : g;
 }
@@ -108,9 +107,32 @@ struct HeadCost {
 template <int THREADS>
 __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& sh, int& units) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    for (int g = tid; g < p.G; g += THREADS) sh.count[g] = p.of ? 0 : p.B;
+    if (!p.of) {  // one prefix, of all sequences
+        const int len = prefix_length(p, 0), n = tiles_of(len);
+        const HeadCost head(p.B * p.rows, n);
+        const unsigned all = p.Hkv * head.sum();
+        units = n ? p.Hkv * (head.whole + (head.rest > 0)) : 0;
+        for (int b = tid; b < p.B; b += THREADS) {
+            sh.order[b] = (unsigned short)b;
+            if (blockIdx.x == 0) p.place[b] = make_int2(0, b);
+        }
+        if (tid == 0) {
+            sh.cost[0] = 0;
+            sh.cost[1] = all;
+            sh.members[0] = 0;
+            sh.members[1] = (unsigned short)p.B;
+            if (blockIdx.x == 0) {
+                if (p.t.len[0] != len) atomicOr(p.c.err, kCacheErrPosition);
+                p.groups[0] = make_int4(0, 0, p.B, n);
+                p.groups[1] = make_int4((int)all, units, 0, 0);
+            }
+        }
+        __syncthreads();
+        return all;
+    }
+    for (int g = tid; g < p.G; g += THREADS) sh.count[g] = 0;
     __syncthreads();
-    if (p.of && warp == 0) {
+    if (warp == 0) {
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             const int g = b < p.B ? prefix_of(p, b) : -1;
@@ -178,7 +200,7 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
     for (int o = 16; o; o /= 2) own_units += __shfl_xor_sync(0xFFFFFFFFu, own_units, o);
     if (lane == 0) sh.scan[0][warp] = own_units;
     for (int b = tid; b < p.B; b += THREADS) {
-        const int g = prefix_of(p, b), r = p.of ? sh.rank[b] : b;
+        const int g = prefix_of(p, b), r = sh.rank[b];
         if (g >= 0) sh.order[sh.members[g] + r] = (unsigned short)b;
         if (blockIdx.x == 0) p.place[b] = g < 0 ? make_int2(-1, 0) : make_int2(g, r);
     }
@@ -236,55 +258,94 @@ __device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared
     s.at += to - off;
 }
 
-// Largest of a row's scores; columns from `live` on do not count.
-template <bool MASKED>
-__device__ __forceinline__ float row_max(uint32_t t_s, int live) {
-    float m[4];
+// Scores of 32 columns; those from `live` on become -inf.
+template <bool MASKED, int OFF, int N>
+__device__ __forceinline__ void mask_columns(uint32_t (&r)[N], int c0, int live) {
+    if (MASKED) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = __int_as_float(0xFF800000);
-#pragma unroll
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(t_s + c0, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            const float a = MASKED && c0 + e >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[e]);
-            const float b = MASKED && c0 + e + 1 >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[e + 1]);
-            m[(e >> 1) & 3] = fmax3(m[(e >> 1) & 3], a, b);
-        }
+        for (int e = 0; e < 32; ++e)
+            if (c0 + e >= live) r[OFF + e] = 0xFF800000u;
     }
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-// Weights 2^(s scale - ref) as bf16 over the scores; returns their sum.  The first half (64 positions) is announced as soon
-// as it is written.
-template <bool MASKED>
-__device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale, float ref, uint32_t bar_half) {
-    const float2 scale2 = make_float2(scale, scale), nref = make_float2(-ref, -ref);
-    float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+template <int OFF, int N>
+__device__ __forceinline__ float max_columns(const uint32_t (&r)[N], float m) {
+    float x[4] = {m, m, m, m};
 #pragma unroll
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(t_s + c0, r);
-        tmem_wait_ld();
+    for (int e = 0; e < 32; e += 2) x[(e >> 1) & 3] = fmax3(x[(e >> 1) & 3], __uint_as_float(r[OFF + e]), __uint_as_float(r[OFF + e + 1]));
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+}
+// Largest of a row's scores.  The first KEEP columns stay in registers for the weights.  A load from tensor memory is under way
+// while the columns before are looked at.
+template <bool MASKED, int KEEP>
+__device__ __forceinline__ float row_max(uint32_t t_s, int live, uint32_t (&kept)[KEEP]) {
+    float m = __int_as_float(0xFF800000);
+    uint32_t r[2][32];
+    tmem_ld32(t_s + KEEP, r[0]);
+    tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float a = MASKED && c0 + 2 * e >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[2 * e]);
-            const float b = MASKED && c0 + 2 * e + 1 >= live ? __int_as_float(0xFF800000) : __uint_as_float(r[2 * e + 1]);
-            const float2 x = __ffma2_rn(make_float2(a, b), scale2, nref);
-            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-            if (e % 2) sum1 = __fadd2_rn(sum1, y);
-            else sum0 = __fadd2_rn(sum0, y);
-            pk[e] = pack_bf16x2(y.x, y.y);
+    for (int c0 = KEEP; c0 < kTile; c0 += 32) {
+        constexpr int kLast = kTile - 32;
+        uint32_t(&now)[32] = r[(c0 - KEEP) / 32 % 2];
+        if (c0 < kLast) {
+            tmem_ld32(t_s + c0 + 32, r[((c0 - KEEP) / 32 + 1) % 2]);
+        } else {
+            tmem_ld32_at<0>(t_s, kept);
+            if constexpr (KEEP == 64) tmem_ld32_at<KEEP - 32>(t_s + 32, kept);
         }
-        tmem_st16(t_s + c0 / 2, pk);  // over columns that this thread has read
-        if (c0 == 32) {
+        mask_columns<MASKED, 0>(now, c0, live);
+        m = max_columns<0>(now, m);
+        tmem_wait_ld();
+    }
+    mask_columns<MASKED, 0>(kept, 0, live);
+    m = max_columns<0>(kept, m);
+    if constexpr (KEEP == 64) {
+        mask_columns<MASKED, KEEP - 32>(kept, 32, live);
+        m = max_columns<KEEP - 32>(kept, m);
+    }
+    return m;
+}
+// Weights 2^(s scale - ref) of 32 columns as bf16 pairs; their sum is added to `sum`.
+template <int OFF, int N>
+__device__ __forceinline__ void weights32(const uint32_t (&r)[N], float2 scale, float2 nref, float2 (&sum)[2], uint32_t (&pk)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[OFF + 2 * e]), __uint_as_float(r[OFF + 2 * e + 1])), scale, nref);
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+        sum[e % 2] = __fadd2_rn(sum[e % 2], y);
+        pk[e] = pack_bf16x2(y.x, y.y);
+    }
+}
+// A row's weights over its scores (P over columns that this thread has read); returns their sum.  The first half (64
+// positions) is announced as soon as it is written.
+template <bool MASKED, int KEEP>
+__device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale, float ref, uint32_t bar_half,
+                                             const uint32_t (&kept)[KEEP]) {
+    const float2 scale2 = make_float2(scale, scale), nref = make_float2(-ref, -ref);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t r[2][32], pk[16];
+    tmem_ld32(t_s + KEEP, r[0]);
+    weights32<0>(kept, scale2, nref, sum, pk);
+    tmem_wait_ld();
+    tmem_st16(t_s, pk);
+    if constexpr (KEEP == 64) {
+        weights32<KEEP - 32>(kept, scale2, nref, sum, pk);
+        tmem_st16(t_s + 16, pk);
+    }
+#pragma unroll
+    for (int c0 = KEEP; c0 < kTile; c0 += 32) {
+        if (c0 == 64) {
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar_half);
         }
+        uint32_t(&now)[32] = r[(c0 - KEEP) / 32 % 2];
+        if (c0 + 32 < kTile) tmem_ld32(t_s + c0 + 32, r[((c0 - KEEP) / 32 + 1) % 2]);
+        mask_columns<MASKED, 0>(now, c0, live);
+        weights32<0>(now, scale2, nref, sum, pk);
+        if (c0 + 32 < kTile) tmem_wait_ld();
+        tmem_st16(t_s + c0 / 2, pk);
     }
-    return (sum0.x + sum0.y) + (sum1.x + sum1.y);
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // 16 codes as bf16 numbers times a power of two (exact), two 16-byte pieces.
@@ -356,6 +417,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
         const uint32_t s_full = smem_u32(&sh.s_full[stream]), p_half = smem_u32(&sh.p_half[stream]);
         const uint32_t p_full = smem_u32(&sh.p_full[stream]), o_full = smem_u32(&sh.o_full[stream]);
         const float ninf = __int_as_float(0xFF800000);
+        constexpr int kKeep = E4M3 ? 32 : 64;  // (as the registers allow)
         int n = 0, stretch = 0, tiles = 0;  // the stream's tiles and stretches, all tiles of the stretches before
         while (s.at < s.end) {
             stretch_open(p, sh, s);
@@ -395,7 +457,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 wait(s_full, n & 1, watch);
                 __syncwarp();
                 tc_fence_after();
-                const float top = (live >= kTile ? row_max<false>(t_s, live) : row_max<true>(t_s, live)) * p.scale_log2;
+                uint32_t kept[kKeep];
+                const float top =
+                    (live >= kTile ? row_max<false>(t_s, live, kept) : row_max<true>(t_s, live, kept)) * p.scale_log2;
                 // the reference moves, for all rows of the warp together, when a score passes it by 2^8 (the values of the
                 // tile before are added by now: these scores were issued behind them)
                 if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
@@ -432,8 +496,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     __syncwarp();
                 }
                 const float ref = m == ninf ? 0.f : m;
-                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, p_half)
-                                   : row_weights<true>(t_s, live, p.scale_log2, ref, p_half);
+                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, p_half, kept)
+                                   : row_weights<true>(t_s, live, p.scale_log2, ref, p_half, kept);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full);
