@@ -858,6 +858,20 @@ class PagedCache:
         return B, (page_table.data_ptr(), page_table.stride(0), wide,
                    _int32("cache_len", cache_len, (B,), self._device))
 
+    def _head_table(self, page_table, cache_len):
+        """The same with a table for each kv head, [B, Hkv, max_pages]; the strides over sequences and heads."""
+        shape = page_table.shape
+        if (page_table.dtype is not torch.int32 or page_table.get_device() != self._device or len(shape) != 3
+                or shape[1] != self.shape[1] or shape[2] < 1):
+            raise ValueError(f"page_table must be an int32 tensor [B, max_pages] or [B, {self.shape[1]}, max_pages] with "
+                             f"contiguous rows on {self.device}")
+        B, heads, wide = shape
+        stride, head_stride, one = page_table.stride()
+        if one != 1:
+            raise ValueError("page_table must have contiguous rows")
+        return B, (page_table.data_ptr(), stride, head_stride if heads > 1 else 0, wide,
+                   _int32("cache_len", cache_len, (B,), self._device))
+
     def write(self, K, V, page_table, cache_len, new_len=None, rope=None, Q=None, Q_out=None, stream=None):
         """Append K, V [B, Hkv, S_new, d] (bf16 views): row i < new_len[b] (int32 CUDA [B]; default S_new) of
         sequence b goes to position cache_len[b] - new_len[b] + i.  With ``rope`` (RotaryPositions) the keys, and
@@ -958,14 +972,14 @@ class PagedDecodeAttention:
             pass
 
     def __call__(self, Q, cache, page_table, cache_len, O=None, LSE=None, stream=None, want_lse=True):
-        B, Hq, Hkv, S_q, d = self.shape
-        heads = page_table.dim() == 3
-        if heads and page_table.shape[1] != Hkv:
-            raise ValueError(f"page_table must have a row for each of {Hkv} kv heads")
-        rows, table = cache._table(page_table[:, 0] if heads else page_table, cache_len)
+        B, Hq, _, S_q, d = self.shape
+        if page_table.dim() == 3:
+            rows, table = cache._head_table(page_table, cache_len)
+        else:
+            rows, (ptr, stride, wide, lens) = cache._table(page_table, cache_len)
+            table = (ptr, stride, 0, wide, lens)
         if rows != B:
             raise ValueError(f"page_table must have {B} rows")
-        table = (*table[:2], page_table.stride(1) if heads and Hkv > 1 else 0, *table[2:])
         shape = (B, Hq, S_q, d)
         for name, t, want, dt in (("Q", Q, shape, torch.bfloat16), ("O", O, shape, torch.bfloat16),
                                   ("LSE", LSE, shape[:3], torch.float32)):
@@ -1073,6 +1087,17 @@ class SharedPrefixAttention:
             raise AttnError(st, "attn_prefix_set_watchdog")
 
 
+def _step_queries(Q, B, cache):
+    """Shape of a step's queries [B, Hq, S_q, d] for a cache."""
+    shape = Q.shape
+    _, Hkv, _, d = cache.shape
+    if (len(shape) != 4 or shape[0] != B or shape[3] != d or shape[1] < 1 or shape[1] % Hkv or shape[2] < 1
+            or Q.dtype is not torch.bfloat16 or Q.get_device() != cache._device or not Q.is_contiguous()):
+        raise ValueError(f"Q must be a contiguous bfloat16 tensor [{B}, Hq, S_q, {d}] on {cache.device}, Hq a "
+                         f"multiple of {Hkv}, S_q at least 1")
+    return shape
+
+
 class PageBounds:
     """Bounds of the keys of a PagedCache's pages, and the pages that they select (``attn_bounds_*``).
 
@@ -1120,25 +1145,27 @@ class PageBounds:
         scores for Q [B, Hq, S_q, d] between them, ``keep`` in all.  Returns (table, length), int32 [B, Hkv, keep] and
         [B], for PagedDecodeAttention; table[b, h] has -1 behind the chosen pages."""
         cache = self.cache
-        _, Hkv, page, d = cache.shape
+        _, Hkv, page, _ = cache.shape
         B, tab = cache._table(page_table, cache_len)
-        if (Q.dim() != 4 or Q.shape[0] != B or Q.shape[3] != d or Q.shape[1] < 1 or Q.shape[1] % Hkv or Q.shape[2] < 1
-                or Q.dtype is not torch.bfloat16 or Q.get_device() != self._device or not Q.is_contiguous()):
-            raise ValueError(f"Q must be a contiguous bfloat16 tensor [{B}, Hq, S_q, {d}] on {cache.device}, Hq a "
-                             f"multiple of {Hkv}, S_q at least 1")
+        _, Hq, S_q, _ = _step_queries(Q, B, cache)
         keep, sinks, recent = _int(keep), _int(sinks), _int(recent)
-        least = 1 - (1 - Q.shape[2]) // page
+        least = 1 - (1 - S_q) // page
         if sinks < 0 or recent < least or keep < sinks + recent:
             raise ValueError(f"recent must be at least {least}, sinks at least 0, keep at least sinks + recent")
         if table is None:
             table = _new((B, Hkv, keep), torch.int32, cache.device, stream)
+            tp = table.data_ptr()
+        else:
+            tp = _int32("table", table, (B, Hkv, keep), self._device)
         if length is None:
             length = _new((B,), torch.int32, cache.device, stream)
+            lp = length.data_ptr()
+        else:
+            lp = _int32("length", length, (B,), self._device)
         if B:
             st = _call(self._device, stream, _lib.attn_bounds_select,
-                       (cache.handle, self.codes.data_ptr(), self.exponents.data_ptr(), B, Q.shape[1], Q.shape[2],
-                        Q.data_ptr(), *tab, keep, sinks, recent, _int32("table", table, (B, Hkv, keep), self._device),
-                        _int32("length", length, (B,), self._device)),
+                       (cache.handle, self.codes.data_ptr(), self.exponents.data_ptr(), B, Hq, S_q, Q.data_ptr(), *tab, keep,
+                        sinks, recent, tp, lp),
                        (Q, page_table, cache_len, table, length, self.codes, self.exponents))
             if st != ATTN_OK:
                 raise AttnError(st, "attn_bounds_select",
@@ -1179,18 +1206,15 @@ class PageWeights:
         """Multiply the weights of all positions by decay and add those of a decode step: Q [B, Hq, S_q, d] bf16 and
         LSE [B, Hq, S_q] float32 as PagedDecodeAttention took and gave them, its scale, kind and window."""
         cache = self.cache
-        _, Hkv, _, d = cache.shape
         B, table = cache._table(page_table, cache_len)
-        if (Q.dim() != 4 or Q.shape[0] != B or Q.shape[3] != d or Q.shape[1] < 1 or Q.shape[1] % Hkv or Q.shape[2] < 1
-                or Q.dtype is not torch.bfloat16 or Q.get_device() != self._device or not Q.is_contiguous()):
-            raise ValueError(f"Q must be a contiguous bfloat16 tensor [{B}, Hq, S_q, {d}] on {cache.device}, Hq a "
-                             f"multiple of {Hkv}, S_q at least 1")
-        if (LSE.shape != Q.shape[:3] or LSE.dtype is not torch.float32 or LSE.get_device() != self._device
+        shape = _step_queries(Q, B, cache)
+        _, Hq, S_q, d = shape
+        if (LSE.shape != shape[:3] or LSE.dtype is not torch.float32 or LSE.get_device() != self._device
                 or not LSE.is_contiguous()):
-            raise ValueError(f"LSE must be a contiguous float32 tensor of shape {tuple(Q.shape[:3])} on {cache.device}")
+            raise ValueError(f"LSE must be a contiguous float32 tensor of shape {tuple(shape[:3])} on {cache.device}")
         if B:
             st = _call(self._device, stream, _lib.attn_weights_accumulate,
-                       (cache.handle, self.weights.data_ptr(), B, Q.shape[1], Q.shape[2], Q.data_ptr(), LSE.data_ptr(),
+                       (cache.handle, self.weights.data_ptr(), B, Hq, S_q, Q.data_ptr(), LSE.data_ptr(),
                         float(scale) if scale is not None else d ** -0.5, _int(kind), _int(window), float(decay), *table),
                        (Q, LSE, page_table, cache_len, self.weights, cache.pages, cache.scales))
             if st != ATTN_OK:
@@ -1216,12 +1240,17 @@ class PageWeights:
         shape = (B, cache.shape[1], keep + recent)
         if length is None:
             length = _new((B,), torch.int32, cache.device, stream)
+            lp = length.data_ptr()
+        else:
+            lp = _int32("length", length, (B,), self._device)
         if kept is None:
             kept = _new(shape, torch.int32, cache.device, stream)
+            kp = kept.data_ptr()
+        else:
+            kp = _int32("kept", kept, shape, self._device)
         if B:
             st = _call(self._device, stream, _lib.attn_weights_evict,
-                       (cache.handle, self.weights.data_ptr(), B, *table, keep, recent, *to[:3],
-                        _int32("length", length, (B,), self._device), _int32("kept", kept, shape, self._device)),
+                       (cache.handle, self.weights.data_ptr(), B, *table, keep, recent, *to[:3], lp, kp),
                        (page_table, cache_len, to_table, length, kept, self.weights, cache.pages, cache.scales))
             if st != ATTN_OK:
                 raise AttnError(st, "attn_weights_evict")
