@@ -52,6 +52,7 @@ struct Shared {
     unsigned short members[kPagedMaxBatch + 1];  // sequences of the prefixes before g
     unsigned short order[kPagedMaxBatch];     // sequences by prefix
     unsigned short rank[kPagedMaxBatch];      // a sequence's place among those of its prefix
+    short of[kPagedMaxBatch];                 // its prefix, -1: none
     unsigned count[kPagedMaxBatch];           // sequences of prefix g
     unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], q_full;
     unsigned scan[2][16];
@@ -80,10 +81,8 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
-__device__ __forceinline__ int prefix_length(const PrefixParams& p, int g) {
-    const int n = p.t.len[g];
-    return n < 0 || n > p.t.max_pages * p.c.page ? 0 : n;
-}
+__device__ __forceinline__ int followed(const PrefixParams& p, int n) { return n < 0 || n > p.t.max_pages * p.c.page ? 0 : n; }
+__device__ __forceinline__ int prefix_length(const PrefixParams& p, int g) { return followed(p, p.t.len[g]); }
 __device__ __forceinline__ int prefix_of(const PrefixParams& p, int b) {
     const int g = p.of[b];
     return g < 0 || g >= p.G ? -1 : g;
@@ -131,12 +130,17 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
         return all;
     }
     for (int g = tid; g < p.G; g += THREADS) sh.count[g] = 0;
+    const int first_len = tid < p.G ? p.t.len[tid] : 0;  // (on its way meanwhile)
+    for (int b = tid; b < p.B; b += THREADS) {
+        const int g = prefix_of(p, b);
+        sh.of[b] = (short)g;
+        if (blockIdx.x == 0 && g < 0 && p.of[b] != -1) atomicOr(p.c.err, kCacheErrPosition);
+    }
     __syncthreads();
     if (warp == 0) {
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            const int g = b < p.B ? prefix_of(p, b) : -1;
-            if (blockIdx.x == 0 && b < p.B && g < 0 && p.of[b] != -1) atomicOr(p.c.err, kCacheErrPosition);
+            const int g = b < p.B ? sh.of[b] : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, g);
             if (g >= 0) {
                 const unsigned before = sh.count[g];
@@ -158,8 +162,8 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
         const int g = g0 + tid;
         unsigned c = 0, m = 0;
         if (g < p.G) {
-            const int n = tiles_of(prefix_length(p, g));
-            if (blockIdx.x == 0 && p.t.len[g] != prefix_length(p, g)) atomicOr(p.c.err, kCacheErrPosition);
+            const int given = g0 ? p.t.len[g] : first_len, len = followed(p, given), n = tiles_of(len);
+            if (blockIdx.x == 0 && given != len) atomicOr(p.c.err, kCacheErrPosition);
             m = sh.count[g];
             const HeadCost head((int)m * p.rows, n);
             c = p.Hkv * head.sum();
@@ -200,7 +204,7 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
     for (int o = 16; o; o /= 2) own_units += __shfl_xor_sync(0xFFFFFFFFu, own_units, o);
     if (lane == 0) sh.scan[0][warp] = own_units;
     for (int b = tid; b < p.B; b += THREADS) {
-        const int g = prefix_of(p, b), r = sh.rank[b];
+        const int g = sh.of[b], r = sh.rank[b];
         if (g >= 0) sh.order[sh.members[g] + r] = (unsigned short)b;
         if (blockIdx.x == 0) p.place[b] = g < 0 ? make_int2(-1, 0) : make_int2(g, r);
     }
