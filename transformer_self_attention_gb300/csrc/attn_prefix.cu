@@ -40,7 +40,8 @@ namespace {
 
 constexpr int kTile = 128;         // rows of a stream, and positions of a tile
 constexpr int kRows = 2 * kTile;   // of a unit, at most
-// Costs are counted in products of a tile of rows with a tile of positions.
+// Costs are counted in products of a tile of rows with a tile of positions: w for a tile of positions, two or one, as there
+// are rows; and what a unit costs beside them, `over`.
 constexpr PagedShape kShape{kTile, 4, 4};
 
 template <bool E4M3>
@@ -90,44 +91,68 @@ __device__ __forceinline__ int prefix_of(const PrefixParams& p, int b) {
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 // Units of one prefix and kv head: `whole` of 256 rows, and one of the rest (up to 128 rows cost half).
 struct HeadCost {
-    int whole, rest;           // units of 256 rows; rows of the last one, 0: none
-    unsigned per, last;        // their costs
-    __device__ __forceinline__ HeadCost(int rows, int tiles) {
+    int whole, rest;     // units of 256 rows; rows of the last one, 0: none
+    unsigned per, last;  // their costs
+    __device__ __forceinline__ HeadCost(int rows, int tiles, unsigned over) {
+        const PagedShape shape{kTile, over, kShape.least};
         whole = rows / kRows;
         rest = rows - whole * kRows;
-        per = paged_cost(2 * tiles, kShape);
-        last = rest == 0 ? 0 : rest > kTile ? per : paged_cost(tiles, kShape);
+        per = paged_cost(2 * tiles, shape);
+        last = rest == 0 ? 0 : rest > kTile ? per : paged_cost(tiles, shape);
     }
     __device__ __forceinline__ unsigned sum() const { return whole * per + last; }
 };
+// The line of cost and its cuts.
+struct Line {
+    unsigned W, C, over;
+    __device__ __forceinline__ PagedCuts cuts() const {
+        PagedCuts c(0, 0, 1, kShape);
+        c.C = C;
+        c.q = W / C;
+        c.r = W - c.q * C;
+        return c;
+    }
+};
 
-// Members by prefix and costs, by all threads; CTA 0 leaves them for the joining kernel.  Returns the line's length and,
-// in `units`, how many units there are.
+// Members by prefix and costs, by all threads; CTA 0 leaves them for the joining kernel.
 template <int THREADS>
-__device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& sh, int& units) {
+__device__ __forceinline__ Line prefix_plan(const PrefixParams& p, Shared& sh) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (!p.of) {  // one prefix, of all sequences
         const int len = prefix_length(p, 0), n = tiles_of(len);
-        const HeadCost head(p.B * p.rows, n);
-        const unsigned all = p.Hkv * head.sum();
-        units = n ? p.Hkv * (head.whole + (head.rest > 0)) : 0;
+        Line line{0, 1, kShape.overhead};
+        HeadCost head(p.B * p.rows, n, line.over);
+        const unsigned units = p.Hkv * (head.whole + (head.rest > 0));
+        if (n && (head.whole == 0 || head.rest == 0 || head.rest > kTile) && units <= gridDim.x) {
+            // units of the same cost: k CTAs to each, and `over` such that the cuts fall on the units' ends (a CTA with two
+            // stretches would fill its pipeline twice: 78 us for a 32K prefix, and 72.5 so)
+            const unsigned work = head.whole || head.rest > kTile ? 2 * n : n;
+            const unsigned k = max(1u, min(gridDim.x / units, work / 2));
+            const unsigned share = (max(work, kShape.least) + 1 + k - 1) / k;
+            line.over = share * k - max(work, kShape.least);
+            head = HeadCost(p.B * p.rows, n, line.over);
+            line.C = units * k;
+        } else if (n) {
+            line.C = PagedCuts(p.Hkv * head.sum(), units, gridDim.x, kShape).C;
+        }
+        line.W = p.Hkv * head.sum();
         for (int b = tid; b < p.B; b += THREADS) {
             sh.order[b] = (unsigned short)b;
             if (blockIdx.x == 0) p.place[b] = make_int2(0, b);
         }
         if (tid == 0) {
             sh.cost[0] = 0;
-            sh.cost[1] = all;
+            sh.cost[1] = line.W;
             sh.members[0] = 0;
             sh.members[1] = (unsigned short)p.B;
             if (blockIdx.x == 0) {
                 if (p.t.len[0] != len) atomicOr(p.c.err, kCacheErrPosition);
                 p.groups[0] = make_int4(0, 0, p.B, n);
-                p.groups[1] = make_int4((int)all, units, 0, 0);
+                p.groups[1] = make_int4((int)line.W, (int)line.C, (int)line.over, 0);
             }
         }
         __syncthreads();
-        return all;
+        return line;
     }
     for (int g = tid; g < p.G; g += THREADS) sh.count[g] = 0;
     const int first_len = tid < p.G ? p.t.len[tid] : 0;  // (on its way meanwhile)
@@ -165,7 +190,7 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
             const int given = g0 ? p.t.len[g] : first_len, len = followed(p, given), n = tiles_of(len);
             if (blockIdx.x == 0 && given != len) atomicOr(p.c.err, kCacheErrPosition);
             m = sh.count[g];
-            const HeadCost head((int)m * p.rows, n);
+            const HeadCost head((int)m * p.rows, n, kShape.overhead);
             c = p.Hkv * head.sum();
             if (n) own_units += p.Hkv * (head.whole + (head.rest > 0));
         }
@@ -209,16 +234,17 @@ __device__ __forceinline__ unsigned prefix_plan(const PrefixParams& p, Shared& s
         if (blockIdx.x == 0) p.place[b] = g < 0 ? make_int2(-1, 0) : make_int2(g, r);
     }
     __syncthreads();
-    units = 0;
+    unsigned units = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) units += sh.scan[0][w];
+    const Line line{carry_c, PagedCuts(carry_c, units, gridDim.x, kShape).C, kShape.overhead};
     if (blockIdx.x == 0) {
         for (int g = tid; g < p.G; g += THREADS)
             p.groups[g] = make_int4((int)sh.cost[g], sh.members[g], sh.members[g + 1] - sh.members[g],
                                     tiles_of(prefix_length(p, g)));
-        if (tid == 0) p.groups[p.G] = make_int4((int)carry_c, units, 0, 0);
+        if (tid == 0) p.groups[p.G] = make_int4((int)line.W, (int)line.C, (int)line.over, 0);
     }
-    return carry_c;
+    return line;
 }
 
 // A CTA's part of a unit: tiles [g0, g1) of prefix g for rows of kv head h, from row `row0` of the prefix's rows on.
@@ -243,11 +269,11 @@ __device__ __forceinline__ Stretch stretch_begin(const PrefixParams& p, const Pa
     s.g = lo;
     return s;
 }
-__device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared& sh, Stretch& s) {
+__device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared& sh, unsigned over, Stretch& s) {
     while (sh.cost[s.g + 1] <= s.at) ++s.g;
     s.len = prefix_length(p, s.g);
     const int n = tiles_of(s.len), all = (sh.members[s.g + 1] - sh.members[s.g]) * p.rows;
-    const HeadCost head(all, n);
+    const HeadCost head(all, n, over);
     const unsigned into = s.at - sh.cost[s.g], sum = head.sum();
     s.h = (int)(into / sum);
     const unsigned in_head = into - s.h * sum;
@@ -257,8 +283,8 @@ __device__ __forceinline__ void stretch_open(const PrefixParams& p, const Shared
     s.row0 = unit * kRows;
     s.rows = min(kRows, all - s.row0);
     const int w = s.two() ? 2 : 1;
-    s.g0 = min(n, max(0, (int)off - (int)kShape.overhead) / w);
-    s.g1 = min(n, max(0, (int)to - (int)kShape.overhead) / w);
+    s.g0 = min(n, max(0, (int)off - (int)over) / w);
+    s.g1 = min(n, max(0, (int)to - (int)over) / w);
     s.at += to - off;
 }
 
@@ -397,11 +423,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
     }
     fence_barrier_init();
     wait_for_kernel_before();
-    int units;
-    const unsigned W = prefix_plan<R::kThreads>(p, sh, units);
-    const PagedCuts cuts(W, units, gridDim.x, kShape);
+    const Line line = prefix_plan<R::kThreads>(p, sh);
+    const PagedCuts cuts = line.cuts();
+    const unsigned over = line.over;
     let_kernel_behind_in();
-    if (blockIdx.x >= cuts.C || W == 0) return;
+    if (blockIdx.x >= cuts.C || line.W == 0) return;
     if (warp == R::kMma) {
         tmem_alloc(smem_u32(&sh.tmem), C::kCols);
         tmem_relinquish();
@@ -424,7 +450,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
         constexpr int kKeep = E4M3 ? 32 : 64;  // (as the registers allow)
         int n = 0, stretch = 0, tiles = 0;  // the stream's tiles and stretches, all tiles of the stretches before
         while (s.at < s.end) {
-            stretch_open(p, sh, s);
+            stretch_open(p, sh, over, s);
             if (s.g0 >= s.g1) continue;
             // ---- the queries, 16-byte pieces of rows in the layout of the products (128-byte swizzle), once both streams
             // are through with those before
@@ -542,7 +568,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
         int n = 0;
         bool ok = true;
         while (s.at < s.end && ok) {
-            stretch_open(p, sh, s);
+            stretch_open(p, sh, over, s);
             auto page_at = [&](int g) {
                 const int pos = g * kTile + mine;
                 if (lane >= copies || g >= s.g1 || pos >= s.len) return -1;
@@ -589,7 +615,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             uint32_t e[kEach];  // exponent byte; 0 beside codes of zeros where there is nothing
         };
         while (s.at < s.end && ok) {
-            stretch_open(p, sh, s);
+            stretch_open(p, sh, over, s);
             // lane i < 8 of every warp: the page of positions 16 i .. of the tile
             auto page_at = [&](int g) {
                 const int pos = g * kTile + 16 * lane;
@@ -676,7 +702,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             int n = 0, stretch = 0, done = 0;  // all tiles of the stretches before; the stream's
             bool ok = true;
             while (s.at < s.end && ok) {
-                stretch_open(p, sh, s);
+                stretch_open(p, sh, over, s);
                 if (s.g0 >= s.g1) continue;
                 const bool two = s.two();
                 const int steps = s.steps(stream);
@@ -760,10 +786,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         const int4 g = __ldcg(&p.groups[place.x]), total = __ldcg(&p.groups[p.G]);
         const int all = g.z * p.rows, x = place.y * p.rows + r;
         if (g.w > 0) {
-            const PagedCuts cuts((unsigned)total.x, (unsigned)total.y, own.prefix_grid, kShape);
-            const HeadCost head(all, g.w);
+            const PagedCuts cuts = Line{(unsigned)total.x, (unsigned)total.y, 0}.cuts();
+            const HeadCost head(all, g.w, total.z);
             const int unit = x / kRows, rows = min(kRows, all - unit * kRows), w = rows > kTile ? 2 : 1;
-            const unsigned u0 = (unsigned)g.x + h * head.sum() + unit * head.per + kShape.overhead;
+            const unsigned u0 = (unsigned)g.x + h * head.sum() + unit * head.per + total.z;
             // a tile is the CTA's that its last product's cost belongs to
             c0 = (int)cuts.owner(u0 + w - 1);
             streams = w == 2 ? 1 : 2;

@@ -232,7 +232,6 @@ attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, c
     j.whole_o = own.whole_o; j.whole_ml = own.whole_ml;
     j.part_o = s->d_part; j.part_ml = s->d_ml; j.cut = own.cut;
     j.rows_pad = own.rows_pad; j.row_blocks = own.row_blocks;
-    j.prefix_grid = grid;
     j.o = O; j.lse = LSE;
     return done(attn::launch_join(p, j, st));
 }

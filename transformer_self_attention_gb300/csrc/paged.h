@@ -186,19 +186,19 @@ struct PrefixParams {
     float* part_o;    // [.][d]
     float2* part_ml;  // [.]: reference (base 2) and sum
     int4* groups;     // [G + 1]: cost of the prefixes before, their sequences, sequences of this one, its tiles; last: the
-                      // whole cost, and the units
+                      // whole cost, the CTAs that share it, a unit's overhead
     int2* place;      // [B]: prefix and place among its sequences
     float scale_log2;
     long long watchdog_ns;
     int withhold;
 };
-struct JoinParams {  // of the own positions, as PagedParams; prefix_grid: the first kernel's CTAs
+struct JoinParams {  // of the own positions, as PagedParams
     const float* whole_o;
     const float2* whole_ml;
     const float* part_o;
     const float2* part_ml;
     const int2* cut;
-    int rows_pad, row_blocks, prefix_grid;
+    int rows_pad, row_blocks;
     void* o;
     float* lse;
 };
