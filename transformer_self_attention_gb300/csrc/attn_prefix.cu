@@ -22,7 +22,9 @@
 //
 //   warps 0-3, 4-7: a stream each, one thread a row: the queries to shared memory, weights, the row's part to global memory
 //   bf16 pages: a warp for the TMA loads, boxes of 16 to 128 positions with 128 bytes of each row
-//   E4M3 pages: four warps that load codes, widen them (code * 2^k is a bf16 number) and write the tiles themselves
+//   E4M3 pages: a warp loads codes and exponents to places of their own, and four warps widen them to bf16 tiles (code *
+//   2^k is a bf16 number).  (Loaded by the four warps to registers, a tile ahead, the codes came late: 68 us for 16 sequences
+//   of 16 rows to a head behind 16K positions.)
 //   last two warps: a stream each, one thread issues its products (one thread for both left gaps between them: a wait
 //   that is already over costs it 130 cycles, four of them to 1030 cycles of products)
 #include <cuda_bf16.h>
@@ -46,7 +48,7 @@ constexpr PagedShape kShape{kTile, 4, 4};
 
 template <bool E4M3>
 struct Roles {
-    static constexpr int kLoad = 8, kLoaders = E4M3 ? 4 : 1, kMma = kLoad + kLoaders, kThreads = 32 * (kMma + 2);
+    static constexpr int kWiden = 8, kLoad = E4M3 ? 12 : 8, kMma = kLoad + 1, kThreads = 32 * (kMma + 2);
 };
 struct Shared {
     unsigned cost[kPagedMaxBatch + 1];        // of the prefixes before g
@@ -56,17 +58,21 @@ struct Shared {
     short of[kPagedMaxBatch];                 // its prefix, -1: none
     unsigned count[kPagedMaxBatch];           // sequences of prefix g
     unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], q_full;
+    unsigned long long c_full[3], c_empty[3];  // E4M3: places of codes
+    alignas(16) uint8_t exps[3][kTile];
     unsigned scan[2][16];
     uint32_t tmem;
     int abort;
 };
-template <int D>
+template <int D, bool E4M3>
 struct Cfg {
-    static constexpr int kStages = 2;
+    static constexpr int kKeyStages = E4M3 ? 1 : 2, kValueStages = 2, kCodeStages = 3;
     static constexpr int kParts = D / 64;           // of a row, 128 bytes each
     static constexpr int kPart = kTile * 128;
     static constexpr int kBytes = kParts * kPart;   // of a tile of queries, keys or values
-    static constexpr int kOffK = 2 * kBytes, kOffV = kOffK + kStages * kBytes, kOffShared = kOffV + kStages * kBytes;
+    static constexpr int kCodes = kTile * D;        // of a tile of codes
+    static constexpr int kOffK = 2 * kBytes, kOffV = kOffK + kKeyStages * kBytes, kOffCodes = kOffV + kValueStages * kBytes;
+    static constexpr int kOffShared = kOffCodes + (E4M3 ? kCodeStages * kCodes : 0);
     static constexpr int kSmem = 1024 + kOffShared + (int)sizeof(Shared);
     static constexpr uint32_t kCols = 512, kColO = 256;  // scores of the streams at 0 and 128, outputs at 256 and 384
     static_assert(kSmem <= 232448, "shared memory");
@@ -123,11 +129,12 @@ __device__ __forceinline__ Line prefix_plan(const PrefixParams& p, Shared& sh) {
         Line line{0, 1, kShape.overhead};
         HeadCost head(p.B * p.rows, n, line.over);
         const unsigned units = p.Hkv * (head.whole + (head.rest > 0));
-        if (n && (head.whole == 0 || head.rest == 0 || head.rest > kTile) && units <= gridDim.x) {
+        const unsigned work = head.whole || head.rest > kTile ? 2 * n : n;  // of a unit
+        const unsigned k = max(1u, min(gridDim.x / units, work / 2));
+        if (n && (head.whole == 0 || head.rest == 0 || head.rest > kTile) && units <= gridDim.x &&
+            (k < gridDim.x / units || 10 * units * k >= 9 * gridDim.x)) {
             // units of the same cost: k CTAs to each, and `over` such that the cuts fall on the units' ends (a CTA with two
-            // stretches would fill its pipeline twice: 78 us for a 32K prefix, and 72.5 so)
-            const unsigned work = head.whole || head.rest > kTile ? 2 * n : n;
-            const unsigned k = max(1u, min(gridDim.x / units, work / 2));
+            // stretches would fill its pipeline twice: 78 us for a 32K prefix, and 72.5 so), unless that leaves CTAs idle
             const unsigned share = (max(work, kShape.least) + 1 + k - 1) / k;
             line.over = share * k - max(work, kShape.least);
             head = HeadCost(p.B * p.rows, n, line.over);
@@ -396,9 +403,9 @@ __device__ __forceinline__ void widen16(const uint4& v, float f, uint4& lo, uint
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E4M3>;
     using R = Roles<E4M3>;
-    constexpr int kStages = C::kStages;
+    constexpr int kKeyStages = C::kKeyStages, kValueStages = C::kValueStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffShared);
@@ -406,11 +413,15 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
     const uint32_t s_q = smem_u32(smem), s_k = s_q + C::kOffK, s_v = s_q + C::kOffV;
     if (tid == 0) {
         prefetch_tmap(&p.tm);
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.k_full[i]), E4M3 ? 4 : 1);
             mbar_init(smem_u32(&sh.v_full[i]), E4M3 ? 4 : 1);
             mbar_init(smem_u32(&sh.k_empty[i]), 2);
             mbar_init(smem_u32(&sh.v_empty[i]), 2);
+        }
+        for (int i = 0; i < C::kCodeStages; ++i) {
+            mbar_init(smem_u32(&sh.c_full[i]), 1);
+            mbar_init(smem_u32(&sh.c_empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
@@ -513,8 +524,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 if (!E4M3 && live < kTile) {
                     // positions past the end may hold anything: weight zero times a NaN is a NaN, so their values become
                     // zero (by either stream: neither waits for the other)
-                    const int t = tiles + s.tile(stream, i) - s.g0, st = t % kStages;
-                    wait(smem_u32(&sh.v_full[st]), (t / kStages) & 1, watch);
+                    const int t = tiles + s.tile(stream, i) - s.g0, st = t % kValueStages;
+                    wait(smem_u32(&sh.v_full[st]), (t / kValueStages) & 1, watch);
                     if (row >= live)
 #pragma unroll
                         for (int x = 0; x < 8 * C::kParts; ++x)
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             }
             tc_fence_before();
         }
-    } else if (warp < R::kMma && !E4M3) {
+    } else if (!E4M3 && warp == R::kLoad) {
         // =================================================== loads, a box or more to a lane
         const int box = p.box_rows, copies = kTile / box * C::kParts;  // of a tile of keys, at most 16
         const int mine = lane / C::kParts * box, part = lane % C::kParts;
@@ -581,15 +592,16 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             };
             int page = page_at(s.g0);
             for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
-                const int st = n % kStages, next = page_at(g + 1);
+                const int next = page_at(g + 1);
                 const bool need = page >= 0;
                 const int slot = (int)((unsigned)(g * kTile + mine) % (unsigned)p.c.page), unit = page * p.Hkv + s.h;
                 const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, need)) * box * 128;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
+                    const int stages = kv ? kValueStages : kKeyStages, st = n % stages;
                     const uint32_t full = smem_u32(kv ? &sh.v_full[st] : &sh.k_full[st]);
-                    if (ok && n >= kStages)
-                        ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (n / kStages - 1) & 1, watch);
+                    if (ok && n >= stages)
+                        ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (n / stages - 1) & 1, watch);
                     if (n + 1 == p.withhold) ok = false;
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
@@ -604,21 +616,16 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 page = next;
             }
         }
-    } else if (warp < R::kMma) {
-        // =================================================== E4M3: codes to tiles of bf16 numbers
-        constexpr int kLanes = D / 16, kRows = 128 / kLanes, kEach = kTile / kRows;  // lanes of a row, rows at once
-        const int ltid = tid - 32 * R::kLoad, r0 = ltid / kLanes, c = ltid % kLanes;
-        int n = 0;
+    } else if (warp == R::kLoad) {
+        // =================================================== E4M3: codes and exponents, 16 positions to each of eight lanes
+        const int box = p.box_rows, row = 16 * lane;
+        const uint32_t codes0 = smem_u32(smem) + C::kOffCodes;
+        int n = 0;  // tiles of keys and of values
         bool ok = true;
-        struct Codes {
-            uint4 v[kEach];
-            uint32_t e[kEach];  // exponent byte; 0 beside codes of zeros where there is nothing
-        };
         while (s.at < s.end && ok) {
             stretch_open(p, sh, over, s);
-            // lane i < 8 of every warp: the page of positions 16 i .. of the tile
             auto page_at = [&](int g) {
-                const int pos = g * kTile + 16 * lane;
+                const int pos = g * kTile + row;
                 if (lane >= 8 || g >= s.g1 || pos >= s.len) return -1;
                 int page = p.t.pages[s.g * p.t.stride + (unsigned)pos / (unsigned)p.c.page];
                 if (page < 0 || page >= p.c.n_pages) {
@@ -627,67 +634,100 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 }
                 return page;
             };
-            auto fetch = [&](int g, int pages, int kv, Codes& f) {
+            int page = page_at(s.g0);
+            for (int g = s.g0; g < s.g1 && ok; ++g) {
+                const int next = page_at(g + 1);
+                const int slot = (int)((unsigned)(g * kTile + row) % (unsigned)p.c.page), unit = page * p.Hkv + s.h;
+                const bool need = page >= 0, head = need && row % box == 0;  // a box begins here
+                const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, head)) * box * D + __popc(__ballot_sync(0xFFFFFFFFu, need)) * 16;
 #pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const int row = i * kRows + r0, pos = g * kTile + row;
-                    const int page = __shfl_sync(0xFFFFFFFFu, pages, row / 16);
-                    f.v[i] = make_uint4(0, 0, 0, 0);
-                    f.e[i] = 0;
-                    if (pos >= s.len) continue;
-                    const int slot = (int)((unsigned)pos % (unsigned)p.c.page);
-                    const long long unit = (long long)page * p.Hkv + s.h;
-                    f.v[i] = *reinterpret_cast<const uint4*>(p.c.pages + ((unit * 2 + kv) * p.c.page + slot) * D + 16 * c);
-                    f.e[i] = p.c.scales[(unit * (p.c.page / 16) + slot / 16) * 32 + 16 * kv + slot % 16];
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int st = n % C::kCodeStages;
+                    const uint32_t full = smem_u32(&sh.c_full[st]);
+                    if (ok && n >= C::kCodeStages) ok = wait(smem_u32(&sh.c_empty[st]), (n / C::kCodeStages - 1) & 1, watch);
+                    if (n / 2 + 1 == p.withhold) ok = false;
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (head)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(codes0 + st * C::kCodes + row * D),
+                            "l"(reinterpret_cast<uint64_t>(&p.tm)), "r"(0), "r"(slot), "r"(kv), "r"(unit), "r"(full)
+                            : "memory");
+                    if (need)
+                        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(
+                                         smem_u32(&sh.exps[st][row])),
+                                     "l"(p.c.scales + ((long long)unit * (p.c.page / 16) + slot / 16) * 32 + 16 * kv), "r"(full)
+                                     : "memory");
                 }
-            };
-            auto put = [&](const Codes& f, uint32_t dst) {
+                page = next;
+            }
+        }
+    } else if (warp < R::kLoad) {
+        // =================================================== E4M3: codes to tiles of bf16 numbers
+        constexpr int kLanes = D / 16, kAtOnce = 128 / kLanes, kEach = kTile / kAtOnce;  // lanes of a row, rows at once
+        const int ltid = tid - 32 * R::kWiden, r0 = ltid / kLanes, c = ltid % kLanes;
+        const uint32_t codes0 = smem_u32(smem) + C::kOffCodes;
+        int n = 0, t = 0;  // tiles of keys and of values; of positions
+        bool ok = true;
+        while (s.at < s.end && ok) {
+            stretch_open(p, sh, over, s);
+            for (int g = s.g0; g < s.g1 && ok; ++g, ++t) {
+                const int live = s.len - g * kTile;
 #pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const int row = i * kRows + r0;
-                    // 2^(e - 127); 255 goes with NaN codes
-                    const float factor = __uint_as_float(max(f.e[i] << 23, 0x00400000u));
-                    uint4 lo, hi;
-                    widen16(f.v[i], factor, lo, hi);
-                    const uint32_t at = dst + (c / 4) * C::kPart + row * 128;
-                    const int x = 2 * (c % 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x ^ (row & 7)) * 16)), "r"(lo.x),
-                                 "r"(lo.y), "r"(lo.z), "r"(lo.w)
-                                 : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((x + 1) ^ (row & 7)) * 16)), "r"(hi.x),
-                                 "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                                 : "memory");
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int from = n % C::kCodeStages, stages = kv ? kValueStages : kKeyStages, st = t % stages;
+                    ok = ok && wait(smem_u32(&sh.c_full[from]), (n / C::kCodeStages) & 1, watch);
+                    uint4 v[kEach];
+                    uint32_t e[kEach];
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) {
+                        const int row = i * kAtOnce + r0, sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        e[i] = 0;
+                        if (row < live) {
+                            const uint32_t at = codes0 + from * C::kCodes + row * D + 16 * sw;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                                         : "r"(at)
+                                         : "memory");
+                            e[i] = sh.exps[from][row];
+                        }
+                    }
+                    if (ok && t >= stages)
+                        ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (t / stages - 1) & 1, watch);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
+                    const uint32_t dst = (kv ? s_v : s_k) + st * C::kBytes + (c / 4) * C::kPart;
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) {
+                        const int row = i * kAtOnce + r0, x = 2 * (c % 4);
+                        // 2^(e - 127); 255 goes with NaN codes
+                        uint4 lo, hi;
+                        widen16(v[i], __uint_as_float(max(e[i] << 23, 0x00400000u)), lo, hi);
+                        // the lanes of a row's second half begin with the other piece: all 32 banks at once
+                        const bool turned = c >= 4;
+                        const uint4 a = turned ? hi : lo, b = turned ? lo : hi;
+                        const uint32_t at = dst + row * 128;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x + turned) ^ (row & 7)) * 16),
+                                     "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w)
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x + !turned) ^ (row & 7)) * 16),
+                                     "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(kv ? &sh.v_full[st] : &sh.k_full[st]));
                 }
-            };
-            auto give = [&](unsigned long long* full) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(full));
-            };
-            if (s.g0 >= s.g1) continue;
-            Codes a, b;
-            int pages = page_at(s.g0);
-            fetch(s.g0, pages, 0, a);
-            for (int g = s.g0; g < s.g1 && ok; ++g, ++n) {
-                const int st = n % kStages;
-                fetch(g, pages, 1, b);
-                pages = page_at(g + 1);
-                if (n >= kStages) ok = wait(smem_u32(&sh.k_empty[st]), (n / kStages - 1) & 1, watch);
-                if (n + 1 == p.withhold) ok = false;
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                put(a, s_k + st * C::kBytes);
-                give(&sh.k_full[st]);
-                if (g + 1 < s.g1) fetch(g + 1, pages, 0, a);
-                if (n >= kStages) ok = wait(smem_u32(&sh.v_empty[st]), (n / kStages - 1) & 1, watch);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                put(b, s_v + st * C::kBytes);
-                give(&sh.v_full[st]);
             }
         }
     } else {
@@ -708,11 +748,17 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 const int steps = s.steps(stream);
                 const uint32_t q = s_q + (two ? stream * C::kBytes : 0);
                 ok = wait(smem_u32(&sh.q_full), stretch++ & 1, watch);
+                // Keys of a tile that the other stream uses, where there is one place for all: each stream sees every filling
+                // of it (a wait tells one from the next, not from the one after that), and gives the place free.
+                auto skip = [&](int t) {
+                    if (t >= n + s.g1 - s.g0 || !(ok = ok && wait(k_full, t & 1, watch))) return;
+                    mbar_arrive(k_empty);
+                };
                 // scores of tile t; their columns hold the weights of the tile before, whose product with the values, issued
                 // earlier, has read them by the time they are written
                 auto scores = [&](int t) {
-                    const int st = t % kStages;
-                    if (!(ok = ok && wait(k_full + 8 * st, (t / kStages) & 1, watch))) return;
+                    const int st = t % kKeyStages;
+                    if (!(ok = ok && wait(k_full + 8 * st, (t / kKeyStages) & 1, watch))) return;
                     tc_fence_after();
                     const uint32_t k0 = s_k + st * C::kBytes;
 #pragma unroll
@@ -722,14 +768,17 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     }
                     mma_commit(s_full);
                     mma_commit(k_empty + 8 * st);
-                    if (!two) mma_commit(k_empty + 8 * st);  // for the other stream, which does not look at it
+                    if (two) return;
+                    if (kKeyStages > 1) mma_commit(k_empty + 8 * st);  // for the other stream, which does not look at it
+                    else skip(t + 1);
                 };
                 int t = two ? n : n + stream;
+                if (!two && kKeyStages == 1 && stream == 1) skip(n);
                 if (steps > 0) scores(t);
                 for (int i = 0; i < steps && ok; ++i) {
-                    const int st = t % kStages;
+                    const int st = t % kValueStages;
                     const uint32_t v = s_v + st * C::kBytes;
-                    ok = wait(v_full + 8 * st, (t / kStages) & 1, watch) && wait(p_half, done & 1, watch);
+                    ok = wait(v_full + 8 * st, (t / kValueStages) & 1, watch) && wait(p_half, done & 1, watch);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -882,10 +931,10 @@ cudaError_t launch_prefix(const PrefixParams& p, bool e4m3, int grid, cudaStream
         return e != cudaSuccess ? e : launch_dependent(f, dim3((unsigned)grid), threads, smem, stream, p);
     };
     if (p.c.d == 64)
-        return e4m3 ? go(prefix_kernel<64, true>, Roles<true>::kThreads, Cfg<64>::kSmem)
-                    : go(prefix_kernel<64, false>, Roles<false>::kThreads, Cfg<64>::kSmem);
-    return e4m3 ? go(prefix_kernel<128, true>, Roles<true>::kThreads, Cfg<128>::kSmem)
-                : go(prefix_kernel<128, false>, Roles<false>::kThreads, Cfg<128>::kSmem);
+        return e4m3 ? go(prefix_kernel<64, true>, Roles<true>::kThreads, Cfg<64, true>::kSmem)
+                    : go(prefix_kernel<64, false>, Roles<false>::kThreads, Cfg<64, false>::kSmem);
+    return e4m3 ? go(prefix_kernel<128, true>, Roles<true>::kThreads, Cfg<128, true>::kSmem)
+                : go(prefix_kernel<128, false>, Roles<false>::kThreads, Cfg<128, false>::kSmem);
 }
 
 cudaError_t launch_join(const PrefixParams& p, const JoinParams& own, cudaStream_t stream) {

@@ -211,7 +211,7 @@ attn_status attn_prefix_forward(attn_prefix_handle h, attn_cache_handle cache, c
     if (2 * tiles * s->Hkv * ((long long)n_prefix + (long long)s->B * rows / attn::kPrefixTile) > 0x7FFFFFFFLL)
         return ATTN_ERR_UNSUPPORTED;
     attn::PrefixParams p{};
-    p.tm = cache->rows_map;
+    p.tm = cache->e4m3 ? cache->map : cache->rows_map;
     p.c = cache->c;
     p.t = table_of(prefix_table, prefix_stride, prefix_max_pages, prefix_len);
     p.of = prefix_of;

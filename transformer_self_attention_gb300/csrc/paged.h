@@ -174,7 +174,7 @@ cudaError_t launch_paged_merge(const PagedParams& p, int grid, int rows_pad, cud
 
 // ---------------------------------------------------------------- shared prefixes
 struct PrefixParams {
-    CUtensorMap tm;  // bf16 pages: boxes of box_rows positions and 128 bytes of a row
+    CUtensorMap tm;  // boxes of box_rows positions: 128 bytes of a row (bf16), or a row (E4M3)
     CacheView c;
     PageTable t;     // of the prefixes, [G, max_pages] and [G]
     const int* of;   // [B]: the prefix of a sequence, -1: none; null: the only one
