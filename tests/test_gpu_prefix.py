@@ -168,6 +168,36 @@ def test_values_and_queries_that_are_not_finite():
     assert O[2, 0].isnan().any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top", [100, 134, 135, 200])
+def test_codes_and_exponents_of_all_kinds(d, top):
+    """E4M3 prefixes of all codes, subnormal ones among them, with exponents up to `top` (one multiplication up to 134, two
+    beyond), small keys and large values; then a NaN code beside a usual exponent, and a row of exponent 255."""
+    page, n = 16, 200
+    cache, vals, ptab, table = _make([n], [3, 9], 1, page, d, "e4m3")
+    g = torch.Generator().manual_seed(4)
+    codes = torch.randint(0, 256, cache.pages.shape, generator=g).to(torch.uint8)
+    codes = torch.where(codes & 0x7F == 0x7F, codes & 0x87, codes)
+    exps = torch.randint(96, 112, cache.scales.shape, generator=g).to(torch.uint8)
+    exps[:, :, :, 1] = torch.randint(top - 12, top + 1, exps[:, :, :, 1].shape, generator=g).to(torch.uint8)
+    cache.pages.view(torch.uint8).copy_(codes.cuda())
+    cache.scales.copy_(exps.cuda())
+    Q = torch.randn((2, 4, 1, d), generator=g).to(torch.bfloat16)
+    args = (Q.cuda(), cache, ptab.cuda(), _int32([n]), table.cuda(), _int32([3, 9]))
+    plan = tsa.SharedPrefixAttention(2, 4, 1, 1, d)
+    O, L = plan(*args)
+    vals = pu.values(cache.pages, cache.scales)
+    ref = _reference(Q, vals, ptab, [n], [0, 0], table, page, [3, 9], d ** -0.5, CAUSAL)
+    # the own positions' weights: 2^-22 of the largest weight times the largest value factor, times codes up to 448
+    coarse = torch.full((2, 4, 1), 128 * 448 * 2.0 ** -22 * 2.0 ** (top - 127), dtype=torch.float64)
+    pu.check_decode(O, L, ref, d, more=coarse)
+    cache.pages.view(torch.uint8)[int(ptab[0, 2]), 0, 1, 5, 7] = 0xFF
+    O = plan(*args)[0].cpu()
+    assert O[..., 7].isnan().all() and O.isfinite().sum() == O.numel() - 8
+    cache.scales[int(ptab[0, 2]), 0, 0, 1, 6] = 255
+    assert plan(*args)[0].isnan().all()
+
+
 @pytest.mark.parametrize("what", ["prefix length", "prefix page", "prefix number", "length", "page"])
 @pytest.mark.parametrize("store", ["bf16", "e4m3"])
 def test_numbers_that_are_not_followed(what, store):

@@ -710,9 +710,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
 #pragma unroll
                     for (int i = 0; i < kEach; ++i) {
                         const int row = i * kAtOnce + r0, x = 2 * (c % 4);
-                        // 2^(e - 127); 255 goes with NaN codes
+                        // 2^(e - 127); 255 makes the whole row NaN
                         uint4 lo, hi;
-                        widen16(v[i], __uint_as_float(max(e[i] << 23, 0x00400000u)), lo, hi);
+                        widen16(v[i], __uint_as_float(e[i] == 255 ? 0x7FC00000u : max(e[i] << 23, 0x00400000u)), lo, hi);
                         // the lanes of a row's second half begin with the other piece: all 32 banks at once
                         const bool turned = c >= 4;
                         const uint4 a = turned ? hi : lo, b = turned ? lo : hi;
