@@ -1168,10 +1168,7 @@ class PageBounds:
                         sinks, recent, tp, lp),
                        (Q, page_table, cache_len, table, length, self.codes, self.exponents))
             if st != ATTN_OK:
-                raise AttnError(st, "attn_bounds_select",
-            "attn_weights_accumulate", "attn_weights_evict",
-            "attn_prefix_create", "attn_prefix_forward", "attn_prefix_set_grid_limit", "attn_prefix_set_watchdog",
-            "attn_prefix_destroy")
+                raise AttnError(st, "attn_bounds_select")
         return table, length
 
 
