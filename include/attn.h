@@ -844,9 +844,9 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
  * largest), and the last `recent`.  Their keys, values, row factors and weights become positions 0, 1, .. in their order;
  * the rotation of a key stays that of its old position.  Shorter sequences keep all.
  *   to_table : where the kept rows go: int32 device [B][to_max_pages], row stride to_stride, of pages that hold nothing
- *              of this call's sequences (what was there stays); with room for min(keep + recent, max_pages * page) positions.  NULL: they
- *              move within their own pages; slots behind the new lengths are left as they were, and the pages behind them
- *              are free.
+ *              of this call's sequences (what was there stays); with room for min(keep + recent, max_pages * page)
+ *              positions.  NULL: they move within their own pages; slots behind the new lengths are left as they were, and
+ *              the pages behind them are free.
  *   out_len  : int32 device [B], min(n, keep + recent).   kept : int32 device [B, Hkv, keep + recent], the old positions of
  *              the new ones, then -1.  Neither may be an input.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.  A sequence whose length is not followed counts as
@@ -864,9 +864,12 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
  * sequence of the prefix's positions followed by its own, with ATTN_MASK_FULL or ATTN_MASK_CAUSAL (S_q new rows, the last of
  * the own positions).  Prefixes and own positions are pages of one cache; either may end inside a page.
  *
- * Rounding: over the prefix scores and sums are float32, weights are rounded to bf16 (2^-9 of a weight) for the second
- * product, after their sum is taken; over the own positions as in attn_paged_forward.  Parts are joined in float32,
- * and O is rounded once.  What is said there of infinities and of queries that are not finite holds here.
+ * Rounding: over the prefix scores and sums are float32; weights are rounded for the second product, after their sum is taken:
+ * over bf16 pages to bf16 (2^-9 of a weight).  Over E4M3 pages to fp16 (2^-12 of a weight, and 2^-31 of the largest
+ * product of weight and value factor); queries, keys and values are held to 2^-40 of their row's largest element and of
+ * the largest factor among 128 positions, values of tiles with smaller factors to 2^-72 of the largest factor before them.  Over
+ * the own positions as in attn_paged_forward.  Parts are joined in float32, and O is rounded once.  What is said there of
+ * infinities and of queries that are not finite holds here.
  *
  * A handle owns the parts' memory; it must not be used by two calls in flight at once, captured graphs included.
  */

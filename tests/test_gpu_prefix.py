@@ -198,6 +198,44 @@ def test_codes_and_exponents_of_all_kinds(d, top):
     assert plan(*args)[0].isnan().all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("values", [[60, 130, 200, 90, 128], [200, 60, 61, 62, 63], [240, 1, 1, 1, 1], [1, 1, 1, 1, 240], [0, 0, 0, 0, 0]])
+@pytest.mark.parametrize("grid", [None, 1])
+def test_tiles_of_very_different_exponents(d, values, grid):
+    """E4M3 prefixes whose tiles of 128 positions have value exponents far apart, keys' exponents spread within each tile, and
+    queries from 2^-100 to 2^6: numbers are held in 16 bits relative to their row's or tile's exponent."""
+    page, n, Hq = 16, 600, 8
+    cache, _, ptab, table = _make([n], [0], 1, page, d, "e4m3")
+    g = torch.Generator().manual_seed(21)
+    codes = torch.randint(0, 256, cache.pages.shape, generator=g).to(torch.uint8)
+    codes = torch.where(codes & 0x7F == 0x7F, codes & 0x87, codes)
+    exps = torch.randint(100, 123, cache.scales.shape, generator=g).to(torch.uint8)  # (what is behind the end stays whatever)
+    for j in range(n):
+        exps[int(ptab[0, j // page]), :, j % page // 16, 1, j % 16] = max(0, values[j // 128] - j % 3)
+    cache.pages.view(torch.uint8).copy_(codes.cuda())
+    cache.scales.copy_(exps.cuda())
+    Q = torch.randn((1, Hq, 1, d), generator=g) * 2.0 ** torch.tensor([-100, -40, -12, -4, -1, 0, 3, 6.0])[None, :, None, None]
+    Q = Q.to(torch.bfloat16)
+    plan = tsa.SharedPrefixAttention(1, Hq, 1, 1, d)
+    if grid:
+        plan.set_grid_limit(grid)
+    O, L = plan(Q.cuda(), cache, ptab.cuda(), _int32([n]), table.cuda(), _int32([0]))
+    vals = pu.values(cache.pages, cache.scales)
+    ref = pu.decode(Q, vals, ptab, page, [n], d ** -0.5, FULL, 0)
+    # A weight is an fp16 number relative to a reference M of weight times factor, at most twice 2^-7 of the largest of these:
+    # half a step of the smallest is 2^-25, with a code of 448 off by 448 * 2^-31 of that largest, for each position.
+    # Values below 2^-40 of the largest factor so far are off by half a step of theirs, 2^-25 - 7 - 40 of it.
+    K, _ = pu.dense(vals, ptab, page, 0, n)
+    p = torch.softmax(torch.einsum("hd,jd->hj", Q[0, :, 0].double(), K[0]) * d ** -0.5, -1)
+    big, most = torch.zeros(Hq, dtype=torch.float64), 0.0
+    for t in range(5):
+        f = 2.0 ** (values[t] - 127)
+        most = max(most, f)
+        big = torch.maximum(big, p[:, 128 * t:128 * t + 128].amax(-1) * max(f, most * 2.0 ** -40))
+    pu.check_decode(O, L, ref, d, more=(n * 448 * 2.0 ** -31 * big + most * 2.0 ** -72 + 2.0 ** -133)[None, :, None])
+    assert cache.poll_device_error() == (tsa.ATTN_OK, 0)
+
+
 @pytest.mark.parametrize("what", ["prefix length", "prefix page", "prefix number", "length", "page"])
 @pytest.mark.parametrize("store", ["bf16", "e4m3"])
 def test_numbers_that_are_not_followed(what, store):

@@ -6,8 +6,8 @@
 // Three kernels.  The first attends to the prefixes: the rows of all members of a prefix, for one kv head, are the rows of
 // a matrix, and a tile of 128 of them meets tiles of 128 positions,
 //     S [128 x 128] = Q K^T,   O [128 x d] += P V,   P = 2^(scale' S - m),
-// with tcgen05.mma: S and O in tensor memory, P written over S as bf16 (weights of at most 2^8 relative to a reference m
-// that moves only when a score passes it by 2^8; their sum is taken in float32 before they are rounded).  The decode
+// with tcgen05.mma: S and O in tensor memory, P written over S in 16 bits (weights of at most 2^8 relative to a reference m
+// that moves only when a score passes it by 2^8; their sum is taken in float32 before they are rounded to bf16).  The decode
 // kernels (attn_paged.cu, attn_paged_e4m3.cu) attend to the own positions and leave unscaled sums in float32.  The
 // third joins the parts of every row: O = sum_k 2^(m_k - M) O_k / L, M = max m_k, L = sum_k 2^(m_k - M) l_k.
 //
@@ -22,9 +22,12 @@
 //
 //   warps 0-3, 4-7: a stream each, one thread a row: the queries to shared memory, weights, the row's part to global memory
 //   bf16 pages: a warp for the TMA loads, boxes of 16 to 128 positions with 128 bytes of each row
-//   E4M3 pages: a warp loads codes and exponents to places of their own, and four warps widen them to bf16 tiles (code *
-//   2^k is a bf16 number).  (Loaded by the four warps to registers, a tile ahead, the codes came late: 68 us for 16 sequences
-//   of 16 rows to a head behind 16K positions.)
+//   E4M3 pages: a warp loads codes and exponents to places of their own, and four warps widen them to tiles of fp16 numbers,
+//   relative to the tile's largest exponent (below).  Every operand is fp16 then: the queries relative to their row's
+//   largest element, the weights relative to the largest product of weight and factor.  A pair of codes costs a
+//   conversion and a product; as bf16 numbers, which need no common exponents, it was six instructions of warps that the products
+//   wait for: 429 against 354 us for 4096 rows to a head behind 16K positions, 54.5 against 52 us for 256 (bf16 pages: 264 us for
+//   the first).  (Loaded by the four warps to registers, a tile ahead, the codes came late: 68 us.)
 //   last two warps: a stream each, one thread issues its products (one thread for both left gaps between them: a wait
 //   that is already over costs it 130 cycles, four of them to 1030 cycles of products)
 #include <cuda_bf16.h>
@@ -60,6 +63,8 @@ struct Shared {
     unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], q_full;
     unsigned long long c_full[3], c_empty[3];  // E4M3: places of codes
     alignas(16) uint8_t exps[3][kTile];
+    int tile_exp[2][4];                       // E4M3: common exponents of tiles of keys and of values
+    short q_exp[kRows];                       // and of the queries' rows
     unsigned scan[2][16];
     uint32_t tmem;
     int abort;
@@ -78,6 +83,14 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory");
 };
 constexpr float kRescale = 8.f;  // log2 of how far a score may pass the reference
+// E4M3: tiles of codes become fp16 numbers, code * 2^(e - E + 7) with E the largest exponent of the tile's rows: 448 * 2^7 is the
+// most, and factors of at least 2^-15 are exact.  Rows of the queries become fp16 numbers below 2^15.
+constexpr int kUp = 7, kOne = 127 + kUp;
+// Weights are fp16 numbers too, relative to a reference M of weight times 2^E: from 2^7 for the largest when M moves, up to 2^15.
+constexpr float kMost = 15.f, kFirst = 7.f;
+// A tile of values has an exponent of at least the largest so far less kApart, so that the weights of a tile of tiny
+// values stay numbers; what is lost is below 2^-72 of the largest factor.
+constexpr int kApart = 40;
 
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int part, int kv,
                                              int unit) {
@@ -341,31 +354,50 @@ __device__ __forceinline__ float row_max(uint32_t t_s, int live, uint32_t (&kept
     }
     return m;
 }
-// Weights 2^(s scale - ref) of 32 columns as bf16 pairs; their sum is added to `sum`.
-template <int OFF, int N>
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+// Weights 2^(s scale - ref) of 32 columns as pairs of 16-bit numbers; their sum is added to `sum`.
+template <bool F16, int OFF, int N>
 __device__ __forceinline__ void weights32(const uint32_t (&r)[N], float2 scale, float2 nref, float2 (&sum)[2], uint32_t (&pk)[16]) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[OFF + 2 * e]), __uint_as_float(r[OFF + 2 * e + 1])), scale, nref);
         const float2 y = make_float2(ex2(x.x), ex2(x.y));
         sum[e % 2] = __fadd2_rn(sum[e % 2], y);
-        pk[e] = pack_bf16x2(y.x, y.y);
+        pk[e] = F16 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
     }
+}
+// A row's sums so far times `fix`.
+template <int D>
+__device__ __forceinline__ void scale_row(uint32_t t_o, float fix) {
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(t_o + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fix);
+        tmem_st32(t_o + c0, r);
+    }
+    tmem_wait_st();
 }
 // A row's weights over its scores (P over columns that this thread has read); returns their sum.  The first half (64
 // positions) is announced as soon as it is written.
-template <bool MASKED, int KEEP>
+template <bool MASKED, bool F16, int KEEP>
 __device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale, float ref, uint32_t bar_half,
                                              const uint32_t (&kept)[KEEP]) {
     const float2 scale2 = make_float2(scale, scale), nref = make_float2(-ref, -ref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     uint32_t r[2][32], pk[16];
     tmem_ld32(t_s + KEEP, r[0]);
-    weights32<0>(kept, scale2, nref, sum, pk);
+    weights32<F16, 0>(kept, scale2, nref, sum, pk);
     tmem_wait_ld();
     tmem_st16(t_s, pk);
     if constexpr (KEEP == 64) {
-        weights32<KEEP - 32>(kept, scale2, nref, sum, pk);
+        weights32<F16, KEEP - 32>(kept, scale2, nref, sum, pk);
         tmem_st16(t_s + 16, pk);
     }
 #pragma unroll
@@ -378,27 +410,53 @@ __device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale
         uint32_t(&now)[32] = r[(c0 - KEEP) / 32 % 2];
         if (c0 + 32 < kTile) tmem_ld32(t_s + c0 + 32, r[((c0 - KEEP) / 32 + 1) % 2]);
         mask_columns<MASKED, 0>(now, c0, live);
-        weights32<0>(now, scale2, nref, sum, pk);
+        weights32<F16, 0>(now, scale2, nref, sum, pk);
         if (c0 + 32 < kTile) tmem_wait_ld();
         tmem_st16(t_s + c0 / 2, pk);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// 16 codes as bf16 numbers times a power of two (exact), two 16-byte pieces.
-__device__ __forceinline__ void widen16(const uint4& v, float f, uint4& lo, uint4& hi) {
+// 16 codes as fp16 numbers times f (two of them), two 16-byte pieces.
+__device__ __forceinline__ void widen16(const uint4& v, uint32_t f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w[i / 2] >> 16 * (i % 2))));
-        float a, b;
-        asm("{.reg .f16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h2));
-        o[i] = pack_bf16x2(a * f, b * f);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[i]) : "h"((uint16_t)(w[i / 2] >> 16 * (i % 2))));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(f));
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+// The largest of a tile's exponents in front of position `live`; 255, a row of NaN, does not count.  By a whole warp.
+__device__ __forceinline__ int largest_exponent(const uint8_t* exps, int live) {
+    const int lane = threadIdx.x % 32;
+    uint32_t four = *reinterpret_cast<const uint32_t*>(exps + 4 * lane);
+    four = ((four & 0x7F7F7F7Fu) + 0x01010101u) ^ (four & 0x80808080u);  // one more, 0 for 255
+    if (live < 4 * lane + 4) four &= live <= 4 * lane ? 0u : 0xFFFFFFFFu >> (32 - 8 * (live - 4 * lane));
+    const uint32_t most = max(max(four & 255u, four >> 8 & 255u), max(four >> 16 & 255u, four >> 24));
+    return max(0, (int)__reduce_max_sync(0xFFFFFFFFu, most) - 1);
+}
+// 2^x, x <= kUp, as two fp16 numbers; below 2^-24 zero.
+__device__ __forceinline__ uint32_t half_power(int x) {
+    return (x >= -14 ? (uint32_t)(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u) * 0x10001u;
+}
+// The bits of the largest finite magnitude of 8 bf16 numbers.
+__device__ __forceinline__ uint32_t largest_bits(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+        most = max(most, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+    return most;
+}
+// 8 bf16 numbers times f as fp16 numbers.
+__device__ __forceinline__ uint4 to_f16(const uint4& v, float f) {
+    auto two = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f); };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
 }
 
 template <int D, bool E4M3>
@@ -481,6 +539,21 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) +
                                                            ((b * p.Hkv + s.h) * p.rows + (x - member * p.rows)) * D + 8 * c);
                 }
+                if (E4M3) {
+                    uint32_t most[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) most[k] = largest_bits(v[k]);
+#pragma unroll
+                    for (int x = kLanes / 2; x > 0; x /= 2)
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k) most[k] = max(most[k], __shfl_xor_sync(0xFFFFFFFFu, most[k], x));
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int up = min(141 - (int)(most[k] >> 7), 127);  // the row's numbers come below 2^15
+                        v[k] = to_f16(v[k], __uint_as_float((uint32_t)(up + 127) << 23));
+                        if (c == 0) sh.q_exp[r0 + k * kAtOnce] = (short)-up;
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
                     const int r = r0 + k * kAtOnce;
@@ -491,16 +564,47 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+            int q_exp = 0;
+            if (E4M3) {
+                named_bar_sync(1, 256);
+                q_exp = sh.q_exp[s.two() ? stream * kTile + row : row];
+            }
             const int steps = s.steps(stream);
-            float m = ninf, l = 0.f;
+            float m = ninf, l = 0.f, M = ninf;  // (M: E4M3)
             for (int i = 0; i < steps; ++i, ++n) {
-                const int live = s.len - s.tile(stream, i) * kTile;
+                const int live = s.len - s.tile(stream, i) * kTile, t = tiles + s.tile(stream, i) - s.g0;
                 wait(s_full, n & 1, watch);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t kept[kKeep];
+                float scale = p.scale_log2;
+                if (E4M3) {  // in the units of the row and the tile, a positive number whatever these are
+                    const int x = q_exp + *reinterpret_cast<volatile int*>(&sh.tile_exp[0][t % 4]) - kOne;
+                    scale = fminf(fmaxf(scale * __uint_as_float((uint32_t)(max(-126, min(x, 96)) + 127) << 23), 1.2e-38f), 3e38f);
+                }
                 const float top =
-                    (live >= kTile ? row_max<false>(t_s, live, kept) : row_max<true>(t_s, live, kept)) * p.scale_log2;
+                    (live >= kTile ? row_max<false>(t_s, live, kept) : row_max<true>(t_s, live, kept)) * scale;
+                if constexpr (E4M3) {
+                    const float ev = (float)*reinterpret_cast<volatile int*>(&sh.tile_exp[1][t % 4]);
+                    // the reference of weight times factor moves (as below; a whole number, so that M - ev is exact)
+                    if (__any_sync(0xFFFFFFFFu, top + ev > M + kMost)) {
+                        const float to = fmaxf(M, ceilf(top + ev) - kFirst);
+                        const float fix = to == M ? 1.f : ex2(M - to);
+                        M = to;
+                        if (i > 0) scale_row<D>(t_o, fix);
+                    }
+                    const float ref = M == ninf ? 0.f : M - ev;
+                    const float sum = live >= kTile ? row_weights<false, true>(t_s, live, scale, ref, p_half, kept)
+                                                    : row_weights<true, true>(t_s, live, scale, ref, p_half, kept);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full);
+                    // the sum of the weights, relative to the largest score
+                    const float to = fmaxf(m, top);
+                    if (to != ninf) l = (m == to ? l : l * ex2(m - to)) + sum * ex2(ref - to);
+                    m = to;
+                    continue;
+                }
                 // the reference moves, for all rows of the warp together, when a score passes it by 2^8 (the values of the
                 // tile before are added by now: these scores were issued behind them)
                 if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
@@ -508,23 +612,12 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     const float fix = to == m ? 1.f : ex2(m - to);
                     m = to;
                     l *= fix;
-                    if (i > 0) {
-#pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(t_o + c0, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fix);
-                            tmem_st32(t_o + c0, r);
-                        }
-                        tmem_wait_st();
-                    }
+                    if (i > 0) scale_row<D>(t_o, fix);
                 }
-                if (!E4M3 && live < kTile) {
+                if (live < kTile) {
                     // positions past the end may hold anything: weight zero times a NaN is a NaN, so their values become
                     // zero (by either stream: neither waits for the other)
-                    const int t = tiles + s.tile(stream, i) - s.g0, st = t % kValueStages;
+                    const int st = t % kValueStages;
                     wait(smem_u32(&sh.v_full[st]), (t / kValueStages) & 1, watch);
                     if (row >= live)
 #pragma unroll
@@ -537,8 +630,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     __syncwarp();
                 }
                 const float ref = m == ninf ? 0.f : m;
-                l += live >= kTile ? row_weights<false>(t_s, live, p.scale_log2, ref, p_half, kept)
-                                   : row_weights<true>(t_s, live, p.scale_log2, ref, p_half, kept);
+                l += live >= kTile ? row_weights<false, false>(t_s, live, scale, ref, p_half, kept)
+                                   : row_weights<true, false>(t_s, live, scale, ref, p_half, kept);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full);
@@ -556,11 +649,15 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             tc_fence_after();
             ++stretch;
             float* o = p.part_o + at * D;
+            const float half = !E4M3 || m == ninf ? 1.f : ex2(0.5f * (M - m - kOne));  // (its square may pass a float's range)
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t r[32];
                 tmem_ld32(t_o + c0, r);
                 tmem_wait_ld();
+                if (E4M3)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * half * half);
                 if (mine) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -668,7 +765,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             }
         }
     } else if (warp < R::kLoad) {
-        // =================================================== E4M3: codes to tiles of bf16 numbers
+        // =================================================== E4M3: codes to tiles of fp16 numbers
         constexpr int kLanes = D / 16, kAtOnce = 128 / kLanes, kEach = kTile / kAtOnce;  // lanes of a row, rows at once
         const int ltid = tid - 32 * R::kWiden, r0 = ltid / kLanes, c = ltid % kLanes;
         const uint32_t codes0 = smem_u32(smem) + C::kOffCodes;
@@ -676,28 +773,37 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
         bool ok = true;
         while (s.at < s.end && ok) {
             stretch_open(p, sh, over, s);
+            int most = 0;  // the largest exponent of the stretch's tiles of values
             for (int g = s.g0; g < s.g1 && ok; ++g, ++t) {
                 const int live = s.len - g * kTile;
+                int top[2];  // the largest exponents of the tile's keys and values
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int from = n % C::kCodeStages, stages = kv ? kValueStages : kKeyStages, st = t % stages;
-                    ok = ok && wait(smem_u32(&sh.c_full[from]), (n / C::kCodeStages) & 1, watch);
+                    if (!kv) {  // (the values' exponents early: the weights wait for them)
+                        ok = ok && wait(smem_u32(&sh.c_full[from]), (n / C::kCodeStages) & 1, watch) &&
+                             wait(smem_u32(&sh.c_full[(n + 1) % C::kCodeStages]), ((n + 1) / C::kCodeStages) & 1, watch);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) top[x] = largest_exponent(sh.exps[(n + x) % C::kCodeStages], live);
+                        most = max(most, top[1]);
+                        top[1] = max(top[1], most - kApart);
+                    }
+                    const int my_row = c * kAtOnce + r0, my_e = sh.exps[from][my_row];  // (row i = c of this lane's below)
                     uint4 v[kEach];
-                    uint32_t e[kEach];
 #pragma unroll
                     for (int i = 0; i < kEach; ++i) {
                         const int row = i * kAtOnce + r0, sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
                         v[i] = make_uint4(0, 0, 0, 0);
-                        e[i] = 0;
                         if (row < live) {
                             const uint32_t at = codes0 + from * C::kCodes + row * D + 16 * sw;
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
                                          : "r"(at)
                                          : "memory");
-                            e[i] = sh.exps[from][row];
                         }
                     }
+                    const uint32_t factor =
+                        my_row >= live ? 0u : my_e == 255 ? 0x7E007E00u : half_power(my_e - top[kv] + kUp);  // (255: NaN)
                     if (ok && t >= stages)
                         ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (t / stages - 1) & 1, watch);
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -706,13 +812,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
+                    // (of four tiles: keys come two tiles ahead of the weights, where a stream has every other tile)
+                    if (!kv && ltid < 2) *reinterpret_cast<volatile int*>(&sh.tile_exp[ltid][t % 4]) = ltid ? top[1] : top[0];
                     const uint32_t dst = (kv ? s_v : s_k) + st * C::kBytes + (c / 4) * C::kPart;
 #pragma unroll
                     for (int i = 0; i < kEach; ++i) {
                         const int row = i * kAtOnce + r0, x = 2 * (c % 4);
-                        // 2^(e - 127); 255 makes the whole row NaN
                         uint4 lo, hi;
-                        widen16(v[i], __uint_as_float(e[i] == 255 ? 0x7FC00000u : max(e[i] << 23, 0x00400000u)), lo, hi);
+                        widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor, i, kLanes), lo, hi);
                         // the lanes of a row's second half begin with the other piece: all 32 banks at once
                         const bool turned = c >= 4;
                         const uint4 a = turned ? hi : lo, b = turned ? lo : hi;
@@ -733,7 +840,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
     } else {
         // =================================================== products of a stream (lane 0)
         if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false), idesc_o = idesc_bf16_f32(kTile, D, true);
+            constexpr uint32_t idesc_s = E4M3 ? idesc_f16_f32(kTile, kTile, false) : idesc_bf16_f32(kTile, kTile, false);
+            constexpr uint32_t idesc_o = E4M3 ? idesc_f16_f32(kTile, D, true) : idesc_bf16_f32(kTile, D, true);
             const int stream = warp - R::kMma;
             const uint32_t t_s = tmem + stream * kTile, t_o = tmem + C::kColO + stream * kTile;
             const uint32_t s_full = smem_u32(&sh.s_full[stream]), p_half = smem_u32(&sh.p_half[stream]);

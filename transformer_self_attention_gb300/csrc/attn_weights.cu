@@ -467,8 +467,9 @@ __device__ __forceinline__ long long weight_at(const EvictParams& p, RowAt r, in
     return ((long long)r.page * p.c.Hkv + h) * p.c.page + r.slot;
 }
 
-// Into other pages: a warp takes 32 rows of one head after another (eight where there are too few for all warps), a lane looks up one row, and all lanes copy them, 512
-// bytes at a time, eight loads under way; the next rows are looked up meanwhile.
+// Into other pages: a warp takes 32 rows of one head after another (eight where there are too few for all warps), a lane
+// looks up one row, and all lanes copy them, 512 bytes at a time, eight loads under way; the next rows are looked up
+// meanwhile.
 constexpr int kMoveBlocks = 4;  // a multiprocessor, all at once
 template <int ROWB>  // bytes of a key
 __global__ void __launch_bounds__(kThreads, kMoveBlocks) move_kernel(const __grid_constant__ EvictParams p, int groups, int per) {
