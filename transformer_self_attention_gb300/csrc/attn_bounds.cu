@@ -75,23 +75,16 @@ struct RowBounds {
     }
     __device__ __forceinline__ void take(const uint4& v, uint32_t, uint32_t) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        join(w, w);
-    }
-    __device__ __forceinline__ void join(const uint32_t* l, const uint32_t* h) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            lo[i] = min2_nan(lo[i], l[i]);
-            hi[i] = max2_nan(hi[i], h[i]);
+            lo[i] = least(lo[i], w[i]);
+            hi[i] = most(hi[i], w[i]);
         }
     }
-    __device__ __forceinline__ void get(float* l, float* h, uint32_t) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            l[2 * i] = __uint_as_float(lo[i] << 16);
-            l[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
-            h[2 * i] = __uint_as_float(hi[i] << 16);
-            h[2 * i + 1] = __uint_as_float(hi[i] & 0xFFFF0000u);
-        }
+    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) { return min2_nan(a, b); }
+    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) { return max2_nan(a, b); }
+    static __device__ __forceinline__ float2 value(uint32_t w, uint32_t) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     }
 };
 // E4M3: both bounds of a pair of channels as packed 16-bit numbers.  Where the rows' exponents lie within 14 of the largest
@@ -152,30 +145,11 @@ struct CodeBounds {
             hi[2 * i + 1] = most(hi[2 * i + 1], y);
         }
     }
-    __device__ __forceinline__ void join(const uint32_t* l, const uint32_t* h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo[i] = least(lo[i], l[i]);
-            hi[i] = most(hi[i], h[i]);
-        }
-    }
-    __device__ __forceinline__ void get(float* l, float* h, uint32_t top) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (WIDE) {
-                l[2 * i] = __uint_as_float(lo[i] << 16);
-                l[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
-                h[2 * i] = __uint_as_float(hi[i] << 16);
-                h[2 * i + 1] = __uint_as_float(hi[i] & 0xFFFF0000u);
-            } else {
-                const float f = __uint_as_float(max(top << 23, 0x00400000u));
-                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo[i]));
-                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-                l[2 * i] = a.x * f; l[2 * i + 1] = a.y * f;
-                h[2 * i] = b.x * f; h[2 * i + 1] = b.y * f;
-            }
-        }
-        if (nan) l[0] = __int_as_float(0x7FFFFFFF);
+    static __device__ __forceinline__ float2 value(uint32_t w, uint32_t top) {
+        if constexpr (WIDE) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        const float f = __uint_as_float(max(top << 23, 0x00400000u));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return make_float2(x.x * f, x.y * f);
     }
 };
 
@@ -219,7 +193,7 @@ struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
 };
 template <int D, bool E4M3, class R>
 __device__ __forceinline__ void page_bounds(const BoundsParams& p, long long unit, int rows, uint32_t top, int part, int share,
-                                            Rows<D, E4M3>& x, uint32_t (*joint)[2][32][8]) {
+                                            Rows<D, E4M3>& x, uint32_t (*joint)[2][32][2]) {
     using X = Rows<D, E4M3>;
     constexpr int kLanes = X::kLanes, kWords = R::kChannels / 2;
     const int lane = threadIdx.x % 32;
@@ -231,66 +205,76 @@ __device__ __forceinline__ void page_bounds(const BoundsParams& p, long long uni
         r0 += share * X::kRound;
         if (r0 < rows) x.load(p, unit, rows, r0);
     }
+    // over the lanes that hold the same channels of other rows, which are left with half of the channels after each step
+    uint32_t(&l)[kWords] = run.lo, (&h)[kWords] = run.hi;
+    int first = 0;  // of the lane's words
 #pragma unroll
-    for (int o = kLanes; o < 32; o *= 2) {
-        uint32_t l[kWords], h[kWords];
+    for (int o = kLanes, n = kWords / 2; o < 32; o *= 2, n /= 2) {
+        const bool up = lane & o;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            l[i] = __shfl_xor_sync(0xFFFFFFFFu, run.lo[i], o);
-            h[i] = __shfl_xor_sync(0xFFFFFFFFu, run.hi[i], o);
+        for (int i = 0; i < n; ++i) {
+            const uint32_t l_in = __shfl_xor_sync(0xFFFFFFFFu, up ? l[i] : l[n + i], o);
+            const uint32_t h_in = __shfl_xor_sync(0xFFFFFFFFu, up ? h[i] : h[n + i], o);
+            l[i] = R::least(up ? l[n + i] : l[i], l_in);
+            h[i] = R::most(up ? h[n + i] : h[i], h_in);
         }
-        run.join(l, h);
+        first += up ? n : 0;
     }
+    constexpr int kMine = kWords * kLanes / 32;  // words of a lane now: D channels over the warp
+    static_assert(kMine == 1 || kMine == 2, "channels of a lane");
+    bool nan = false;
+    if constexpr (E4M3) nan = run.nan != 0;
     if (share > 1) {
-        if (lane < kLanes)
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                joint[part][0][lane][i] = run.lo[i];
-                joint[part][1][lane][i] = run.hi[i];
-            }
-        bool nan = false;
-        if constexpr (E4M3) nan = run.nan != 0;
+        for (int i = 0; i < kMine; ++i) {
+            joint[part][0][lane][i] = l[i];
+            joint[part][1][lane][i] = h[i];
+        }
         nan = __syncthreads_or(nan);
         if (part) return;
-        for (int w = 1; w < share; ++w) run.join(joint[w][0][lane % kLanes], joint[w][1][lane % kLanes]);
-        if constexpr (E4M3) run.nan = nan;
-    }
-    float l[R::kChannels], u[R::kChannels];
-    run.get(l, u, top);
-    uint32_t big = 0;  // as bits: a NaN is above an infinity
+        for (int w = 1; w < share; ++w)
 #pragma unroll
-    for (int i = 0; i < R::kChannels; ++i)
-        big = max(big, max(__float_as_uint(l[i]) & 0x7FFFFFFFu, __float_as_uint(u[i]) & 0x7FFFFFFFu));
+            for (int i = 0; i < kMine; ++i) {
+                l[i] = R::least(l[i], joint[w][0][lane][i]);
+                h[i] = R::most(h[i], joint[w][1][lane][i]);
+            }
+    }
+    uint32_t big = nan ? 0x7FFFFFFFu : 0;  // as bits: a NaN is above an infinity
+    float2 u[kMine], v[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        u[i] = R::value(l[i], top);
+        v[i] = R::value(h[i], top);
+        for (const float y : {u[i].x, u[i].y, v[i].x, v[i].y}) big = max(big, __float_as_uint(y) & 0x7FFFFFFFu);
+    }
     big = __reduce_max_sync(0xFFFFFFFFu, big);
     const bool bad = big >= 0x7F800000u;
     const int k = bad ? 0 : power_of(big);
-    if (lane < kLanes) {
-        const float f = exp2_of(-k);
-        uint32_t cl[R::kChannels / 4], cu[R::kChannels / 4];
+    const float f = exp2_of(-k);
+    uint32_t below = 0, above = 0;
 #pragma unroll
-        for (int i = 0; i < R::kChannels / 4; ++i) {
-            cl[i] = cu[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int a = bad ? 0 : __float2int_rd(l[4 * i + j] * f), c = bad ? 0 : __float2int_ru(u[4 * i + j] * f);
-                cl[i] |= (uint32_t)(a & 0xFF) << 8 * j;
-                cu[i] |= (uint32_t)(c & 0xFF) << 8 * j;
-            }
-        }
-        uint32_t* out = reinterpret_cast<uint32_t*>(p.codes + unit * 2 * D) + lane * (R::kChannels / 4);
-#pragma unroll
-        for (int i = 0; i < R::kChannels / 4; ++i) {
-            out[i] = cl[i];
-            out[D / 4 + i] = cu[i];
-        }
-        if (lane == 0) p.exps[unit] = (uint8_t)(bad ? 255 : k + 127);
+    for (int i = 0; i < kMine; ++i) {
+        const int a = __float2int_rd(u[i].x * f), b = __float2int_rd(u[i].y * f);
+        const int c = __float2int_ru(v[i].x * f), d = __float2int_ru(v[i].y * f);
+        below |= (uint32_t)((a & 0xFF) | (b & 0xFF) << 8) << 16 * i;
+        above |= (uint32_t)((c & 0xFF) | (d & 0xFF) << 8) << 16 * i;
     }
+    if (bad) below = above = 0;
+    int8_t* out = p.codes + unit * 2 * D + lane % kLanes * R::kChannels + 2 * first;
+    if constexpr (kMine == 2) {
+        *reinterpret_cast<uint32_t*>(out) = below;
+        *reinterpret_cast<uint32_t*>(out + D) = above;
+    } else {
+        *reinterpret_cast<uint16_t*>(out) = (uint16_t)below;
+        *reinterpret_cast<uint16_t*>(out + D) = (uint16_t)above;
+    }
+    if (lane == 0) p.exps[unit] = (uint8_t)(bad ? 255 : k + 127);
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int kWarps = kUpdateThreads / 32;
-    __shared__ uint32_t joint[kWarps][2][32][8];
+    __shared__ uint32_t joint[kWarps][2][32][2];
     __shared__ unsigned first[kPagedMaxBatch + 1];  // changed pages of the sequences before b
     __shared__ unsigned scan[kUpdateThreads / 32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -326,9 +310,13 @@ __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_ke
     const long long items = (long long)carry * p.c.Hkv;
     const int share = items <= (long long)gridDim.x ? kWarps : 1, part = share > 1 ? warp : 0;
     const long long step = (long long)gridDim.x * kWarps / share;
-    for (long long item = ((long long)blockIdx.x * kWarps + warp) / share; item < items; item += step) {
+    struct Item {
+        int page, h, rows;
+    };
+    auto look_up = [&](long long item) {  // (its page is looked at an item later)
+        Item x{0, 0, 0};
+        if (item >= items) return x;
         const unsigned entry = (unsigned)(item / p.c.Hkv);
-        const int h = (int)(item - (long long)entry * p.c.Hkv);
         int b = 0, top = p.B - 1;  // the last b with first[b] <= entry
         while (b < top) {
             const int mid = (b + top + 1) / 2;
@@ -338,13 +326,20 @@ __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_ke
         int n, lo, hi;
         changed_pages(p, b, false, n, lo, hi);
         const int index = lo + (int)(entry - first[b]);
-        const int page = p.t.pages[b * p.t.stride + index];
+        x.page = p.t.pages[b * p.t.stride + index];
+        x.h = (int)(item - (long long)entry * p.c.Hkv);
+        x.rows = min(p.c.page, n - index * p.c.page);
+        return x;
+    };
+    long long item = ((long long)blockIdx.x * kWarps + warp) / share;
+    for (Item now = look_up(item), next; item < items; item += step, now = next) {
+        next = look_up(item + step);
+        const int page = now.page, rows = now.rows;
         if (page < 0 || page >= p.c.n_pages) {
             if (lane == 0) atomicOr(p.c.err, kCacheErrPage);
             continue;  // (all warps that share the page)
         }
-        const long long unit = (long long)page * p.c.Hkv + h;
-        const int rows = min(p.c.page, n - index * p.c.page);
+        const long long unit = (long long)page * p.c.Hkv + now.h;
         Rows<D, E4M3> x;
         x.load(p, unit, rows, min(part * Rows<D, E4M3>::kRound, rows - 1));
         if constexpr (E4M3) {
