@@ -787,8 +787,8 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
  *   codes, exponents : device, as above; codes 16-byte aligned.
  *   new_len : int32 device [B], or NULL: all positions.  More than cache_len[b] counts as that.
  * A page that appears twice with different lengths gets the bounds of one of them.
- * Errors: as attn_cache_write (ATTN_ERR_UNSUPPORTED also for max_pages * page > 2^30).  Lengths and page numbers that are
- * not followed are recorded in the cache's error word.
+ * Errors: as attn_cache_write (ATTN_ERR_UNSUPPORTED also for max_pages * page > 2^30 and B * max_pages * Hkv >= 2^31).
+ * Lengths and page numbers that are not followed are recorded in the cache's error word.
  */
 attn_status attn_bounds_update(attn_cache_handle h, void* codes, void* exponents, int B, const int* page_table,
                                long long table_stride, int max_pages, const int* cache_len, const int* new_len,

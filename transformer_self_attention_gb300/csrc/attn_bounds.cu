@@ -12,7 +12,9 @@
 //
 // Update: bound by memory, the changed pages' keys read once, or by latency where one page a sequence changes.  A warp takes
 // a page and head, or the whole block does where there are fewer of them than blocks; the lanes hold 16 bytes of a row
-// each, several rows at once, eight loads under way.
+// each, several rows at once, eight loads under way, and the next page's are begun before this one's bounds are
+// joined and written (235 MB of codes: 56 us with all lanes joining all channels and nothing ahead, 44 so; 470 MB of bf16
+// keys 74 us).  Pages of 16 positions are bound by instructions: 158 us for 235 MB of codes with d 64, 95 with d 128.
 // Select: a cluster of one to eight blocks for each sequence and kv head.  With the negative and the positive parts of a
 // query behind one another, a score is one product of 2 d whole numbers, lo first, then hi: m16n8k16 products of fp16 numbers,
 // which hold them exactly, as float32 holds their sums, with the rows as the first operand and eight pages as the second.
@@ -91,7 +93,7 @@ struct RowBounds {
 // (WIDE false), codes become fp16 numbers times 2^(e - largest), exactly; otherwise bf16 numbers: a code's exponent and
 // mantissa, moved to where a bf16 number has them, stand for 2^-120 of it (subnormal codes become subnormal numbers), and two
 // multiplications by powers of two give the element, as exactly as a bf16 number can (beyond 2^128: infinities).  The second
-// form takes twice the instructions: 88 us for 235 MB.
+// form takes twice the instructions: 69 against 44 us for 235 MB (d 128, pages of 64).
 template <bool WIDE>
 struct CodeBounds {
     static constexpr int kChannels = 16;
@@ -169,10 +171,12 @@ struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
     static constexpr int kRound = kAhead * kAtOnce;
     uint4 v[kAhead];
     uint32_t e[kAhead];
+    int used;  // of them
     __device__ __forceinline__ void load(const BoundsParams& p, long long unit, int rows, int r0) {
         const int lane = threadIdx.x % 32;
         const char* src = p.c.pages + unit * 2 * p.c.page * kRow + 16 * (lane % kLanes);
         const uint8_t* sc = E4M3 ? p.c.scales + unit * (p.c.page / 16) * 32 : nullptr;
+        used = E4M3 ? min(kAhead, (rows - r0 + kAtOnce - 1) / kAtOnce) : kAhead;
         if (r0 % 16 == 0 && r0 + kRound <= rows) {  // one address, and constants
             src += (r0 + lane / kLanes) * (long long)kRow;
             if (E4M3) sc += r0 * 2 + lane / kLanes;
@@ -185,26 +189,35 @@ struct Rows {  // a warp's loads of some rows: 16 bytes a lane and row
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
+            if (E4M3 && i >= used) break;
             const int row = min(r0 + i * kAtOnce + lane / kLanes, rows - 1);  // the last row again changes nothing
             v[i] = *reinterpret_cast<const uint4*>(src + (long long)row * kRow);
             e[i] = E4M3 ? sc[(row / 16) * 32 + row % 16] : 0;
         }
     }
 };
-template <int D, bool E4M3, class R>
+// `ahead` starts the loads of the page behind this one.
+template <int D, bool E4M3, class R, class F>
 __device__ __forceinline__ void page_bounds(const BoundsParams& p, long long unit, int rows, uint32_t top, int part, int share,
-                                            Rows<D, E4M3>& x, uint32_t (*joint)[2][32][2]) {
+                                            Rows<D, E4M3>& x, uint32_t (*joint)[2][32][2], F ahead) {
     using X = Rows<D, E4M3>;
     constexpr int kLanes = X::kLanes, kWords = R::kChannels / 2;
     const int lane = threadIdx.x % 32;
     R run;
     run.clear();
     for (int r0 = part * X::kRound; r0 < rows;) {  // (the first rows have been loaded)
+        if (!E4M3 || x.used == X::kAhead) {
 #pragma unroll
-        for (int i = 0; i < X::kAhead; ++i) run.take(x.v[i], x.e[i], top);
+            for (int i = 0; i < X::kAhead; ++i) run.take(x.v[i], x.e[i], top);
+        } else {
+#pragma unroll
+            for (int i = 0; i < X::kAhead - 1; ++i)
+                if (i < x.used) run.take(x.v[i], x.e[i], top);
+        }
         r0 += share * X::kRound;
         if (r0 < rows) x.load(p, unit, rows, r0);
     }
+    ahead();
     // over the lanes that hold the same channels of other rows, which are left with half of the channels after each step
     uint32_t(&l)[kWords] = run.lo, (&h)[kWords] = run.hi;
     int first = 0;  // of the lane's words
@@ -307,16 +320,17 @@ __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_ke
         carry = all;
         __syncthreads();
     }
-    const long long items = (long long)carry * p.c.Hkv;
-    const int share = items <= (long long)gridDim.x ? kWarps : 1, part = share > 1 ? warp : 0;
-    const long long step = (long long)gridDim.x * kWarps / share;
+    const unsigned items = carry * p.c.Hkv;
+    const unsigned share = items <= gridDim.x ? kWarps : 1, part = share > 1 ? warp : 0, step = gridDim.x * kWarps / share;
+    // The warp's items, `step` apart: the page of the next one is looked at an item later.
     struct Item {
         int page, h, rows;
     };
-    auto look_up = [&](long long item) {  // (its page is looked at an item later)
+    unsigned item = (blockIdx.x * kWarps + warp) / share;
+    auto look_up = [&] {
         Item x{0, 0, 0};
         if (item >= items) return x;
-        const unsigned entry = (unsigned)(item / p.c.Hkv);
+        const unsigned entry = item / (unsigned)p.c.Hkv;
         int b = 0, top = p.B - 1;  // the last b with first[b] <= entry
         while (b < top) {
             const int mid = (b + top + 1) / 2;
@@ -327,29 +341,46 @@ __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_ke
         changed_pages(p, b, false, n, lo, hi);
         const int index = lo + (int)(entry - first[b]);
         x.page = p.t.pages[b * p.t.stride + index];
-        x.h = (int)(item - (long long)entry * p.c.Hkv);
+        x.h = (int)(item - entry * (unsigned)p.c.Hkv);
         x.rows = min(p.c.page, n - index * p.c.page);
+        item += step;
         return x;
     };
-    long long item = ((long long)blockIdx.x * kWarps + warp) / share;
-    for (Item now = look_up(item), next; item < items; item += step, now = next) {
-        next = look_up(item + step);
-        const int page = now.page, rows = now.rows;
-        if (page < 0 || page >= p.c.n_pages) {
+    Rows<D, E4M3> x;
+    uint32_t e[2];  // E4M3: exponents of rows `lane` and 32 + `lane`
+    auto good = [&](const Item& i) { return i.page >= 0 && i.page < p.c.n_pages; };
+    auto load = [&](const Item& i) {
+        if (i.rows <= 0 || !good(i)) return;
+        const long long unit = (long long)i.page * p.c.Hkv + i.h;
+        x.load(p, unit, i.rows, min(part * Rows<D, E4M3>::kRound, i.rows - 1));
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = min(32 * k + lane, i.rows - 1);
+                e[k] = p.c.scales[unit * (p.c.page / 16) * 32 + (r / 16) * 32 + r % 16];
+            }
+        }
+    };
+    Item now = look_up(), next;
+    load(now);
+    for (; now.rows > 0; now = next) {
+        next = look_up();
+        if (!good(now)) {
             if (lane == 0) atomicOr(p.c.err, kCacheErrPage);
+            load(next);
             continue;  // (all warps that share the page)
         }
-        const long long unit = (long long)page * p.c.Hkv + now.h;
-        Rows<D, E4M3> x;
-        x.load(p, unit, rows, min(part * Rows<D, E4M3>::kRound, rows - 1));
+        const int rows = now.rows;
+        const long long unit = (long long)now.page * p.c.Hkv + now.h;
+        auto ahead = [&] { load(next); };
         if constexpr (E4M3) {
             // the largest and the smallest exponent of the rows
             const uint8_t* sc = p.c.scales + unit * (p.c.page / 16) * 32;
-            uint32_t most = 0, least = 255;
-            for (int r = lane; r < rows; r += 32) {
-                const uint32_t e = sc[(r / 16) * 32 + r % 16];
-                most = max(most, e);
-                least = min(least, e);
+            uint32_t most = max(e[0], e[1]), least = min(e[0], e[1]);
+            for (int r = 64 + lane; r < rows; r += 32) {
+                const uint32_t y = sc[(r / 16) * 32 + r % 16];
+                most = max(most, y);
+                least = min(least, y);
             }
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             least = __reduce_min_sync(0xFFFFFFFFu, least);
@@ -358,13 +389,14 @@ __global__ void __launch_bounds__(kUpdateThreads, update_blocks(E4M3)) update_ke
                     for (int i = lane; i < 2 * D / 4; i += 32) reinterpret_cast<uint32_t*>(p.codes + unit * 2 * D)[i] = 0;
                     if (lane == 0) p.exps[unit] = 255;
                 }
+                load(next);
             } else if (most - least <= 14) {
-                page_bounds<D, true, CodeBounds<false>>(p, unit, rows, most, part, share, x, joint);
+                page_bounds<D, true, CodeBounds<false>>(p, unit, rows, most, part, share, x, joint, ahead);
             } else {
-                page_bounds<D, true, CodeBounds<true>>(p, unit, rows, most, part, share, x, joint);
+                page_bounds<D, true, CodeBounds<true>>(p, unit, rows, most, part, share, x, joint, ahead);
             }
         } else {
-            page_bounds<D, false, RowBounds>(p, unit, rows, 0, part, share, x, joint);
+            page_bounds<D, false, RowBounds>(p, unit, rows, 0, part, share, x, joint, ahead);
         }
         if (share > 1) __syncthreads();
     }

@@ -539,20 +539,22 @@ __global__ void __launch_bounds__(kThreads, kMoveBlocks) move_kernel(const __gri
     }
 }
 
-// In place: a block takes a head's keys (blockIdx.y 0) or values from front to back, kRows rows a round.  A round's loads
-// are all done (the barrier) before its first store; the next round's may come before them too: rows are read at
-// their place or behind it.
+// In place: a block takes SLICE bytes of each of a head's keys or values (blockIdx.y) from front to back, kRows rows a
+// round.  A round's loads are all done (the barrier) before its first store; the next round's may come before them too:
+// rows are read at their place or behind it.  Slices of 64 bytes make more blocks and rounds of more rows: 186 us for 64 heads of
+// 32K positions of 256 bytes cut to 8448, 294 with whole rows; with blocks enough whole rows are better (512 heads of 2K cut to 768:
+// 110 us, 124 with slices).
 constexpr int kPlaceThreads = 512;
-template <int ROWB>
+template <int ROWB, int SLICE>
 __global__ void __launch_bounds__(kPlaceThreads) move_in_place_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int kLanes = ROWB / 16, kEach = 4, kStep = kPlaceThreads / kLanes, kRows = kEach * kStep;
-    const int tid = threadIdx.x, unit = blockIdx.x, b = unit / p.c.Hkv, h = unit - b * p.c.Hkv, kv = blockIdx.y;
+    constexpr int kLanes = SLICE / 16, kEach = 4, kStep = kPlaceThreads / kLanes, kRows = kEach * kStep;
+    const int tid = threadIdx.x, unit = blockIdx.x, b = unit / p.c.Hkv, h = unit - b * p.c.Hkv, kv = blockIdx.y % 2;
     wait_for_kernel_before();
     let_kernel_behind_in();
     const int stay = p.keep + p.recent;
     const int* row = p.t.pages + b * p.t.stride;
     const int* kept = p.kept + (long long)unit * stay;
-    const int sub = tid / kLanes, off = 16 * (tid % kLanes);
+    const int sub = tid / kLanes, off = blockIdx.y / 2 * SLICE + 16 * (tid % kLanes);
     int n = p.t.len[b];
     if (n <= stay || n > p.t.max_pages * p.c.page) return;  // every row stays where it is
     for (int r0 = 0; r0 < stay; r0 += kRows) {
@@ -625,10 +627,14 @@ cudaError_t launch_evict(EvictParams p, bool e4m3, int n_sm, cudaStream_t stream
     if (e != cudaSuccess) return e;
     const int rowb = p.c.d * (e4m3 ? 1 : 2);
     if (p.in_place) {
-        const dim3 grid((unsigned)units, 2);
-        auto go = [&](auto* f) { return launch_dependent(f, grid, kPlaceThreads, 0, stream, p); };
-        return rowb == 64 ? go(move_in_place_kernel<64>) : rowb == 128 ? go(move_in_place_kernel<128>)
-                                                                       : go(move_in_place_kernel<256>);
+        const bool whole = 2 * units >= 4 * n_sm;
+        auto go = [&](auto width) {
+            constexpr int W = decltype(width)::value;
+            return whole ? launch_dependent(move_in_place_kernel<W, W>, dim3((unsigned)units, 2), kPlaceThreads, 0, stream, p)
+                         : launch_dependent(move_in_place_kernel<W, 64>, dim3((unsigned)units, 2 * W / 64), kPlaceThreads, 0, stream, p);
+        };
+        return rowb == 64 ? go(std::integral_constant<int, 64>{})
+                          : rowb == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
     }
     const int rows = (int)std::min<long long>(stay, (long long)p.t.max_pages * p.c.page), most = kMoveBlocks * n_sm;
     const int per = (long long)units * rows >= 32LL * kWarps * most ? 32 : 8, groups = (rows + per - 1) / per;

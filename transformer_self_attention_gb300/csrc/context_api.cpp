@@ -48,7 +48,9 @@ attn_status attn_bounds_update(attn_cache_handle h, void* codes, void* exponents
                                void* stream) {
     if (!h || !codes || !aligned(codes, 16) || !exponents || B < 1) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len) || !aligned(new_len, 4)) return ATTN_ERR_INVALID_ARG;
-    if (B > ATTN_DECODE_MAX_BATCH || !room_ok(h, max_pages)) return ATTN_ERR_UNSUPPORTED;
+    // (changed pages and heads are counted in 31 bits)
+    if (B > ATTN_DECODE_MAX_BATCH || !room_ok(h, max_pages) || (long long)B * max_pages > 0x7FFFFFFFLL / h->c.Hkv)
+        return ATTN_ERR_UNSUPPORTED;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
     attn::BoundsParams p{};
     p.c = h->c;
