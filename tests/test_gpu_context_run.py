@@ -347,6 +347,13 @@ def test_calls_that_are_refused():
     refused(tsa.ATTN_ERR_UNSUPPORTED, lambda: bounds.select(Q, long, n, 4))
     refused(tsa.ATTN_ERR_UNSUPPORTED, lambda: bounds.select(Q, table, n, 40961))
     refused(tsa.ATTN_ERR_INVALID_ARG, lambda: bounds.select(Q, table, n, 4, length=n))
+    both = torch.zeros((1, 2, 3), dtype=torch.int32).cuda()  # (an output and an input, or two outputs, in one place)
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: bounds.select(Q, both.view(1, 6), n, 3, table=both))
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: bounds.select(Q, table, n, 3, table=both, length=both.view(6)[:1]))
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: bounds.select(Q, table, both.view(6)[:1], 3, table=both))
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: weights.evict(table, both.view(6)[:1], 3, kept=both))
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: weights.evict(table, n, 3, kept=both, length=both.view(6)[:1]))
+    refused(tsa.ATTN_ERR_INVALID_ARG, lambda: weights.evict(table, n, 3, to_table=both.view(1, 6), kept=both))
     many = torch.zeros((1, 4, 33, 64), dtype=torch.bfloat16, device="cuda")
     refused(tsa.ATTN_ERR_UNSUPPORTED, lambda: bounds.select(many, table, n, 8, recent=3))
     refused(tsa.ATTN_ERR_INVALID_ARG, lambda: weights.evict(table, n, 4, length=n))

@@ -195,6 +195,13 @@ def test_weights_that_are_equal_or_not_finite(in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("store,d", [("bf16", 128), ("e4m3", 64)])
+def test_eviction_of_many_heads(store, d, in_place):
+    """More heads than blocks that run at once."""
+    _evict([(37 * b) % 90 for b in range(180)], 2, 16, d, store, 30, 11, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_eviction_of_a_long_sequence(in_place):
     """More weights than fit in shared memory, and several rounds of a block in place."""
     _evict([50000, 9000], 1, 128, 64, "bf16", 4000, 500, in_place)

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <new>
 
 #include "attn.h"
@@ -37,6 +38,8 @@ attn::PageTable table_of(const int* page_table, long long stride, int max_pages,
 // Positions of a row of the table fit an int with room for differences.
 bool room_ok(attn_cache_handle h, int max_pages) { return (long long)max_pages * h->c.page <= attn::kPagedMostPositions; }
 
+bool one_of(const void* p, std::initializer_list<const void*> those) { return std::find(those.begin(), those.end(), p) != those.end(); }
+
 attn_status done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
 }  // namespace
@@ -68,8 +71,8 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
                                void* stream) {
     if (!h || !codes || !aligned(codes, 16) || !exponents || !Q || !aligned(Q, 16)) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
-    if (!out_table || !aligned(out_table, 4) || out_table == page_table || !out_len || !aligned(out_len, 4) ||
-        out_len == cache_len)
+    if (!out_table || !aligned(out_table, 4) || !out_len || !aligned(out_len, 4) || out_table == out_len ||
+        one_of(out_table, {page_table, cache_len}) || one_of(out_len, {page_table, cache_len}))
         return ATTN_ERR_INVALID_ARG;
     const attn_status vs = attn::validate_paged(B, Hq, h->c.Hkv, S_q, ATTN_MASK_CAUSAL, 0);
     if (vs != ATTN_OK) return vs;
@@ -131,11 +134,12 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
     if (!h || !weights || !aligned(weights, 16) || B < 1) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (keep < 0 || recent < 0 || (long long)keep + recent < 1 || !out_len || !aligned(out_len, 4) || !kept ||
-        !aligned(kept, 4) || out_len == cache_len || kept == page_table)
+        !aligned(kept, 4) || out_len == kept || one_of(out_len, {cache_len, page_table, to_table}) ||
+        one_of(kept, {cache_len, page_table, to_table}))
         return ATTN_ERR_INVALID_ARG;
     const long long stay = (long long)keep + recent, room = (long long)max_pages * h->c.page;
     if (to_table) {
-        if (!table_ok(to_table, to_stride, to_max_pages, cache_len) || to_table == page_table || kept == to_table ||
+        if (!table_ok(to_table, to_stride, to_max_pages, cache_len) || to_table == page_table ||
             (long long)to_max_pages * h->c.page < std::min(stay, room))
             return ATTN_ERR_INVALID_ARG;
     }
