@@ -831,6 +831,7 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
  *   scale, kind, window : the step's, as attn_paged_create.
  *   decay  : 0 .. 1.
  * Sums are float32; a sum has a fixed order.  Slots at or past the lengths are left as they were.
+ * With decay 1 and a window, positions in front of every row's window are not looked at: their pages may be gone.
  * Errors: as attn_paged_forward, ATTN_ERR_UNSUPPORTED above B * Hkv * max_pages * page of about 2^35.
  */
 attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, int Hq, int S_q, const void* Q,

@@ -95,7 +95,9 @@ def weigh(Q, LSE, W, vals, table, page, lens, scale, kind, window, decay):
         q = Q[b].double().view(Hkv, -1, S_q, d)
         lse = LSE[b].double().view(Hkv, -1, S_q)
         j = torch.arange(n)
-        p, slot = table[b].long()[j // page].clamp(0, W.shape[0] - 1), j % page
+        p, slot = table[b].long()[j // page], j % page
+        held = (p >= 0) & (p < W.shape[0])  # (pages before every row's window may be gone: nobody's weights)
+        p = p.clamp(0, W.shape[0] - 1)
         new = out[p, :, slot].T * decay  # [Hkv, n]
         new[:, max(0, n - S_q):] = 0
         err = new.abs() * 2.0 ** -24
@@ -115,8 +117,9 @@ def weigh(Q, LSE, W, vals, table, page, lens, scale, kind, window, decay):
             r = (big * (d + 8) + torch.where(live, x.abs(), torch.zeros_like(x)) * 2) * 2.0 ** -23 + (2 + Hq * S_q) * 2.0 ** -24
             new[:, lo:hi] += w.sum(1)
             err[:, lo:hi] += (w * r).sum(1)
-        out[p, :, slot] = new.T
-        bound[p, :, slot] = err.T + out[p, :, slot].abs() * 2.0 ** -23
+        p, slot = p[held], slot[held]
+        out[p, :, slot] = new.T[held]
+        bound[p, :, slot] = err.T[held] + out[p, :, slot].abs() * 2.0 ** -23
     return out, bound
 
 

@@ -77,6 +77,12 @@ def test_masks_and_decay(store, kind, window, decay):
     _weigh([0, 1, 2, 40, 129, 700], 6, 2, 3, 128, 32, store, kind, window, decay)
 
 
+def test_released_pages_before_the_window():
+    """Sequences whose first pages are gone, beside one whose page is the pool's first."""
+    for seed in range(8):
+        _weigh([255, 99, 128, 0, 17, 602, 1], 4, 4, 2, 64, 80, "bf16", kind=WINDOW, window=17, seed=seed)
+
+
 def test_steps_add_up():
     _weigh([300, 20], 4, 2, 1, 64, 16, "bf16", decay=0.5, reps=1)
     a = _weigh([2000, 900, 30], 8, 2, 1, 128, 64, "bf16", seed=4)
