@@ -417,6 +417,14 @@ __device__ __forceinline__ float row_weights(uint32_t t_s, int live, float scale
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 // 16 codes as fp16 numbers times f (two of them), two 16-byte pieces.
 __device__ __forceinline__ void widen16(const uint4& v, uint32_t f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -472,14 +480,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
     if (tid == 0) {
         prefetch_tmap(&p.tm);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.k_full[i]), E4M3 ? 4 : 1);
-            mbar_init(smem_u32(&sh.v_full[i]), E4M3 ? 4 : 1);
+            mbar_init(smem_u32(&sh.k_full[i]), E4M3 ? 2 : 1);
+            mbar_init(smem_u32(&sh.v_full[i]), E4M3 ? 2 : 1);
             mbar_init(smem_u32(&sh.k_empty[i]), 2);
             mbar_init(smem_u32(&sh.v_empty[i]), 2);
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
             mbar_init(smem_u32(&sh.c_full[i]), 1);
-            mbar_init(smem_u32(&sh.c_empty[i]), 4);
+            mbar_init(smem_u32(&sh.c_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
@@ -585,6 +593,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 const float top =
                     (live >= kTile ? row_max<false>(t_s, live, kept) : row_max<true>(t_s, live, kept)) * scale;
                 if constexpr (E4M3) {
+                    wait(smem_u32(&sh.v_full[t % kValueStages]), (t / kValueStages) & 1, watch);
+                    __syncwarp();
                     const float ev = (float)*reinterpret_cast<volatile int*>(&sh.tile_exp[1][t % 4]);
                     // the reference of weight times factor moves (as below; a whole number, so that M - ev is exact)
                     if (__any_sync(0xFFFFFFFFu, top + ev > M + kMost)) {
@@ -765,76 +775,64 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             }
         }
     } else if (warp < R::kLoad) {
-        // =================================================== E4M3: codes to tiles of fp16 numbers
-        constexpr int kLanes = D / 16, kAtOnce = 128 / kLanes, kEach = kTile / kAtOnce;  // lanes of a row, rows at once
-        const int ltid = tid - 32 * R::kWiden, r0 = ltid / kLanes, c = ltid % kLanes;
-        const uint32_t codes0 = smem_u32(smem) + C::kOffCodes;
-        int n = 0, t = 0;  // tiles of keys and of values; of positions
+        // =================================================== E4M3: codes to tiles of fp16 numbers, two warps the keys', two the
+        // values': a tile's waits, loads and fence are a chain of 1000 clocks and more, and so two of them run at once
+        constexpr int kLanes = D / 16, kAtOnce = 64 / kLanes, kEach = kTile / kAtOnce;  // lanes of a row, rows at once
+        static_assert(kEach == 2 * kLanes, "a lane has the factors of two rows");
+        const int gtid = tid % 64, r0 = gtid / kLanes, c = gtid % kLanes, kv = warp / 2 % 2;
+        const int stages = kv ? kValueStages : kKeyStages;
+        const uint32_t codes0 = smem_u32(smem) + C::kOffCodes, places = kv ? s_v : s_k;
+        const uint32_t full = smem_u32(kv ? sh.v_full : sh.k_full), empty = smem_u32(kv ? sh.v_empty : sh.k_empty);
+        int n = kv, t = 0;  // tiles of keys and of values; of positions
         bool ok = true;
         while (s.at < s.end && ok) {
             stretch_open(p, sh, over, s);
             int most = 0;  // the largest exponent of the stretch's tiles of values
-            for (int g = s.g0; g < s.g1 && ok; ++g, ++t) {
-                const int live = s.len - g * kTile;
-                int top[2];  // the largest exponents of the tile's keys and values
+            for (int g = s.g0; g < s.g1; ++g, ++t, n += 2) {
+                const int live = s.len - g * kTile, from = n % C::kCodeStages, st = t % stages;
+                ok = wait(smem_u32(&sh.c_full[from]), (n / C::kCodeStages) & 1, watch);
+                uint4 v[kEach];
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int from = n % C::kCodeStages, stages = kv ? kValueStages : kKeyStages, st = t % stages;
-                    if (!kv) {  // (the values' exponents early: the weights wait for them)
-                        ok = ok && wait(smem_u32(&sh.c_full[from]), (n / C::kCodeStages) & 1, watch) &&
-                             wait(smem_u32(&sh.c_full[(n + 1) % C::kCodeStages]), ((n + 1) / C::kCodeStages) & 1, watch);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) top[x] = largest_exponent(sh.exps[(n + x) % C::kCodeStages], live);
-                        most = max(most, top[1]);
-                        top[1] = max(top[1], most - kApart);
-                    }
-                    const int my_row = c * kAtOnce + r0, my_e = sh.exps[from][my_row];  // (row i = c of this lane's below)
-                    uint4 v[kEach];
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) {
-                        const int row = i * kAtOnce + r0, sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (row < live) {
-                            const uint32_t at = codes0 + from * C::kCodes + row * D + 16 * sw;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                                         : "r"(at)
-                                         : "memory");
-                        }
-                    }
-                    const uint32_t factor =
-                        my_row >= live ? 0u : my_e == 255 ? 0x7E007E00u : half_power(my_e - top[kv] + kUp);  // (255: NaN)
-                    if (ok && t >= stages)
-                        ok = wait(smem_u32(kv ? &sh.v_empty[st] : &sh.k_empty[st]), (t / stages - 1) & 1, watch);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
-                    // (of four tiles: keys come two tiles ahead of the weights, where a stream has every other tile)
-                    if (!kv && ltid < 2) *reinterpret_cast<volatile int*>(&sh.tile_exp[ltid][t % 4]) = ltid ? top[1] : top[0];
-                    const uint32_t dst = (kv ? s_v : s_k) + st * C::kBytes + (c / 4) * C::kPart;
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) {
-                        const int row = i * kAtOnce + r0, x = 2 * (c % 4);
-                        uint4 lo, hi;
-                        widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor, i, kLanes), lo, hi);
-                        // the lanes of a row's second half begin with the other piece: all 32 banks at once
-                        const bool turned = c >= 4;
-                        const uint4 a = turned ? hi : lo, b = turned ? lo : hi;
-                        const uint32_t at = dst + row * 128;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x + turned) ^ (row & 7)) * 16),
-                                     "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w)
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((x + !turned) ^ (row & 7)) * 16),
-                                     "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(kv ? &sh.v_full[st] : &sh.k_full[st]));
+                for (int i = 0; i < kEach; ++i) {
+                    const int row = i * kAtOnce + r0, sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (row < live) v[i] = lds16(codes0 + from * C::kCodes + row * D + 16 * sw);
                 }
+                int top = largest_exponent(sh.exps[from], live);
+                if (kv) {
+                    most = max(most, top);
+                    top = max(top, most - kApart);
+                }
+                uint32_t factor[2];  // of the lane's rows i = c and kLanes + c
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row = (x * kLanes + c) * kAtOnce + r0, e = sh.exps[from][row];
+                    factor[x] = row >= live ? 0u : e == 255 ? 0x7E007E00u : half_power(e - top + kUp);  // (255: NaN)
+                }
+                if (ok && t >= stages) ok = wait(empty + 8 * st, (t / stages - 1) & 1, watch);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
+                // (of four tiles: keys come two tiles ahead of the weights, where a stream has every other tile)
+                if (gtid == 0) *reinterpret_cast<volatile int*>(&sh.tile_exp[kv][t % 4]) = top;
+                const uint32_t dst = places + st * C::kBytes + (c / 4) * C::kPart;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int row = i * kAtOnce + r0, x = 2 * (c % 4);
+                    uint4 lo, hi;
+                    widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor[i / kLanes], i % kLanes, kLanes), lo, hi);
+                    // the lanes of a row's second half begin with the other piece: all 32 banks at once
+                    const bool turned = c >= 4;
+                    const uint32_t at = dst + row * 128;
+                    sts16(at + ((x + turned) ^ (row & 7)) * 16, turned ? hi : lo);
+                    sts16(at + ((x + !turned) ^ (row & 7)) * 16, turned ? lo : hi);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8 * st);
             }
         }
     } else {
