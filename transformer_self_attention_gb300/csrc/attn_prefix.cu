@@ -25,9 +25,10 @@
 //   E4M3 pages: a warp loads codes and exponents to places of their own, and four warps widen them to tiles of fp16 numbers,
 //   relative to the tile's largest exponent (below).  Every operand is fp16 then: the queries relative to their row's
 //   largest element, the weights relative to the largest product of weight and factor.  A pair of codes costs a
-//   conversion and a product; as bf16 numbers, which need no common exponents, it was six instructions of warps that the products
-//   wait for: 429 against 354 us for 4096 rows to a head behind 16K positions, 54.5 against 52 us for 256 (bf16 pages: 264 us for
-//   the first).  (Loaded by the four warps to registers, a tile ahead, the codes came late: 68 us.)
+//   conversion and a product; as bf16 numbers, which need no common exponents, it was six instructions of warps that the
+//   products wait for: 429 us for 4096 rows to a head behind 16K positions, now 322 (bf16 pages: 264), and 54.5 for 256 rows,
+//   now 51.5.  Two of the warps take the keys and two the values (all four in turn: 354 us; codes loaded to registers by
+//   the four themselves, a tile ahead, came late, 68 us for 256 rows).
 //   last two warps: a stream each, one thread issues its products (one thread for both left gaps between them: a wait
 //   that is already over costs it 130 cycles, four of them to 1030 cycles of products)
 #include <cuda_bf16.h>
