@@ -654,11 +654,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
             const long long at = 2 * ((long long)p.Hkv * p.rows * members0 + (long long)s.h * all + s.row0) +
                                  stream * (s.two() ? kTile : s.rows) + row + (long long)kRows * blockIdx.x;
             if (mine) p.part_ml[at] = make_float2(m, l);
-            if (steps == 0) continue;
-            wait(o_full, stretch & 1, watch);
+            wait(o_full, stretch++ & 1, watch);  // (without tiles, too: the thread of the products has been through the stretch)
             __syncwarp();
             tc_fence_after();
-            ++stretch;
+            if (steps == 0) continue;
             float* o = p.part_o + at * D;
             const float half = !E4M3 || m == ninf ? 1.f : ex2(0.5f * (M - m - kOne));  // (its square may pass a float's range)
 #pragma unroll
@@ -855,6 +854,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                 const int steps = s.steps(stream);
                 const uint32_t q = s_q + (two ? stream * C::kBytes : 0);
                 ok = wait(smem_u32(&sh.q_full), stretch++ & 1, watch);
+                // A stream without tiles announces its output all the same: the rows wait for it before they announce the next
+                // stretch's queries, which would otherwise be the second phase of q_full since this thread last looked, and a
+                // wait does not tell that from the first.
+                if (ok && steps == 0) mbar_arrive(smem_u32(&sh.o_full[stream]));
                 // Keys of a tile that the other stream uses, where there is one place for all: each stream sees every filling
                 // of it (a wait tells one from the next, not from the one after that), and gives the place free.
                 auto skip = [&](int t) {
