@@ -142,7 +142,9 @@ __device__ __forceinline__ void load_parts(uint32_t addr, float (&hi)[8], float 
     }
 }
 
-template <int D, int RP>
+// WHOLE: units that are not cut leave unscaled sums (p.whole_o) in place of O and LSE.  A kernel of its own: as a branch of the
+// same one it cost the others registers, 57.9 -> 59.5 us for 8 sequences of 32 rows a head (107 -> 109 with 64).
+template <int D, int RP, bool WHOLE>
 __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
     paged_e4m3_kernel(const __grid_constant__ PagedParams p) {
     using C = Cfg<D, RP>;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
     if (warp == kLoader) {
         // =================================================== loads: a batch of four tiles, eight lanes each
         int g = 0, st = 0, n = 0;
-        const int box = p.box_rows, part = lane % 8;
+        const int box = p.box_rows, part = lane % 8, halves = p.units > p.Hkv;  // (a head's rows in two blocks)
         const uint32_t box_bytes = 2 * box * D + 2 * box;
         struct Batch {
             int tiles, unit, slot;
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
             if (lane / 8 < f.tiles && 16 * part % box == 0 && pos < w.len && pos + box > w.seen) {
                 const int index = (unsigned)pos / (unsigned)p.c.page;
                 f.slot = pos - index * p.c.page;
-                const int head = w.h / (p.units / p.Hkv);
+                const int head = w.h >> halves;
                 int page = p.t.pages[w.b * p.t.stride + head * p.t.head_stride + index];
                 if (page < 0 || page >= p.c.n_pages) {
                     atomicOr(p.c.err, kCacheErrPage);
@@ -538,10 +540,10 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const float by = __shfl_sync(0xFFFFFFFFu, inv, r);
-                out[r] = !final || p.whole_o ? acc[r] : none >> r & 1 ? 0.f : acc[r] * by;
+                out[r] = !final || WHOLE ? acc[r] : none >> r & 1 ? 0.f : acc[r] * by;
             }
             if (gtid < D) {
-                if (final && p.whole_o) {
+                if (WHOLE && final) {
                     float* o = p.whole_o + (out0 + row0) * D + gtid;
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
                 for (int r = 1; r < kRows; ++r) ref = mine == r ? m[r] : ref;
                 const float2 ml = make_float2(unset >> mine & 1 ? ninf : ref, L);
                 if (!final) __stcg(&p.part_ml[slot + my_row], ml);
-                else if (p.whole_o) __stcg(&p.whole_ml[out0 + my_row], ml);
+                else if (WHOLE) __stcg(&p.whole_ml[out0 + my_row], ml);
                 else if (p.lse) p.lse[out0 + my_row] = (ref + log2f(L)) * 0.6931471805599453f;
             }
             if (w.g0 == 0 && tid == 0) paged_record_cut(p, cuts, shape, sh.cost, w, final);
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(Shared<RP>::kThreads, (RP <= 16 ? 2 : 1))
 
 template <int D, int RP>
 cudaError_t launch_rp(const PagedParams& p, int grid, cudaStream_t stream) {
-    auto* f = paged_e4m3_kernel<D, RP>;
+    auto* f = p.whole_o ? paged_e4m3_kernel<D, RP, true> : paged_e4m3_kernel<D, RP, false>;
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(f), Cfg<D, RP>::kSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(f, dim3((unsigned)grid), Cfg<D, RP>::kThreads, Cfg<D, RP>::kSmem, stream, p);
