@@ -567,7 +567,9 @@ __global__ void __launch_bounds__(kSelectThreads, RT == 1 ? kSelectBlocks : 2) s
             for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], o));
             const uint32_t ek = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * pair + k));
             const int i = i0 + 2 * pair + k;
-            if (quad == k && i < m) first_keys[i] = ek == 255 ? 0xFF800000u : ordered(best[k] * __uint_as_float(ek << 23));
+            // (2^-20 of the score: below 2^128 for every exponent, and down to 2^-146, still exactly)
+            if (quad == k && i < m)
+                first_keys[i] = ek == 255 ? 0xFF800000u : ordered(best[k] * 0x1p-20f * __uint_as_float(ek << 23));
         }
     }
     if (astray && h == 0) atomicOr(p.c.err, kCacheErrPage);
