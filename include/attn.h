@@ -867,9 +867,9 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
  *
  * Rounding: over the prefix scores and sums are float32; weights are rounded for the second product, after their sum is taken:
  * over bf16 pages to bf16 (2^-9 of a weight).  Over E4M3 pages to fp16 (2^-12 of a weight, and 2^-31 of the largest
- * product of weight and value factor); queries, keys and values are held to 2^-40 of their row's largest element and of
- * the largest factor among 128 positions, values of tiles with smaller factors to 2^-72 of the largest factor before them.  Over
- * the own positions as in attn_paged_forward.  Parts are joined in float32, and O is rounded once.  What is said there of
+ * product of weight and value factor); queries are held to 2^-39 of their row's largest element, keys and values to 2^-32 of
+ * the largest factor among 128 positions, and values of 128 positions with factors below 2^-40 of the largest before them to
+ * 2^-72 of that.  Over the own positions as in attn_paged_forward.  Parts are joined in float32, and O is rounded once.  What is said there of
  * infinities and of queries that are not finite holds here.
  *
  * A handle owns the parts' memory; it must not be used by two calls in flight at once, captured graphs included.

@@ -85,8 +85,10 @@ struct Cfg {
 };
 constexpr float kRescale = 8.f;  // log2 of how far a score may pass the reference
 // E4M3: tiles of codes become fp16 numbers, code * 2^(e - E + 7) with E the largest exponent of the tile's rows: 448 * 2^7 is the
-// most, and factors of at least 2^-15 are exact.  Rows of the queries become fp16 numbers below 2^15.
-constexpr int kUp = 7, kOne = 127 + kUp;
+// most, and factors of at least 2^-15 are exact.  Below that a code is rounded to a step of 2^-24, off by 2^-32 of 2^E at
+// most: once, by a factor of 2^-24 or more as an fp16 number, by two (the first of them exact) for smaller ones.  Rows of the
+// queries become fp16 numbers below 2^15.
+constexpr int kUp = 7, kOne = 127 + kUp, kExact = -15, kSmallest = -24;
 // Weights are fp16 numbers too, relative to a reference M of weight times 2^E: from 2^7 for the largest when M moves, up to 2^15.
 constexpr float kMost = 15.f, kFirst = 7.f;
 // A tile of values has an exponent of at least the largest so far less kApart, so that the weights of a tile of tiny
@@ -425,6 +427,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Eight fp16 numbers times f (two of them).
+__device__ __forceinline__ void scale8(uint4& v, uint32_t f) {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v.x) : "r"(f));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v.y) : "r"(f));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v.z) : "r"(f));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v.w) : "r"(f));
 }
 // 16 codes as fp16 numbers times f (two of them), two 16-byte pieces.
 __device__ __forceinline__ void widen16(const uint4& v, uint32_t f, uint4& lo, uint4& hi) {
@@ -804,11 +813,23 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     top = max(top, most - kApart);
                 }
                 uint32_t factor[2];  // of the lane's rows i = c and kLanes + c
+                int power[2];        // log2 of it
+                bool far = false;    // a row of the warp needs two factors
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int row = (x * kLanes + c) * kAtOnce + r0, e = sh.exps[from][row];
-                    factor[x] = row >= live ? 0u : e == 255 ? 0x7E007E00u : half_power(e - top + kUp);  // (255: NaN)
+                    power[x] = row >= live || e == 255 ? 0 : e - top + kUp;
+                    factor[x] = row >= live ? 0u : e == 255 ? 0x7E007E00u : half_power(power[x]);  // (255: NaN)
+                    far |= power[x] < kSmallest;
                 }
+                far = __any_sync(0xFFFFFFFFu, far);
+                uint32_t rest[2] = {0, 0};
+                if (far)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (power[x] < kExact) factor[x] = half_power(kExact);
+                        rest[x] = half_power(min(0, power[x] - kExact));
+                    }
                 if (ok && t >= stages) ok = wait(empty + 8 * st, (t / stages - 1) & 1, watch);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
@@ -824,6 +845,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     const int row = i * kAtOnce + r0, x = 2 * (c % 4);
                     uint4 lo, hi;
                     widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor[i / kLanes], i % kLanes, kLanes), lo, hi);
+                    if (far) {
+                        const uint32_t f = __shfl_sync(0xFFFFFFFFu, rest[i / kLanes], i % kLanes, kLanes);
+                        scale8(lo, f);
+                        scale8(hi, f);
+                    }
                     // the lanes of a row's second half begin with the other piece: all 32 banks at once
                     const bool turned = c >= 4;
                     const uint32_t at = dst + row * 128;
