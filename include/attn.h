@@ -776,7 +776,8 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
  * nearest whole numbers r of at most 127 times one power of two for all of the rows, the smallest that serves,
  *   2^k max over rows sum_c max(r_c lo_c, r_c hi_c),
  * in exact arithmetic: no product of a rounded query with a key of the page is larger.  A page with exponent 255 has
- * the score +infinity.  Queries that are not finite make all scores of their sequence and head equal.
+ * the score +infinity.  Queries that are not finite count as zeros, all of their sequence and head: the scores of its other
+ * pages are equal then.
  *
  * Both calls run on the cache's device and need no workspace; codes and exponents are the caller's.
  */

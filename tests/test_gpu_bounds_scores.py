@@ -72,3 +72,18 @@ def test_keys_of_far_powers(store):
     Q = (torch.rand((1, 4, 1, d), generator=g) + 0.5).to(torch.bfloat16)
     chosen = _check(cache, codes, exps, table, n, Q, 12)
     assert chosen[0][:11] != list(range(11))
+
+
+def test_queries_that_are_not_finite_still_choose_unknown_pages_first():
+    """Pages whose keys are not all finite have the largest score there is, for queries that are not finite too; the others are
+    equal then, and the first of them follow."""
+    pages, page, d = 50, 16, 64
+    g = torch.Generator().manual_seed(6)
+    codes = torch.randint(-127, 128, (pages, 1, 2, d), generator=g).sort(dim=2).values.to(torch.int8)
+    exps = torch.full((pages, 1), 120, dtype=torch.uint8)
+    exps[30] = exps[44] = 255
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    cache = tsa.PagedCache(pages, 1, page, d)
+    Q = torch.randn((1, 2, 1, d), generator=g).to(torch.bfloat16)
+    Q[0, 1, 0, 9] = float("nan")
+    assert _check(cache, codes, exps, table, pages * page, Q, 6)[0] == [0, 1, 2, 30, 44, 49]

@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kSelectThreads, RT == 1 ? kSelectBlocks : 2) s
     if (lane == 0) sh.big[warp] = big;
     __syncthreads();
     big = __reduce_max_sync(0xFFFFFFFFu, sh.big[lane % kSelectWarps]);
-    const bool bad = big >= 0x7F80u;  // queries that are not finite choose the first pages
+    const bool bad = big >= 0x7F80u;  // not finite: zeros (the first pages, behind those of exponent 255)
     const float f = bad ? 0.f : exp2_of(-power_of(big << 16));
     const int tiles = (p.rows + 15) / 16;
 #pragma unroll
