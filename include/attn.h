@@ -784,7 +784,8 @@ attn_status attn_paged_split_host(int B, int Hkv, int S_q, int d, attn_dtype dty
 
 /*
  * attn_bounds_update -- compute the bounds of the pages that hold the last new_len[b] positions of each sequence (those
- * pages' other positions count too); other pages' bounds are left as they were.
+ * pages' other positions count too); other pages' bounds are left as they were.  To be called for all positions wherever
+ * rows have come into pages in another way than behind the last ones: eviction, copies, pages of another sequence.
  *   codes, exponents : device, as above; codes 16-byte aligned.
  *   new_len : int32 device [B], or NULL: all positions.  More than cache_len[b] counts as that.
  * A page that appears twice with different lengths gets the bounds of one of them.
@@ -849,6 +850,8 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
  *              of this call's sequences (what was there stays); with room for min(keep + recent, max_pages * page)
  *              positions.  NULL: they move within their own pages; slots behind the new lengths are left as they were, and
  *              the pages behind them are free.
+ * Bounds of pages (attn_bounds_update) are not looked at: those of the pages that rows move to are out of date then, and
+ * attn_bounds_update with new_len = NULL, the new lengths and the table of those pages computes them again.
  *   out_len  : int32 device [B], min(n, keep + recent).   kept : int32 device [B, Hkv, keep + recent], the old positions of
  *              the new ones, then -1.  Neither may be an input.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.  A sequence whose length is not followed counts as

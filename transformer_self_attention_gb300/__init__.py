@@ -1108,6 +1108,8 @@ class PageBounds:
         cache.write(K, V, page_table, cache_len, ...)
         bounds.update(page_table, cache_len, new_len)
         O, LSE = step(Q, cache, *bounds.select(Q, page_table, cache_len, keep=32))
+
+    Nothing else keeps them up to date: after PageWeights.evict, update(page_table or to_table, the new lengths).
     """
 
     def __init__(self, cache, codes=None, exponents=None):
@@ -1221,7 +1223,8 @@ class PageWeights:
         """Cut every sequence down to keep + recent positions: for each kv head the heaviest among all but the last
         ``recent``, and those.  They move to the front of the pages of to_table (int32 CUDA [B, pages], pages that hold
         nothing of these sequences), or of their own.  Returns (length, kept): the new lengths, int32 [B], and the old
-        positions of the new ones, int32 [B, Hkv, keep + recent], -1 behind them."""
+        positions of the new ones, int32 [B, Hkv, keep + recent], -1 behind them.  PageBounds of the cache are out of
+        date then where rows have moved: update(page_table or to_table, length) for all positions."""
         cache = self.cache
         B, table = cache._table(page_table, cache_len)
         keep, recent = _int(keep), _int(recent)
