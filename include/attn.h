@@ -870,8 +870,9 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
  * the own positions).  Prefixes and own positions are pages of one cache; either may end inside a page.
  *
  * Rounding: over the prefix scores and sums are float32; weights are rounded for the second product, after their sum is taken:
- * over bf16 pages to bf16 (2^-9 of a weight).  Over E4M3 pages to fp16 (2^-12 of a weight, and 2^-31 of the largest
- * product of weight and value factor); queries are held to 2^-39 of their row's largest element, keys and values to 2^-32 of
+ * over bf16 pages to bf16 (2^-8 of a weight; attn_paged_forward with up to 32 rows to a kv head: 2^-16).  Over E4M3 pages to
+ * fp16 (2^-11 of a weight, or 2^-31 of the largest product so far of the largest weight and the largest value factor among
+ * 128 positions, where that is more); queries are held to 2^-39 of their row's largest element, keys and values to 2^-32 of
  * the largest factor among 128 positions, and values of 128 positions with factors below 2^-40 of the largest before them to
  * 2^-72 of that.  Over the own positions as in attn_paged_forward.  Parts are joined in float32, and O is rounded once.  What is said there of
  * infinities and of queries that are not finite holds here.

@@ -7,7 +7,10 @@
 // a matrix, and a tile of 128 of them meets tiles of 128 positions,
 //     S [128 x 128] = Q K^T,   O [128 x d] += P V,   P = 2^(scale' S - m),
 // with tcgen05.mma: S and O in tensor memory, P written over S in 16 bits (weights of at most 2^8 relative to a reference m
-// that moves only when a score passes it by 2^8; their sum is taken in float32 before they are rounded to bf16).  The decode
+// that moves only when a score passes it by 2^8; their sum is taken in float32 before they are rounded to bf16).  Over bf16 pages
+// a weight is one bf16 number, off by 2^-8 of itself, where the decode kernel has two of them up to 32 rows to a head: O is 0.0023
+// of its norm off the exact one instead of its own rounding's 0.0017.  Two would make three products of two (one with each half),
+// 3900 clocks at the measured peak for two tiles of 128 x 128 that take 3800 now.  The decode
 // kernels (attn_paged.cu, attn_paged_e4m3.cu) attend to the own positions and leave unscaled sums in float32.  The
 // third joins the parts of every row: O = sum_k 2^(m_k - M) O_k / L, M = max m_k, L = sum_k 2^(m_k - M) l_k.
 //
