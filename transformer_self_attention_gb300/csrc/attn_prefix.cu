@@ -91,7 +91,7 @@ constexpr float kRescale = 8.f;  // log2 of how far a score may pass the referen
 // most, and factors of at least 2^-15 are exact.  Below that a code is rounded to a step of 2^-24, off by 2^-32 of 2^E at
 // most: once, by a factor of 2^-24 or more as an fp16 number, by two (the first of them exact) for smaller ones.  Rows of the
 // queries become fp16 numbers below 2^15.
-constexpr int kUp = 7, kOne = 127 + kUp, kExact = -15, kSmallest = -24;
+constexpr int kUp = 7, kOne = 127 + kUp, kExact = -15, kSmallest = -24, kNothing = -34;  // (448 * 2^-34 is rounded to zero)
 // Weights are fp16 numbers too, relative to a reference M of weight times 2^E: from 2^7 for the largest when M moves, up to 2^15.
 constexpr float kMost = 15.f, kFirst = 7.f;
 // A tile of values has an exponent of at least the largest so far less kApart, so that the weights of a tile of tiny
@@ -816,48 +816,55 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) prefix_kernel(const 
                     top = max(top, most - kApart);
                 }
                 uint32_t factor[2];  // of the lane's rows i = c and kLanes + c
-                int power[2];        // log2 of it
-                bool far = false;    // a row of the warp needs two factors
+                bool far = false;    // one of them is zero where two factors would not be
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int row = (x * kLanes + c) * kAtOnce + r0, e = sh.exps[from][row];
-                    power[x] = row >= live || e == 255 ? 0 : e - top + kUp;
-                    factor[x] = row >= live ? 0u : e == 255 ? 0x7E007E00u : half_power(power[x]);  // (255: NaN)
-                    far |= power[x] < kSmallest;
+                    const int row = (x * kLanes + c) * kAtOnce + r0, e = sh.exps[from][row], power = e - top + kUp;
+                    factor[x] = row >= live ? 0u : e == 255 ? 0x7E007E00u : half_power(power);  // (255: NaN)
+                    far |= row < live && (unsigned)(power - kNothing - 1) < kSmallest - kNothing - 1;
                 }
-                far = __any_sync(0xFFFFFFFFu, far);
-                uint32_t rest[2] = {0, 0};
-                if (far)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (power[x] < kExact) factor[x] = half_power(kExact);
-                        rest[x] = half_power(min(0, power[x] - kExact));
-                    }
                 if (ok && t >= stages) ok = wait(empty + 8 * st, (t / stages - 1) & 1, watch);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                const bool one = __all_sync(0xFFFFFFFFu, ok && !far);  // (one vote for both on the usual way)
+                if (!one && !__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
+                if (lane == 0 && one) mbar_arrive(smem_u32(&sh.c_empty[from]));  // (the warp's codes are in registers)
                 // (of four tiles: keys come two tiles ahead of the weights, where a stream has every other tile)
                 if (gtid == 0) *reinterpret_cast<volatile int*>(&sh.tile_exp[kv][t % 4]) = top;
                 const uint32_t dst = places + st * C::kBytes + (c / 4) * C::kPart;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const int row = i * kAtOnce + r0, x = 2 * (c % 4);
-                    uint4 lo, hi;
-                    widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor[i / kLanes], i % kLanes, kLanes), lo, hi);
-                    if (far) {
-                        const uint32_t f = __shfl_sync(0xFFFFFFFFu, rest[i / kLanes], i % kLanes, kLanes);
-                        scale8(lo, f);
-                        scale8(hi, f);
-                    }
+                auto store = [&](int row, const uint4& lo, const uint4& hi) {
                     // the lanes of a row's second half begin with the other piece: all 32 banks at once
                     const bool turned = c >= 4;
+                    const int x = 2 * (c % 4);
                     const uint32_t at = dst + row * 128;
                     sts16(at + ((x + turned) ^ (row & 7)) * 16, turned ? hi : lo);
                     sts16(at + ((x + !turned) ^ (row & 7)) * 16, turned ? lo : hi);
+                };
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    uint4 lo, hi;
+                    widen16(v[i], __shfl_sync(0xFFFFFFFFu, factor[i / kLanes], i % kLanes, kLanes), lo, hi);
+                    store(i * kAtOnce + r0, lo, hi);
+                }
+                if (!one) {
+                    // the rows that one factor takes to zero again, from the codes, in a loop of their own: a second factor in
+                    // the usual one, or a second copy of that, took 342 to 375 us for 4096 rows behind 16K where nothing is
+                    // far; 328 so (322 without any of this), and 416 where every tile has such rows
+#pragma unroll 1
+                    for (int i = 0; i < kEach; ++i) {
+                        const int row = i * kAtOnce + r0, power = sh.exps[from][row] - top + kUp;
+                        if (row >= live || power >= kSmallest || power <= kNothing) continue;
+                        const int sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+                        uint4 lo, hi;
+                        widen16(lds16(codes0 + from * C::kCodes + row * D + 16 * sw), half_power(kExact), lo, hi);
+                        scale8(lo, half_power(power - kExact));
+                        scale8(hi, half_power(power - kExact));
+                        store(row, lo, hi);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
