@@ -29,7 +29,7 @@
 //   relative to the tile's largest exponent (below).  Every operand is fp16 then: the queries relative to their row's
 //   largest element, the weights relative to the largest product of weight and factor.  A pair of codes costs a
 //   conversion and a product; as bf16 numbers, which need no common exponents, it was six instructions of warps that the
-//   products wait for: 429 us for 4096 rows to a head behind 16K positions, now 322 (bf16 pages: 264), and 54.5 for 256 rows,
+//   products wait for: 429 us for 4096 rows to a head behind 16K positions, now 328 (bf16 pages: 264), and 54.5 for 256 rows,
 //   now 51.5.  Two of the warps take the keys and two the values (all four in turn: 354 us; codes loaded to registers by
 //   the four themselves, a tile ahead, came late, 68 us for 256 rows).
 //   last two warps: a stream each, one thread issues its products (one thread for both left gaps between them: a wait
@@ -153,7 +153,9 @@ __device__ __forceinline__ Line prefix_plan(const PrefixParams& p, Shared& sh) {
         if (n && (head.whole == 0 || head.rest == 0 || head.rest > kTile) && units <= gridDim.x &&
             (k < gridDim.x / units || 10 * units * k >= 9 * gridDim.x)) {
             // units of the same cost: k CTAs to each, and `over` such that the cuts fall on the units' ends (a CTA with two
-            // stretches would fill its pipeline twice: 78 us for a 32K prefix, and 72.5 so), unless that leaves CTAs idle
+            // stretches would fill its pipeline twice: 78 us for a 32K prefix, and 72.5 so), unless that leaves CTAs idle.  Only
+            // here: with prefix_of the members and costs of prefixes are known after the scan below, and units of different
+            // costs have no such cuts; a caller with one prefix for all leaves prefix_of out
             const unsigned share = (max(work, kShape.least) + 1 + k - 1) / k;
             line.over = share * k - max(work, kShape.least);
             head = HeadCost(p.B * p.rows, n, line.over);

@@ -12,7 +12,7 @@
 //
 // Eviction: of each sequence and kv head the `keep` positions of largest W among all but the last `recent`, and those,
 // moved to the front in their order.  One block finds the chosen positions of a head (select.h); then rows are
-// copied, two loads and stores of 16 bytes a lane and row.  Into other pages all rows are copied at once; in place a
+// copied, 16 bytes a lane at a time.  Into other pages all rows are copied at once, eight loads under way; in place a
 // block takes a head's keys or values from front to back: a row moves forward or stays, so that what a store
 // overwrites has been read as long as the rows before it have.
 #include <cuda_bf16.h>
