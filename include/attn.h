@@ -804,7 +804,7 @@ attn_status attn_bounds_update(attn_cache_handle h, void* codes, void* exponents
  *   recent    : at least 1 + ceil((S_q - 1) / page), so that the new rows' own positions are among the chosen.
  *   out_table : int32 device [B, Hkv, keep]: the chosen entries of the page table in their order, then -1.
  *   out_len   : int32 device [B]: the positions in the chosen pages (the same for every head, as only the last page is
- *               not full).  Neither may be an input.
+ *               not full).  Neither may share memory with the other, the page table's rows or the lengths.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (rows, or max_pages or keep above 40960), ATTN_ERR_CUDA.
  */
 attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const void* exponents, int B, int Hq, int S_q,
@@ -853,7 +853,7 @@ attn_status attn_weights_accumulate(attn_cache_handle h, float* weights, int B, 
  * Bounds of pages (attn_bounds_update) are not looked at: those of the pages that rows move to are out of date then, and
  * attn_bounds_update with new_len = NULL, the new lengths and the table of those pages computes them again.
  *   out_len  : int32 device [B], min(n, keep + recent).   kept : int32 device [B, Hkv, keep + recent], the old positions of
- *              the new ones, then -1.  Neither may be an input.
+ *              the new ones, then -1.  Neither may share memory with the other, the tables' rows or the lengths.
  * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.  A sequence whose length is not followed counts as
  * empty, rows whose page is out of range are not moved; both are recorded in the cache's error word.
  */

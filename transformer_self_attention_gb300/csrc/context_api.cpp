@@ -5,8 +5,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 #include <new>
+#include <utility>
 
 #include "attn.h"
 #include "paged.h"
@@ -38,7 +38,15 @@ attn::PageTable table_of(const int* page_table, long long stride, int max_pages,
 // Positions of a row of the table fit an int with room for differences.
 bool room_ok(attn_cache_handle h, int max_pages) { return (long long)max_pages * h->c.page <= attn::kPagedMostPositions; }
 
-bool one_of(const void* p, std::initializer_list<const void*> those) { return std::find(those.begin(), those.end(), p) != those.end(); }
+// Whether `count` ints at p share memory with a row of an int array: `rows` rows of `width`, `stride` ints apart.
+bool meets(const int* p, long long count, const int* array, long long rows, long long width, long long stride) {
+    if (!array) return false;
+    const long long lo = ((long long)reinterpret_cast<uintptr_t>(p) - (long long)reinterpret_cast<uintptr_t>(array)) / 4;
+    const long long hi = lo + count;  // (both are aligned) row r holds [r stride, r stride + width)
+    if (stride == 0 || rows == 1) return lo < width && hi > 0;
+    const long long last = hi <= 0 ? -1 : std::min(rows - 1, (hi - 1) / stride);  // the last row that begins in front of hi
+    return last >= 0 && last * stride + width > lo;
+}
 
 attn_status done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
@@ -71,9 +79,7 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
                                void* stream) {
     if (!h || !codes || !aligned(codes, 16) || !exponents || !Q || !aligned(Q, 16)) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
-    if (!out_table || !aligned(out_table, 4) || !out_len || !aligned(out_len, 4) || out_table == out_len ||
-        one_of(out_table, {page_table, cache_len}) || one_of(out_len, {page_table, cache_len}))
-        return ATTN_ERR_INVALID_ARG;
+    if (!out_table || !aligned(out_table, 4) || !out_len || !aligned(out_len, 4)) return ATTN_ERR_INVALID_ARG;
     const attn_status vs = attn::validate_paged(B, Hq, h->c.Hkv, S_q, ATTN_MASK_CAUSAL, 0);
     if (vs != ATTN_OK) return vs;
     // the new rows' own positions lie in the latest pages
@@ -82,6 +88,11 @@ attn_status attn_bounds_select(attn_cache_handle h, const void* codes, const voi
     if (max_pages > attn::kSelectMostPages || keep > attn::kSelectMostPages || !room_ok(h, max_pages) ||
         (long long)B * h->c.Hkv > (1LL << 24))
         return ATTN_ERR_UNSUPPORTED;
+    const long long places = (long long)B * h->c.Hkv * keep;
+    if (meets(out_len, B, out_table, 1, places, 0)) return ATTN_ERR_INVALID_ARG;
+    for (const auto& [out, count] : {std::pair{out_table, places}, std::pair{out_len, (long long)B}})
+        if (meets(out, count, page_table, B, max_pages, table_stride) || meets(out, count, cache_len, 1, B, 0))
+            return ATTN_ERR_INVALID_ARG;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
     attn::SelectParams p{};
     p.c = h->c;
@@ -134,8 +145,7 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
     if (!h || !weights || !aligned(weights, 16) || B < 1) return ATTN_ERR_INVALID_ARG;
     if (!table_ok(page_table, table_stride, max_pages, cache_len)) return ATTN_ERR_INVALID_ARG;
     if (keep < 0 || recent < 0 || (long long)keep + recent < 1 || !out_len || !aligned(out_len, 4) || !kept ||
-        !aligned(kept, 4) || out_len == kept || one_of(out_len, {cache_len, page_table, to_table}) ||
-        one_of(kept, {cache_len, page_table, to_table}))
+        !aligned(kept, 4))
         return ATTN_ERR_INVALID_ARG;
     const long long stay = (long long)keep + recent, room = (long long)max_pages * h->c.page;
     if (to_table) {
@@ -146,6 +156,12 @@ attn_status attn_weights_evict(attn_cache_handle h, float* weights, int B, const
     if (B > ATTN_DECODE_MAX_BATCH || !room_ok(h, max_pages) || stay > attn::kPagedMostPositions ||
         (long long)B * h->c.Hkv * ((std::min(stay, room) + 7) / 8) > (1LL << 30))
         return ATTN_ERR_UNSUPPORTED;
+    const long long places = (long long)B * h->c.Hkv * stay;
+    if (meets(out_len, B, kept, 1, places, 0)) return ATTN_ERR_INVALID_ARG;
+    for (const auto& [out, count] : {std::pair{kept, places}, std::pair{out_len, (long long)B}})
+        if (meets(out, count, page_table, B, max_pages, table_stride) || meets(out, count, cache_len, 1, B, 0) ||
+            meets(out, count, to_table, B, to_max_pages, to_stride))
+            return ATTN_ERR_INVALID_ARG;
     if (!on_device(h->device)) return ATTN_ERR_INVALID_ARG;
     attn::EvictParams p{};
     p.c = h->c;
