@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kPlaceThreads) move_in_place_kernel(const __gr
             dst[k].page = -1;
             if (i >= stay) continue;
             const int from = kept[i];
-            if (from == i) continue;
+            if (from <= i) continue;  // (it stays; nothing moves back, and -1 is no place)
             const RowAt src = row_at(p, row, from);
             dst[k] = row_at(p, row, i);
             if (src.page < 0) dst[k].page = -1;
